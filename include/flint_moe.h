@@ -110,7 +110,8 @@ typedef struct {
   int32_t offset_mode;  /* FLINT_OFFSET_LOGIT or FLINT_OFFSET_SELECT */
 } flint_moe_dims;
 
-/* Largest batch (tokens per call) any entry point accepts. */
+/* Largest batch (tokens per call) of every entry point but the paged KV-cache
+ * calls, which have limits of their own. */
 #define FLINT_MOE_MAX_BATCH 256
 
 /* Human-readable name of a status code.  Never NULL. */
@@ -335,6 +336,133 @@ flint_status flint_qk_norm_rope_kv_bf16(const flint_attn_dims* dims, int32_t bat
                                         const int32_t* slot_mapping, float rope_theta, float eps,
                                         void* q_out_bf16, void* k_cache_bf16, void* v_cache_bf16,
                                         int64_t cache_slots, cudaStream_t stream);
+
+/* ---- the paged KV cache and its attention ---------------------------------
+ *
+ * A cache of n_pages pages of page_size tokens each, shared by all sequences.
+ * Token row r = page * page_size + offset of a cache holds n_kv_heads heads of
+ * head_dim values: bf16, the layout flint_qk_norm_rope_kv_bf16 writes (its slot
+ * is r), or OCP E4M3FN codes with one fp32 scale per block of FLINT_KV_BLOCK
+ * consecutive token rows and KV head (value = code * scale, the scale a power
+ * of two in [2^-40, 2^40]).  The pages give the bf16 cache ("BF16 KV cache")
+ * and the attention these calls compute -- grouped queries, causal, sliding
+ * window on some layers, learned attention sinks ([vLLM Day-0 Support for
+ * Recursive's Flint, "Flint Model Architecture"]) -- but no page layout and no
+ * 8-bit cache: those are this library's.
+ *
+ * Head layouts: head_dim 128, n_kv_heads 1, 2, 4 or 8, and 1, 2, 4 or 8 query
+ * heads per KV head (query head h reads KV head h / group); anything else is
+ * FLINT_ERR_UNSUPPORTED. */
+#define FLINT_KV_BLOCK 16
+#define FLINT_PAGED_MAX_SEQS 256
+#define FLINT_PAGED_MAX_TOKENS 8192
+
+/* Which tokens a paged call brings, and where their sequences' caches lie.  The
+ * struct is read on the host during the call, its arrays on the device when
+ * the call's kernels run.
+ *   n_seqs     sequences, 1 .. FLINT_PAGED_MAX_SEQS
+ *   max_q_len  >= 1: an upper bound of the new tokens of any one sequence.  It
+ *              chooses the attention kernel (1: next tokens; more: drafts and
+ *              prompts); the appends ignore it
+ *   page_size  tokens per page: a power of two, 16 .. 1024
+ *   max_pages  columns of page_table (>= 1; max_pages * page_size <= 2^30)
+ *   n_pages    pages of the caches (>= 1; n_pages * page_size <= 2^30)
+ *   q_start    [n_seqs + 1] int32: sequence s brings the token rows
+ *              q_start[s] .. q_start[s + 1] - 1 (none if they are equal)
+ *   kv_len     [n_seqs] int32: its tokens in the cache, the new ones included,
+ *              so that its new row i has position kv_len - (rows) + i
+ *   page_table [n_seqs, max_pages] int32: the page of its tokens
+ *              p * page_size .. (p + 1) * page_size - 1
+ * What the host cannot check is kept in bounds on the device: row numbers are
+ * clamped to the call's rows and lengths to max_pages * page_size; a page
+ * outside [0, n_pages) holds nothing (an append writes nothing there, the
+ * attention sees none of its tokens).  Rows behind the last sequence are left
+ * as they were.  Sequences may share pages they only read; a block that a call
+ * appends to must belong to one sequence.  A sequence that brings more than
+ * max_q_len rows gets undefined attention outputs for its rows. */
+typedef struct {
+  int32_t n_seqs, max_q_len, page_size, max_pages, n_pages;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+} flint_paged_batch;
+
+/* flint_qk_norm_rope_kv_bf16 for a paged cache, for next tokens and prompts
+ * alike: n_tokens rows (1 .. FLINT_PAGED_MAX_TOKENS) of any number of
+ * sequences, the head layouts above, positions and cache rows from the batch.
+ *   qkv_bf16  [n_tokens, (nq + 2 nkv) * D], q_norm_bf16 / k_norm_bf16 [D],
+ *   rope_theta, eps: as there
+ *   q_out_bf16 [n_tokens, nq, D]
+ *   k_cache_bf16, v_cache_bf16 [n_pages * page_size, nkv, D]
+ * A row whose position is negative (kv_len below the sequence's rows) writes no
+ * key and no value.  Errors (before any launch): FLINT_ERR_UNSUPPORTED for
+ * other dims; FLINT_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes;
+ * 4 for the batch's arrays and the scales), a number outside its range, a
+ * negative or non-finite rope_theta or eps, or overlapping outputs / inputs. */
+flint_status flint_qk_norm_rope_kv_paged_bf16(const flint_attn_dims* dims,
+                                              const flint_paged_batch* batch, int32_t n_tokens,
+                                              const void* qkv_bf16, const void* q_norm_bf16,
+                                              const void* k_norm_bf16, float rope_theta, float eps,
+                                              void* q_out_bf16, void* k_cache_bf16,
+                                              void* v_cache_bf16, cudaStream_t stream);
+
+/* The same into an E4M3 cache.
+ *   k_cache_e4m3, v_cache_e4m3 [n_pages * page_size, nkv, D] codes
+ *   k_scale, v_scale [n_pages * page_size / FLINT_KV_BLOCK, nkv] fp32
+ * For every block and KV head the call appends to, s is the smallest power of
+ * two whose 448-fold holds every finite new value (fp32, before any rounding),
+ * within [2^-40, 2^40].  A block that held earlier tokens of its sequence
+ * keeps the larger of s and its old scale, and if that is s their codes are
+ * rewritten to it: exact but for values that reach E4M3's subnormals.  A new
+ * value becomes the code nearest to value / s (ties to even); infinities and
+ * values beyond 448 * 2^40 saturate, NaN stays NaN. */
+flint_status flint_qk_norm_rope_kv_paged_fp8(const flint_attn_dims* dims,
+                                             const flint_paged_batch* batch, int32_t n_tokens,
+                                             const void* qkv_bf16, const void* q_norm_bf16,
+                                             const void* k_norm_bf16, float rope_theta, float eps,
+                                             void* q_out_bf16, uint8_t* k_cache_e4m3,
+                                             uint8_t* v_cache_e4m3, float* k_scale, float* v_scale,
+                                             cudaStream_t stream);
+
+/* Bytes of workspace the attention calls need (0 for unsupported dims): room
+ * for the partial results of a sequence that several CTAs share.  It depends
+ * on the dims only; one workspace serves every call, one call at a time. */
+size_t flint_attn_workspace_bytes(const flint_attn_dims* dims);
+
+/* Clears a workspace's counters (cudaMemsetAsync on `stream`).  Once before the
+ * first call that uses it; every call leaves it ready for the next one. */
+flint_status flint_attn_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Grouped-query attention over a paged bf16 cache: for the new row t of a
+ * sequence, at position p, and query head h of KV head g,
+ *   out[t,h] = sum_j e_j V[j,g] / (sum_j e_j + exp(sinks[h])),
+ *   e_j = exp(softmax_scale * q[t,h] . K[j,g]),
+ * over the cached tokens j of its sequence with p - window < j <= p (window =
+ * 0: j <= p) whose page is held.  A row that sees no token gets zeros.
+ *   q_bf16   [n_tokens, nq, D] (q_out of the append)
+ *   k_cache_bf16, v_cache_bf16 [n_pages * page_size, nkv, D]
+ *   sinks    [nq] fp32 or NULL (no term in the denominator)
+ *   softmax_scale >= 0, finite; window >= 0
+ *   out_bf16 [n_tokens, nq, D]
+ *   workspace (16-byte aligned) as flint_attn_workspace_bytes says
+ * Cache rows that no new row of a call may see do not matter, whatever bits
+ * they hold.  Scores, the running maximum, sums and outputs are fp32; each
+ * output is rounded to bf16 once.  Results do not depend on timing: the same
+ * call gives the same bits.  Errors as the appends', and FLINT_ERR_WORKSPACE
+ * for a NULL, misaligned or too small workspace. */
+flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_paged_batch* batch,
+                                   int32_t n_tokens, const void* q_bf16, const void* k_cache_bf16,
+                                   const void* v_cache_bf16, const float* sinks,
+                                   float softmax_scale, int32_t window, void* out_bf16,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* The same over an E4M3 cache with its scales. */
+flint_status flint_attn_paged_fp8(const flint_attn_dims* dims, const flint_paged_batch* batch,
+                                  int32_t n_tokens, const void* q_bf16,
+                                  const uint8_t* k_cache_e4m3, const uint8_t* v_cache_e4m3,
+                                  const float* k_scale, const float* v_scale, const float* sinks,
+                                  float softmax_scale, int32_t window, void* out_bf16,
+                                  void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Fault-injection hook for tests: arms a one-shot device-side wait, in the
  * next routing launch on this workspace, on a workspace flag that nothing ever

@@ -43,6 +43,9 @@ EXPORTS = (
     "flint_moe_debug_arm_stall", "flint_moe_gateup_bf16", "flint_moe_down_bf16",
     "flint_moe_decode_bf16_noalloc", "flint_qk_norm_rope_kv_bf16",
     "flint_moe_decode_bf16_prenorm",
+    "flint_qk_norm_rope_kv_paged_bf16", "flint_qk_norm_rope_kv_paged_fp8",
+    "flint_attn_workspace_bytes", "flint_attn_workspace_init",
+    "flint_attn_paged_bf16", "flint_attn_paged_fp8",
 )
 NOALLOC_MAX_BATCH = 8
 # Batches up to which flint_moe_decode_bf16_prenorm is one launch (the
@@ -80,6 +83,17 @@ class AttnDims(ctypes.Structure):
 
 
 ATTN_DIMS = AttnDims(N_Q_HEADS, N_KV_HEADS, HEAD_DIM)
+
+# The paged KV cache (flint_qk_norm_rope_kv_paged_*, flint_attn_paged_*).
+KV_BLOCK = 16                  # token rows that share a scale in an E4M3 cache
+PAGED_MAX_SEQS, PAGED_MAX_TOKENS = 256, 8192
+
+
+class _PagedBatchStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seqs", "max_q_len", "page_size", "max_pages",
+                                               "n_pages")] +
+                [(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")])
+
 
 _lib = None
 _P = ctypes.c_void_p
@@ -128,6 +142,22 @@ def lib() -> ctypes.CDLL:
     L.flint_qk_norm_rope_kv_bf16.restype = ctypes.c_int
     L.flint_qk_norm_rope_kv_bf16.argtypes = ([_P, _I32] + [_P] * 5 + [ctypes.c_float] * 2 +
                                              [_P] * 3 + [ctypes.c_int64, _P])
+    L.flint_qk_norm_rope_kv_paged_bf16.restype = ctypes.c_int
+    L.flint_qk_norm_rope_kv_paged_bf16.argtypes = ([_P, _P, _I32] + [_P] * 3 +
+                                                   [ctypes.c_float] * 2 + [_P] * 4)
+    L.flint_qk_norm_rope_kv_paged_fp8.restype = ctypes.c_int
+    L.flint_qk_norm_rope_kv_paged_fp8.argtypes = ([_P, _P, _I32] + [_P] * 3 +
+                                                  [ctypes.c_float] * 2 + [_P] * 6)
+    L.flint_attn_workspace_bytes.restype = _SZ
+    L.flint_attn_workspace_bytes.argtypes = [_P]
+    L.flint_attn_workspace_init.restype = ctypes.c_int
+    L.flint_attn_workspace_init.argtypes = [_P, _SZ, _P]
+    L.flint_attn_paged_bf16.restype = ctypes.c_int
+    L.flint_attn_paged_bf16.argtypes = ([_P, _P, _I32] + [_P] * 4 + [ctypes.c_float, _I32] +
+                                        [_P, _P, _SZ, _P])
+    L.flint_attn_paged_fp8.restype = ctypes.c_int
+    L.flint_attn_paged_fp8.argtypes = ([_P, _P, _I32] + [_P] * 6 + [ctypes.c_float, _I32] +
+                                       [_P, _P, _SZ, _P])
     _lib = L
     return L
 
@@ -429,6 +459,155 @@ def flint_qk_norm_rope_kv_bf16(qkv, q_norm, k_norm, positions, slot_mapping, q_o
                                             float(eps), *outs, slots, _stream(stream)), f)
 
 
+# ---------------------------------------------------------------- the paged KV cache
+
+class PagedBatch:
+    """Which tokens a paged call brings and where their sequences' caches lie
+    (flint_paged_batch): q_start int32 [n + 1], kv_len int32 [n] (the new tokens
+    included) and page_table int32 [n, max_pages], contiguous tensors on one
+    CUDA device, which a program may refill in place between calls; page_size
+    tokens per page (a power of two, 16 to 1024); max_q_len an upper bound of
+    the new tokens of any one sequence (1: the next token of each).  Checked
+    here once; the calls only check that they run on its device."""
+
+    def __init__(self, q_start, kv_len, page_table, page_size: int, max_q_len: int):
+        f = "PagedBatch"
+        if not (isinstance(page_table, torch.Tensor) and page_table.is_cuda and
+                page_table.dim() == 2):
+            _bad(f, "page_table", "a [sequences, pages] tensor on a CUDA device", page_table)
+        n, max_pages = page_table.shape
+        dev = page_table.device
+        if not (1 <= n <= PAGED_MAX_SEQS and max_pages >= 1):
+            _bad(f, "page_table", "of 1 to %d sequences and at least one page" % PAGED_MAX_SEQS,
+                 page_table)
+        page_size, max_q_len = int(page_size), int(max_q_len)
+        if page_size not in (16, 32, 64, 128, 256, 512, 1024) or max_q_len < 1:
+            raise FlintError(FLINT_ERR_INVALID_ARG, "%s: page_size %d, max_q_len %d" %
+                             (f, page_size, max_q_len))
+        self.tensors = (q_start, kv_len, page_table)  # kept alive with the batch
+        self.device, self.n_seqs, self.page_size, self.max_q_len = dev, n, page_size, max_q_len
+        self._fields = (n, max_q_len, page_size, max_pages)
+        self._pointers = (_arg(f, "q_start", q_start, _I32T, (n + 1,), dev),
+                          _arg(f, "kv_len", kv_len, _I32T, (n,), dev),
+                          _arg(f, "page_table", page_table, _I32T, (n, max_pages), dev))
+        self._struct = None
+
+    def _ref(self, n_pages):
+        """The C struct for a cache of n_pages pages."""
+        st = self._struct
+        if st is None or st.n_pages != n_pages:
+            st = self._struct = _PagedBatchStruct(*self._fields, n_pages, *self._pointers)
+        return st
+
+
+def _paged(where, name, rows, batch, k_cache, d):
+    """(rows, device, pages, C struct) of a paged call after checking its batch
+    and device; rows [n_tokens, ...] on the current CUDA device."""
+    if not isinstance(batch, PagedBatch):
+        raise FlintError(FLINT_ERR_INVALID_ARG, "%s: batch must be a PagedBatch, got %s" %
+                         (where, type(batch).__name__))
+    dev = batch.device
+    if not (isinstance(rows, torch.Tensor) and rows.device == dev and rows.dim() >= 2 and
+            1 <= rows.shape[0] <= PAGED_MAX_TOKENS):
+        _bad(where, name, "of 1 to %d token rows on %s" % (PAGED_MAX_TOKENS, dev), rows)
+    if dev.index != torch.cuda.current_device():
+        _on_current_device(where, name, rows)
+    if not (isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 and k_cache.shape[0] >= 1):
+        _bad(where, "k_cache", "a [pages, %d, %d, %d] tensor" % (batch.page_size, d.n_kv_heads,
+                                                                d.head_dim), k_cache)
+    pages = k_cache.shape[0]
+    return rows.shape[0], dev, pages, batch._ref(pages)
+
+
+def _append(f, qkv, q_norm, k_norm, batch, q_out, k_cache, v_cache, scales, dtype, rope_theta, eps,
+            stream, dims):
+    d = ATTN_DIMS if dims is None else dims
+    nq, nkv, hd = d.n_q_heads, d.n_kv_heads, d.head_dim
+    T, dev, pages, st = _paged(f, "qkv", qkv, batch, k_cache, d)
+    cache = (pages, batch.page_size, nkv, hd)
+    blocks = (pages, batch.page_size // KV_BLOCK, nkv)
+    args = (_arg(f, "qkv", qkv, _BF16, (T, (nq + 2 * nkv) * hd), dev),
+            _arg(f, "q_norm", q_norm, _BF16, (hd,), dev),
+            _arg(f, "k_norm", k_norm, _BF16, (hd,), dev))
+    outs = (_arg(f, "q_out", q_out, _BF16, (T, nq, hd), dev),
+            _arg(f, "k_cache", k_cache, dtype, cache, dev),
+            _arg(f, "v_cache", v_cache, dtype, cache, dev))
+    outs += tuple(_arg(f, n, t, _F32, blocks, dev) for n, t in scales)
+    _check(getattr(lib(), f)(ctypes.byref(d), ctypes.byref(st), T, *args, float(rope_theta),
+                             float(eps), *outs, _stream(stream)), f)
+
+
+def flint_qk_norm_rope_kv_paged_bf16(qkv, q_norm, k_norm, batch: PagedBatch, q_out, k_cache,
+                                     v_cache, rope_theta: float, eps: float = 1e-6, stream=None,
+                                     dims: AttnDims | None = None):
+    """Per-head Q/K RMSNorm + RoPE (rope_theta = 0: none) of the projection rows
+    qkv [T, (nq + 2 nkv) * 128] of a PagedBatch: query heads to q_out
+    [T, nq, 128], keys and values to k_cache / v_cache [pages, page_size, nkv,
+    128] (bf16) at the rows the batch's page table gives."""
+    _append("flint_qk_norm_rope_kv_paged_bf16", qkv, q_norm, k_norm, batch, q_out, k_cache,
+            v_cache, (), _BF16, rope_theta, eps, stream, dims)
+
+
+def flint_qk_norm_rope_kv_paged_fp8(qkv, q_norm, k_norm, batch: PagedBatch, q_out, k_cache,
+                                    v_cache, k_scale, v_scale, rope_theta: float,
+                                    eps: float = 1e-6, stream=None, dims: AttnDims | None = None):
+    """flint_qk_norm_rope_kv_paged_bf16 into an E4M3 cache: uint8 codes
+    [pages, page_size, nkv, 128] and fp32 power-of-two scales
+    [pages, page_size / 16, nkv] per 16-token block and head."""
+    _append("flint_qk_norm_rope_kv_paged_fp8", qkv, q_norm, k_norm, batch, q_out, k_cache, v_cache,
+            (("k_scale", k_scale), ("v_scale", v_scale)), _U8, rope_theta, eps, stream, dims)
+
+
+def flint_attn_workspace_bytes(dims: AttnDims | None = None) -> int:
+    return int(lib().flint_attn_workspace_bytes(ctypes.byref(ATTN_DIMS if dims is None else dims)))
+
+
+def flint_attn_workspace_init(workspace: torch.Tensor, stream=None):
+    wp, wb = _ws_only("flint_attn_workspace_init", workspace)
+    _check(lib().flint_attn_workspace_init(wp, wb, _stream(stream)), "flint_attn_workspace_init")
+
+
+def _attend(f, q, k_cache, v_cache, scales, dtype, batch, out, workspace, sinks, window,
+            softmax_scale, stream, dims):
+    d = ATTN_DIMS if dims is None else dims
+    nq, nkv, hd = d.n_q_heads, d.n_kv_heads, d.head_dim
+    T, dev, pages, st = _paged(f, "q", q, batch, k_cache, d)
+    cache = (pages, batch.page_size, nkv, hd)
+    blocks = (pages, batch.page_size // KV_BLOCK, nkv)
+    args = (_arg(f, "q", q, _BF16, (T, nq, hd), dev),
+            _arg(f, "k_cache", k_cache, dtype, cache, dev),
+            _arg(f, "v_cache", v_cache, dtype, cache, dev))
+    args += tuple(_arg(f, n, t, _F32, blocks, dev) for n, t in scales)
+    args += (_arg(f, "sinks", sinks, _F32, (nq,), dev, optional=True),)
+    o = _arg(f, "out", out, _BF16, (T, nq, hd), dev)
+    wp, wb = _ws_arg(f, workspace, dev)
+    scale = hd ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _check(getattr(lib(), f)(ctypes.byref(d), ctypes.byref(st), T, *args, scale, int(window), o, wp,
+                             wb, _stream(stream)), f)
+
+
+def flint_attn_paged_bf16(q, k_cache, v_cache, batch: PagedBatch, out, workspace, sinks=None,
+                          window: int = 0, softmax_scale: float | None = None, stream=None,
+                          dims: AttnDims | None = None):
+    """Grouped-query attention of the rows q [T, nq, 128] of a PagedBatch over
+    its bf16 cache [pages, page_size, nkv, 128], causal, over the last `window`
+    positions (0: all), with optional learned sinks fp32 [nq] in the softmax's
+    denominator, into out [T, nq, 128].  softmax_scale defaults to 128 ** -0.5;
+    workspace: new_attn_workspace()."""
+    _attend("flint_attn_paged_bf16", q, k_cache, v_cache, (), _BF16, batch, out, workspace, sinks,
+            window, softmax_scale, stream, dims)
+
+
+def flint_attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, batch: PagedBatch, out, workspace,
+                         sinks=None, window: int = 0, softmax_scale: float | None = None,
+                         stream=None, dims: AttnDims | None = None):
+    """flint_attn_paged_bf16 over an E4M3 cache (uint8 codes and fp32 scales as
+    flint_qk_norm_rope_kv_paged_fp8 writes them)."""
+    _attend("flint_attn_paged_fp8", q, k_cache, v_cache,
+            (("k_scale", k_scale), ("v_scale", v_scale)), _U8, batch, out, workspace, sinks, window,
+            softmax_scale, stream, dims)
+
+
 # ---------------------------------------------------------------- conveniences
 
 def new_workspace(max_batch: int, device="cuda", wait_limit_ns: int = 0) -> torch.Tensor:
@@ -438,4 +617,15 @@ def new_workspace(max_batch: int, device="cuda", wait_limit_ns: int = 0) -> torc
         raise FlintError(FLINT_ERR_INVALID_ARG, "new_workspace")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     flint_moe_workspace_init(ws, wait_limit_ns)
+    return ws
+
+
+def new_attn_workspace(device="cuda", dims: AttnDims | None = None) -> torch.Tensor:
+    """Allocates (through torch) and initialises a workspace of the paged
+    attention calls."""
+    n = flint_attn_workspace_bytes(dims)
+    if n == 0:
+        raise FlintError(FLINT_ERR_UNSUPPORTED, "new_attn_workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    flint_attn_workspace_init(ws)
     return ws

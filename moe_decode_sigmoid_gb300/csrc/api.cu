@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "flint_moe.h"
+#include "host_checks.h"
 #include "kernels.h"
 #include "qk_rope.h"
 
@@ -25,19 +26,6 @@ bool dims_supported(const flint_moe_dims* d) {
          (d->offset_mode == FLINT_OFFSET_LOGIT || d->offset_mode == FLINT_OFFSET_SELECT);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Required pointer: non-null and 16-byte aligned.
-bool req(const void* p) { return p != nullptr && aligned16(p); }
-// Small fp32 / int32 vectors (offsets, routing outputs): 4-byte alignment.
-bool req4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool opt4(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + bn && b0 < a0 + an;
-}
-
 flint_status check_common(const flint_moe_dims* dims, int32_t batch, void* ws, size_t ws_bytes) {
   if (dims == nullptr) return FLINT_ERR_INVALID_ARG;
   if (!dims_supported(dims)) return FLINT_ERR_UNSUPPORTED;
@@ -45,19 +33,6 @@ flint_status check_common(const flint_moe_dims* dims, int32_t batch, void* ws, s
   if (ws == nullptr || !aligned16(ws) || ws_bytes < WsLayout::total(batch))
     return FLINT_ERR_WORKSPACE;
   return FLINT_OK;
-}
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
-
-flint_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return FLINT_OK;
-  (void)cudaGetLastError();  // clear a non-sticky launch error
-  return FLINT_ERR_CUDA;
 }
 
 // Output / input aliasing rule of the decode calls.

@@ -1,0 +1,211 @@
+// api_paged.cu — the C ABI of the paged KV cache (include/flint_moe.h): the
+// append with Q/K norm and rotary embedding, and the attention over the cache.
+// Host-side argument checks, argument blocks and launches; nothing here
+// allocates or synchronises.
+#include <cmath>
+
+#include "flint_moe.h"
+#include "host_checks.h"
+#include "paged.h"
+
+using namespace flint;
+
+namespace {
+
+constexpr long long MAX_ROWS = 1ll << 30;
+
+flint_status dims_status(const flint_attn_dims* d) {
+  if (d == nullptr) return FLINT_ERR_INVALID_ARG;
+  if (d->head_dim != pg::HD) return FLINT_ERR_UNSUPPORTED;
+  const int n = d->n_kv_heads;
+  if (n != 1 && n != 2 && n != 4 && n != 8) return FLINT_ERR_UNSUPPORTED;
+  for (int g = 1; g <= pg::MAX_GROUP; g *= 2)
+    if (d->n_q_heads == n * g) return FLINT_OK;
+  return FLINT_ERR_UNSUPPORTED;
+}
+
+bool finite_nonneg(float v) { return v >= 0.0f && v <= 3.0e38f; }
+
+// Checks the dims, the batch and the call's rows, and fills the view.
+flint_status batch_view(const flint_attn_dims* dims, const flint_paged_batch* b, int32_t n_tokens,
+                        PagedView& v) {
+  const flint_status st = dims_status(dims);
+  if (st != FLINT_OK) return st;
+  if (b == nullptr || n_tokens < 1 || n_tokens > FLINT_PAGED_MAX_TOKENS || b->n_seqs < 1 ||
+      b->n_seqs > FLINT_PAGED_MAX_SEQS || b->max_q_len < 1 || b->max_pages < 1 || b->n_pages < 1)
+    return FLINT_ERR_INVALID_ARG;
+  int shift = 4;
+  while (shift < 10 && (1 << shift) != b->page_size) ++shift;
+  if ((1 << shift) != b->page_size || ((long long)b->max_pages << shift) > MAX_ROWS ||
+      ((long long)b->n_pages << shift) > MAX_ROWS)
+    return FLINT_ERR_INVALID_ARG;
+  if (!req4(b->q_start) || !req4(b->kv_len) || !req4(b->page_table)) return FLINT_ERR_INVALID_ARG;
+  v.q_start = b->q_start;
+  v.kv_len = b->kv_len;
+  v.page_table = b->page_table;
+  v.n_seqs = b->n_seqs;
+  v.n_tokens = n_tokens;
+  v.max_q = b->max_q_len;
+  v.page_shift = shift;
+  v.max_pages = b->max_pages;
+  v.n_pages = b->n_pages;
+  v.nkv = dims->n_kv_heads;
+  v.group = dims->n_q_heads / dims->n_kv_heads;
+  return FLINT_OK;
+}
+
+size_t cache_bytes(const PagedView& v, bool fp8) {
+  return ((size_t)v.n_pages << v.page_shift) * v.nkv * pg::HD * (fp8 ? 1 : 2);
+}
+size_t scale_bytes(const PagedView& v) {
+  return (((size_t)v.n_pages << v.page_shift) / pg::BLOCK) * v.nkv * 4;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+// True if one of the first n_out spans overlaps any other span.
+bool any_overlap(const Span* s, int n, int n_out) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = 0; j < n; ++j)
+      if (i != j && s[i].p != nullptr && s[j].p != nullptr && overlap(s[i].p, s[i].n, s[j].p, s[j].n))
+        return true;
+  return false;
+}
+
+flint_status append(bool fp8, const flint_attn_dims* dims, const flint_paged_batch* batch,
+                    int32_t n_tokens, const void* qkv, const void* q_norm, const void* k_norm,
+                    float rope_theta, float eps, void* q_out, void* k_cache, void* v_cache,
+                    float* k_scale, float* v_scale, cudaStream_t stream) {
+  PagedAppendArgs a;
+  const flint_status st = batch_view(dims, batch, n_tokens, a.b);
+  if (st != FLINT_OK) return st;
+  if (!req(qkv) || !req(q_norm) || !req(k_norm) || !req(q_out) || !req(k_cache) || !req(v_cache) ||
+      (fp8 && (!req4(k_scale) || !req4(v_scale))) || !finite_nonneg(rope_theta) ||
+      !finite_nonneg(eps))
+    return FLINT_ERR_INVALID_ARG;
+  const int nq = a.b.nkv * a.b.group;
+  const size_t c = cache_bytes(a.b, fp8), sc = scale_bytes(a.b);
+  const Span spans[] = {{q_out, (size_t)n_tokens * nq * pg::HD * 2},
+                        {k_cache, c},
+                        {v_cache, c},
+                        {k_scale, sc},
+                        {v_scale, sc},
+                        {qkv, (size_t)n_tokens * (nq + 2 * a.b.nkv) * pg::HD * 2},
+                        {q_norm, pg::HD * 2},
+                        {k_norm, pg::HD * 2},
+                        {a.b.q_start, (size_t)(a.b.n_seqs + 1) * 4},
+                        {a.b.kv_len, (size_t)a.b.n_seqs * 4},
+                        {a.b.page_table, (size_t)a.b.n_seqs * a.b.max_pages * 4}};
+  if (any_overlap(spans, 11, 5)) return FLINT_ERR_INVALID_ARG;
+  a.qkv = static_cast<const uint16_t*>(qkv);
+  a.q_norm = static_cast<const uint16_t*>(q_norm);
+  a.k_norm = static_cast<const uint16_t*>(k_norm);
+  a.rope = rope_theta > 0.0f;
+  for (int i = 0; i < pg::HD / 2; ++i)
+    a.inv_freq[i] = a.rope ? std::pow((double)rope_theta, -2.0 * i / pg::HD) : 0.0;
+  a.eps = eps;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return cuda_status(launch_paged_append(a, fp8, stream));
+}
+
+flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_batch* batch,
+                    int32_t n_tokens, const void* q, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const float* sinks,
+                    float softmax_scale, int32_t window, void* out, void* workspace,
+                    size_t ws_bytes, cudaStream_t stream) {
+  PagedAttnArgs a;
+  const flint_status st = batch_view(dims, batch, n_tokens, a.b);
+  if (st != FLINT_OK) return st;
+  if (!req(q) || !req(k_cache) || !req(v_cache) || !req(out) || !opt4(sinks) ||
+      (fp8 && (!req4(k_scale) || !req4(v_scale))) || !finite_nonneg(softmax_scale) || window < 0)
+    return FLINT_ERR_INVALID_ARG;
+  if (!req(workspace) || ws_bytes < paged_attn_workspace_bytes()) return FLINT_ERR_WORKSPACE;
+  const int nq = a.b.nkv * a.b.group;
+  const size_t c = cache_bytes(a.b, fp8), sc = scale_bytes(a.b);
+  const Span spans[] = {{out, (size_t)n_tokens * nq * pg::HD * 2},
+                        {workspace, ws_bytes},
+                        {q, (size_t)n_tokens * nq * pg::HD * 2},
+                        {k_cache, c},
+                        {v_cache, c},
+                        {k_scale, sc},
+                        {v_scale, sc},
+                        {sinks, (size_t)nq * 4},
+                        {a.b.q_start, (size_t)(a.b.n_seqs + 1) * 4},
+                        {a.b.kv_len, (size_t)a.b.n_seqs * 4},
+                        {a.b.page_table, (size_t)a.b.n_seqs * a.b.max_pages * 4}};
+  if (any_overlap(spans, 11, 2)) return FLINT_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return FLINT_ERR_CUDA;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.sinks = sinks;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.window = window;
+  a.out = static_cast<uint16_t*>(out);
+  a.ws = workspace;
+  return cuda_status(launch_paged_attn(a, fp8, sms, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+flint_status flint_qk_norm_rope_kv_paged_bf16(const flint_attn_dims* dims,
+                                              const flint_paged_batch* batch, int32_t n_tokens,
+                                              const void* qkv_bf16, const void* q_norm_bf16,
+                                              const void* k_norm_bf16, float rope_theta, float eps,
+                                              void* q_out_bf16, void* k_cache_bf16,
+                                              void* v_cache_bf16, cudaStream_t stream) {
+  return append(false, dims, batch, n_tokens, qkv_bf16, q_norm_bf16, k_norm_bf16, rope_theta, eps,
+                q_out_bf16, k_cache_bf16, v_cache_bf16, nullptr, nullptr, stream);
+}
+
+flint_status flint_qk_norm_rope_kv_paged_fp8(const flint_attn_dims* dims,
+                                             const flint_paged_batch* batch, int32_t n_tokens,
+                                             const void* qkv_bf16, const void* q_norm_bf16,
+                                             const void* k_norm_bf16, float rope_theta, float eps,
+                                             void* q_out_bf16, uint8_t* k_cache_e4m3,
+                                             uint8_t* v_cache_e4m3, float* k_scale, float* v_scale,
+                                             cudaStream_t stream) {
+  return append(true, dims, batch, n_tokens, qkv_bf16, q_norm_bf16, k_norm_bf16, rope_theta, eps,
+                q_out_bf16, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, stream);
+}
+
+size_t flint_attn_workspace_bytes(const flint_attn_dims* dims) {
+  return dims_status(dims) == FLINT_OK ? paged_attn_workspace_bytes() : 0;
+}
+
+flint_status flint_attn_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!req(workspace) || ws_bytes < paged_attn_workspace_bytes()) return FLINT_ERR_WORKSPACE;
+  return cuda_status(cudaMemsetAsync(workspace, 0, paged_attn_workspace_clear_bytes(), stream));
+}
+
+flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_paged_batch* batch,
+                                   int32_t n_tokens, const void* q_bf16, const void* k_cache_bf16,
+                                   const void* v_cache_bf16, const float* sinks,
+                                   float softmax_scale, int32_t window, void* out_bf16,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return attend(false, dims, batch, n_tokens, q_bf16, k_cache_bf16, v_cache_bf16, nullptr, nullptr,
+                sinks, softmax_scale, window, out_bf16, workspace, ws_bytes, stream);
+}
+
+flint_status flint_attn_paged_fp8(const flint_attn_dims* dims, const flint_paged_batch* batch,
+                                  int32_t n_tokens, const void* q_bf16,
+                                  const uint8_t* k_cache_e4m3, const uint8_t* v_cache_e4m3,
+                                  const float* k_scale, const float* v_scale, const float* sinks,
+                                  float softmax_scale, int32_t window, void* out_bf16,
+                                  void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return attend(true, dims, batch, n_tokens, q_bf16, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale,
+                sinks, softmax_scale, window, out_bf16, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
