@@ -57,6 +57,8 @@ struct PagedAttnArgs {
   uint16_t* out;           // [n_tokens, nq, HD] bf16
   void* ws;
 };
+// One row a sequence (max_q 1), and the choice between the two.
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
 
 size_t paged_attn_workspace_bytes();

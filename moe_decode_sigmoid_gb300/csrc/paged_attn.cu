@@ -1,5 +1,6 @@
 // paged_attn.cu — grouped-query attention over a paged KV cache.
 #include "paged.cuh"
+#include "paged_work.cuh"
 
 namespace flint {
 namespace {
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_attn_kernel(const __grid_con
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
-  (void)sms;
+  if (a.b.max_q == 1) return launch_paged_decode(a, fp8, sms, stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.b.n_tokens, a.b.nkv * a.b.group, 1);
   cfg.blockDim = dim3(WARPS * 32, 1, 1);
@@ -112,7 +113,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool fp8, int sms, cudaStr
              : cudaLaunchKernelEx(&cfg, paged_attn_kernel<false>, a);
 }
 
-size_t paged_attn_workspace_clear_bytes() { return 8192; }
-size_t paged_attn_workspace_bytes() { return 8192; }
+size_t paged_attn_workspace_clear_bytes() { return pg::WS_TICKETS; }
+size_t paged_attn_workspace_bytes() { return pg::attn_ws_bytes(); }
 
 }  // namespace flint
