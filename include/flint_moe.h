@@ -365,7 +365,7 @@ flint_status flint_qk_norm_rope_kv_bf16(const flint_attn_dims* dims, int32_t bat
  *              chooses the attention kernel (1: next tokens; more: drafts and
  *              prompts); the appends ignore it
  *   page_size  tokens per page: a power of two, 16 .. 1024
- *   max_pages  columns of page_table (>= 1; max_pages * page_size <= 2^30)
+ *   max_pages  columns of page_table (>= 1; max_pages * page_size <= 2^23)
  *   n_pages    pages of the caches (>= 1; n_pages * page_size <= 2^30)
  *   q_start    [n_seqs + 1] int32: sequence s brings the token rows
  *              q_start[s] .. q_start[s + 1] - 1 (none if they are equal)

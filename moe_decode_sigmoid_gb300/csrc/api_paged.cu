@@ -12,7 +12,8 @@ using namespace flint;
 
 namespace {
 
-constexpr long long MAX_ROWS = 1ll << 30;
+constexpr long long MAX_ROWS = 1ll << 30;    // token rows of a cache
+constexpr long long MAX_LENGTH = 1ll << 23;  // tokens of a sequence
 
 flint_status dims_status(const flint_attn_dims* d) {
   if (d == nullptr) return FLINT_ERR_INVALID_ARG;
@@ -36,7 +37,7 @@ flint_status batch_view(const flint_attn_dims* dims, const flint_paged_batch* b,
     return FLINT_ERR_INVALID_ARG;
   int shift = 4;
   while (shift < 10 && (1 << shift) != b->page_size) ++shift;
-  if ((1 << shift) != b->page_size || ((long long)b->max_pages << shift) > MAX_ROWS ||
+  if ((1 << shift) != b->page_size || ((long long)b->max_pages << shift) > MAX_LENGTH ||
       ((long long)b->n_pages << shift) > MAX_ROWS)
     return FLINT_ERR_INVALID_ARG;
   if (!req4(b->q_start) || !req4(b->kv_len) || !req4(b->page_table)) return FLINT_ERR_INVALID_ARG;

@@ -12,20 +12,25 @@
 //
 // Bound: the cache bytes.  16 (E4M3) or 8 (bf16) operations a byte at 8 query
 // heads a KV head are far below the tensor cores' ridge but above the CUDA
-// cores', so both products run on mma.sync m16n8k16 with the operands loaded
-// straight from global memory into fragments, without shared memory: the order
-// of the 128 elements inside a dot product and of the outputs is free, so a
-// lane's 16-byte loads are its operand words, and only V's keys have to be
-// paired (one byte permute per two codes).
-//   S = Q K^T:    A = 8 query heads (rows 8..15 zero), B = 8 keys a tile
+// cores', so both products run on mma.sync m16n8k16:
+//   S = Q K^T:     A = 8 query heads (rows 8..15 zero), B = 8 keys a tile
 //   O^T = V^T P^T: A = V^T (16 elements x 16 keys), B = P^T: the score tile's
 //                  accumulator registers are its operand registers.
+// The order of the 128 elements inside a dot product and of the outputs is
+// free, so a lane's 16-byte shared-memory loads are its operand words, and only
+// V's keys have to be paired (one byte permute per two codes).  What a
+// streaming kernel lives on is loads in flight: every warp copies its granules
+// (16 keys: 4 KiB of codes, 8 KiB of bf16) into a ring of its own with cp.async,
+// two or three of them on the way at any time, ~190 KiB an SM, with no barrier
+// between warps.  (With the granule on its way in registers instead, 64 KiB an
+// SM, 32 x 100K E4M3 took 440 us, 5.0 TB/s.)
 // Work: the (sequence, KV head) rows' 16-key granules laid end to end and cut
 // into equal shares, one per CTA (one per SM); a share's warps take its
 // granules in turn.  A row cut between CTAs leaves partial results in the
 // workspace, and the CTA that arrives last joins them in their order, so the
-// bits do not depend on timing.  The lengths are on the device: every CTA
-// computes the cut itself, by a scan over the sequences.
+// bits do not depend on timing.  Short rows are not cut (the cut moves to their
+// nearer end): a join costs microseconds.  The lengths are on the device: every
+// CTA computes the cuts itself, by a scan over the sequences.
 #include "nv_util.cuh"
 #include "paged.cuh"
 #include "paged_work.cuh"
@@ -37,19 +42,28 @@ using namespace pg;
 
 template <bool FP8>
 struct Cfg {
-  // Loads in flight are what a streaming kernel lives on: a warp keeps one
-  // granule's K and V (4 KiB of codes, 8 KiB of bf16) in registers on the way.
-  static constexpr int WARPS = FP8 ? 16 : 12;
+  static constexpr int WARPS = FP8 ? 16 : 8;
+  static constexpr int SLOTS = 3;                    // granules of a warp's ring
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int KW = FP8 ? 16 : 32;  // registers of a granule's keys (and values)
-  static constexpr int SMEM = WARPS * DEC_O * 4;
+  static constexpr int ROW = FP8 ? HD : 2 * HD;      // bytes of a head's key
+  static constexpr int SLOT = 2 * BLOCK * ROW;       // bytes of a granule: keys, then values
+  static constexpr int SMEM = WARPS * SLOTS * SLOT;  // the warps' results reuse it
+  static_assert(SMEM >= WARPS * DEC_O * 4, "the joint buffer fits");
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+               : "r"(addr));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -58,17 +72,15 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// What a warp needs of one granule besides its bytes.
-struct Granule {
-  int row;      // cache row of its first key; -1: its page is not there
-  float ks;     // E4M3: scale of its keys
-  float lv;     // E4M3: log2 of the scale of its values
-  float iv;     // E4M3: 1 / that scale
-};
+// Row r of a slot holds its 16-byte chunk c at chunk c ^ mix(r) (of each
+// 128-byte half): the two rows an 8-lane load phase of the keys touches, and
+// the four of the values, fall into distinct banks.
+__device__ __forceinline__ int mix(int r) { return ((r & 1) << 2) | ((r >> 1) & 3); }
 
-template <bool FP8>
-struct Tile {
-  uint32_t k[Cfg<FP8>::KW], v[Cfg<FP8>::KW];
+// Where the warp's granules lie: lane l holds granule 32 * batch + l.
+struct Batch {
+  int row;        // cache row of its first key; -1: its page is not there
+  float ks, vs;   // E4M3: scales of its keys and values
 };
 
 }  // namespace
@@ -76,15 +88,15 @@ struct Tile {
 template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int WARPS = Cfg<FP8>::WARPS, THREADS = Cfg<FP8>::THREADS, KW = Cfg<FP8>::KW;
-  constexpr int ES = FP8 ? 1 : 2;  // bytes of a cached element
-  extern __shared__ __align__(16) float s_o[];  // [WARPS][DEC_O]
-  __shared__ long long s_pre[MAX_SEQS + 1];     // granules (of all heads) before each sequence
-  __shared__ int4 s_seq[MAX_SEQS];              // {position, row, first granule, granules}
-  __shared__ long long s_scan[MAX_SEQS / 32];
+  constexpr int WARPS = Cfg<FP8>::WARPS, THREADS = Cfg<FP8>::THREADS, SLOTS = Cfg<FP8>::SLOTS;
+  constexpr int ROW = Cfg<FP8>::ROW, SLOT = Cfg<FP8>::SLOT;
+  extern __shared__ __align__(128) float s_o[];  // the rings; then [WARPS][DEC_O]
+  __shared__ int s_pre[MAX_SEQS + 1];            // granules (of all heads) before each sequence
+  __shared__ int4 s_seq[MAX_SEQS];               // {position, row, first granule, granules}
+  __shared__ int s_scan[MAX_SEQS / 32];
   __shared__ float s_m[WARPS * 8], s_l[WARPS * 8];
   __shared__ float s_jm[MAX_CTAS * 8], s_jl[MAX_CTAS * 8];
-  __shared__ int s_first, s_last;
+  __shared__ int s_cut[2], s_first, s_last;
   pdl_wait();
   pdl_trigger();
   const PagedView& b = a.b;
@@ -92,150 +104,166 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   const int g = lane >> 2, t = lane & 3;
   const int nq = b.nkv * b.group;
 
-  // ---- the cut: granules before every sequence -------------------------------
-  long long cnt = 0;
-  if (tid < MAX_SEQS && tid < b.n_seqs) {
-    const Seq q = load_seq(b, tid);
-    const int pos = q.first;  // one row a sequence
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int g0 = lo >> 4, n = q.n > 0 && pos >= 0 ? (pos >> 4) + 1 - g0 : 0;
-    s_seq[tid] = make_int4(q.n > 0 ? pos : -1, q.n > 0 ? q.q0 : -1, g0, n);
-    cnt = (long long)n * b.nkv;
-  }
+  // ---- the cuts ---------------------------------------------------------------
+  // Lengths are below 2^23 tokens, so 256 sequences of 8 heads stay below 2^31
+  // granules.
+  int cnt = 0, pre = 0;
+  int4 info = make_int4(-1, -1, 0, 0);
   if (tid < MAX_SEQS) {
-    long long incl = cnt;
+    if (tid < b.n_seqs) {
+      const Seq q = load_seq(b, tid);
+      const int pos = q.first;  // one row a sequence
+      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      if (q.n > 0) {
+        info = make_int4(pos, q.q0, lo >> 4, pos >= 0 ? (pos >> 4) + 1 - (lo >> 4) : 0);
+        cnt = info.w * b.nkv;
+      }
+      s_seq[tid] = info;
+    }
+    pre = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += v;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    cnt = incl;
+    if (lane == 31) s_scan[warp] = pre;
+    pre -= cnt;
   }
+  if (tid < 2) s_cut[tid] = -1;
   __syncthreads();
-  if (tid < MAX_SEQS) {
-    for (int w = 0; w < warp; ++w) cnt += s_scan[w];
-    s_pre[tid + 1] = cnt;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < MAX_SEQS / 32; ++w) {
+    if (w == warp) pre += total;
+    total += s_scan[w];
+  }
+  const int share = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), DEC_MIN_SHARE);
+  const int margin = share >> 4;
+  if (tid < MAX_SEQS && tid < b.n_seqs) {
+    s_pre[tid + 1] = pre + cnt;
     if (tid == 0) s_pre[0] = 0;
-  }
-  __syncthreads();
-  const long long total = s_pre[b.n_seqs];
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)DEC_MIN_SHARE);
-  long long cur = share * blockIdx.x;
-  const long long end = min(cur + share, total);
-  if (tid < b.n_seqs && tid < MAX_SEQS) {
-    if (s_pre[tid] <= cur && cur < s_pre[tid + 1]) s_first = tid;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long x = (long long)share * (blockIdx.x + k);
+      if (pre <= x && x < pre + cnt) {  // this sequence holds the cut: move it to a near row end
+        const int off = (int)(x - pre) % info.w, rest = info.w - off;
+        const int near = min(off, rest);
+        s_cut[k] = (int)x + (info.w <= DEC_WHOLE || near <= margin ? (off <= rest ? -off : rest) : 0);
+        if (k == 0) s_first = tid;
+      }
+    }
     // A row that sees nothing: zeros.
-    if (s_seq[tid].w == 0 && s_seq[tid].y >= 0 && tid % gridDim.x == blockIdx.x) {
-      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s_seq[tid].y * nq * HD);
+    if (info.w == 0 && info.y >= 0 && tid % gridDim.x == blockIdx.x) {
+      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)info.y * nq * HD);
       for (int i = 0; i < nq * HD / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   __syncthreads();
-  if (cur >= end) return;
+  int cur = s_cut[0];
+  const int end = s_cut[1] < 0 ? total : s_cut[1];
+  if (cur < 0 || cur >= end) return;
   int s = s_first;
 
-  const size_t tok_bytes = (size_t)b.nkv * HD * ES;  // one token row of a cache
+  const size_t tok_bytes = (size_t)b.nkv * ROW;  // one token row of a cache
+  const uint32_t ring = smem_addr(s_o) + warp * SLOTS * SLOT;
 
   while (cur < end) {
     while (cur >= s_pre[s + 1]) ++s;
     const int4 sq = s_seq[s];
-    const int rel = (int)(cur - s_pre[s]);
+    const int rel = cur - s_pre[s];
     const int kvh = rel / sq.w, off = rel - kvh * sq.w;
-    const int n = (int)min((long long)(sq.w - off), end - cur);  // granules of this segment
+    const int n = min(sq.w - off, end - cur);  // granules of this segment
     const int first_key = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
+    const int g0 = sq.z + off;                 // the first of them
 
-    // ---- the group's queries as A fragments ---------------------------------
+    // The queries' words, to arrive while the granules are looked up.
+    uint4 qw[4];
+    {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(
+          a.q + ((size_t)sq.y * nq + kvh * b.group + g) * HD);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // E4M3: elements 16t .. 16t + 15 and 64 + 16t ..; bf16: 32i + 8t .. + 7
+        const int at = FP8 ? (i >> 1) * 128 + 32 * t + (i & 1) * 16 : 64 * i + 16 * t;
+        qw[i] = g < b.group ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+
+    const int mine_n = n > warp ? (n - warp + WARPS - 1) / WARPS : 0;
+    Batch now{-1, 0.0f, 0.0f}, old{-1, 0.0f, 0.0f};
+    auto look_up = [&](int batch) {
+      const int i = warp + WARPS * (32 * batch + lane);
+      old = now;
+      now.row = -1;
+      if (i < n) {
+        now.row = cache_row(b, s, (g0 + i) << 4);
+        if (FP8 && now.row >= 0) {
+          const size_t at = (size_t)(now.row >> 4) * b.nkv + kvh;
+          now.ks = __ldg(a.k_scale + at);
+          now.vs = __ldg(a.v_scale + at);
+        }
+      }
+    };
+    // Granule i of the warp on its way into slot i % SLOTS.
+    const int cr = FP8 ? lane >> 3 : lane >> 4, cc = FP8 ? lane & 7 : lane & 15;
+    const size_t src0 = (size_t)cr * tok_bytes + (size_t)kvh * ROW + 16 * cc;
+    auto issue = [&](int i) {
+      if (i < mine_n) {
+        if ((i & 31) == 0) look_up(i >> 5);
+        const int row = __shfl_sync(0xffffffffu, now.row, i & 31);
+        if (row >= 0) {
+          constexpr int STEP = FP8 ? 4 : 2;  // rows a warp copies at a time
+          const size_t at = (size_t)row * tok_bytes + src0;
+          const uint8_t* k = static_cast<const uint8_t*>(a.k_cache) + at;
+          const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
+          const uint32_t dst = ring + (i % SLOTS) * SLOT + cr * ROW;
+#pragma unroll
+          for (int j = 0; j < BLOCK / STEP; ++j) {
+            const int c = cc ^ mix(cr + STEP * j);
+            cp_async16(dst + j * STEP * ROW + 16 * c, k + (size_t)(STEP * j) * tok_bytes);
+            cp_async16(dst + BLOCK * ROW + j * STEP * ROW + 16 * c, v + (size_t)(STEP * j) * tok_bytes);
+          }
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) issue(i);
+
+    // ---- the group's queries as A fragments -----------------------------------
     // E4M3: f16, each head scaled by a power of two so that its largest element
     // lies in [2^14, 2^15): a bf16 element is then exact down to 2^-31 of it.
     uint32_t qa[8][2];
     float qs = a.scale_log2;
-    {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(
-          a.q + ((size_t)sq.y * nq + kvh * b.group + g) * HD);
-      const bool live = g < b.group;
-      if constexpr (FP8) {
-        uint4 w[4];  // elements 16t .. 16t + 15 and 64 + 16t ..
+    if constexpr (FP8) {
+      float mx = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = live ? *reinterpret_cast<const uint4*>(src + (i >> 1) * 128 + 32 * t + (i & 1) * 16)
-                      : make_uint4(0u, 0u, 0u, 0u);
-        float mx = 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(x[j])), fabsf(bf_hi(x[j]))));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      qs *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(x[j])), fabsf(bf_hi(x[j]))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        qs *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int j = 0; j < 4; ++j)
+          qa[2 * i + (j >> 1)][j & 1] = nvu::f16x2_of(bf_lo(x[j]) * up, bf_hi(x[j]) * up);
+      }
+    } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            qa[2 * i + (j >> 1)][j & 1] = nvu::f16x2_of(bf_lo(x[j]) * up, bf_hi(x[j]) * up);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // elements 32i + 8t .. + 7
-          const uint4 w = live ? *reinterpret_cast<const uint4*>(src + 64 * i + 16 * t)
-                               : make_uint4(0u, 0u, 0u, 0u);
-          qa[2 * i][0] = w.x;
-          qa[2 * i][1] = w.y;
-          qa[2 * i + 1][0] = w.z;
-          qa[2 * i + 1][1] = w.w;
-        }
+      for (int i = 0; i < 4; ++i) {
+        qa[2 * i][0] = qw[i].x;
+        qa[2 * i][1] = qw[i].y;
+        qa[2 * i + 1][0] = qw[i].z;
+        qa[2 * i + 1][1] = qw[i].w;
       }
     }
-
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + (size_t)kvh * HD * ES + 16 * t;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + (size_t)kvh * HD * ES + 16 * g;
-    const int g0 = sq.z + off;  // first granule
-
-    // Lane l looks up the warp's granule 32 * batch + l.
-    Granule mine{-1, 0.0f, 0.0f, 1.0f};
-    auto look_up = [&](int batch) {
-      const int i = warp + WARPS * (32 * batch + lane);
-      mine = Granule{-1, 0.0f, 0.0f, 1.0f};
-      if (i < n) {
-        mine.row = cache_row(b, s, (g0 + i) << 4);
-        if (FP8 && mine.row >= 0) {
-          const size_t at = (size_t)(mine.row >> 4) * b.nkv + kvh;
-          // A scale of zero would take a block's weights out of the sum.
-          const float vs = fmaxf(__ldg(a.v_scale + at), 7.8886090522101181e-31f);  // 2^-100
-          mine.ks = __ldg(a.k_scale + at);
-          mine.lv = log2f(vs);
-          mine.iv = 1.0f / vs;
-        }
-      }
-    };
-    Tile<FP8> tile;
-    auto load_k = [&](int row) {
-      const uint8_t* p = kbase + (size_t)(row + g) * tok_bytes;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < KW / 8; ++i) {
-          const uint4 w = ldg_stream(p + (size_t)(8 * nt) * tok_bytes + 64 * i);
-          uint32_t* d = tile.k + nt * (KW / 2) + 4 * i;
-          d[0] = w.x; d[1] = w.y; d[2] = w.z; d[3] = w.w;
-        }
-    };
-    auto load_v = [&](int row) {
-      const uint8_t* p = vbase + (size_t)(row + 2 * t) * tok_bytes;
-#pragma unroll
-      for (int key = 0; key < 4; ++key)  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-        for (int i = 0; i < KW / 16; ++i) {
-          const uint4 w = ldg_stream(p + (size_t)((key & 1) + 8 * (key >> 1)) * tok_bytes + 128 * i);
-          uint32_t* d = tile.v + key * (KW / 4) + 4 * i;
-          d[0] = w.x; d[1] = w.y; d[2] = w.z; d[3] = w.w;
-        }
-    };
 
     float o[8][4];
 #pragma unroll
@@ -244,120 +272,143 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    const int mine_n = n > warp ? (n - warp + WARPS - 1) / WARPS : 0;
-    if (mine_n > 0) {
-      look_up(0);
-      Granule cg;
-      auto pick = [&](int i) {
-        Granule x;
-        x.row = __shfl_sync(0xffffffffu, mine.row, i & 31);
-        x.ks = FP8 ? __shfl_sync(0xffffffffu, mine.ks, i & 31) : 1.0f;
-        x.lv = FP8 ? __shfl_sync(0xffffffffu, mine.lv, i & 31) : 0.0f;
-        x.iv = FP8 ? __shfl_sync(0xffffffffu, mine.iv, i & 31) : 1.0f;
-        return x;
-      };
-      cg = pick(0);
-      if (cg.row >= 0) {
-        load_k(cg.row);
-        load_v(cg.row);
+    for (int it = 0; it < mine_n; ++it) {
+      issue(it + SLOTS - 1);
+      cp_wait<SLOTS - 1>();
+      __syncwarp();  // the other lanes' copies of granule `it` too
+      // The batch of granule `it`: the issue may already be in the next one.
+      const bool behind = (it >> 5) != (min(it + SLOTS - 1, mine_n - 1) >> 5);
+      const int row = __shfl_sync(0xffffffffu, behind ? old.row : now.row, it & 31);
+      if (row < 0) continue;
+      float f = qs, lv = 0.0f, iv = 1.0f;
+      if constexpr (FP8) {
+        f *= __shfl_sync(0xffffffffu, behind ? old.ks : now.ks, it & 31);
+        // A scale of zero would take a block's weights out of the sum: 2^-100.
+        const float vs = fmaxf(__shfl_sync(0xffffffffu, behind ? old.vs : now.vs, it & 31),
+                               7.8886090522101181e-31f);
+        lv = log2f(vs);
+        iv = 1.0f / vs;
       }
-      for (int it = 0; it < mine_n; ++it) {
-        // The next granule.
-        Granule ng{-1, 0.0f, 0.0f, 1.0f};
-        if (it + 1 < mine_n) {
-          if (((it + 1) & 31) == 0) look_up((it + 1) >> 5);
-          ng = pick(it + 1);
-        }
-        float p[4];
-        if (cg.row >= 0) {
-          float c[2][4] = {};
+      const uint32_t ks = ring + (it % SLOTS) * SLOT, vsm = ks + BLOCK * ROW;
+      const int key0 = (g0 + warp + WARPS * it) << 4;
+      const bool cut = key0 < first_key || key0 + 15 > sq.x;  // a granule cut by the mask
+
+      float c[2][4] = {};
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+      for (int nt = 0; nt < 2; ++nt) {
+        const uint32_t kr = ks + (8 * nt + g) * ROW;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              if constexpr (FP8) {
-                const uint32_t w = tile.k[nt * 8 + kk];
-                nvu::mma_f16(c[nt], qa[kk][0], 0u, qa[kk][1], 0u, e4m3x2_to_f16x2(w & 0xffffu),
-                             e4m3x2_to_f16x2(w >> 16));
-              } else {
-                mma_bf16(c[nt], qa[kk][0], 0u, qa[kk][1], 0u, tile.k[nt * 16 + 2 * kk],
-                         tile.k[nt * 16 + 2 * kk + 1]);
-              }
-            }
-          const float f = FP8 ? qs * cg.ks : qs;
-          p[0] = fmaf(c[0][0], f, cg.lv);
-          p[1] = fmaf(c[0][1], f, cg.lv);
-          p[2] = fmaf(c[1][0], f, cg.lv);
-          p[3] = fmaf(c[1][1], f, cg.lv);
-          const int key0 = (g0 + warp + WARPS * it) << 4;
-          if (key0 < first_key || key0 + 15 > sq.x) {  // a granule cut by the mask
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
-              if (key < first_key || key > sq.x) {
-                p[i] = -INFINITY;
-                // whatever bits the cache holds there, they must not meet a zero weight
-#pragma unroll
-                for (int w = 0; w < KW / 4; ++w) tile.v[i * (KW / 4) + w] = 0u;
-              }
-            }
-          }
-        }
-        if (ng.row >= 0) load_k(ng.row);
-        if (cg.row >= 0) {
-          float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // The maximum moves only when it grows by more than 2^8 (or from
-          // nothing): weights stay below 2^8, and the outputs are rarely scaled.
-          if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
-            const float mn = fmaxf(m, mx);
-            const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
-            l *= f;
-            m = mn;
-            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              o[j][0] *= f0;
-              o[j][1] *= f1;
-              o[j][2] *= f0;
-              o[j][3] *= f1;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m);
-          l = fmaf((p[0] + p[1]) + (p[2] + p[3]), cg.iv, l);
+        for (int i = 0; i < ROW / 64; ++i) {  // chunks t, t + 4, ...
+          const uint4 w = lds128(kr + 16 * ((4 * i + t) ^ mix(g)));
           if constexpr (FP8) {
-            const uint32_t b0 = nvu::f16x2_of(p[0], p[1]), b1 = nvu::f16x2_of(p[2], p[3]);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {  // elements 16g + 4w + 2h, + 1
-                const uint32_t x = __byte_perm(tile.v[w], tile.v[4 + w], h ? 0x7362 : 0x5140);
-                const uint32_t y = __byte_perm(tile.v[8 + w], tile.v[12 + w], h ? 0x7362 : 0x5140);
-                nvu::mma_f16(o[2 * w + h], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                             e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), b0, b1);
-              }
+            for (int j = 0; j < 4; ++j)
+              nvu::mma_f16(c[nt], qa[4 * i + j][0], 0u, qa[4 * i + j][1], 0u,
+                           e4m3x2_to_f16x2(x[j] & 0xffffu), e4m3x2_to_f16x2(x[j] >> 16));
           } else {
-            // A weight as a bf16 pair hi + lo: 16 significant bits.
-            uint32_t h0, l0, h1, l1;
-            split_bf2(p[0], p[1], h0, l0);
-            split_bf2(p[2], p[3], h1, l1);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {  // elements 64 (w / 4) + 8g + 2 (w % 4), + 1
-              const uint32_t x0 = __byte_perm(tile.v[w], tile.v[8 + w], 0x5410);
-              const uint32_t x1 = __byte_perm(tile.v[w], tile.v[8 + w], 0x7632);
-              const uint32_t y0 = __byte_perm(tile.v[16 + w], tile.v[24 + w], 0x5410);
-              const uint32_t y1 = __byte_perm(tile.v[16 + w], tile.v[24 + w], 0x7632);
-              mma_bf16(o[w], x0, x1, y0, y1, h0, h1);
-              mma_bf16(o[w], x0, x1, y0, y1, l0, l1);
-            }
+            mma_bf16(c[nt], qa[2 * i][0], 0u, qa[2 * i][1], 0u, w.x, w.y);
+            mma_bf16(c[nt], qa[2 * i + 1][0], 0u, qa[2 * i + 1][1], 0u, w.z, w.w);
           }
         }
-        if (ng.row >= 0) load_v(ng.row);
-        cg = ng;
       }
+      float p[4];
+      p[0] = fmaf(c[0][0], f, lv);
+      p[1] = fmaf(c[0][1], f, lv);
+      p[2] = fmaf(c[1][0], f, lv);
+      p[3] = fmaf(c[1][1], f, lv);
+      uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+      if (cut) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
+          if (key < first_key || key > sq.x) {
+            p[i] = -INFINITY;
+            seen[i] = 0u;  // whatever bits the cache holds there must not meet a zero weight
+          }
+        }
+      }
+      float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // The maximum moves only when it grows by more than 2^8 (or from
+      // nothing): weights stay below 2^8, and the outputs are rarely scaled.
+      if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
+        const float mn = fmaxf(m, mx);
+        const float r = m > -INFINITY ? ex2(m - mn) : 0.0f;
+        l *= r;
+        m = mn;
+        const float r0 = __shfl_sync(0xffffffffu, r, 8 * t), r1 = __shfl_sync(0xffffffffu, r, 8 * t + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j][0] *= r0;
+          o[j][1] *= r1;
+          o[j][2] *= r0;
+          o[j][3] *= r1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m);
+      l = fmaf((p[0] + p[1]) + (p[2] + p[3]), iv, l);
+      // Keys 2t, 2t + 1, 2t + 8, 2t + 9; chunk pi(g) of each.
+      const int vc = (g >> 1) | ((g & 1) << 2);
+      if constexpr (FP8) {
+        const uint32_t b0 = nvu::f16x2_of(p[0], p[1]), b1 = nvu::f16x2_of(p[2], p[3]);
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+          w[i] = lds128(vsm + r * ROW + 16 * (vc ^ mix(r)));
+          if (cut) {
+            w[i].x &= seen[i];
+            w[i].y &= seen[i];
+            w[i].z &= seen[i];
+            w[i].w &= seen[i];
+          }
+        }
+        const uint32_t x0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, x1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+        const uint32_t y0[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, y1[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // elements 16 pi(g) + 2j, + 1
+          const uint32_t x = __byte_perm(x0[j >> 1], x1[j >> 1], j & 1 ? 0x7362 : 0x5140);
+          const uint32_t y = __byte_perm(y0[j >> 1], y1[j >> 1], j & 1 ? 0x7362 : 0x5140);
+          nvu::mma_f16(o[j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
+                       e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), b0, b1);
+        }
+      } else {
+        // A weight as a bf16 pair hi + lo: 16 significant bits.
+        uint32_t h0, l0, h1, l1;
+        split_bf2(p[0], p[1], h0, l0);
+        split_bf2(p[2], p[3], h1, l1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+            w[i] = lds128(vsm + r * ROW + 16 * ((8 * half + vc) ^ mix(r)));
+            if (cut) {
+              w[i].x &= seen[i];
+              w[i].y &= seen[i];
+              w[i].z &= seen[i];
+              w[i].w &= seen[i];
+            }
+          }
+          const uint32_t x0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, x1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+          const uint32_t y0[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, y1[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // elements 64 half + 8 pi(g) + 2j, + 1
+            const uint32_t a0 = __byte_perm(x0[j], x1[j], 0x5410), a1 = __byte_perm(x0[j], x1[j], 0x7632);
+            const uint32_t a2 = __byte_perm(y0[j], y1[j], 0x5410), a3 = __byte_perm(y0[j], y1[j], 0x7632);
+            mma_bf16(o[4 * half + j], a0, a1, a2, a3, h0, h1);
+            mma_bf16(o[4 * half + j], a0, a1, a2, a3, l0, l1);
+          }
+        }
+      }
+      __syncwarp();  // the slot is free for granule it + SLOTS
     }
+    cp_wait<0>();
+    __syncthreads();  // the rings are done with: their memory takes the results
 
     // ---- the warps' results ---------------------------------------------------
     l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -374,10 +425,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         *reinterpret_cast<float2*>(s_o + warp * DEC_O + ((2 * j + e) * 8 + g) * 8 + 2 * t) =
             make_float2(o[j][2 * e], o[j][2 * e + 1]);
     __syncthreads();
-    const bool whole = n == sq.w;
-    // CTAs that share the row, and this one's slot.
-    const long long row0 = cur - off;
-    const int c0 = (int)(row0 / share), c1 = (int)((row0 + sq.w - 1) / share);
+    // The cuts inside the row (none: it is whole here), the CTAs that share it.
+    const int row0 = cur - off;
+    const int cut0 = (row0 + margin) / share + 1, cut1 = (row0 + sq.w - margin - 1) / share;
+    const bool whole = sq.w <= DEC_WHOLE || cut0 > cut1;
+    const int c0 = cut0 - 1, c1 = cut1;
     float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0);
     for (int i = tid; i < 512; i += THREADS) {  // (tile j, lane row, head): elements d, d + 1
       const int h = i & 7, r = i >> 3, j = r >> 3, gg = r & 7;
@@ -394,7 +446,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         o1 = fmaf(src[64], f, o1);
       }
       if (whole) {
-        const int d = FP8 ? 16 * gg + 2 * j : 64 * (j >> 2) + 8 * gg + 2 * (j & 3);
+        const int pg = (gg >> 1) | ((gg & 1) << 2);
+        const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
         if (h < b.group) dec_store(a, sq.y, kvh * b.group + h, d, mm, ll, o0, o1);
       } else {
         __stcg(slot + DEC_ML + (16 * j + gg) * 8 + h, o0);
@@ -442,7 +495,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
             o0 = fmaf(__ldcg(src), f, o0);
             o1 = fmaf(__ldcg(src + 64), f, o1);
           }
-          const int d = FP8 ? 16 * gg + 2 * j : 64 * (j >> 2) + 8 * gg + 2 * (j & 3);
+          const int pg = (gg >> 1) | ((gg & 1) << 2);
+        const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
           if (h < b.group) dec_store(a, sq.y, kvh * b.group + h, d, mm, ll, o0, o1);
         }
       }

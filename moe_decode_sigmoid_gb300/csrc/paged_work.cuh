@@ -17,8 +17,8 @@ static_assert(MAX_CTAS * 4 <= WS_TICKETS, "tickets fit");
 
 // A slot of the next-token kernel: 8 maxima, 8 sums, 128 x 8 outputs.
 constexpr int DEC_ML = 16, DEC_O = HD * 8, DEC_SLOT = DEC_ML + DEC_O;
-// Fewest granules in a CTA's share.
-constexpr int DEC_MIN_SHARE = 16;
+// Fewest granules in a CTA's share, and the longest row that is never cut.
+constexpr int DEC_MIN_SHARE = 16, DEC_WHOLE = 64;
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
   return WS_TICKETS + sizeof(float) * 2 * MAX_CTAS * (size_t)DEC_SLOT;

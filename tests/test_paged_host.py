@@ -27,7 +27,7 @@ def _batch(**kw):
 
 
 BAD_BATCHES = [dict(n_seqs=0), dict(n_seqs=257), dict(max_q_len=0), dict(page_size=8), dict(page_size=48),
-               dict(page_size=2048), dict(max_pages=0), dict(n_pages=0), dict(max_pages=(1 << 26) + 1),
+               dict(page_size=2048), dict(max_pages=0), dict(n_pages=0), dict(max_pages=(1 << 19) + 1),
                dict(n_pages=(1 << 26) + 1), dict(q_start=None), dict(kv_len=A + 2), dict(page_table=None)]
 BAD_DIMS = [(32, 4, 64), (32, 3, 128), (12, 4, 128), (64, 4, 128), (0, 0, 128), (16, 16, 128), (4, 8, 128)]
 
