@@ -429,9 +429,15 @@ flint_status flint_qk_norm_rope_kv_paged_fp8(const flint_attn_dims* dims,
  * on the dims only; one workspace serves every call, one call at a time. */
 size_t flint_attn_workspace_bytes(const flint_attn_dims* dims);
 
-/* Clears a workspace's counters (cudaMemsetAsync on `stream`).  Once before the
- * first call that uses it; every call leaves it ready for the next one. */
+/* Clears a workspace's counters and error word (cudaMemsetAsync on `stream`).
+ * Once before the first call that uses it, and again after a call whose device
+ * status was not FLINT_OK; every other call leaves it ready for the next one. */
 flint_status flint_attn_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Synchronises `stream`, then reads and returns the workspace's error word:
+ * FLINT_OK, or FLINT_ERR_DEVICE_TIMEOUT if a wait inside a kernel (each is
+ * bounded by one second) ran out; that call's outputs are undefined. */
+flint_status flint_attn_get_device_status(const void* workspace, cudaStream_t stream);
 
 /* Grouped-query attention over a paged bf16 cache: for the new row t of a
  * sequence, at position p, and query head h of KV head g,

@@ -1,7 +1,7 @@
 // api_paged.cu — the C ABI of the paged KV cache (include/flint_moe.h): the
 // append with Q/K norm and rotary embedding, and the attention over the cache.
 // Host-side argument checks, argument blocks and launches; nothing here
-// allocates or synchronises.
+// allocates, and only flint_attn_get_device_status synchronises.
 #include <cmath>
 
 #include "flint_moe.h"
@@ -153,7 +153,8 @@ flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.window = window;
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
-  return cuda_status(launch_paged_attn(a, fp8, sms, stream));
+  return cuda_status(a.b.max_q == 1 ? launch_paged_decode(a, fp8, sms, stream)
+                                    : launch_paged_prompt(a, fp8, sms, stream));
 }
 
 }  // namespace
@@ -188,6 +189,18 @@ size_t flint_attn_workspace_bytes(const flint_attn_dims* dims) {
 flint_status flint_attn_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!req(workspace) || ws_bytes < paged_attn_workspace_bytes()) return FLINT_ERR_WORKSPACE;
   return cuda_status(cudaMemsetAsync(workspace, 0, paged_attn_workspace_clear_bytes(), stream));
+}
+
+flint_status flint_attn_get_device_status(const void* workspace, cudaStream_t stream) {
+  if (!req(workspace)) return FLINT_ERR_WORKSPACE;
+  uint32_t code = 0;
+  if (cudaMemcpyAsync(&code, static_cast<const char*>(workspace) + paged_attn_workspace_error_at(),
+                      sizeof(code), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FLINT_ERR_CUDA;
+  }
+  return static_cast<flint_status>(code);
 }
 
 flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_paged_batch* batch,

@@ -57,12 +57,14 @@ struct PagedAttnArgs {
   uint16_t* out;           // [n_tokens, nq, HD] bf16
   void* ws;
 };
-// One row a sequence (max_q 1), and the choice between the two.
+// One row a sequence (max_q 1), and any number.
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
 
 size_t paged_attn_workspace_bytes();
 // Leading bytes of the workspace that flint_attn_workspace_init clears.
 size_t paged_attn_workspace_clear_bytes();
+// Where its error word (a device error code) lies.
+size_t paged_attn_workspace_error_at();
 
 }  // namespace flint

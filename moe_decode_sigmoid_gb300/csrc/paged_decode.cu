@@ -72,6 +72,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ void store2(const PagedAttnArgs& a, int row, int head, int d, float o0,
+                                       float o1, float f) {
+  const size_t nq = (size_t)a.b.nkv * a.b.group;
+  *reinterpret_cast<uint32_t*>(a.out + ((size_t)row * nq + head) * HD + d) = pack_bf2(o0 * f, o1 * f);
+}
+
 // Row r of a slot holds its 16-byte chunk c at chunk c ^ mix(r) (of each
 // 128-byte half): the two rows an 8-lane load phase of the keys touches, and
 // the four of the values, fall into distinct banks.
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       if (whole) {
         const int pg = (gg >> 1) | ((gg & 1) << 2);
         const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
-        if (h < b.group) dec_store(a, sq.y, kvh * b.group + h, d, mm, ll, o0, o1);
+        if (h < b.group) store2(a, sq.y, kvh * b.group + h, d, o0, o1, row_factor(a, kvh * b.group + h, mm, ll));
       } else {
         __stcg(slot + DEC_ML + (16 * j + gg) * 8 + h, o0);
         __stcg(slot + DEC_ML + (16 * j + gg) * 8 + h + 64, o1);
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           }
           const int pg = (gg >> 1) | ((gg & 1) << 2);
         const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
-          if (h < b.group) dec_store(a, sq.y, kvh * b.group + h, d, mm, ll, o0, o1);
+          if (h < b.group) store2(a, sq.y, kvh * b.group + h, d, o0, o1, row_factor(a, kvh * b.group + h, mm, ll));
         }
       }
     }
@@ -525,5 +531,9 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaS
   return fp8 ? cudaLaunchKernelEx(&cfg, paged_decode_kernel<true>, a)
              : cudaLaunchKernelEx(&cfg, paged_decode_kernel<false>, a);
 }
+
+size_t paged_attn_workspace_bytes() { return attn_ws_bytes(); }
+size_t paged_attn_workspace_clear_bytes() { return WS_HEAD; }
+size_t paged_attn_workspace_error_at() { return WS_ERROR; }
 
 }  // namespace flint
