@@ -88,6 +88,46 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// a * k + d of two floats at once, and a + b.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t k, uint64_t d) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(k), "l"(d));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Two weights as the second product takes them (the first in the low half).
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  uint32_t r;
+  if constexpr (FP8)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Registers a thread of the calling warpgroup: 2 * 128 * 192 + 2 * 128 * 64 are
+// the 512 * 128 the block starts with.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
                : "memory");
@@ -267,6 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 8) {
     // ===== softmax, and the item's queries and outputs ===========================
+    more_registers<192>();
     const int x = warp >> 2;               // tile A or B
     const int r = tid & 127;               // row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -339,31 +380,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int slot = (tiles_before + j) & (INFO - 1);
         const int key0 = (p.kt0 + j) << 7;
         const bool masked = key0 + TILE - 1 > hi_all || key0 < lo_all;
-        const int mlo = lo - key0, mhi = hi - key0;  // columns seen
+        // What a block's scores are multiplied by; not 0, lest a masked score
+        // becomes NaN (a query of zeros, a scale of 0).
+        auto factor = [&](int blk) {
+          return fmaxf(FP8 ? qs * sh.ks[slot][blk] : qs, 1.17549435e-38f);
+        };
+        uint32_t v[4][32];  // the row's scores, then its weights
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld32(s_tm + 32 * c, v[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::wait_ld(v[c]);
+        if (masked) {  // columns outside [mlo, mhi] are not seen
+          const int mlo = lo - key0, mhi = hi - key0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i < mlo || 32 * c + i > mhi) v[c][i] = 0xff800000u;  // -infinity
+        }
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tc::ld32(s_tm + 32 * c, v);
-          tc::wait_ld(v);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float k = FP8 ? qs * sh.ks[slot][2 * c + h] : qs, lv = sh.lv[slot][2 * c + h];
-            if (!masked) {
-              float bm = __uint_as_float(v[16 * h]);
+          for (int h = 0; h < 2; ++h) {  // a block of 16 keys
+            float b4[4];
 #pragma unroll
-              for (int i = 1; i < 16; ++i) bm = fmaxf(bm, __uint_as_float(v[16 * h + i]));
-              mx = fmaxf(mx, fmaf(bm, k, lv));
-            } else {
+            for (int i = 0; i < 4; ++i) b4[i] = __uint_as_float(v[c][16 * h + i]);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int col = 32 * c + 16 * h + i;
-                const float y = fmaf(__uint_as_float(v[16 * h + i]), k, lv);
-                mx = col >= mlo && col <= mhi ? fmaxf(mx, y) : mx;
-              }
-            }
+            for (int i = 4; i < 16; ++i) b4[i & 3] = fmaxf(b4[i & 3], __uint_as_float(v[c][16 * h + i]));
+            const float bm = fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3]));
+            const float k = factor(2 * c + h);
+            mx = fmaxf(mx, fmaf(bm, k, sh.lv[slot][2 * c + h]));
           }
-        }
         const bool grow = mx > m + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = fmaxf(m, mx);
@@ -372,43 +420,49 @@ __global__ void __launch_bounds__(THREADS, 1)
           m = mn;
           if (any) {  // the products so far
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tc::ld32(o_tm + 32 * c, v);
-              tc::wait_ld(v);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t w[16];
+              tc::ld16(o_tm + 16 * c, w);
+              tc::wait_ld(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tc::st32(o_tm + 32 * c, v);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+              tc::st16(o_tm + 16 * c, w);
             }
           }
         }
         any = true;
         const float mu = m > -INFINITY ? m : 0.0f;
+        uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], w[16];
-          tc::ld32(s_tm + 32 * c, v);
-          tc::wait_ld(v);
+          uint32_t w[16];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float k = FP8 ? qs * sh.ks[slot][2 * c + h] : qs, d = sh.lv[slot][2 * c + h] - mu;
-            float sum = 0.0f;
+            const float k = factor(2 * c + h), d = sh.lv[slot][2 * c + h] - mu;
+            const uint64_t k2 = pair(k, k), d2 = pair(d, d);
+            if constexpr (FP8) sums[0] = sums[1] = 0ull;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float y0 = fmaf(__uint_as_float(v[16 * h + i]), k, d);
-              float y1 = fmaf(__uint_as_float(v[16 * h + i + 1]), k, d);
-              if (masked) {
-                const int col = 32 * c + 16 * h + i;
-                y0 = col >= mlo && col <= mhi ? y0 : -INFINITY;
-                y1 = col + 1 >= mlo && col + 1 <= mhi ? y1 : -INFINITY;
-              }
-              const float p0 = ex2(y0), p1 = ex2(y1);
-              sum += p0 + p1;
-              w[8 * h + (i >> 1)] = FP8 ? nvu::f16x2_of(p0, p1) : pack_bf2(p0, p1);
+            for (int i = 0; i < 8; ++i) {
+              float y0, y1;
+              unpair(fma2(pair(__uint_as_float(v[c][16 * h + 2 * i]),
+                               __uint_as_float(v[c][16 * h + 2 * i + 1])), k2, d2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              sums[i & 1] = add2(sums[i & 1], pair(y0, y1));
+              w[8 * h + i] = pack_p<FP8>(y0, y1);
             }
-            l = FP8 ? fmaf(sum, sh.iv[slot][2 * c + h], l) : l + sum;
+            if constexpr (FP8) {
+              float y0, y1;
+              unpair(add2(sums[0], sums[1]), y0, y1);
+              l = fmaf(y0 + y1, sh.iv[slot][2 * c + h], l);
+            }
           }
           tc::st16(s_tm + 16 * c, w);
+        }
+        if constexpr (!FP8) {
+          float y0, y1;
+          unpair(add2(sums[0], sums[1]), y0, y1);
+          l += y0 + y1;
         }
         tc::wait_st();
         tc::fence_before();
@@ -528,6 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp < 12) {
     // ===== K and V tiles ===========================================================
+    fewer_registers<64>();
     const int w4 = warp - 8;   // this warp brings keys 32 w4 .. + 31 of every tile
     constexpr int ES = FP8 ? 1 : 2;
     const size_t tok_bytes = (size_t)b.nkv * HD * ES;
@@ -668,95 +723,114 @@ __global__ void __launch_bounds__(THREADS, 1)
       tiles_before += p.n;
     }
     cp_wait<0>();
-  } else if (warp == 12 && lane == 0) {
-    // ===== the products ============================================================
-    constexpr uint32_t s_desc = tc::inst_desc(!FP8, false), o_desc = tc::inst_desc(!FP8, true);
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-    int u = 0;
-    bool ok = true;
-    auto tile_in = [&](int n) { return wait(sh, sh.full[n % C::RING], (n / C::RING) & 1); };
-    auto scores = [&](int x, int q, int n) {  // S_x = Q_q (tile in slot n)^T
+  } else {
+    // ===== the products: one warp, of which one thread issues ======================
+    fewer_registers<64>();
+    if (warp == 12) {
+      constexpr uint32_t s_desc = tc::inst_desc(!FP8, false), o_desc = tc::inst_desc(!FP8, true);
+      // Whatever steers the products is broadcast, so that it is uniform for
+      // the compiler too.
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = tc::desc_lo(q_smem, 16), k_lo = tc::desc_lo(ring, 16);
+      const uint32_t v_lo = tc::desc_lo(ring, HALF);
+      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      int u = 0;
+      bool ok = true;
+      auto tile_in = [&](int n) { return warp_wait(sh, sh.full[n % C::RING], (n / C::RING) & 1); };
+      auto scores = [&](int x, int q, int n) {  // S_x = Q_q (tile in slot n)^T
+        const uint32_t slot = (uint32_t)(n % C::RING) * (OPER >> 4);
+        if (tc::one_thread()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
-        tc::mma_ss(tmem + 128 * x, tc::smem_desc(q_smem + q * OPER + off, 16),
-                   tc::smem_desc(ring + (n % C::RING) * OPER + off, 16), s_desc, k > 0);
-      }
-      tc::commit(smem_addr(&sh.s_full[x]));
-    };
-    auto product = [&](int x, int n, bool add) {  // O_x += P_x (tile in slot n)
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
+            tc::mma_ss(tm + 128 * x, q_lo + q * (OPER >> 4) + off, k_lo + slot + off, s_desc, k > 0);
+          }
+          tc::commit(smem_addr(&sh.s_full[x]));
+        }
+        __syncwarp();
+      };
+      auto product = [&](int x, int n, bool add, bool last) {  // O_x += P_x (tile in slot n)
+        const uint32_t slot = (uint32_t)(n % C::RING) * (OPER >> 4);
+        if (tc::one_thread()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc::mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k,
-                   tc::smem_desc(ring + (n % C::RING) * OPER + k * 2048, HALF), o_desc, add || k > 0);
-    };
-    auto release = [&](int n) { tc::commit(smem_addr(&sh.empty[n % C::RING])); };
-    for (int cur = begin, it = sh.first; ok && cur < end;) {
-      const Item p = part(cur, it);
-      cur += p.n;
-      const int ld = min(p.split ? 2 : 1, p.n);
-      // Places of K_j and V_j in the order of the loads.
-      auto k_at = [&](int j) { return u + (j < ld ? j : ld + 2 * (j - ld) + 1); };
-      auto v_at = [&](int j) { return u + (j < p.n - ld ? ld + 2 * j : p.n + j); };
-      for (int q = 0; ok && q < (p.split ? 1 : 2); ++q) {
-        ok = wait(sh, sh.q_full[q], q_phase[q]);
-        q_phase[q] ^= 1;
-      }
-      tc::fence_after();
-      if (!p.split) {
-        if (!ok || !(ok = tile_in(k_at(0)))) break;
-        tc::fence_after();
-        scores(0, 0, k_at(0));
-        scores(1, 1, k_at(0));
-        release(k_at(0));
-        for (int j = 0; ok && j < p.n; ++j) {
-          const bool more = j + 1 < p.n;
-          for (int x = 0; x < 2; ++x) {
-            if (!(ok = wait(sh, sh.p_full[x], p_phase[x]))) break;
-            p_phase[x] ^= 1;
-            if (x == 0 && !(ok = tile_in(v_at(j)))) break;
-            tc::fence_after();
-            product(x, v_at(j), j > 0);
-            if (!more) tc::commit(smem_addr(&sh.o_full[x]));
-            if (x == 1) release(v_at(j));
-            if (more) {
-              if (x == 0 && !(ok = tile_in(k_at(j + 1)))) break;
+          for (int k = 0; k < 8; ++k)
+            tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, v_lo + slot + k * (2048 >> 4), o_desc,
+                       k > 0 ? 1u : (uint32_t)add);
+          if (last) tc::commit(smem_addr(&sh.o_full[x]));
+        }
+        __syncwarp();
+      };
+      auto release = [&](int n) {
+        if (tc::one_thread()) tc::commit(smem_addr(&sh.empty[n % C::RING]));
+        __syncwarp();
+      };
+      for (int cur = begin, it = sh.first; ok && cur < end;) {
+        const Item p = part(cur, it);
+        cur += p.n;
+        const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
+        const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
+        const int ld = min(split ? 2 : 1, tiles);
+        // Places of K_j and V_j in the order of the loads.
+        auto k_at = [&](int j) { return u + (j < ld ? j : ld + 2 * (j - ld) + 1); };
+        auto v_at = [&](int j) { return u + (j < tiles - ld ? ld + 2 * j : tiles + j); };
+        for (int q = 0; ok && q < (split ? 1 : 2); ++q) {
+          ok = warp_wait(sh, sh.q_full[q], q_phase[q]);
+          q_phase[q] ^= 1;
+        }
+        if (!split) {
+          if (!ok || !(ok = tile_in(k_at(0)))) break;
+          tc::fence_after();
+          scores(0, 0, k_at(0));
+          scores(1, 1, k_at(0));
+          release(k_at(0));
+          for (int j = 0; ok && j < tiles; ++j) {
+            const bool more = j + 1 < tiles;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!(ok = warp_wait(sh, sh.p_full[x], p_phase[x]))) break;
+              p_phase[x] ^= 1;
+              if (x == 0 && !(ok = tile_in(v_at(j)))) break;
               tc::fence_after();
-              scores(x, x, k_at(j + 1));
-              if (x == 1) release(k_at(j + 1));
+              product(x, v_at(j), j > 0, !more);
+              if (x == 1) release(v_at(j));
+              if (more) {
+                if (x == 0 && !(ok = tile_in(k_at(j + 1)))) break;
+                tc::fence_after();
+                scores(x, x, k_at(j + 1));
+                if (x == 1) release(k_at(j + 1));
+              }
+            }
+          }
+        } else {
+          for (int j = 0; ok && j < ld; ++j) {
+            if (!(ok = tile_in(k_at(j)))) break;
+            tc::fence_after();
+            scores(j, 0, k_at(j));
+            release(k_at(j));
+          }
+          for (int j = 0; ok && j < tiles; ++j) {
+            const int x = j & 1;
+            if (!(ok = warp_wait(sh, sh.p_full[x], p_phase[x]))) break;
+            p_phase[x] ^= 1;
+            if (!(ok = tile_in(v_at(j)))) break;
+            tc::fence_after();
+            product(x, v_at(j), j > 1, j + 2 >= tiles);
+            release(v_at(j));
+            if (j + 2 < tiles) {
+              if (!(ok = tile_in(k_at(j + 2)))) break;
+              tc::fence_after();
+              scores(x, 0, k_at(j + 2));
+              release(k_at(j + 2));
             }
           }
         }
-      } else {
-        for (int j = 0; ok && j < ld; ++j) {
-          if (!(ok = tile_in(k_at(j)))) break;
-          tc::fence_after();
-          scores(j, 0, k_at(j));
-          release(k_at(j));
-        }
-        for (int j = 0; ok && j < p.n; ++j) {
-          const int x = j & 1;
-          if (!(ok = wait(sh, sh.p_full[x], p_phase[x]))) break;
-          p_phase[x] ^= 1;
-          if (!(ok = tile_in(v_at(j)))) break;
-          tc::fence_after();
-          product(x, v_at(j), j > 1);
-          if (j + 2 >= p.n) tc::commit(smem_addr(&sh.o_full[x]));
-          release(v_at(j));
-          if (j + 2 < p.n) {
-            if (!(ok = tile_in(k_at(j + 2)))) break;
-            tc::fence_after();
-            scores(x, 0, k_at(j + 2));
-            release(k_at(j + 2));
-          }
-        }
+        u += 2 * tiles;
       }
-      u += 2 * p.n;
+      // Every product is complete before the TMEM is given back.
+      if (tc::one_thread()) tc::commit(smem_addr(&sh.drained));
+      __syncwarp();
+      mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
     }
-    // Every product is complete before the TMEM is given back.
-    tc::commit(smem_addr(&sh.drained));
-    const uint64_t deadline = globaltimer_ns() + 1000000000ull;
-    mbar_wait(smem_addr(&sh.drained), 0, deadline);
   }
   __syncwarp();
   tc::fence_before();
