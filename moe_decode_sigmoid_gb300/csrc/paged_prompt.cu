@@ -21,10 +21,14 @@
 // tiles of a prompt (they share the keys they load), or, where a sequence
 // brings no more than one tile, the even and the odd key tiles of that one.
 //   warps 0-3, 4-7: softmax of A, of B; a thread has a row (TMEM lane)
-//   warps 8-11:     bring K and V tiles into a ring in the operands' layout
-//                   (cp.async; E4M3 codes by a staging ring, widened to f16);
-//                   rows that no query of the item sees are zeroed there
-//   warp 12:        one thread issues every mma
+//   warp 13:        looks pages up and copies K and V tiles by TMA, a box a page
+//                   (16 to 128 keys): bf16 into the operand ring, E4M3 codes into
+//                   a staging ring; a page that is not there is a box beyond the
+//                   cache, which fills with zeros
+//   warps 8-11:     widen the codes to f16 into the operand ring (E4M3), and zero
+//                   the rows of V that no query of the item sees: whatever bits
+//                   lie there must not meet a zero weight
+//   warp 12:        issues every mma
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each; P takes its S's place.  O is
 // rescaled only when a row's maximum grows by more than 2^8.
 //
@@ -35,6 +39,7 @@
 #include "paged.cuh"
 #include "paged_work.cuh"
 #include "tcgen05.cuh"
+#include "tmap.h"
 
 namespace flint {
 namespace {
@@ -53,13 +58,15 @@ template <bool FP8>
 struct Cfg {
   static constexpr int RING = FP8 ? 3 : 4;     // operand tiles
   static constexpr int STAGES = FP8 ? 3 : 0;   // tiles of codes on their way
-  static constexpr int AHEAD = 2;              // tiles copied ahead of the one handed over
+  // Warps that hand a tile over: all four widen, one looks after bf16's edges.
+  static constexpr int HANDS = FP8 ? 4 : 1;
   static constexpr int SMEM = 2 * OPER + RING * OPER + STAGES * STAGE + 1024;
 };
 
 struct Shared {
-  uint64_t full[8], empty[8];        // ring slots: brought, used
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+  uint64_t landed[4], taken[4];      // copies: into a stage (bf16: ring slot), out of a stage
+  uint64_t full[4], empty[4];        // ring slots: ready, used
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drained;
   uint32_t tmem;
   int fail, last, cut[2], first, n_items;
   int scan[16];
@@ -74,6 +81,12 @@ struct Shared {
 static_assert(Cfg<true>::SMEM + sizeof(Shared) <= 227 * 1024, "fits");
 static_assert(Cfg<false>::SMEM + sizeof(Shared) <= 227 * 1024, "fits");
 
+// The caches as (elements of a token, token rows), boxes of 128 bytes x a page's
+// keys (at most a tile's).
+struct Maps {
+  CUtensorMap k, v;
+};
+
 // One share's part of an item.
 struct Item {
   int seq, kvh, kt0, n;     // first key tile of this part, key tiles
@@ -86,6 +99,11 @@ struct Item {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
   return r;
 }
 // a * k + d of two floats at once, and a + b.
@@ -128,14 +146,12 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 
 // Waits for a phase, a second at most; a wait that runs out (in any warp) ends
@@ -163,7 +179,7 @@ __device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, uint32_t pa
 
 template <bool FP8>
 __global__ void __launch_bounds__(THREADS, 1)
-    paged_prompt_kernel(const __grid_constant__ PagedAttnArgs a) {
+    paged_prompt_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<FP8>;
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared sh;
@@ -176,14 +192,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t q_smem = base, ring = base + 2 * OPER, stages = ring + C::RING * OPER;
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), 128);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_addr(&sh.landed[i]), 1);
+      mbar_init(smem_addr(&sh.taken[i]), C::HANDS);
+      mbar_init(smem_addr(&sh.full[i]), C::HANDS);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 128);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), 128);
+      mbar_init(smem_addr(&sh.p_half[i]), 4);
+      mbar_init(smem_addr(&sh.p_full[i]), 4);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       sh.cut[i] = -1;
     }
@@ -305,9 +324,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     return p;
   };
 
+  // Load i of an item's part: K of the first tiles (one; two where A and B have a
+  // tile each), then V_j and K_(j + that many) in turn; {tile, V?}.
+  auto load_of = [&](const Item& p, int i) {
+    const int ld = min(p.split ? 2 : 1, p.n);
+    if (i < ld) return make_int2(i, 0);
+    const int k = i - ld;
+    if (k < 2 * (p.n - ld)) return make_int2((k >> 1) + (k & 1 ? ld : 0), k & 1 ? 0 : 1);
+    return make_int2(k - (p.n - ld), 1);
+  };
+
+  if (warp < 8)
+    more_registers<192>();
+  else
+    fewer_registers<64>();
+
   if (warp < 8) {
     // ===== softmax, and the item's queries and outputs ===========================
-    more_registers<192>();
     const int x = warp >> 2;               // tile A or B
     const int r = tid & 127;               // row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -331,36 +364,36 @@ __global__ void __launch_bounds__(THREADS, 1)
       {
         const uint8_t* src = reinterpret_cast<const uint8_t*>(
             a.q + ((size_t)(p.q_row + (live ? tok : 0)) * nq + head) * HD);
-        float up = 1.0f;
+        uint4 w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = *reinterpret_cast<const uint4*>(src + 16 * c);
         if constexpr (FP8) {
           float mx = 0.0f;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + 16 * c);
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(v[j])), fabsf(bf_hi(v[j]))));
           }
           const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
-          up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
           qs *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            w[c].x = nvu::f16x2_of(bf_lo(w[c].x) * up, bf_hi(w[c].x) * up);
+            w[c].y = nvu::f16x2_of(bf_lo(w[c].y) * up, bf_hi(w[c].y) * up);
+            w[c].z = nvu::f16x2_of(bf_lo(w[c].z) * up, bf_hi(w[c].z) * up);
+            w[c].w = nvu::f16x2_of(bf_lo(w[c].w) * up, bf_hi(w[c].w) * up);
+          }
         }
         if (!p.split || x == 0) {
           const uint32_t dst = q_smem + x * OPER + r * 128;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            uint4 w = live ? *reinterpret_cast<const uint4*>(src + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (FP8) {
-              w.x = nvu::f16x2_of(bf_lo(w.x) * up, bf_hi(w.x) * up);
-              w.y = nvu::f16x2_of(bf_lo(w.y) * up, bf_hi(w.y) * up);
-              w.z = nvu::f16x2_of(bf_lo(w.z) * up, bf_hi(w.z) * up);
-              w.w = nvu::f16x2_of(bf_lo(w.w) * up, bf_hi(w.w) * up);
-            }
+          for (int c = 0; c < 16; ++c)
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                              dst + (c >> 3) * HALF + (((c & 7) ^ (r & 7)) << 4)),
-                         "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                         "r"(w[c].x), "r"(w[c].y), "r"(w[c].z), "r"(w[c].w)
                          : "memory");
-          }
           tc::fence_smem_to_mma();
           mbar_arrive(smem_addr(&sh.q_full[x]));
         }
@@ -403,12 +436,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // a block of 16 keys
-            float b4[4];
+            float b4[5];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b4[i] = __uint_as_float(v[c][16 * h + i]);
-#pragma unroll
-            for (int i = 4; i < 16; ++i) b4[i & 3] = fmaxf(b4[i & 3], __uint_as_float(v[c][16 * h + i]));
-            const float bm = fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3]));
+            for (int i = 0; i < 5; ++i) b4[i] = max3(v[c][16 * h + 3 * i], v[c][16 * h + 3 * i + 1],
+                                                     v[c][16 * h + 3 * i + 2]);
+            const float bm = fmaxf(fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3])),
+                                   fmaxf(b4[4], __uint_as_float(v[c][16 * h + 15])));
             const float k = factor(2 * c + h);
             mx = fmaxf(mx, fmaf(bm, k, sh.lv[slot][2 * c + h]));
           }
@@ -458,6 +491,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           tc::st16(s_tm + 16 * c, w);
+          if (c == 1) {  // the second product may begin
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.p_half[x]));
+          }
         }
         if constexpr (!FP8) {
           float y0, y1;
@@ -466,7 +505,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc::wait_st();
         tc::fence_before();
-        mbar_arrive(smem_addr(&sh.p_full[x]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[x]));
       }
       tiles_before += p.n;
 
@@ -581,151 +621,173 @@ __global__ void __launch_bounds__(THREADS, 1)
       named_sync(1, 256);
     }
   } else if (warp < 12) {
-    // ===== K and V tiles ===========================================================
-    fewer_registers<64>();
-    const int w4 = warp - 8;   // this warp brings keys 32 w4 .. + 31 of every tile
-    constexpr int ES = FP8 ? 1 : 2;
-    const size_t tok_bytes = (size_t)b.nkv * HD * ES;
-    int u = 0;                 // tiles handed over (K and V alike)
+    // ===== tiles from copies to operands =============================================
+    const int w4 = warp - 8;
+    int u = 0;  // tiles handed over (K and V alike)
+    bool ok = warp - 8 < C::HANDS;
+    for (int cur = begin, it = sh.first; ok && cur < end;) {
+      const Item p = part(cur, it);
+      cur += p.n;
+      const int see_hi = p.pos0 + p.tokens - 1;
+      const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
+      for (int i = 0; i < 2 * p.n; ++i, ++u) {
+        const int2 kv = load_of(p, i);
+        const int key0 = (p.kt0 + kv.x) << 7;
+        const uint32_t dst = ring + (u % C::RING) * OPER;
+        if constexpr (FP8) {
+          const int st = u % C::STAGES, slot = u % C::RING;
+          if (!(ok = warp_wait(sh, sh.landed[st], (u / C::STAGES) & 1))) break;
+          uint4 w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // 4 keys a time, a chunk of 16 codes a lane
+            const int r = 32 * w4 + 4 * j + (lane >> 3), c = lane & 7;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[j].x), "=r"(w[j].y), "=r"(w[j].z), "=r"(w[j].w)
+                         : "r"(stages + st * STAGE + r * HD + ((c ^ (r & 7)) << 4)));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.taken[st]));
+          if (u >= C::RING && !(ok = warp_wait(sh, sh.empty[slot], ((u / C::RING) & 1) ^ 1))) break;
+          const bool edge = key0 < see_lo || key0 + TILE - 1 > see_hi;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = 32 * w4 + 4 * j + (lane >> 3), c = lane & 7;
+            if (edge && (key0 + r < see_lo || key0 + r > see_hi)) w[j] = make_uint4(0u, 0u, 0u, 0u);
+            // Operand chunks 2c and 2c + 1; the upper lanes store the odd one
+            // first, so that the eight lanes of a phase fall into distinct banks.
+            const bool odd = (c & 4) != 0;
+            uint32_t x[8] = {e4m3x2_to_f16x2(w[j].x & 0xffffu), e4m3x2_to_f16x2(w[j].x >> 16),
+                             e4m3x2_to_f16x2(w[j].y & 0xffffu), e4m3x2_to_f16x2(w[j].y >> 16),
+                             e4m3x2_to_f16x2(w[j].z & 0xffffu), e4m3x2_to_f16x2(w[j].z >> 16),
+                             e4m3x2_to_f16x2(w[j].w & 0xffffu), e4m3x2_to_f16x2(w[j].w >> 16)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int ch = 2 * c + (odd ? 1 - h : h);
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = odd ? x[4 * (1 - h) + k] : x[4 * h + k];
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               dst + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                           "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                           : "memory");
+            }
+          }
+          tc::fence_smem_to_mma();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
+        } else {
+          const int slot = u % C::RING;
+          if (!(ok = warp_wait(sh, sh.landed[slot], (u / C::RING) & 1))) break;
+          if (kv.y && (key0 < see_lo || key0 + TILE - 1 > see_hi)) {
+            for (int r = lane >> 4; r < TILE; r += 2)
+              if (key0 + r < see_lo || key0 + r > see_hi) {
+                const int c = lane & 15;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 dst + (c >> 3) * HALF + r * 128 + ((c & 7) << 4)),
+                             "r"(0u)
+                             : "memory");
+              }
+            tc::fence_smem_to_mma();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
+        }
+      }
+    }
+  } else if (warp == 13) {
+    // ===== K and V tiles, copied ======================================================
+    const int box_keys = min(1 << b.page_shift, TILE), boxes = TILE / box_keys;
+    const int n_rows = b.n_pages << b.page_shift;
+    int u = 0;             // tiles copied (K and V alike)
     int tiles_before = 0;
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
       cur += p.n;
-      // Keys some query of the item sees; anything else is zeroed.
+      // Keys some query of the item sees.
       const int see_hi = p.pos0 + p.tokens - 1;
       const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
-      const int lead = p.split ? 2 : 1, loads = 2 * p.n;
-      // Load i of the item: K of the first `lead` tiles, then V_j, K_(j + lead)
-      // in turn; {tile, V?}.
-      auto which = [&](int i) {
-        const int ld = min(lead, p.n);
-        if (i < ld) return make_int2(i, 0);
-        const int k = i - ld;
-        if (k < 2 * (p.n - ld)) return make_int2((k >> 1) + (k & 1 ? ld : 0), k & 1 ? 0 : 1);
-        return make_int2(k - (p.n - ld), 1);
+      // Where the 16-key blocks lie: lane l holds block l % 8 of tile 4 batch +
+      // l / 8; the rows two batches and the scales one batch ahead of their use.
+      auto rows_of = [&](int batch) {
+        const int tile = 4 * batch + (lane >> 3);
+        const int key = ((p.kt0 + tile) << 7) + 16 * (lane & 7);
+        const int box = key & ~(box_keys - 1);
+        return tile < p.n && box <= see_hi && box + box_keys - 1 >= see_lo ? cache_row(b, p.seq, key) : -1;
       };
-      // Where the blocks lie: lane l holds block 2 w4 + l % 2 of tile 16 batch + l / 2.
-      int now_row = -1, next_row = -1, have = -1;
-      float now_ks = 0.0f, now_vs = 1.0f;
-      auto look_up = [&](int batch) {
-        const int tile = 16 * batch + (lane >> 1);
-        const int key = ((p.kt0 + tile) << 7) + 32 * w4 + 16 * (lane & 1);
-        return tile < p.n && key <= see_hi ? cache_row(b, p.seq, key) : -1;
-      };
-      // Copies load i; K also leaves its tile's block table.
-      auto issue = [&](int i) {
-        if (i < loads) {
-          const int2 kv = which(i);
-          const int tile = kv.x;
-          if (kv.y == 0) {
-            if ((tile >> 4) != have) {
-              now_row = have < 0 ? look_up(0) : next_row;
-              have = tile >> 4;
-              next_row = look_up(have + 1);
-              if constexpr (FP8) {
-                if (now_row >= 0) {
-                  const size_t at = (size_t)(now_row >> 4) * b.nkv + p.kvh;
-                  now_ks = __ldg(a.k_scale + at);
-                  // A scale of zero would take a block's weights out of the sum: 2^-100.
-                  now_vs = fmaxf(__ldg(a.v_scale + at), 7.8886090522101181e-31f);
-                }
-              }
-            }
-            const int src = 2 * (tile & 15) + (lane & 1);
-            const int row = __shfl_sync(0xffffffffu, now_row, src);
-            const float ks = FP8 ? __shfl_sync(0xffffffffu, now_ks, src) : 1.0f;
-            const float vs = FP8 ? __shfl_sync(0xffffffffu, now_vs, src) : 1.0f;
-            if (lane < 2) {
-              const int slot = (tiles_before + tile) & (INFO - 1), blk = 2 * w4 + lane;
-              sh.row[(tiles_before + tile) & 15][blk] = row;
-              sh.ks[slot][blk] = row >= 0 ? ks : 0.0f;
-              sh.lv[slot][blk] = row < 0 ? -INFINITY : FP8 ? log2f(vs) : 0.0f;
-              sh.iv[slot][blk] = row >= 0 && FP8 ? 1.0f / vs : 1.0f;
-            }
-            __syncwarp();
-          }
-          const uint8_t* cache = static_cast<const uint8_t*>(kv.y ? a.v_cache : a.k_cache);
-          const int key0 = ((p.kt0 + tile) << 7) + 32 * w4;
-          constexpr int CH = FP8 ? 8 : 16;       // 16-byte chunks of a key
-          constexpr int STEP = 32 / CH;          // keys copied at a time
-          const int cr = lane / CH, cc = lane % CH;
-          const uint32_t dst = FP8 ? stages + ((u + i) % (FP8 ? C::STAGES : 1)) * STAGE
-                                   : ring + ((u + i) % C::RING) * OPER;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = sh.row[(tiles_before + tile) & 15][2 * w4 + h];
-            const uint8_t* src = cache + (size_t)max(row, 0) * tok_bytes + (size_t)p.kvh * HD * ES + 16 * cc;
-#pragma unroll
-            for (int j = 0; j < 16 / STEP; ++j) {
-              const int k = STEP * j + cr, r = 32 * w4 + 16 * h + k;  // row of the tile
-              const int key = key0 + 16 * h + k;
-              const bool live = row >= 0 && key >= see_lo && key <= see_hi;
-              const uint32_t at = FP8 ? r * HD + ((cc ^ ((r & 1) << 2)) << 4)
-                                      : (cc >> 3) * HALF + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
-              cp_async16(dst + at, src + (size_t)k * tok_bytes, live);
-            }
+      int row[3] = {-1, -1, -1};
+      float ks[2] = {0.0f, 0.0f}, vs[2] = {1.0f, 1.0f};
+      auto scales_of = [&](int i) {
+        if constexpr (FP8) {
+          if (row[i] >= 0) {
+            const size_t at = (size_t)(row[i] >> 4) * b.nkv + p.kvh;
+            ks[i] = __ldg(a.k_scale + at);
+            vs[i] = __ldg(a.v_scale + at);
           }
         }
-        cp_commit();
       };
-      auto free_slot = [&](int i) {  // the ring slot of load i
-        const int n = u + i;
-        return n < C::RING || warp_wait(sh, sh.empty[n % C::RING], ((n / C::RING) & 1) ^ 1);
-      };
-      if constexpr (FP8) {
-        for (int i = 0; i < C::AHEAD; ++i) issue(i);
-        for (int i = 0; i < loads; ++i) {
-          issue(i + C::AHEAD);
-          cp_wait<C::AHEAD>();
-          __syncwarp();
-          if (!(ok = free_slot(i))) break;
-          const uint32_t src = stages + ((u + i) % C::STAGES) * STAGE, dst = ring + ((u + i) % C::RING) * OPER;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {  // 8 keys x 4 chunks of codes a time
-            const int r = 32 * w4 + 8 * (j >> 1) + (lane >> 2), c = (lane & 3) + 4 * (j & 1);
-            uint4 w;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "r"(src + r * HD + ((c ^ ((r & 1) << 2)) << 4)));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int ch = 2 * c + h;  // chunk of the operand row
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               dst + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                           "r"(e4m3x2_to_f16x2(x[2 * h] & 0xffffu)), "r"(e4m3x2_to_f16x2(x[2 * h] >> 16)),
-                           "r"(e4m3x2_to_f16x2(x[2 * h + 1] & 0xffffu)),
-                           "r"(e4m3x2_to_f16x2(x[2 * h + 1] >> 16))
-                           : "memory");
-            }
+      row[1] = rows_of(0);
+      row[2] = rows_of(1);
+      scales_of(1);
+      for (int i = 0; i < 2 * p.n; ++i, ++u) {
+        const int2 kv = load_of(p, i);
+        const int tile = kv.x;
+        if (kv.y == 0 && (tile & 3) == 0) {
+          row[0] = row[1];
+          ks[0] = ks[1];
+          vs[0] = vs[1];
+          row[1] = row[2];
+          scales_of(1);
+          row[2] = rows_of((tile >> 2) + 2);
+        }
+        constexpr int SLOTS = FP8 ? C::STAGES : C::RING;
+        const int slot = u % SLOTS;
+        if (u >= SLOTS && !(ok = warp_wait(sh, FP8 ? sh.taken[slot] : sh.empty[slot],
+                                           ((u / SLOTS) & 1) ^ 1)))
+          break;
+        const uint32_t bar = smem_addr(&sh.landed[slot]);
+        const uint32_t dst = FP8 ? stages + slot * STAGE : ring + slot * OPER;
+        const int blk = 8 * (tile & 3) + (lane & 7);  // the lane with this lane's block
+        int at = __shfl_sync(0xffffffffu, row[0], blk);
+        if (kv.y == 0) {
+          if (lane < 8) sh.row[(tiles_before + tile) & 15][lane] = at;
+        } else {
+          at = sh.row[(tiles_before + tile) & 15][lane & 7];
+        }
+        // Box i of the tile starts at its block i * box_keys / 16.
+        const int box = FP8 ? lane : lane >> 1, half = FP8 ? 0 : lane & 1;
+        int y = __shfl_sync(0xffffffffu, at, (box * (box_keys >> 4)) & 7);
+        if (y < 0) y = n_rows;
+        if (box < boxes)
+          tma_box(dst + half * HALF + box * box_keys * 128, kv.y ? &maps.v : &maps.k,
+                  p.kvh * HD + 64 * half, y, bar);
+        if (kv.y == 0) {  // the tile's block table
+          const float k = FP8 ? __shfl_sync(0xffffffffu, ks[0], blk) : 1.0f;
+          // A scale of zero would take a block's weights out of the sum: 2^-100.
+          const float v = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs[0], blk), 7.8886090522101181e-31f) : 1.0f;
+          if (lane < 8) {
+            const int info = (tiles_before + tile) & (INFO - 1);
+            const int key = ((p.kt0 + tile) << 7) + 16 * lane;
+            // A block that nothing sees may have any scale.
+            const bool live = at >= 0 && key <= see_hi && key + BLOCK - 1 >= see_lo;
+            sh.ks[info][lane] = live ? k : 0.0f;
+            sh.lv[info][lane] = live ? (FP8 ? log2f(v) : 0.0f) : -INFINITY;
+            sh.iv[info][lane] = live && FP8 ? 1.0f / v : 1.0f;
           }
-          __syncwarp();  // the stage is read before it is copied into again
-          tc::fence_smem_to_mma();
-          mbar_arrive(smem_addr(&sh.full[(u + i) % C::RING]));
         }
-      } else {
-        for (int i = 0; i < C::AHEAD && ok; ++i) {
-          if (i < loads) ok = free_slot(i);
-          if (ok) issue(i);
-        }
-        for (int i = 0; ok && i < loads; ++i) {
-          if (i + C::AHEAD < loads && !(ok = free_slot(i + C::AHEAD))) break;
-          issue(i + C::AHEAD);
-          cp_wait<C::AHEAD>();
-          tc::fence_smem_to_mma();
-          mbar_arrive(smem_addr(&sh.full[(u + i) % C::RING]));
-        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar, FP8 ? STAGE : OPER);
       }
-      cp_wait<0>();
-      __syncwarp();
-      u += loads;
       tiles_before += p.n;
     }
-    cp_wait<0>();
+    if (!ok) {  // nothing may land after the CTA has left
+      constexpr int SLOTS = FP8 ? C::STAGES : C::RING;
+      const uint64_t deadline = globaltimer_ns() + 1000000000ull;
+      for (int n = max(0, u - SLOTS); n < u; ++n)
+        mbar_wait(smem_addr(&sh.landed[n % SLOTS]), (n / SLOTS) & 1, deadline);
+    }
   } else {
     // ===== the products: one warp, of which one thread issues ======================
-    fewer_registers<64>();
     if (warp == 12) {
       constexpr uint32_t s_desc = tc::inst_desc(!FP8, false), o_desc = tc::inst_desc(!FP8, true);
       // Whatever steers the products is broadcast, so that it is uniform for
@@ -749,16 +811,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       };
-      auto product = [&](int x, int n, bool add, bool last) {  // O_x += P_x (tile in slot n)
+      // O_x += P_x (tile in slot n), the weights of keys 0-63 and 64-127 as they come.
+      auto product = [&](int x, int n, bool add, bool last) {
         const uint32_t slot = (uint32_t)(n % C::RING) * (OPER >> 4);
-        if (tc::one_thread()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, v_lo + slot + k * (2048 >> 4), o_desc,
-                       k > 0 ? 1u : (uint32_t)add);
-          if (last) tc::commit(smem_addr(&sh.o_full[x]));
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = warp_wait(sh, h ? sh.p_full[x] : sh.p_half[x], p_phase[x]))) return false;
+          tc::fence_after();
+          if (tc::one_thread()) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, v_lo + slot + k * (2048 >> 4), o_desc,
+                         k > 0 ? 1u : (uint32_t)add);
+            if (h && last) tc::commit(smem_addr(&sh.o_full[x]));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        p_phase[x] ^= 1;
+        return true;
       };
       auto release = [&](int n) {
         if (tc::one_thread()) tc::commit(smem_addr(&sh.empty[n % C::RING]));
@@ -787,11 +857,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool more = j + 1 < tiles;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!(ok = warp_wait(sh, sh.p_full[x], p_phase[x]))) break;
-              p_phase[x] ^= 1;
               if (x == 0 && !(ok = tile_in(v_at(j)))) break;
-              tc::fence_after();
-              product(x, v_at(j), j > 0, !more);
+              if (!product(x, v_at(j), j > 0, !more)) break;
               if (x == 1) release(v_at(j));
               if (more) {
                 if (x == 0 && !(ok = tile_in(k_at(j + 1)))) break;
@@ -810,11 +877,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           for (int j = 0; ok && j < tiles; ++j) {
             const int x = j & 1;
-            if (!(ok = warp_wait(sh, sh.p_full[x], p_phase[x]))) break;
-            p_phase[x] ^= 1;
             if (!(ok = tile_in(v_at(j)))) break;
-            tc::fence_after();
-            product(x, v_at(j), j > 1, j + 2 >= tiles);
+            if (!product(x, v_at(j), j > 1, j + 2 >= tiles)) break;
             release(v_at(j));
             if (j + 2 < tiles) {
               if (!(ok = tile_in(k_at(j + 2)))) break;
@@ -842,12 +906,31 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+namespace {
+bool encode_cache(CUtensorMap* map, const PagedAttnArgs& a, const void* base, bool fp8) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return false;
+  const int es = fp8 ? 1 : 2, page = 1 << a.b.page_shift;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.b.nkv * HD, (cuuint64_t)a.b.n_pages << a.b.page_shift};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.b.nkv * HD * es};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)(page < TILE ? page : TILE)};
+  const cuuint32_t elem[2] = {1, 1};
+  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done[2];
   const int smem = fp8 ? Cfg<true>::SMEM : Cfg<false>::SMEM;
   const cudaError_t e = fp8 ? set_smem_limit_once(paged_prompt_kernel<true>, smem, done[1])
                             : set_smem_limit_once(paged_prompt_kernel<false>, smem, done[0]);
   if (e != cudaSuccess) return e;
+  Maps maps;
+  if (!encode_cache(&maps.k, a, a.k_cache, fp8) || !encode_cache(&maps.v, a, a.v_cache, fp8))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < MAX_CTAS ? sms : MAX_CTAS, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
@@ -858,8 +941,8 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return fp8 ? cudaLaunchKernelEx(&cfg, paged_prompt_kernel<true>, a)
-             : cudaLaunchKernelEx(&cfg, paged_prompt_kernel<false>, a);
+  return fp8 ? cudaLaunchKernelEx(&cfg, paged_prompt_kernel<true>, a, maps)
+             : cudaLaunchKernelEx(&cfg, paged_prompt_kernel<false>, a, maps);
 }
 
 }  // namespace flint
