@@ -198,6 +198,9 @@ def _arg(where, name, t, dtype, shape, dev, optional=False, min_numel=None):
     """Device pointer of t after checking it against the layout the C call
     assumes: dtype, exact shape (or at least min_numel elements), contiguous,
     on device dev."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous() and t.device == dev and
+            t.shape == shape):
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
@@ -245,8 +248,8 @@ def _d(dims):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream() without the Stream object it makes
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

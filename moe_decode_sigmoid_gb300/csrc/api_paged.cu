@@ -104,8 +104,14 @@ flint_status append(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.q_norm = static_cast<const uint16_t*>(q_norm);
   a.k_norm = static_cast<const uint16_t*>(k_norm);
   a.rope = rope_theta > 0.0f;
-  for (int i = 0; i < pg::HD / 2; ++i)
-    a.inv_freq[i] = a.rope ? std::pow((double)rope_theta, -2.0 * i / pg::HD) : 0.0;
+  // theta^(-2i/128) for i = 8 hi + lo, from 16 powers: a product of two is off by
+  // 2^-52 or so, and 64 calls of pow() cost more than the launch.
+  double hi[8] = {}, lo[8] = {};
+  for (int i = 0; a.rope && i < 8; ++i) {
+    hi[i] = std::pow((double)rope_theta, -16.0 * i / pg::HD);
+    lo[i] = std::pow((double)rope_theta, -2.0 * i / pg::HD);
+  }
+  for (int i = 0; i < pg::HD / 2; ++i) a.inv_freq[i] = hi[i >> 3] * lo[i & 7];
   a.eps = eps;
   a.q_out = static_cast<uint16_t*>(q_out);
   a.k_cache = k_cache;

@@ -16,33 +16,50 @@
 // sequence (at most 16 tokens, the unit that shares a scale) and one KV head
 // with its query heads, so that no scale needs a second kernel or an exchange
 // between CTAs.  It finds its block by a scan of the sequences' block counts:
-// the host does not know them.
+// the host does not know them.  A head's row belongs to 16 lanes (16 bytes
+// each), and every lane's up to ten rows are loaded before the first is used:
+// one round trip to memory instead of one a row.
 #include "paged.cuh"
 
 namespace flint {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int THREADS = 256, WARPS = THREADS / 32, ROWS = THREADS / 16;
+constexpr int MOST = (pg::MAX_GROUP + 2) * pg::BLOCK / ROWS;  // rows a 16-lane group has at most
 
 // Blocks of its cache a sequence appends to.
 __device__ __forceinline__ int blocks_of(const pg::Seq& q) {
   return q.n > 0 ? ((q.len - 1) >> 4) - (q.first >> 4) + 1 : 0;
 }
 
-// 4 bf16 (8 bytes) -> 4 fp32.
-__device__ __forceinline__ void bf4(const uint2& w, float (&x)[4]) {
-  x[0] = bf_lo(w.x);
-  x[1] = bf_hi(w.x);
-  x[2] = bf_lo(w.y);
-  x[3] = bf_hi(w.y);
-}
-__device__ __forceinline__ float finite_max(const float (&x)[4]) {
-  float m = 0.0f;
+// 8 bf16 (16 bytes) -> 8 fp32.
+__device__ __forceinline__ void bf8(const uint4& w, float (&x)[8]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    x[2 * j] = bf_lo(v[j]);
+    x[2 * j + 1] = bf_hi(v[j]);
+  }
+}
+__device__ __forceinline__ uint4 to_bf8(const float (&x)[8]) {
+  return make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]),
+                    pack_bf2(x[6], x[7]));
+}
+__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float f) {
+  return make_uint2(
+      pg::f32x2_to_e4m3x2(x[0] * f, x[1] * f) | pg::f32x2_to_e4m3x2(x[2] * f, x[3] * f) << 16,
+      pg::f32x2_to_e4m3x2(x[4] * f, x[5] * f) | pg::f32x2_to_e4m3x2(x[6] * f, x[7] * f) << 16);
+}
+// Largest finite magnitude of a row: over this lane's 8 elements, then 16 lanes.
+__device__ __forceinline__ float finite_max(const float (&x)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
     const float a = fabsf(x[j]);
     m = a <= 3.402823466e38f ? fmaxf(m, a) : m;
   }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
@@ -57,12 +74,14 @@ __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t
 }  // namespace
 
 template <bool FP8>
-__global__ void __launch_bounds__(THREADS) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+__global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   using namespace pg;
   __shared__ int s_warp[WARPS];
-  __shared__ int s_seq, s_blk;
-  __shared__ float2 s_cs[BLOCK][HD / 2];
-  __shared__ float s_amax[2][WARPS];
+  __shared__ Seq s_seq;
+  __shared__ int s_blk, s_which;
+  __shared__ __align__(16) float s_cos[BLOCK][HD / 2];  // read four at a time
+  __shared__ __align__(16) float s_sin[BLOCK][HD / 2];
+  __shared__ int s_amax[2];  // of the new keys and values, as bits
   pdl_wait();  // the projection rows come from the preceding kernel
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y;
@@ -75,160 +94,189 @@ __global__ void __launch_bounds__(THREADS) paged_append_kernel(const __grid_cons
     mine = load_seq(b, tid);
     cnt = blocks_of(mine);
   }
-  int incl = cnt;
+  int before = cnt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
   }
-  if (lane == 31) s_warp[warp] = incl;
-  if (tid == 0) s_seq = -1;
+  if (lane == 31) s_warp[warp] = before;
+  before -= cnt;
+  if (tid == 0) s_which = -1;
+  if (tid < 2) s_amax[tid] = 0;
   __syncthreads();
-  int before = incl - cnt;
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w)
+    if (w < warp) before += s_warp[w];
   const int task = blockIdx.x;
   if (task >= before && task < before + cnt) {
-    s_seq = tid;
+    s_which = tid;
+    s_seq = mine;
     s_blk = task - before;
   }
   __syncthreads();
-  const int s = s_seq;
+  const int s = s_which;
   if (s < 0) return;
-  const Seq q = load_seq(b, s);
+  const Seq q = s_seq;
   const int base = ((q.first >> 4) + s_blk) << 4;  // first position of the block
   const int lo = max(base, q.first), hi = min(base + BLOCK, q.len);
   const int n = hi - lo;                            // tokens of this CTA
   const int t0 = q.q0 + (lo - q.first);             // their first row
+  const int nq = b.nkv * b.group;
+
+  // Row i: token i % n of head i / n, the key, the value, then the queries.
+  // This lane's rows are hw, hw + 16, ...; it holds elements 8l .. 8l + 7.
+  const int hw = tid >> 4, l = tid & 15, rows = n * (b.group + 2);
+  const int recip = (65536 + n - 1) / n;  // i / n for i < 160
+  auto head_of = [&](int i) { return (i * recip) >> 16; };
+  auto src_of = [&](int i) {
+    const int j = head_of(i), tok = i - j * n;
+    const int head = j == 0 ? nq + kvh : j == 1 ? nq + b.nkv + kvh : kvh * b.group + j - 2;
+    return a.qkv + ((size_t)(t0 + tok) * (nq + 2 * b.nkv) + head) * HD + 8 * l;
+  };
+  uint4 raw[MOST];
+#pragma unroll
+  for (int k = 0; k < MOST; ++k)
+    if (hw + ROWS * k < rows) raw[k] = *reinterpret_cast<const uint4*>(src_of(hw + ROWS * k));
+  const uint4 k_gain = *reinterpret_cast<const uint4*>(a.k_norm + 8 * l);
+  const uint4 q_gain = *reinterpret_cast<const uint4*>(a.q_norm + 8 * l);
   // Blocks divide pages, so one look-up serves the block.
   const int row0 = base >= 0 ? cache_row(b, s, base) : -1;
+  const int kept = lo - base;  // earlier tokens of the block
+  const size_t sc = (size_t)(max(row0, 0) >> 4) * b.nkv + kvh;
+  float old_k = 0.0f, old_v = 0.0f;
+  if (FP8 && row0 >= 0 && kept > 0) {
+    old_k = a.k_scale[sc];
+    old_v = a.v_scale[sc];
+  }
 
+  // The first token's angles in fp64 (a position of 2^18 times a frequency near
+  // 1 would leave an fp32 angle 0.03 rad off), reduced to [-pi, pi]; the others
+  // turn on from there by at most 15 steps, whose angles fp32 holds to 2^-21.
+  // (fp64 for all of them: at two operations a clock and SM it took longer than
+  // the block's bytes.)
   if (a.rope) {
     constexpr double INV_TWO_PI = 0.15915494309189535;  // 1 / (2 pi)
     constexpr double TWO_PI_HI = 6.283185307179586;     // 2 pi = HI + LO
     constexpr double TWO_PI_LO = 2.4492935982947064e-16;
-    for (int i = tid; i < n * (HD / 2); i += THREADS) {
-      const double ang = (double)(lo + (i >> 6)) * a.inv_freq[i & 63];
+    if (tid < HD / 2) {
+      const double ang = (double)lo * a.inv_freq[tid];
       const double k = rint(ang * INV_TWO_PI);
       const double r = fma(-k, TWO_PI_LO, fma(-k, TWO_PI_HI, ang));
       float sn, cs;
       sincosf((float)r, &sn, &cs);
-      s_cs[i >> 6][i & 63] = make_float2(cs, sn);
+      s_cos[0][tid] = cs;
+      s_sin[0][tid] = sn;
+    }
+    if (n > 1) {
+      __syncthreads();
+      for (int i = tid + HD / 2; i < n * (HD / 2); i += THREADS) {
+        const int tok = i >> 6, e = i & 63;
+        float sn, cs;
+        sincosf((float)tok * (float)a.inv_freq[e], &sn, &cs);
+        const float c0 = s_cos[0][e], s0 = s_sin[0][e];
+        s_cos[tok][e] = c0 * cs - s0 * sn;
+        s_sin[tok][e] = s0 * cs + c0 * sn;
+      }
     }
   }
   __syncthreads();
 
-  const int nq = b.nkv * b.group;
-  const size_t row_len = (size_t)(nq + 2 * b.nkv) * HD;
-  // One head's row: lane l holds elements 4l .. 4l + 3, whose rotation partners
-  // are lane l ^ 16's.
-  auto normed = [&](const uint16_t* src, const uint16_t* gain, int tok, float (&x)[4]) {
-    bf4(*reinterpret_cast<const uint2*>(src + 4 * lane), x);
-    float g[4];
-    bf4(*reinterpret_cast<const uint2*>(gain + 4 * lane), g);
-    const float ss = warp_sum(fmaf(x[0], x[0], fmaf(x[1], x[1], fmaf(x[2], x[2], x[3] * x[3]))));
+  // Norm and rotation of a row; element e's rotation partner is lane l ^ 8's.
+  auto turned = [&](const uint4& w, const uint4& gain, int tok, float (&x)[8]) {
+    bf8(w, x);
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float inv = 1.0f / sqrtf(ss / (float)HD + a.eps);
+    float g[8];
+    bf8(gain, g);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = x[j] * inv * g[j];
+    for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
     if (a.rope) {
+      const float4* c4 = reinterpret_cast<const float4*>(&s_cos[tok][8 * (l & 7)]);
+      const float4* s4 = reinterpret_cast<const float4*>(&s_sin[tok][8 * (l & 7)]);
+      const float4 c[2] = {c4[0], c4[1]}, sn[2] = {s4[0], s4[1]};
+      const float cs[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+      const float si[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float other = __shfl_xor_sync(0xffffffffu, x[j], 16);
-        const float2 cs = s_cs[tok][(lane & 15) * 4 + j];
-        x[j] = x[j] * cs.x + (lane < 16 ? -other : other) * cs.y;
+      for (int j = 0; j < 8; ++j) {
+        const float other = __shfl_xor_sync(0xffffffffu, x[j], 8);
+        x[j] = x[j] * cs[j] + (l < 8 ? -other : other) * si[j];
       }
     }
   };
 
-  // Keys and values: warp w has tokens w and w + 8.
-  constexpr int TPW = BLOCK / WARPS;
-  float k[TPW][4], v[TPW][4];
-  float mk = 0.0f, mv = 0.0f;
+  // The keys are among the lanes' first rows, the values among the first two;
+  // E4M3 keeps them until the block's scale is known.
+  float key[8];
 #pragma unroll
-  for (int i = 0; i < TPW; ++i) {
-    const int tok = warp + i * WARPS;
-    if (tok < n) {
-      const uint16_t* row = a.qkv + (size_t)(t0 + tok) * row_len;
-      normed(row + (size_t)(nq + kvh) * HD, a.k_norm, tok, k[i]);
-      bf4(*reinterpret_cast<const uint2*>(row + (size_t)(nq + b.nkv + kvh) * HD + 4 * lane), v[i]);
-      mk = fmaxf(mk, finite_max(k[i]));
-      mv = fmaxf(mv, finite_max(v[i]));
+  for (int k = 0; k < MOST; ++k) {
+    const int i = hw + ROWS * k;
+    if (!__any_sync(0xffffffffu, i < rows)) break;  // shuffles need the whole warp
+    const bool live = i < rows;
+    const int j = live ? head_of(i) : 2, tok = live ? i - j * n : 0;
+    const uint4 w = live ? raw[k] : make_uint4(0u, 0u, 0u, 0u);
+    float x[8];
+    turned(w, j == 0 ? k_gain : q_gain, tok, x);
+    if (k < 2 && __any_sync(0xffffffffu, j < 2)) {
+      if constexpr (FP8) {
+        float v[8];
+        bf8(w, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (j == 1) x[e] = v[e];
+          if (k == 0) key[e] = x[e];
+        }
+        const float m = finite_max(x);
+        if (j < 2 && l == 0) atomicMax(&s_amax[j], __float_as_int(m));
+      } else if (j < 2 && row0 >= 0) {
+        uint16_t* cache = static_cast<uint16_t*>(j ? a.v_cache : a.k_cache);
+        *reinterpret_cast<uint4*>(cache + ((size_t)(row0 + kept + tok) * b.nkv + kvh) * HD + 8 * l) =
+            j ? w : to_bf8(x);  // a value as it came, bit for bit
+      }
     }
+    if (live && j >= 2)
+      *reinterpret_cast<uint4*>(a.q_out + ((size_t)(t0 + tok) * nq + kvh * b.group + j - 2) * HD + 8 * l) =
+          to_bf8(x);
   }
   if constexpr (FP8) {
-    mk = warp_max(mk);
-    mv = warp_max(mv);
-    if (lane == 0) {
-      s_amax[0][warp] = mk;
-      s_amax[1][warp] = mv;
-    }
     __syncthreads();
-    if (row0 >= 0) {
-      const size_t sc = (size_t)(row0 >> 4) * b.nkv + kvh;
-      const int kept = lo - base;  // earlier tokens of the block
-      const float old_k = kept > 0 ? a.k_scale[sc] : 0.0f;
-      const float old_v = kept > 0 ? a.v_scale[sc] : 0.0f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        mk = fmaxf(mk, s_amax[0][w]);
-        mv = fmaxf(mv, s_amax[1][w]);
+    if (row0 < 0) return;
+    const float new_k = fmaxf(exp2i(scale_exp(__int_as_float(s_amax[0]))), old_k);
+    const float new_v = fmaxf(exp2i(scale_exp(__int_as_float(s_amax[1]))), old_v);
+    uint8_t* kc = static_cast<uint8_t*>(a.k_cache);
+    uint8_t* vc = static_cast<uint8_t*>(a.v_cache);
+    auto rewrite = [&](uint8_t* cache, float ratio) {
+      for (int r = warp; r < kept; r += WARPS) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(cache + ((size_t)(row0 + r) * b.nkv + kvh) * HD) + lane;
+        const uint32_t w = *p;
+        const float2 x = f16x2_to_f32(e4m3x2_to_f16x2(w & 0xffffu));
+        const float2 y = f16x2_to_f32(e4m3x2_to_f16x2(w >> 16));
+        *p = f32x2_to_e4m3x2(x.x * ratio, x.y * ratio) | f32x2_to_e4m3x2(y.x * ratio, y.y * ratio) << 16;
       }
-      const float new_k = fmaxf(exp2i(scale_exp(mk)), old_k);
-      const float new_v = fmaxf(exp2i(scale_exp(mv)), old_v);
-      uint8_t* kc = static_cast<uint8_t*>(a.k_cache);
-      uint8_t* vc = static_cast<uint8_t*>(a.v_cache);
-      auto rewrite = [&](uint8_t* cache, float ratio) {
-        for (int r = warp; r < kept; r += WARPS) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(cache + ((size_t)(row0 + r) * b.nkv + kvh) * HD) + lane;
-          const uint32_t w = *p;
-          const float2 x = f16x2_to_f32(e4m3x2_to_f16x2(w & 0xffffu));
-          const float2 y = f16x2_to_f32(e4m3x2_to_f16x2(w >> 16));
-          *p = f32x2_to_e4m3x2(x.x * ratio, x.y * ratio) | f32x2_to_e4m3x2(y.x * ratio, y.y * ratio) << 16;
-        }
-      };
-      if (kept > 0 && new_k > old_k) rewrite(kc, old_k / new_k);
-      if (kept > 0 && new_v > old_v) rewrite(vc, old_v / new_v);
-      __syncthreads();  // every thread has read the old scales
-      if (tid == 0) {
-        a.k_scale[sc] = new_k;
-        a.v_scale[sc] = new_v;
-      }
-      const float ik = 1.0f / new_k, iv = 1.0f / new_v;  // powers of two: exact
+    };
+    if (kept > 0 && new_k > old_k) rewrite(kc, old_k / new_k);
+    if (kept > 0 && new_v > old_v) rewrite(vc, old_v / new_v);
+    if (tid == 0) {
+      a.k_scale[sc] = new_k;
+      a.v_scale[sc] = new_v;
+    }
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        const int tok = warp + i * WARPS;
-        if (tok < n) {
-          const size_t at = ((size_t)(row0 + (lo - base) + tok) * b.nkv + kvh) * HD + 4 * lane;
-          *reinterpret_cast<uint32_t*>(kc + at) =
-              f32x2_to_e4m3x2(k[i][0] * ik, k[i][1] * ik) | f32x2_to_e4m3x2(k[i][2] * ik, k[i][3] * ik) << 16;
-          *reinterpret_cast<uint32_t*>(vc + at) =
-              f32x2_to_e4m3x2(v[i][0] * iv, v[i][1] * iv) | f32x2_to_e4m3x2(v[i][2] * iv, v[i][3] * iv) << 16;
-        }
+    for (int k = 0; k < 2; ++k) {
+      const int i = hw + ROWS * k, j = i < rows ? head_of(i) : 2;
+      if (j < 2) {  // 1 / a power of two: exact
+        float x[8];
+        bf8(raw[k], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = j ? x[e] : key[e];
+        *reinterpret_cast<uint2*>((j ? vc : kc) +
+                                  ((size_t)(row0 + kept + i - j * n) * b.nkv + kvh) * HD + 8 * l) =
+            to_e4m3(x, 1.0f / (j ? new_v : new_k));
       }
     }
-  } else if (row0 >= 0) {
-    uint16_t* kc = static_cast<uint16_t*>(a.k_cache);
-    uint16_t* vc = static_cast<uint16_t*>(a.v_cache);
-#pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      const int tok = warp + i * WARPS;
-      if (tok < n) {
-        const size_t at = ((size_t)(row0 + (lo - base) + tok) * b.nkv + kvh) * HD + 4 * lane;
-        *reinterpret_cast<uint2*>(kc + at) = make_uint2(pack_bf2(k[i][0], k[i][1]), pack_bf2(k[i][2], k[i][3]));
-        // bf16 values widened and narrowed again: bit for bit the input but for
-        // a NaN's payload, so the words are copied instead.
-        *reinterpret_cast<uint2*>(vc + at) = *reinterpret_cast<const uint2*>(
-            a.qkv + (size_t)(t0 + tok) * row_len + (size_t)(nq + b.nkv + kvh) * HD + 4 * lane);
-      }
-    }
-  }
-
-  // The group's query heads.
-  for (int i = warp; i < n * b.group; i += WARPS) {
-    const int tok = i / b.group, h = kvh * b.group + i % b.group;
-    float x[4];
-    normed(a.qkv + (size_t)(t0 + tok) * row_len + (size_t)h * HD, a.q_norm, tok, x);
-    *reinterpret_cast<uint2*>(a.q_out + ((size_t)(t0 + tok) * nq + h) * HD + 4 * lane) =
-        make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
   }
 }
 
