@@ -16,9 +16,9 @@
 // sequence (at most 16 tokens, the unit that shares a scale) and one KV head
 // with its query heads, so that no scale needs a second kernel or an exchange
 // between CTAs.  It finds its block by a scan of the sequences' block counts:
-// the host does not know them.  A head's row belongs to 16 lanes (16 bytes
-// each), and every lane's up to ten rows are loaded before the first is used:
-// one round trip to memory instead of one a row.
+// the host does not know them.  A head's row belongs to 16 lanes, and a lane
+// loads five of its up to ten rows before it uses the first: two round trips to
+// memory instead of ten, with room for four CTAs on an SM.
 #include "paged.cuh"
 
 namespace flint {
@@ -26,29 +26,42 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32, ROWS = THREADS / 16;
 constexpr int MOST = (pg::MAX_GROUP + 2) * pg::BLOCK / ROWS;  // rows a 16-lane group has at most
+constexpr int BATCH = MOST / 2;                               // of them loaded at a time
 
 // Blocks of its cache a sequence appends to.
 __device__ __forceinline__ int blocks_of(const pg::Seq& q) {
   return q.n > 0 ? ((q.len - 1) >> 4) - (q.first >> 4) + 1 : 0;
 }
 
-// 8 bf16 (16 bytes) -> 8 fp32.
-__device__ __forceinline__ void bf8(const uint4& w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+// A lane's share of a row: elements 4l .. 4l + 3 and 64 + 4l .. 64 + 4l + 3, so
+// that a rotation's pairs meet in one lane.
+struct Row {
+  uint2 a, b;
+};
+__device__ __forceinline__ Row load_row(const uint16_t* p) {
+  return Row{*reinterpret_cast<const uint2*>(p), *reinterpret_cast<const uint2*>(p + pg::HD / 2)};
+}
+__device__ __forceinline__ void widen(const Row& w, float (&x)[8]) {
+  const uint32_t v[4] = {w.a.x, w.a.y, w.b.x, w.b.y};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     x[2 * j] = bf_lo(v[j]);
     x[2 * j + 1] = bf_hi(v[j]);
   }
 }
-__device__ __forceinline__ uint4 to_bf8(const float (&x)[8]) {
-  return make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]),
-                    pack_bf2(x[6], x[7]));
+__device__ __forceinline__ Row narrow(const float (&x)[8]) {
+  return Row{make_uint2(pg::pack_bf16(x[0], x[1]), pg::pack_bf16(x[2], x[3])),
+             make_uint2(pg::pack_bf16(x[4], x[5]), pg::pack_bf16(x[6], x[7]))};
 }
-__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float f) {
-  return make_uint2(
-      pg::f32x2_to_e4m3x2(x[0] * f, x[1] * f) | pg::f32x2_to_e4m3x2(x[2] * f, x[3] * f) << 16,
-      pg::f32x2_to_e4m3x2(x[4] * f, x[5] * f) | pg::f32x2_to_e4m3x2(x[6] * f, x[7] * f) << 16);
+__device__ __forceinline__ void store_row(uint16_t* p, const Row& w) {
+  *reinterpret_cast<uint2*>(p) = w.a;
+  *reinterpret_cast<uint2*>(p + pg::HD / 2) = w.b;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[8], float f) {
+  *reinterpret_cast<uint32_t*>(p) =
+      pg::f32x2_to_e4m3x2(x[0] * f, x[1] * f) | pg::f32x2_to_e4m3x2(x[2] * f, x[3] * f) << 16;
+  *reinterpret_cast<uint32_t*>(p + pg::HD / 2) =
+      pg::f32x2_to_e4m3x2(x[4] * f, x[5] * f) | pg::f32x2_to_e4m3x2(x[6] * f, x[7] * f) << 16;
 }
 // Largest finite magnitude of a row: over this lane's 8 elements, then 16 lanes.
 __device__ __forceinline__ float finite_max(const float (&x)[8]) {
@@ -74,7 +87,7 @@ __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t
 }  // namespace
 
 template <bool FP8>
-__global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+__global__ void __launch_bounds__(THREADS, 4) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   using namespace pg;
   __shared__ int s_warp[WARPS];
   __shared__ Seq s_seq;
@@ -125,21 +138,25 @@ __global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_c
   const int nq = b.nkv * b.group;
 
   // Row i: token i % n of head i / n, the key, the value, then the queries.
-  // This lane's rows are hw, hw + 16, ...; it holds elements 8l .. 8l + 7.
+  // This lane's rows are hw, hw + 16, ...
   const int hw = tid >> 4, l = tid & 15, rows = n * (b.group + 2);
   const int recip = (65536 + n - 1) / n;  // i / n for i < 160
   auto head_of = [&](int i) { return (i * recip) >> 16; };
   auto src_of = [&](int i) {
     const int j = head_of(i), tok = i - j * n;
     const int head = j == 0 ? nq + kvh : j == 1 ? nq + b.nkv + kvh : kvh * b.group + j - 2;
-    return a.qkv + ((size_t)(t0 + tok) * (nq + 2 * b.nkv) + head) * HD + 8 * l;
+    return a.qkv + ((size_t)(t0 + tok) * (nq + 2 * b.nkv) + head) * HD + 4 * l;
   };
-  uint4 raw[MOST];
+  Row raw[BATCH];
+  auto load_batch = [&](int first) {
 #pragma unroll
-  for (int k = 0; k < MOST; ++k)
-    if (hw + ROWS * k < rows) raw[k] = *reinterpret_cast<const uint4*>(src_of(hw + ROWS * k));
-  const uint4 k_gain = *reinterpret_cast<const uint4*>(a.k_norm + 8 * l);
-  const uint4 q_gain = *reinterpret_cast<const uint4*>(a.q_norm + 8 * l);
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = hw + ROWS * (first + k);
+      raw[k] = i < rows ? load_row(src_of(i)) : Row{make_uint2(0u, 0u), make_uint2(0u, 0u)};
+    }
+  };
+  load_batch(0);
+  const Row k_gain = load_row(a.k_norm + 4 * l), q_gain = load_row(a.q_norm + 4 * l);
   // Blocks divide pages, so one look-up serves the block.
   const int row0 = base >= 0 ? cache_row(b, s, base) : -1;
   const int kept = lo - base;  // earlier tokens of the block
@@ -182,29 +199,28 @@ __global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_c
   }
   __syncthreads();
 
-  // Norm and rotation of a row; element e's rotation partner is lane l ^ 8's.
-  auto turned = [&](const uint4& w, const uint4& gain, int tok, float (&x)[8]) {
-    bf8(w, x);
+  // Norm and rotation of a row.
+  auto turned = [&](const Row& w, const Row& gain, int tok, float (&x)[8]) {
+    widen(w, x);
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = 1.0f / sqrtf(ss / (float)HD + a.eps);
+    const float inv = rsqrtf(ss / (float)HD + a.eps);
     float g[8];
-    bf8(gain, g);
+    widen(gain, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
     if (a.rope) {
-      const float4* c4 = reinterpret_cast<const float4*>(&s_cos[tok][8 * (l & 7)]);
-      const float4* s4 = reinterpret_cast<const float4*>(&s_sin[tok][8 * (l & 7)]);
-      const float4 c[2] = {c4[0], c4[1]}, sn[2] = {s4[0], s4[1]};
-      const float cs[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
-      const float si[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
+      const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[tok][4 * l]);
+      const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[tok][4 * l]);
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float other = __shfl_xor_sync(0xffffffffu, x[j], 8);
-        x[j] = x[j] * cs[j] + (l < 8 ? -other : other) * si[j];
+      for (int j = 0; j < 4; ++j) {
+        const float lo = x[j], hi = x[4 + j];
+        x[j] = lo * c[j] - hi * sn[j];
+        x[4 + j] = hi * c[j] + lo * sn[j];
       }
     }
   };
@@ -212,35 +228,37 @@ __global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_c
   // The keys are among the lanes' first rows, the values among the first two;
   // E4M3 keeps them until the block's scale is known.
   float key[8];
+  Row val[2];
 #pragma unroll
   for (int k = 0; k < MOST; ++k) {
     const int i = hw + ROWS * k;
     if (!__any_sync(0xffffffffu, i < rows)) break;  // shuffles need the whole warp
+    if (k == BATCH) load_batch(BATCH);
     const bool live = i < rows;
     const int j = live ? head_of(i) : 2, tok = live ? i - j * n : 0;
-    const uint4 w = live ? raw[k] : make_uint4(0u, 0u, 0u, 0u);
+    const Row w = raw[k % BATCH];
     float x[8];
     turned(w, j == 0 ? k_gain : q_gain, tok, x);
     if (k < 2 && __any_sync(0xffffffffu, j < 2)) {
       if constexpr (FP8) {
         float v[8];
-        bf8(w, v);
+        widen(w, v);
+        val[k] = w;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (j == 1) x[e] = v[e];
           if (k == 0) key[e] = x[e];
+          if (j == 1) x[e] = v[e];
         }
         const float m = finite_max(x);
         if (j < 2 && l == 0) atomicMax(&s_amax[j], __float_as_int(m));
       } else if (j < 2 && row0 >= 0) {
-        uint16_t* cache = static_cast<uint16_t*>(j ? a.v_cache : a.k_cache);
-        *reinterpret_cast<uint4*>(cache + ((size_t)(row0 + kept + tok) * b.nkv + kvh) * HD + 8 * l) =
-            j ? w : to_bf8(x);  // a value as it came, bit for bit
+        store_row(static_cast<uint16_t*>(j ? a.v_cache : a.k_cache) +
+                      ((size_t)(row0 + kept + tok) * b.nkv + kvh) * HD + 4 * l,
+                  j ? w : narrow(x));  // a value as it came, bit for bit
       }
     }
     if (live && j >= 2)
-      *reinterpret_cast<uint4*>(a.q_out + ((size_t)(t0 + tok) * nq + kvh * b.group + j - 2) * HD + 8 * l) =
-          to_bf8(x);
+      store_row(a.q_out + ((size_t)(t0 + tok) * nq + kvh * b.group + j - 2) * HD + 4 * l, narrow(x));
   }
   if constexpr (FP8) {
     __syncthreads();
@@ -269,12 +287,11 @@ __global__ void __launch_bounds__(THREADS, 3) paged_append_kernel(const __grid_c
       const int i = hw + ROWS * k, j = i < rows ? head_of(i) : 2;
       if (j < 2) {  // 1 / a power of two: exact
         float x[8];
-        bf8(raw[k], x);
+        widen(val[k], x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = j ? x[e] : key[e];
-        *reinterpret_cast<uint2*>((j ? vc : kc) +
-                                  ((size_t)(row0 + kept + i - j * n) * b.nkv + kvh) * HD + 8 * l) =
-            to_e4m3(x, 1.0f / (j ? new_v : new_k));
+        store_codes((j ? vc : kc) + ((size_t)(row0 + kept + i - j * n) * b.nkv + kvh) * HD + 4 * l, x,
+                    1.0f / (j ? new_v : new_k));
       }
     }
   }
