@@ -35,6 +35,8 @@
 // Work: items (tile pair of a sequence, KV head) of so many key tiles, laid end
 // to end and cut into equal shares, as the next-token kernel cuts its rows; cut
 // items are joined through the workspace by the CTA that arrives last.
+#include <type_traits>
+
 #include "nv_util.cuh"
 #include "paged.cuh"
 #include "paged_work.cuh"
@@ -74,7 +76,7 @@ struct Shared {
   int4 item[MAX_ITEMS];              // {sequence, pair, first key tile, key tiles}
   int qpre[MAX_SEQS + 1];            // items before each sequence
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
-  float ks[INFO][8], lv[INFO][8], iv[INFO][8];   // a key tile's blocks
+  alignas(16) float ks[INFO][8], lv[INFO][8], iv[INFO][8];  // a key tile's blocks (read four at a time)
   int row[16][8];                    // a key tile's blocks: cache rows
 };
 
@@ -101,10 +103,18 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
+__device__ __forceinline__ float as_f(float v) { return v; }
+template <class A, class B, class C>
+__device__ __forceinline__ float max3(A a, B b, C c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(as_f(a)), "f"(as_f(b)), "f"(as_f(c)));
   return r;
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 // a * k + d of two floats at once, and a + b.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -413,100 +423,122 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int slot = (tiles_before + j) & (INFO - 1);
         const int key0 = (p.kt0 + j) << 7;
         const bool masked = key0 + TILE - 1 > hi_all || key0 < lo_all;
-        // What a block's scores are multiplied by; not 0, lest a masked score
-        // becomes NaN (a query of zeros, a scale of 0).
-        auto factor = [&](int blk) {
-          return fmaxf(FP8 ? qs * sh.ks[slot][blk] : qs, 1.17549435e-38f);
-        };
-        uint32_t v[4][32];  // the row's scores, then its weights
+        // Two copies of the code, so that a tile that is seen whole pays nothing
+        // for the mask.
+        auto weigh = [&](auto edge) {
+          constexpr bool MASK = decltype(edge)::value;
+          // What the blocks' scores are multiplied by (not 0, lest a masked score
+          // becomes NaN: a query of zeros, a scale of 0) and what is added.
+          float kf[FP8 ? 8 : 1], lv[8];
+          load8(sh.lv[slot], lv);
+          if constexpr (FP8) {
+            load8(sh.ks[slot], kf);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld32(s_tm + 32 * c, v[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::wait_ld(v[c]);
-        if (masked) {  // columns outside [mlo, mhi] are not seen
-          const int mlo = lo - key0, mhi = hi - key0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int i = 0; i < 8; ++i) kf[i] = fmaxf(qs * kf[i], 1.17549435e-38f);
+          } else {
+            kf[0] = fmaxf(qs, 1.17549435e-38f);
+          }
+          // The row's scores twice, 32 columns at a time with the next ones on their
+          // way: for the maximum, then for the weights.  (All 128 in registers at
+          // once: spills, and 8 % slower.)
+          const int mlo = lo - key0, mhi = hi - key0;  // columns seen
+          auto mask = [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i < mlo || 32 * c + i > mhi) v[c][i] = 0xff800000u;  // -infinity
-        }
-        float mx = -INFINITY;
+              if (32 * c + i < mlo || 32 * c + i > mhi) v[i] = 0xff800000u;  // -infinity
+          };
+          uint32_t v[2][32];
+          float mx = -INFINITY;
+          tc::ld32(s_tm, v[0]);
+          tc::wait_ld(v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&y)[32] = v[c & 1];
+            tc::ld32(s_tm + 32 * ((c + 1) & 3), v[(c + 1) & 1]);
+            if constexpr (MASK) mask(c, y);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // a block of 16 keys
-            float b4[5];
+            for (int h = 0; h < 2; ++h) {  // a block of 16 keys
+              float b4[5];
 #pragma unroll
-            for (int i = 0; i < 5; ++i) b4[i] = max3(v[c][16 * h + 3 * i], v[c][16 * h + 3 * i + 1],
-                                                     v[c][16 * h + 3 * i + 2]);
-            const float bm = fmaxf(fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3])),
-                                   fmaxf(b4[4], __uint_as_float(v[c][16 * h + 15])));
-            const float k = factor(2 * c + h);
-            mx = fmaxf(mx, fmaf(bm, k, sh.lv[slot][2 * c + h]));
+              for (int i = 0; i < 5; ++i)
+                b4[i] = max3(y[16 * h + 3 * i], y[16 * h + 3 * i + 1], y[16 * h + 3 * i + 2]);
+              const float bm = fmaxf(max3(b4[0], b4[1], b4[2]), max3(b4[3], b4[4], y[16 * h + 15]));
+              mx = fmaxf(mx, fmaf(bm, kf[FP8 ? 2 * c + h : 0], lv[2 * c + h]));
+            }
+            tc::wait_ld(v[(c + 1) & 1]);
           }
-        const bool grow = mx > m + 8.0f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = fmaxf(m, mx);
-          const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
-          l *= f;
-          m = mn;
-          if (any) {  // the products so far
+          const bool grow = mx > m + 8.0f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = fmaxf(m, mx);
+            const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
+            l *= f;
+            m = mn;
+            if (any) {  // the products so far
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t w[16];
-              tc::ld16(o_tm + 16 * c, w);
-              tc::wait_ld(w);
+              for (int c = 0; c < 8; ++c) {
+                uint32_t w[16];
+                tc::ld16(o_tm + 16 * c, w);
+                tc::wait_ld(w);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-              tc::st16(o_tm + 16 * c, w);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                tc::st16(o_tm + 16 * c, w);
+              }
             }
           }
-        }
-        any = true;
-        const float mu = m > -INFINITY ? m : 0.0f;
-        uint64_t sums[2] = {0ull, 0ull};
+          any = true;
+          const float mu = m > -INFINITY ? m : 0.0f;
+          float iv[8];
+          if constexpr (FP8) load8(sh.iv[slot], iv);
+          uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < 4; ++c) {  // columns 32c .. are in v[c & 1]
+            uint32_t(&y)[32] = v[c & 1];
+            if (c < 3) tc::ld32(s_tm + 32 * (c + 1), v[(c + 1) & 1]);
+            if constexpr (MASK) mask(c, y);
+            uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float k = factor(2 * c + h), d = sh.lv[slot][2 * c + h] - mu;
-            const uint64_t k2 = pair(k, k), d2 = pair(d, d);
-            if constexpr (FP8) sums[0] = sums[1] = 0ull;
+            for (int h = 0; h < 2; ++h) {
+              const int blk = 2 * c + h;
+              const float d = lv[blk] - mu;
+              const uint64_t k2 = pair(kf[FP8 ? blk : 0], kf[FP8 ? blk : 0]), d2 = pair(d, d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float y0, y1;
-              unpair(fma2(pair(__uint_as_float(v[c][16 * h + 2 * i]),
-                               __uint_as_float(v[c][16 * h + 2 * i + 1])), k2, d2), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              sums[i & 1] = add2(sums[i & 1], pair(y0, y1));
-              w[8 * h + i] = pack_p<FP8>(y0, y1);
+              for (int i = 0; i < 8; ++i) {
+                float y0, y1;
+                unpair(fma2(pair(as_f(y[16 * h + 2 * i]), as_f(y[16 * h + 2 * i + 1])), k2, d2), y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                sums[i & 1] = FP8 && i < 2 ? pair(y0, y1) : add2(sums[i & 1], pair(y0, y1));
+                w[8 * h + i] = pack_p<FP8>(y0, y1);
+              }
+              if constexpr (FP8) {
+                float y0, y1;
+                unpair(add2(sums[0], sums[1]), y0, y1);
+                l = fmaf(y0 + y1, iv[blk], l);
+              }
             }
-            if constexpr (FP8) {
-              float y0, y1;
-              unpair(add2(sums[0], sums[1]), y0, y1);
-              l = fmaf(y0 + y1, sh.iv[slot][2 * c + h], l);
+            tc::st16(s_tm + 16 * c, w);
+            if (c == 1) {  // the second product may begin
+              tc::wait_st();
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&sh.p_half[x]));
             }
+            if (c < 3) tc::wait_ld(v[(c + 1) & 1]);
           }
-          tc::st16(s_tm + 16 * c, w);
-          if (c == 1) {  // the second product may begin
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.p_half[x]));
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[x]));
+          if constexpr (!FP8) {
+            float y0, y1;
+            unpair(add2(sums[0], sums[1]), y0, y1);
+            l += y0 + y1;
           }
-        }
-        if constexpr (!FP8) {
-          float y0, y1;
-          unpair(add2(sums[0], sums[1]), y0, y1);
-          l += y0 + y1;
-        }
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[x]));
+        };
+        if (masked)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
       }
       tiles_before += p.n;
 
