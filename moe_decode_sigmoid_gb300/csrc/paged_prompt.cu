@@ -6,13 +6,16 @@
 // 128 keys.  Per tile, with a running maximum m and sum l a row (2^x
 // throughout, the scale carrying log2 e):
 //   S = Q K^T (128 x 128 x 128),  p = 2^(S ks + lv - m),  O += P V
-// E4M3: K and V are the codes as f16 (exact); a 16-key block's ks multiplies
-// its scores, its vs enters the exponent as lv = log2 vs, and l gets p / vs, so
-// P is held in f16 relative to the largest contribution whatever the blocks'
-// scales.  Q is f16 too, each row scaled by a power of two (its largest element
-// in [2^14, 2^15): a bf16 element stays exact down to 2^-31 of it).  bf16: Q, K
-// and V as they are, P rounded to bf16, half a step 2^-8, as the output itself;
-// l sums the weights before that rounding.
+// E4M3: a 16-key block's ks multiplies its scores, its vs enters the exponent
+// as lv = log2 vs, and l gets p / vs.  K's codes are an operand as they lie in
+// the cache; a query row, scaled by a power of two to a largest element in
+// [224, 448], is the sum of two E4M3 rows, hi + lo, exact down to 2^-18 of that
+// element (bf16 has 8 significant bits, each half 4), so S = hi K^T + lo K^T at
+// E4M3's double rate costs what one product of 16-bit operands does.  V's codes
+// are widened to f16 (exact) and P is f16, 2^-11 relative to the largest
+// contribution whatever the blocks' scales: P in E4M3 would lose the small
+// weights of a long context.  bf16: Q, K and V as they are, P rounded to bf16,
+// half a step 2^-8, as the output itself; l sums the weights before rounding.
 //
 // Bound: the tensor cores for prompts (4 * 128 operations a query-key pair
 // against 512 or 256 bytes a key), the cache's bytes for a few drafted tokens.
@@ -22,12 +25,11 @@
 // brings no more than one tile, the even and the odd key tiles of that one.
 //   warps 0-3, 4-7: softmax of A, of B; a thread has a row (TMEM lane)
 //   warp 13:        looks pages up and copies K and V tiles by TMA, a box a page
-//                   (16 to 128 keys): bf16 into the operand ring, E4M3 codes into
-//                   a staging ring; a page that is not there is a box beyond the
-//                   cache, which fills with zeros
-//   warps 8-11:     widen the codes to f16 into the operand ring (E4M3), and zero
-//                   the rows of V that no query of the item sees: whatever bits
-//                   lie there must not meet a zero weight
+//                   (16 to 128 keys), V's codes into a staging ring; a page that
+//                   is not there is a box beyond the cache, which fills with zeros
+//   warps 8-11:     widen V's codes to f16, and zero the rows of V that no query
+//                   of the item sees: whatever bits lie there must not meet a
+//                   zero weight
 //   warp 12:        issues every mma
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each; P takes its S's place.  O is
 // rescaled only when a row's maximum grows by more than 2^8.
@@ -52,32 +54,34 @@ constexpr int THREADS = 512;
 constexpr int TILE = 128;              // rows of a tile, keys of a tile
 constexpr int OPER = TILE * HD * 2;    // bytes of an operand tile (16-bit): 2 blocks of 64 columns
 constexpr int HALF = OPER / 2;
-constexpr int STAGE = TILE * HD;       // bytes of a tile of codes
+constexpr int CODES = TILE * HD;       // bytes of a tile of codes
 constexpr int MAX_ITEMS = 512;         // tile pairs: tokens / (tokens a pair) + sequences
-constexpr int INFO = 8;                // tiles whose block scales are kept
+constexpr int INFO = 8;                // tiles whose block tables are kept
 
 template <bool FP8>
 struct Cfg {
-  static constexpr int RING = FP8 ? 3 : 4;     // operand tiles
-  static constexpr int STAGES = FP8 ? 3 : 0;   // tiles of codes on their way
-  // Warps that hand a tile over: all four widen, one looks after bf16's edges.
+  static constexpr int KB = FP8 ? CODES : OPER;  // bytes of a K tile
+  static constexpr int KR = FP8 ? 3 : 2;         // K tiles
+  static constexpr int VR = 2;                   // V tiles as operands, and as codes
+  // Warps that hand a V tile over: all four widen, one looks after bf16's edges.
   static constexpr int HANDS = FP8 ? 4 : 1;
-  static constexpr int SMEM = 2 * OPER + RING * OPER + STAGES * STAGE + 1024;
+  static constexpr int SMEM = 2 * OPER + KR * KB + VR * OPER + (FP8 ? VR * CODES : 0) + 1024;
 };
 
 struct Shared {
-  uint64_t landed[4], taken[4];      // copies: into a stage (bf16: ring slot), out of a stage
-  uint64_t full[4], empty[4];        // ring slots: ready, used
+  uint64_t k_in[4], k_out[4];        // K tiles: copied, used
+  uint64_t v_in[2], v_taken[2];      // V tiles: copied; codes read
+  uint64_t v_full[2], v_out[2];      // V operands: ready, used
   uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drained;
   uint32_t tmem;
-  int fail, last, cut[2], first, n_items;
+  int fail, last, cut[2], first;
   int scan[16];
   int pre[MAX_ITEMS + 1];            // key tiles (of all heads) before each item
   int4 item[MAX_ITEMS];              // {sequence, pair, first key tile, key tiles}
   int qpre[MAX_SEQS + 1];            // items before each sequence
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
   alignas(16) float ks[INFO][8], lv[INFO][8], iv[INFO][8];  // a key tile's blocks (read four at a time)
-  int row[16][8];                    // a key tile's blocks: cache rows
+  int row[INFO][8];                  // their cache rows
 };
 
 static_assert(Cfg<true>::SMEM + sizeof(Shared) <= 227 * 1024, "fits");
@@ -91,11 +95,11 @@ struct Maps {
 
 // One share's part of an item.
 struct Item {
-  int seq, kvh, kt0, n;     // first key tile of this part, key tiles
-  int tok0, tokens, pos0;   // first token row, tokens of the item, position of the first
-  int q_row;                // row of q / out of tok0
-  bool split;               // one tile: A has the even key tiles, B the odd ones
-  int c0, c1;               // CTAs that share the item (c0 == c1: it is whole here)
+  int seq, kvh, kt0, n;  // first key tile of this part, key tiles
+  int tokens, pos0;      // tokens of the item, position of the first
+  int q_row;             // its row of q / out
+  int row0, all;         // where the whole item begins, its key tiles
+  bool split;            // one tile: A has the even key tiles, B the odd ones
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -111,10 +115,16 @@ __device__ __forceinline__ float max3(A a, B b, C c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(as_f(a)), "f"(as_f(b)), "f"(as_f(c)));
   return r;
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = a.z;
+  x[3] = a.w;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 // a * k + d of two floats at once, and a + b.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -199,14 +209,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int gshift = 31 - __clz(b.group);       // group is a power of two
   const int tile_toks = TILE >> gshift;         // tokens of a tile
   const uint32_t base = (smem_addr(s_raw) + 1023u) & ~1023u;
-  const uint32_t q_smem = base, ring = base + 2 * OPER, stages = ring + C::RING * OPER;
+  const uint32_t q_smem = base, k_smem = base + 2 * OPER, v_smem = k_smem + C::KR * C::KB;
+  const uint32_t v_codes = v_smem + C::VR * OPER;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_addr(&sh.landed[i]), 1);
-      mbar_init(smem_addr(&sh.taken[i]), C::HANDS);
-      mbar_init(smem_addr(&sh.full[i]), C::HANDS);
-      mbar_init(smem_addr(&sh.empty[i]), 1);
+    for (int i = 0; i < C::KR; ++i) {
+      mbar_init(smem_addr(&sh.k_in[i]), 1);
+      mbar_init(smem_addr(&sh.k_out[i]), 1);
+    }
+    for (int i = 0; i < C::VR; ++i) {
+      mbar_init(smem_addr(&sh.v_in[i]), 1);
+      mbar_init(smem_addr(&sh.v_taken[i]), C::HANDS);
+      mbar_init(smem_addr(&sh.v_full[i]), C::HANDS);
+      mbar_init(smem_addr(&sh.v_out[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 128);
@@ -315,33 +330,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int4 e = sh.item[it];
     const int4 sq = sh.seq[e.x];
     Item p;
-    const int rel = cur - sh.pre[it];
-    p.kvh = rel / e.w;
-    const int off = rel - p.kvh * e.w;
+    int off = cur - sh.pre[it];
+    p.kvh = 0;
+    while (off >= e.w) {
+      off -= e.w;
+      ++p.kvh;
+    }
     p.seq = e.x;
     p.kt0 = e.z + off;
     p.n = min(e.w - off, end - cur);
-    p.tok0 = e.y * 2 * tile_toks;
-    p.tokens = min(sq.y - p.tok0, 2 * tile_toks);
-    p.pos0 = sq.z + p.tok0;
-    p.q_row = sq.x + p.tok0;
+    const int tok0 = e.y * 2 * tile_toks;
+    p.tokens = min(sq.y - tok0, 2 * tile_toks);
+    p.pos0 = sq.z + tok0;
+    p.q_row = sq.x + tok0;
     p.split = p.tokens <= tile_toks;
-    const int row0 = cur - off;
-    const int cut0 = (row0 + margin) / share + 1, cut1 = (row0 + e.w - margin - 1) / share;
-    const bool whole = e.w <= PR_WHOLE || cut0 > cut1;
-    p.c0 = whole ? 0 : cut0 - 1;
-    p.c1 = whole ? 0 : cut1;
+    p.row0 = cur - off;
+    p.all = e.w;
     return p;
-  };
-
-  // Load i of an item's part: K of the first tiles (one; two where A and B have a
-  // tile each), then V_j and K_(j + that many) in turn; {tile, V?}.
-  auto load_of = [&](const Item& p, int i) {
-    const int ld = min(p.split ? 2 : 1, p.n);
-    if (i < ld) return make_int2(i, 0);
-    const int k = i - ld;
-    if (k < 2 * (p.n - ld)) return make_int2((k >> 1) + (k & 1 ? ld : 0), k & 1 ? 0 : 1);
-    return make_int2(k - (p.n - ld), 1);
   };
 
   if (warp < 8)
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t s_tm = tmem + lanes + 128 * x, o_tm = tmem + lanes + 256 + 128 * x;
     uint32_t s_phase = 0, o_phase = 0;
     const int head_in_group = r & (b.group - 1), tok_in_tile = r >> gshift;
-    int tiles_before = 0;                  // key tiles this CTA has been through (INFO ring)
+    int tiles_before = 0;                  // key tiles this CTA has been through
     // After a wait that ran out the items are only walked through: the other
     // tile's warps count on this one's arrivals at the joint barriers.
     bool ok = true;
@@ -374,6 +379,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       {
         const uint8_t* src = reinterpret_cast<const uint8_t*>(
             a.q + ((size_t)(p.q_row + (live ? tok : 0)) * nq + head) * HD);
+        const bool mine = !p.split || x == 0;
+        const uint32_t dst = q_smem + x * OPER + r * 128;
         uint4 w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) w[c] = *reinterpret_cast<const uint4*>(src + 16 * c);
@@ -383,27 +390,39 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < 16; ++c) {
             const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(v[j])), fabsf(bf_hi(v[j]))));
+            for (int j = 0; j < 4; ++j) mx = max3(mx, fabsf(bf_lo(v[j])), fabsf(bf_hi(v[j])));
           }
-          const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-          qs *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+          // The power of two that brings it to (224, 448] = (0.875, 1.75] 2^8.
+          const uint32_t bits = __float_as_uint(mx);
+          const int e = min(max((int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 127);
+          // (NaN for a row with an infinity, which E4M3 would turn into 448.)
+          const float up = __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : (uint32_t)(127 + 8 - e) << 23);
+          qs *= __uint_as_float((uint32_t)(127 - 8 + e) << 23);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            w[c].x = nvu::f16x2_of(bf_lo(w[c].x) * up, bf_hi(w[c].x) * up);
-            w[c].y = nvu::f16x2_of(bf_lo(w[c].y) * up, bf_hi(w[c].y) * up);
-            w[c].z = nvu::f16x2_of(bf_lo(w[c].z) * up, bf_hi(w[c].z) * up);
-            w[c].w = nvu::f16x2_of(bf_lo(w[c].w) * up, bf_hi(w[c].w) * up);
+          for (int c = 0; c < 8; ++c) {  // 16 elements: a chunk of hi, a chunk of lo
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v0 = j < 2 ? (j ? w[2 * c].z : w[2 * c].x) : (j == 2 ? w[2 * c + 1].x : w[2 * c + 1].z);
+              const uint32_t v1 = j < 2 ? (j ? w[2 * c].w : w[2 * c].y) : (j == 2 ? w[2 * c + 1].y : w[2 * c + 1].w);
+              const float q[4] = {bf_lo(v0) * up, bf_hi(v0) * up, bf_lo(v1) * up, bf_hi(v1) * up};
+              const uint32_t h0 = f32x2_to_e4m3x2(q[0], q[1]), h1 = f32x2_to_e4m3x2(q[2], q[3]);
+              const float2 g0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), g1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
+              hi[j] = h0 | h1 << 16;
+              lo[j] = f32x2_to_e4m3x2(q[0] - g0.x, q[1] - g0.y) | f32x2_to_e4m3x2(q[2] - g1.x, q[3] - g1.y) << 16;
+            }
+            if (mine) {
+              const uint32_t at = dst + ((c ^ (r & 7)) << 4);
+              sts128(at, hi[0], hi[1], hi[2], hi[3]);
+              sts128(at + CODES, lo[0], lo[1], lo[2], lo[3]);
+            }
           }
-        }
-        if (!p.split || x == 0) {
-          const uint32_t dst = q_smem + x * OPER + r * 128;
+        } else if (mine) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             dst + (c >> 3) * HALF + (((c & 7) ^ (r & 7)) << 4)),
-                         "r"(w[c].x), "r"(w[c].y), "r"(w[c].z), "r"(w[c].w)
-                         : "memory");
+            sts128(dst + (c >> 3) * HALF + (((c & 7) ^ (r & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+        }
+        if (mine) {
           tc::fence_smem_to_mma();
           mbar_arrive(smem_addr(&sh.q_full[x]));
         }
@@ -422,50 +441,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after();
         const int slot = (tiles_before + j) & (INFO - 1);
         const int key0 = (p.kt0 + j) << 7;
-        const bool masked = key0 + TILE - 1 > hi_all || key0 < lo_all;
         // Two copies of the code, so that a tile that is seen whole pays nothing
-        // for the mask.
+        // for the mask.  The scores are read twice, 32 columns at a time with the
+        // next ones on their way: for the maximum, then for the weights.  (All
+        // 128 in registers at once: 8 % slower, for spills.)
         auto weigh = [&](auto edge) {
           constexpr bool MASK = decltype(edge)::value;
-          // What the blocks' scores are multiplied by (not 0, lest a masked score
-          // becomes NaN: a query of zeros, a scale of 0) and what is added.
-          float kf[FP8 ? 8 : 1], lv[8];
-          load8(sh.lv[slot], lv);
-          if constexpr (FP8) {
-            load8(sh.ks[slot], kf);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) kf[i] = fmaxf(qs * kf[i], 1.17549435e-38f);
-          } else {
-            kf[0] = fmaxf(qs, 1.17549435e-38f);
-          }
-          // The row's scores twice, 32 columns at a time with the next ones on their
-          // way: for the maximum, then for the weights.  (All 128 in registers at
-          // once: spills, and 8 % slower.)
           const int mlo = lo - key0, mhi = hi - key0;  // columns seen
-          auto mask = [&](int c, uint32_t (&v)[32]) {
+          auto mask = [&](int col, uint32_t (&v)[32]) {
+            if constexpr (MASK) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i < mlo || 32 * c + i > mhi) v[i] = 0xff800000u;  // -infinity
+              for (int i = 0; i < 32; ++i)
+                if (col + i < mlo || col + i > mhi) v[i] = 0xff800000u;  // -infinity
+            }
           };
-          uint32_t v[2][32];
-          float mx = -INFINITY;
-          tc::ld32(s_tm, v[0]);
-          tc::wait_ld(v[0]);
+          // What a block's scores are multiplied by: not 0, lest a masked score
+          // becomes NaN (a query of zeros, a scale of 0).
+          auto factors = [&](int blk, float (&k)[4]) {
+            if constexpr (FP8) {
+              load4(&sh.ks[slot][blk], k);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&y)[32] = v[c & 1];
-            tc::ld32(s_tm + 32 * ((c + 1) & 3), v[(c + 1) & 1]);
-            if constexpr (MASK) mask(c, y);
+              for (int i = 0; i < 4; ++i) k[i] = fmaxf(qs * k[i], 1.17549435e-38f);
+            } else {
+              k[0] = k[1] = k[2] = k[3] = fmaxf(qs, 1.17549435e-38f);
+            }
+          };
+          uint32_t va[32], vb[32];
+          float mx = -INFINITY;
+          auto highest = [&](const uint32_t (&v)[32], float k0, float k1, float l0, float l1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // a block of 16 keys
-              float b4[5];
-#pragma unroll
-              for (int i = 0; i < 5; ++i)
-                b4[i] = max3(y[16 * h + 3 * i], y[16 * h + 3 * i + 1], y[16 * h + 3 * i + 2]);
-              const float bm = fmaxf(max3(b4[0], b4[1], b4[2]), max3(b4[3], b4[4], y[16 * h + 15]));
-              mx = fmaxf(mx, fmaf(bm, kf[FP8 ? 2 * c + h : 0], lv[2 * c + h]));
+              const uint32_t* y = v + 16 * h;
+              const float a0 = max3(y[0], y[1], y[2]), a1 = max3(y[3], y[4], y[5]), a2 = max3(y[6], y[7], y[8]);
+              const float a3 = max3(y[9], y[10], y[11]), a4 = max3(y[12], y[13], y[14]);
+              mx = fmaxf(mx, fmaf(fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15])), h ? k1 : k0, h ? l1 : l0));
             }
-            tc::wait_ld(v[(c + 1) & 1]);
+          };
+          tc::ld32(s_tm, va);
+          tc::wait_ld(va);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float k[4], lv[4];
+            factors(4 * c, k);
+            load4(&sh.lv[slot][4 * c], lv);
+            tc::ld32(s_tm + 64 * c + 32, vb);
+            mask(64 * c, va);
+            highest(va, k[0], k[1], lv[0], lv[1]);
+            tc::wait_ld(vb);
+            tc::ld32(s_tm + ((64 * c + 64) & 127), va);
+            mask(64 * c + 32, vb);
+            highest(vb, k[2], k[3], lv[2], lv[3]);
+            tc::wait_ld(va);
           }
           const bool grow = mx > m + 8.0f;
           if (__any_sync(0xffffffffu, grow)) {
@@ -474,68 +500,70 @@ __global__ void __launch_bounds__(THREADS, 1)
             l *= f;
             m = mn;
             if (any) {  // the products so far
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tc::ld32(o_tm + 32 * c, vb);
+                tc::wait_ld(vb);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                uint32_t w[16];
-                tc::ld16(o_tm + 16 * c, w);
-                tc::wait_ld(w);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                tc::st16(o_tm + 16 * c, w);
+                for (int i = 0; i < 32; ++i) vb[i] = __float_as_uint(as_f(vb[i]) * f);
+                tc::st32(o_tm + 32 * c, vb);
               }
             }
           }
           any = true;
           const float mu = m > -INFINITY ? m : 0.0f;
-          float iv[8];
-          if constexpr (FP8) load8(sh.iv[slot], iv);
-          uint64_t sums[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // columns 32c .. are in v[c & 1]
-            uint32_t(&y)[32] = v[c & 1];
-            if (c < 3) tc::ld32(s_tm + 32 * (c + 1), v[(c + 1) & 1]);
-            if constexpr (MASK) mask(c, y);
-            uint32_t w[16];
+          float sum = 0.0f;
+          auto weights = [&](const uint32_t (&v)[32], const float* k, const float* lv, const float* iv,
+                             uint32_t (&w)[16]) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int blk = 2 * c + h;
-              const float d = lv[blk] - mu;
-              const uint64_t k2 = pair(kf[FP8 ? blk : 0], kf[FP8 ? blk : 0]), d2 = pair(d, d);
+              const float d = lv[h] - mu;
+              const uint64_t k2 = pair(k[h], k[h]), d2 = pair(d, d);
+              uint64_t s0 = 0, s1 = 0;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float y0, y1;
-                unpair(fma2(pair(as_f(y[16 * h + 2 * i]), as_f(y[16 * h + 2 * i + 1])), k2, d2), y0, y1);
+                unpair(fma2(pair(as_f(v[16 * h + 2 * i]), as_f(v[16 * h + 2 * i + 1])), k2, d2), y0, y1);
                 y0 = ex2(y0);
                 y1 = ex2(y1);
-                sums[i & 1] = FP8 && i < 2 ? pair(y0, y1) : add2(sums[i & 1], pair(y0, y1));
+                const uint64_t y = pair(y0, y1);
+                if (i & 1)
+                  s1 = i == 1 ? y : add2(s1, y);
+                else
+                  s0 = i == 0 ? y : add2(s0, y);
                 w[8 * h + i] = pack_p<FP8>(y0, y1);
               }
-              if constexpr (FP8) {
-                float y0, y1;
-                unpair(add2(sums[0], sums[1]), y0, y1);
-                l = fmaf(y0 + y1, iv[blk], l);
-              }
+              float y0, y1;
+              unpair(add2(s0, s1), y0, y1);
+              sum = FP8 ? fmaf(y0 + y1, iv[h], sum) : sum + (y0 + y1);
             }
-            tc::st16(s_tm + 16 * c, w);
-            if (c == 1) {  // the second product may begin
-              tc::wait_st();
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(&sh.p_half[x]));
-            }
-            if (c < 3) tc::wait_ld(v[(c + 1) & 1]);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float k[4], lv[4], iv[4];
+            factors(4 * c, k);
+            load4(&sh.lv[slot][4 * c], lv);
+            if constexpr (FP8) load4(&sh.iv[slot][4 * c], iv);
+            uint32_t w[16];
+            tc::ld32(s_tm + 64 * c + 32, vb);
+            mask(64 * c, va);
+            weights(va, k, lv, iv, w);
+            tc::st16(s_tm + 32 * c, w);
+            tc::wait_ld(vb);
+            if (c == 0) tc::ld32(s_tm + 64, va);
+            mask(64 * c + 32, vb);
+            weights(vb, k + 2, lv + 2, iv + 2, w);
+            tc::st16(s_tm + 32 * c + 16, w);
+            if (c == 0) tc::wait_ld(va);
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            // The second product may begin with half the weights.
+            if (lane == 0) mbar_arrive(smem_addr(c ? &sh.p_full[x] : &sh.p_half[x]));
           }
-          tc::wait_st();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[x]));
-          if constexpr (!FP8) {
-            float y0, y1;
-            unpair(add2(sums[0], sums[1]), y0, y1);
-            l += y0 + y1;
-          }
+          l += sum;
         };
-        if (masked)
+        if (key0 + TILE - 1 > hi_all || key0 < lo_all)
           weigh(std::true_type{});
         else
           weigh(std::false_type{});
@@ -548,47 +576,45 @@ __global__ void __launch_bounds__(THREADS, 1)
         o_phase ^= 1;
         tc::fence_after();
       }
-      const bool whole = p.c0 == p.c1;
+      // The cuts inside the item (none: it is whole here), the CTAs that share it.
+      const int cut0 = (p.row0 + margin) / share + 1, cut1 = (p.row0 + p.all - margin - 1) / share;
+      const bool whole = p.all <= PR_WHOLE || cut0 > cut1;
+      const int c0 = cut0 - 1, c1 = cut1;
       uint16_t* out = a.out + ((size_t)(p.q_row + tok) * nq + head) * HD;
       if (whole && !p.split) {
         const float inv = row_factor(a, head, m, l);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
           tc::wait_ld(v);
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 w;
-              w.x = pack_bf2(__uint_as_float(v[8 * i]) * inv, __uint_as_float(v[8 * i + 1]) * inv);
-              w.y = pack_bf2(__uint_as_float(v[8 * i + 2]) * inv, __uint_as_float(v[8 * i + 3]) * inv);
-              w.z = pack_bf2(__uint_as_float(v[8 * i + 4]) * inv, __uint_as_float(v[8 * i + 5]) * inv);
-              w.w = pack_bf2(__uint_as_float(v[8 * i + 6]) * inv, __uint_as_float(v[8 * i + 7]) * inv);
-              *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = w;
-            }
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
+                  make_uint4(pack_bf16(as_f(v[8 * i]) * inv, as_f(v[8 * i + 1]) * inv),
+                             pack_bf16(as_f(v[8 * i + 2]) * inv, as_f(v[8 * i + 3]) * inv),
+                             pack_bf16(as_f(v[8 * i + 4]) * inv, as_f(v[8 * i + 5]) * inv),
+                             pack_bf16(as_f(v[8 * i + 6]) * inv, as_f(v[8 * i + 7]) * inv));
           }
         }
         continue;
       }
       // Partial: maxima, sums and unscaled outputs of this tile, [4 columns][row].
       {
-        float* slot = pr_slot(a.ws, blockIdx.x, whole || (int)blockIdx.x == p.c0, x);
+        float* slot = pr_slot(a.ws, blockIdx.x, whole || (int)blockIdx.x == c0, x);
         __stcg(slot + r, m);
         __stcg(slot + TILE + r, any ? l : 0.0f);
         float4* o4 = reinterpret_cast<float4*>(slot + 2 * TILE);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
-          if (any) {
-            tc::ld32(o_tm + 32 * c, v);
-            tc::wait_ld(v);
-          }
+          tc::ld32(o_tm + 32 * c, v);
+          tc::wait_ld(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(o4 + (8 * c + i) * TILE + r,
-                   any ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                     __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                   any ? make_float4(as_f(v[4 * i]), as_f(v[4 * i + 1]), as_f(v[4 * i + 2]), as_f(v[4 * i + 3]))
                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
       }
@@ -596,8 +622,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       named_sync(1, 256);
       if (!whole) {
         if (tid == 0) {
-          uint32_t* ticket = ws_tickets(a.ws) + p.c0;
-          const bool last = atomicAdd(ticket, 1u) == (uint32_t)(p.c1 - p.c0);
+          uint32_t* ticket = ws_tickets(a.ws) + c0;
+          const bool last = atomicAdd(ticket, 1u) == (uint32_t)(c1 - c0);
           if (last) *ticket = 0u;  // ready for the next call
           __threadfence();
           sh.last = last;
@@ -607,131 +633,125 @@ __global__ void __launch_bounds__(THREADS, 1)
         named_sync(1, 256);  // sh.last is read before the next item sets it
         if (!last) continue;
       }
-      // Join: a pair's tile each; a split tile's two halves of the columns.
-      const int segs = whole ? 1 : p.c1 - p.c0 + 1, halves = p.split ? 2 : 1;
-      auto slot_of = [&](int k, int h) {
-        return pr_slot(a.ws, whole ? blockIdx.x : p.c0 + k, whole || k == 0, p.split ? h : x);
+      // Join, in the order of the keys' shares: a pair's tile each (64 columns at
+      // a time); of a split tile the two halves of the columns.
+      const int halves = p.split ? 2 : 1, parts = (whole ? 1 : c1 - c0 + 1) * halves;
+      auto slot_of = [&](int q) {
+        const int k = p.split ? q >> 1 : q, h = p.split ? q & 1 : x;
+        return pr_slot(a.ws, whole ? blockIdx.x : c0 + k, whole || k == 0, h);
       };
       float mm = -INFINITY, ll = 0.0f;
-      for (int k = 0; k < segs; ++k)
-        for (int h = 0; h < halves; ++h) mm = fmaxf(mm, __ldcg(slot_of(k, h) + r));
-      for (int k = 0; k < segs; ++k)
-        for (int h = 0; h < halves; ++h) {
-          const float* s = slot_of(k, h);
-          const float mk = __ldcg(s + r);
-          ll = fmaf(__ldcg(s + TILE + r), mk > -INFINITY ? ex2(mk - mm) : 0.0f, ll);
-        }
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) mm = fmaxf(mm, __ldcg(slot_of(q) + r));
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) {
+        const float* s = slot_of(q);
+        const float mk = __ldcg(s + r), lk = __ldcg(s + TILE + r);
+        ll = fmaf(lk, mk > -INFINITY ? ex2(mk - mm) : 0.0f, ll);
+      }
       const float inv = row_factor(a, head, mm, ll);
-      for (int c = p.split ? 4 * x : 0; c < (p.split ? 4 * x + 4 : 8); ++c) {  // 16 columns
-        float o[16] = {};
-        for (int k = 0; k < segs; ++k)
-          for (int h = 0; h < halves; ++h) {
-            const float* s = slot_of(k, h);
-            const float mk = __ldcg(s + r), f = mk > -INFINITY ? ex2(mk - mm) : 0.0f;
+#pragma unroll 1
+      for (int c = p.split ? x : 0; c < (p.split ? x + 1 : 2); ++c) {
+        float o[64];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 w = __ldcg(reinterpret_cast<const float4*>(s + 2 * TILE) + (4 * c + i) * TILE + r);
-              o[4 * i] = fmaf(w.x, f, o[4 * i]);
-              o[4 * i + 1] = fmaf(w.y, f, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(w.z, f, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(w.w, f, o[4 * i + 3]);
-            }
+        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
+#pragma unroll 1
+        for (int q = 0; q < parts; ++q) {
+          const float* s = slot_of(q);
+          const float4* o4 = reinterpret_cast<const float4*>(s + 2 * TILE) + 16 * c * TILE + r;
+          float4 w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __ldcg(o4 + i * TILE);
+          const float mk = __ldcg(s + r), f = mk > -INFINITY ? ex2(mk - mm) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            o[4 * i] = fmaf(w[i].x, f, o[4 * i]);
+            o[4 * i + 1] = fmaf(w[i].y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(w[i].z, f, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(w[i].w, f, o[4 * i + 3]);
           }
+        }
         if (live) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint4 w;
-            w.x = pack_bf2(o[8 * i] * inv, o[8 * i + 1] * inv);
-            w.y = pack_bf2(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-            w.z = pack_bf2(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-            w.w = pack_bf2(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-            *reinterpret_cast<uint4*>(out + 16 * c + 8 * i) = w;
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(out + 64 * c + 8 * i) =
+                make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                           pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                           pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                           pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
         }
       }
       // Slots that a later item of this CTA writes are read by now.
       named_sync(1, 256);
     }
   } else if (warp < 12) {
-    // ===== tiles from copies to operands =============================================
+    // ===== V tiles from copies to operands ==========================================
     const int w4 = warp - 8;
-    int u = 0;  // tiles handed over (K and V alike)
-    bool ok = warp - 8 < C::HANDS;
+    int t = 0;  // tiles handed over
+    bool ok = w4 < C::HANDS;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
       cur += p.n;
       const int see_hi = p.pos0 + p.tokens - 1;
       const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
-      for (int i = 0; i < 2 * p.n; ++i, ++u) {
-        const int2 kv = load_of(p, i);
-        const int key0 = (p.kt0 + kv.x) << 7;
-        const uint32_t dst = ring + (u % C::RING) * OPER;
+#pragma unroll 1
+      for (int j = 0; j < p.n; ++j, ++t) {
+        const int s = t % C::VR, key0 = (p.kt0 + j) << 7;
+        const uint32_t phase = (t / C::VR) & 1, dst = v_smem + s * OPER;
+        const bool edge = key0 < see_lo || key0 + TILE - 1 > see_hi;
+        if (!(ok = warp_wait(sh, sh.v_in[s], phase))) break;
         if constexpr (FP8) {
-          const int st = u % C::STAGES, slot = u % C::RING;
-          if (!(ok = warp_wait(sh, sh.landed[st], (u / C::STAGES) & 1))) break;
           uint4 w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {  // 4 keys a time, a chunk of 16 codes a lane
-            const int r = 32 * w4 + 4 * j + (lane >> 3), c = lane & 7;
+          for (int i = 0; i < 8; ++i) {  // 4 keys a time, a chunk of 16 codes a lane
+            const int r = 32 * w4 + 4 * i + (lane >> 3), c = lane & 7;
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[j].x), "=r"(w[j].y), "=r"(w[j].z), "=r"(w[j].w)
-                         : "r"(stages + st * STAGE + r * HD + ((c ^ (r & 7)) << 4)));
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "r"(v_codes + s * CODES + r * HD + ((c ^ (r & 7)) << 4)));
+          }
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = key0 + 32 * w4 + 4 * i + (lane >> 3);
+              if (key < see_lo || key > see_hi) w[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.taken[st]));
-          if (u >= C::RING && !(ok = warp_wait(sh, sh.empty[slot], ((u / C::RING) & 1) ^ 1))) break;
-          const bool edge = key0 < see_lo || key0 + TILE - 1 > see_hi;
+          if (lane == 0) mbar_arrive(smem_addr(&sh.v_taken[s]));
+          if (t >= C::VR && !(ok = warp_wait(sh, sh.v_out[s], phase ^ 1))) break;
+          // Operand chunks 2c and 2c + 1; the upper lanes store the odd one first,
+          // so that the eight lanes of a phase fall into distinct banks.
+          const int c = lane & 7, odd = (lane >> 2) & 1;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = 32 * w4 + 4 * j + (lane >> 3), c = lane & 7;
-            if (edge && (key0 + r < see_lo || key0 + r > see_hi)) w[j] = make_uint4(0u, 0u, 0u, 0u);
-            // Operand chunks 2c and 2c + 1; the upper lanes store the odd one
-            // first, so that the eight lanes of a phase fall into distinct banks.
-            const bool odd = (c & 4) != 0;
-            uint32_t x[8] = {e4m3x2_to_f16x2(w[j].x & 0xffffu), e4m3x2_to_f16x2(w[j].x >> 16),
-                             e4m3x2_to_f16x2(w[j].y & 0xffffu), e4m3x2_to_f16x2(w[j].y >> 16),
-                             e4m3x2_to_f16x2(w[j].z & 0xffffu), e4m3x2_to_f16x2(w[j].z >> 16),
-                             e4m3x2_to_f16x2(w[j].w & 0xffffu), e4m3x2_to_f16x2(w[j].w >> 16)};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int ch = 2 * c + (odd ? 1 - h : h);
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = odd ? x[4 * (1 - h) + k] : x[4 * h + k];
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               dst + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                           "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                           : "memory");
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int r = 32 * w4 + 4 * i + (lane >> 3);
+            const uint32_t row = dst + (c >> 2) * HALF + r * 128;
+            const uint32_t x0 = odd ? w[i].z : w[i].x, x1 = odd ? w[i].w : w[i].y;
+            const uint32_t y0 = odd ? w[i].x : w[i].z, y1 = odd ? w[i].y : w[i].w;
+            const int first = (2 * c + odd) & 7;
+            sts128(row + ((first ^ (r & 7)) << 4), e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x0 >> 16),
+                   e4m3x2_to_f16x2(x1 & 0xffffu), e4m3x2_to_f16x2(x1 >> 16));
+            sts128(row + ((first ^ 1 ^ (r & 7)) << 4), e4m3x2_to_f16x2(y0 & 0xffffu),
+                   e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 & 0xffffu), e4m3x2_to_f16x2(y1 >> 16));
           }
           tc::fence_smem_to_mma();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
-        } else {
-          const int slot = u % C::RING;
-          if (!(ok = warp_wait(sh, sh.landed[slot], (u / C::RING) & 1))) break;
-          if (kv.y && (key0 < see_lo || key0 + TILE - 1 > see_hi)) {
-            for (int r = lane >> 4; r < TILE; r += 2)
-              if (key0 + r < see_lo || key0 + r > see_hi) {
-                const int c = lane & 15;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 dst + (c >> 3) * HALF + r * 128 + ((c & 7) << 4)),
-                             "r"(0u)
-                             : "memory");
-              }
-            tc::fence_smem_to_mma();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
+        } else if (edge) {
+          for (int r = lane >> 4; r < TILE; r += 2)
+            if (key0 + r < see_lo || key0 + r > see_hi)
+              sts128(dst + ((lane & 15) >> 3) * HALF + r * 128 + ((lane & 7) << 4), 0u, 0u, 0u, 0u);
+          tc::fence_smem_to_mma();
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[s]));
       }
     }
   } else if (warp == 13) {
     // ===== K and V tiles, copied ======================================================
     const int box_keys = min(1 << b.page_shift, TILE), boxes = TILE / box_keys;
     const int n_rows = b.n_pages << b.page_shift;
-    int u = 0;             // tiles copied (K and V alike)
-    int tiles_before = 0;
+    int t = 0;             // K tiles copied before this item, and V tiles
+    int last_k = 0, last_v = 0;
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
@@ -747,186 +767,158 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int box = key & ~(box_keys - 1);
         return tile < p.n && box <= see_hi && box + box_keys - 1 >= see_lo ? cache_row(b, p.seq, key) : -1;
       };
-      int row[3] = {-1, -1, -1};
-      float ks[2] = {0.0f, 0.0f}, vs[2] = {1.0f, 1.0f};
-      auto scales_of = [&](int i) {
-        if constexpr (FP8) {
-          if (row[i] >= 0) {
-            const size_t at = (size_t)(row[i] >> 4) * b.nkv + p.kvh;
-            ks[i] = __ldg(a.k_scale + at);
-            vs[i] = __ldg(a.v_scale + at);
-          }
+      int row0 = -1, row1 = rows_of(0), row2 = rows_of(1);
+      float ks0 = 0.0f, vs0 = 1.0f, ks1 = 0.0f, vs1 = 1.0f;
+      auto scales = [&]() {
+        if (FP8 && row1 >= 0) {
+          const size_t at = (size_t)(row1 >> 4) * b.nkv + p.kvh;
+          ks1 = __ldg(a.k_scale + at);
+          vs1 = __ldg(a.v_scale + at);
         }
       };
-      row[1] = rows_of(0);
-      row[2] = rows_of(1);
-      scales_of(1);
-      for (int i = 0; i < 2 * p.n; ++i, ++u) {
-        const int2 kv = load_of(p, i);
-        const int tile = kv.x;
-        if (kv.y == 0 && (tile & 3) == 0) {
-          row[0] = row[1];
-          ks[0] = ks[1];
-          vs[0] = vs[1];
-          row[1] = row[2];
-          scales_of(1);
-          row[2] = rows_of((tile >> 2) + 2);
+      scales();
+      // K_j of tile step i where j = i, V of the step `lead` before: K of the first
+      // tiles (one; two where A and B have a tile each), then V and K in turn.
+      const int lead = p.split ? 2 : 1;
+#pragma unroll 1
+      for (int i = 0; ok && i < 2 * (p.n + lead); ++i) {
+        const bool v = (i & 1) == 0;              // V first
+        const int tile = v ? (i >> 1) - lead : i >> 1;
+        if (tile < 0 || tile >= p.n) continue;
+        const int n = t + tile, info = n & (INFO - 1);
+        const int slot = v ? n % C::VR : n % C::KR, turn = v ? n / C::VR : n / C::KR;
+        if (!v && (tile & 3) == 0) {
+          row0 = row1;
+          ks0 = ks1;
+          vs0 = vs1;
+          row1 = row2;
+          scales();
+          row2 = rows_of((tile >> 2) + 2);
         }
-        constexpr int SLOTS = FP8 ? C::STAGES : C::RING;
-        const int slot = u % SLOTS;
-        if (u >= SLOTS && !(ok = warp_wait(sh, FP8 ? sh.taken[slot] : sh.empty[slot],
-                                           ((u / SLOTS) & 1) ^ 1)))
-          break;
-        const uint32_t bar = smem_addr(&sh.landed[slot]);
-        const uint32_t dst = FP8 ? stages + slot * STAGE : ring + slot * OPER;
+        if (turn > 0) {
+          uint64_t& free = v ? (FP8 ? sh.v_taken[slot] : sh.v_out[slot]) : sh.k_out[slot];
+          if (!(ok = warp_wait(sh, free, (turn & 1) ^ 1))) break;
+        }
+        const uint32_t bar = smem_addr(v ? &sh.v_in[slot] : &sh.k_in[slot]);
+        const uint32_t dst = v ? (FP8 ? v_codes + slot * CODES : v_smem + slot * OPER) : k_smem + slot * C::KB;
         const int blk = 8 * (tile & 3) + (lane & 7);  // the lane with this lane's block
-        int at = __shfl_sync(0xffffffffu, row[0], blk);
-        if (kv.y == 0) {
-          if (lane < 8) sh.row[(tiles_before + tile) & 15][lane] = at;
-        } else {
-          at = sh.row[(tiles_before + tile) & 15][lane & 7];
-        }
+        int at = __shfl_sync(0xffffffffu, row0, blk);
+        if (v)
+          at = sh.row[info][lane & 7];
+        else if (lane < 8)
+          sh.row[info][lane] = at;
         // Box i of the tile starts at its block i * box_keys / 16.
         const int box = FP8 ? lane : lane >> 1, half = FP8 ? 0 : lane & 1;
         int y = __shfl_sync(0xffffffffu, at, (box * (box_keys >> 4)) & 7);
         if (y < 0) y = n_rows;
         if (box < boxes)
-          tma_box(dst + half * HALF + box * box_keys * 128, kv.y ? &maps.v : &maps.k,
-                  p.kvh * HD + 64 * half, y, bar);
-        if (kv.y == 0) {  // the tile's block table
-          const float k = FP8 ? __shfl_sync(0xffffffffu, ks[0], blk) : 1.0f;
+          tma_box(dst + half * HALF + box * box_keys * 128, v ? &maps.v : &maps.k, p.kvh * HD + 64 * half, y, bar);
+        if (!v) {  // the tile's block table
+          const float k = FP8 ? __shfl_sync(0xffffffffu, ks0, blk) : 1.0f;
           // A scale of zero would take a block's weights out of the sum: 2^-100.
-          const float v = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs[0], blk), 7.8886090522101181e-31f) : 1.0f;
+          const float z = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs0, blk), 7.8886090522101181e-31f) : 1.0f;
           if (lane < 8) {
-            const int info = (tiles_before + tile) & (INFO - 1);
             const int key = ((p.kt0 + tile) << 7) + 16 * lane;
             // A block that nothing sees may have any scale.
             const bool live = at >= 0 && key <= see_hi && key + BLOCK - 1 >= see_lo;
             sh.ks[info][lane] = live ? k : 0.0f;
-            sh.lv[info][lane] = live ? (FP8 ? log2f(v) : 0.0f) : -INFINITY;
-            sh.iv[info][lane] = live && FP8 ? 1.0f / v : 1.0f;
+            sh.lv[info][lane] = live ? (FP8 ? log2f(z) : 0.0f) : -INFINITY;
+            sh.iv[info][lane] = live && FP8 ? 1.0f / z : 1.0f;
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar, FP8 ? STAGE : OPER);
+        if (lane == 0) mbar_expect_tx(bar, v ? (FP8 ? CODES : OPER) : C::KB);
+        (v ? last_v : last_k) = n + 1;
       }
-      tiles_before += p.n;
+      t += p.n;
     }
     if (!ok) {  // nothing may land after the CTA has left
-      constexpr int SLOTS = FP8 ? C::STAGES : C::RING;
       const uint64_t deadline = globaltimer_ns() + 1000000000ull;
-      for (int n = max(0, u - SLOTS); n < u; ++n)
-        mbar_wait(smem_addr(&sh.landed[n % SLOTS]), (n / SLOTS) & 1, deadline);
+      for (int n = max(0, last_k - C::KR); n < last_k; ++n)
+        mbar_wait(smem_addr(&sh.k_in[n % C::KR]), (n / C::KR) & 1, deadline);
+      for (int n = max(0, last_v - C::VR); n < last_v; ++n)
+        mbar_wait(smem_addr(&sh.v_in[n % C::VR]), (n / C::VR) & 1, deadline);
     }
-  } else {
-    // ===== the products: one warp, of which one thread issues ======================
-    if (warp == 12) {
-      constexpr uint32_t s_desc = tc::inst_desc(!FP8, false), o_desc = tc::inst_desc(!FP8, true);
-      // Whatever steers the products is broadcast, so that it is uniform for
-      // the compiler too.
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t q_lo = tc::desc_lo(q_smem, 16), k_lo = tc::desc_lo(ring, 16);
-      const uint32_t v_lo = tc::desc_lo(ring, HALF);
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      int u = 0;
-      bool ok = true;
-      auto tile_in = [&](int n) { return warp_wait(sh, sh.full[n % C::RING], (n / C::RING) & 1); };
-      auto scores = [&](int x, int q, int n) {  // S_x = Q_q (tile in slot n)^T
-        const uint32_t slot = (uint32_t)(n % C::RING) * (OPER >> 4);
-        if (tc::one_thread()) {
+  } else if (warp == 12) {
+    // ===== the products: one warp, of which one thread issues ==========================
+    constexpr uint32_t s_desc = FP8 ? tc::inst_desc_e4m3() : tc::inst_desc(true, false);
+    constexpr uint32_t o_desc = tc::inst_desc(!FP8, true);
+    // Whatever steers the products is broadcast, so that it is uniform for the
+    // compiler too.
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t q_lo = tc::desc_lo(q_smem, 16), k_lo = tc::desc_lo(k_smem, 16);
+    const uint32_t v_lo = tc::desc_lo(v_smem, HALF);
+    uint32_t q_phase = 0, p_phase = 0;  // a bit a tile
+    int t = 0;
+    bool ok = true;
+    auto flip = [](uint32_t& bits, int x) { bits ^= 1u << x; };
+    auto k_ready = [&](int n) { return warp_wait(sh, sh.k_in[n % C::KR], (n / C::KR) & 1); };
+    // S_x = Q_q (K tile n)^T, and the tile's release.
+    auto scores = [&](int x, int q, int n, bool release) {
+      const uint32_t kt = k_lo + (uint32_t)(n % C::KR) * (C::KB >> 4), qt = q_lo + q * (OPER >> 4);
+      if (tc::one_thread()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
-            tc::mma_ss(tm + 128 * x, q_lo + q * (OPER >> 4) + off, k_lo + slot + off, s_desc, k > 0);
-          }
-          tc::commit(smem_addr(&sh.s_full[x]));
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (FP8)  // hi, then lo: 32 elements a step
+            tc::mma_ss<true>(tm + 128 * x, qt + ((k >> 2) * CODES + (k & 3) * 32 >> 4), kt + ((k & 3) * 32 >> 4),
+                             s_desc, k > 0);
+          else
+            tc::mma_ss<false>(tm + 128 * x, qt + ((k >> 2) * HALF + (k & 3) * 32 >> 4),
+                              kt + ((k >> 2) * HALF + (k & 3) * 32 >> 4), s_desc, k > 0);
         }
-        __syncwarp();
-      };
-      // O_x += P_x (tile in slot n), the weights of keys 0-63 and 64-127 as they come.
-      auto product = [&](int x, int n, bool add, bool last) {
-        const uint32_t slot = (uint32_t)(n % C::RING) * (OPER >> 4);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!(ok = warp_wait(sh, h ? sh.p_full[x] : sh.p_half[x], p_phase[x]))) return false;
-          tc::fence_after();
-          if (tc::one_thread()) {
-#pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k)
-              tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, v_lo + slot + k * (2048 >> 4), o_desc,
-                         k > 0 ? 1u : (uint32_t)add);
-            if (h && last) tc::commit(smem_addr(&sh.o_full[x]));
-          }
-          __syncwarp();
-        }
-        p_phase[x] ^= 1;
-        return true;
-      };
-      auto release = [&](int n) {
-        if (tc::one_thread()) tc::commit(smem_addr(&sh.empty[n % C::RING]));
-        __syncwarp();
-      };
-      for (int cur = begin, it = sh.first; ok && cur < end;) {
-        const Item p = part(cur, it);
-        cur += p.n;
-        const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
-        const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
-        const int ld = min(split ? 2 : 1, tiles);
-        // Places of K_j and V_j in the order of the loads.
-        auto k_at = [&](int j) { return u + (j < ld ? j : ld + 2 * (j - ld) + 1); };
-        auto v_at = [&](int j) { return u + (j < tiles - ld ? ld + 2 * j : tiles + j); };
-        for (int q = 0; ok && q < (split ? 1 : 2); ++q) {
-          ok = warp_wait(sh, sh.q_full[q], q_phase[q]);
-          q_phase[q] ^= 1;
-        }
-        if (!split) {
-          if (!ok || !(ok = tile_in(k_at(0)))) break;
-          tc::fence_after();
-          scores(0, 0, k_at(0));
-          scores(1, 1, k_at(0));
-          release(k_at(0));
-          for (int j = 0; ok && j < tiles; ++j) {
-            const bool more = j + 1 < tiles;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (x == 0 && !(ok = tile_in(v_at(j)))) break;
-              if (!product(x, v_at(j), j > 0, !more)) break;
-              if (x == 1) release(v_at(j));
-              if (more) {
-                if (x == 0 && !(ok = tile_in(k_at(j + 1)))) break;
-                tc::fence_after();
-                scores(x, x, k_at(j + 1));
-                if (x == 1) release(k_at(j + 1));
-              }
-            }
-          }
-        } else {
-          for (int j = 0; ok && j < ld; ++j) {
-            if (!(ok = tile_in(k_at(j)))) break;
-            tc::fence_after();
-            scores(j, 0, k_at(j));
-            release(k_at(j));
-          }
-          for (int j = 0; ok && j < tiles; ++j) {
-            const int x = j & 1;
-            if (!(ok = tile_in(v_at(j)))) break;
-            if (!product(x, v_at(j), j > 1, j + 2 >= tiles)) break;
-            release(v_at(j));
-            if (j + 2 < tiles) {
-              if (!(ok = tile_in(k_at(j + 2)))) break;
-              tc::fence_after();
-              scores(x, 0, k_at(j + 2));
-              release(k_at(j + 2));
-            }
-          }
-        }
-        u += 2 * tiles;
+        tc::commit(smem_addr(&sh.s_full[x]));
+        if (release) tc::commit(smem_addr(&sh.k_out[n % C::KR]));
       }
-      // Every product is complete before the TMEM is given back.
-      if (tc::one_thread()) tc::commit(smem_addr(&sh.drained));
       __syncwarp();
-      mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
+    };
+    for (int cur = begin, it = sh.first; ok && cur < end;) {
+      const Item p = part(cur, it);
+      cur += p.n;
+      const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
+      const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
+      // Step i is tile i & 1 (A, B) with key tile i / 2; split: key tile i.
+      const int steps = split ? tiles : 2 * tiles;
+#pragma unroll 1
+      for (int i = -2; ok && i < steps; ++i) {
+        const int x = i & 1, j = split ? i : i >> 1;
+        if (i >= 0) {  // O_x += P_x V_j, the weights of keys 0-63 and 64-127 as they come
+          const int n = t + j, s = n % C::VR;
+          const uint32_t vt = v_lo + s * (OPER >> 4);
+          if (!(ok = warp_wait(sh, sh.v_full[s], (n / C::VR) & 1))) break;
+          const bool add = split ? i > 1 : j > 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = warp_wait(sh, h ? sh.p_full[x] : sh.p_half[x], (p_phase >> x) & 1))) break;
+            tc::fence_after();
+            if (tc::one_thread()) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, vt + k * (2048 >> 4), o_desc,
+                           k > 0 ? 1u : (uint32_t)add);
+              if (h && i + 2 >= steps) tc::commit(smem_addr(&sh.o_full[x]));
+              if (h && (split || x == 1)) tc::commit(smem_addr(&sh.v_out[s]));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          flip(p_phase, x);
+        } else if (!split || i == -2) {  // the item's queries
+          if (!(ok = warp_wait(sh, sh.q_full[x], (q_phase >> x) & 1))) break;
+          flip(q_phase, x);
+        }
+        if (i + 2 < steps) {  // the scores two steps on
+          const int n = t + (split ? i + 2 : (i + 2) >> 1);
+          if (!(ok = k_ready(n))) break;
+          tc::fence_after();
+          scores(x, split ? 0 : x, n, split || x == 1);
+        }
+      }
+      t += tiles;
     }
+    // Every product is complete before the TMEM is given back.
+    if (tc::one_thread()) tc::commit(smem_addr(&sh.drained));
+    __syncwarp();
+    mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
   }
   __syncwarp();
   tc::fence_before();

@@ -58,17 +58,29 @@ __device__ __forceinline__ bool one_thread() {
   return r != 0;
 }
 
-// D (TMEM) = A B (+ D if add), one K = 16 step; by one thread.
+// The same of kind::f8f6f4: A and B E4M3, both K-major.
+constexpr uint32_t inst_desc_e4m3() { return 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24; }
+
+// D (TMEM) = A B (+ D if add), one step of 32 bytes of K; by one thread.
+template <bool E4M3>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                        uint32_t add) {
-  asm volatile(
-      "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
-      "  mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "r"(DESC_HI)
-      : "memory");
+  if constexpr (E4M3)
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
+        "  mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
+        "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p; }" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "r"(DESC_HI)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
+        "  mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
+        "  tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "r"(DESC_HI)
+        : "memory");
 }
-// The same with A in TMEM (two 16-bit elements a column).
+// A in TMEM (two 16-bit elements a column), kind::f16: one K = 16 step.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
                                        uint32_t add) {
   asm volatile(
@@ -98,15 +110,15 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// The same for 16 columns.
-__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]));
 }
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -123,13 +135,6 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
                "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
                "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
-               :);
-}
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-               "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-               "+r"(r[14]), "+r"(r[15])
                :);
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

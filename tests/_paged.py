@@ -118,6 +118,8 @@ class Case:
           - a score is a dot product of 128 terms in fp32: 128 2^-24 S off at
             most, and the exponent's argument 2^-21 S more; e^s is off by as
             much, in the numerator and the denominator;
+          - over an E4M3 cache a query's elements count to 2^-18 of its largest:
+            F = 2^-18 max |q_d| sum |k_jd| scale at most in a score;
           - the weights enter the second product with p_bits significant bits
             (rounded: 2^-p_bits), and, as f16, with an absolute step of 2^-24 of
             the largest weight-times-scale (half of it is charged for each key);
@@ -159,6 +161,9 @@ class Case:
                 q = self.q[sl, h].double()
                 sc = (q @ k[:, h // g].T) * scale
                 big = float((q.abs() @ k[:, h // g].abs().T).max()) * scale
+                flat = 0.0
+                if self.fmt == "e4m3":
+                    flat = float(q.abs().max() * k[:, h // g].abs().nan_to_num(0.0).sum(1).max()) * scale
                 sc = sc.masked_fill(hide, -math.inf)
                 top = sc.amax(1, keepdim=True)
                 if sinks is not None:
@@ -174,7 +179,7 @@ class Case:
                 out[sl, h] = p @ vh
                 mass = p @ vh.abs()
                 nk = len(keys)
-                c = 2 * (2.0 ** -17 + 2.0 ** -21) * big + 2.0 ** -p_bits + 2.0 ** -21 + \
+                c = 2 * (2.0 ** -17 + 2.0 ** -21) * big + 2 * 2.0 ** -18 * flat + 2.0 ** -p_bits + 2.0 ** -21 + \
                     2.0 ** -23 * (nk / 16 + 64)
                 low_p = 0.0
                 if self.fmt == "e4m3":
