@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           };
           tc::ld32(s_tm, va);
-          tc::wait_ld(va);
+          tc::wait_ld();
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             float k[4], lv[4];
@@ -487,11 +487,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::ld32(s_tm + 64 * c + 32, vb);
             mask(64 * c, va);
             highest(va, k[0], k[1], lv[0], lv[1]);
-            tc::wait_ld(vb);
+            tc::wait_ld();
             tc::ld32(s_tm + ((64 * c + 64) & 127), va);
             mask(64 * c + 32, vb);
             highest(vb, k[2], k[3], lv[2], lv[3]);
-            tc::wait_ld(va);
+            tc::wait_ld();
           }
           const bool grow = mx > m + 8.0f;
           if (__any_sync(0xffffffffu, grow)) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 tc::ld32(o_tm + 32 * c, vb);
-                tc::wait_ld(vb);
+                tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) vb[i] = __float_as_uint(as_f(vb[i]) * f);
                 tc::st32(o_tm + 32 * c, vb);
@@ -549,12 +549,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             mask(64 * c, va);
             weights(va, k, lv, iv, w);
             tc::st16(s_tm + 32 * c, w);
-            tc::wait_ld(vb);
+            tc::wait_ld();
             if (c == 0) tc::ld32(s_tm + 64, va);
             mask(64 * c + 32, vb);
             weights(vb, k + 2, lv + 2, iv + 2, w);
             tc::st16(s_tm + 32 * c + 16, w);
-            if (c == 0) tc::wait_ld(va);
+            if (c == 0) tc::wait_ld();
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
-          tc::wait_ld(v);
+          tc::wait_ld();
           if (live) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
-          tc::wait_ld(v);
+          tc::wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(o4 + (8 * c + i) * TILE + r,
