@@ -22,7 +22,7 @@
 // One CTA per SM takes two tiles A and B at a time: while one tile's scores are
 // with its softmax warps, the other's products run.  A and B are neighbouring
 // tiles of a prompt (they share the keys they load), or, where a sequence
-// brings no more than one tile, the even and the odd key tiles of that one.
+// brings no more than one tile, every other key tile of that one.
 //   warps 0-3, 4-7: softmax of A, of B; a thread has a row (TMEM lane)
 //   warp 13:        looks pages up and copies K and V tiles by TMA, a box a page
 //                   (16 to 128 keys), V's codes into a staging ring; a page that
@@ -30,7 +30,7 @@
 //   warps 8-11:     widen V's codes to f16, and zero the rows of V that no query
 //                   of the item sees: whatever bits lie there must not meet a
 //                   zero weight
-//   warp 12:        issues every mma
+//   warps 12, 14:   issue the products of A, of B
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each; P takes its S's place.  O is
 // rescaled only when a row's maximum grows by more than 2^8.
 //
@@ -61,7 +61,7 @@ constexpr int INFO = 8;                // tiles whose block tables are kept
 template <bool FP8>
 struct Cfg {
   static constexpr int KB = FP8 ? CODES : OPER;  // bytes of a K tile
-  static constexpr int KR = FP8 ? 3 : 2;         // K tiles
+  static constexpr int KR = 2;                   // K tiles
   static constexpr int VR = 2;                   // V tiles as operands, and as codes
   // Warps that hand a V tile over: all four widen, one looks after bf16's edges.
   static constexpr int HANDS = FP8 ? 4 : 1;
@@ -69,7 +69,7 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t k_in[4], k_out[4];        // K tiles: copied, used
+  uint64_t k_in[2], k_out[2];        // K tiles: copied, used
   uint64_t v_in[2], v_taken[2];      // V tiles: copied; codes read
   uint64_t v_full[2], v_out[2];      // V operands: ready, used
   uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drained;
@@ -82,6 +82,7 @@ struct Shared {
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
   alignas(16) float ks[INFO][8], lv[INFO][8], iv[INFO][8];  // a key tile's blocks (read four at a time)
   int row[INFO][8];                  // their cache rows
+  int plain[INFO];                   // all of them are there
 };
 
 static_assert(Cfg<true>::SMEM + sizeof(Shared) <= 227 * 1024, "fits");
@@ -99,7 +100,7 @@ struct Item {
   int tokens, pos0;      // tokens of the item, position of the first
   int q_row;             // its row of q / out
   int row0, all;         // where the whole item begins, its key tiles
-  bool split;            // one tile: A has the even key tiles, B the odd ones
+  bool split;            // one tile: A and B have every other key tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -114,13 +115,6 @@ __device__ __forceinline__ float max3(A a, B b, C c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(as_f(a)), "f"(as_f(b)), "f"(as_f(c)));
   return r;
-}
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  x[0] = a.x;
-  x[1] = a.y;
-  x[2] = a.z;
-  x[3] = a.w;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
@@ -215,13 +209,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::KR; ++i) {
       mbar_init(smem_addr(&sh.k_in[i]), 1);
-      mbar_init(smem_addr(&sh.k_out[i]), 1);
+      mbar_init(smem_addr(&sh.k_out[i]), 2);
     }
     for (int i = 0; i < C::VR; ++i) {
       mbar_init(smem_addr(&sh.v_in[i]), 1);
       mbar_init(smem_addr(&sh.v_taken[i]), C::HANDS);
       mbar_init(smem_addr(&sh.v_full[i]), C::HANDS);
-      mbar_init(smem_addr(&sh.v_out[i]), 1);
+      mbar_init(smem_addr(&sh.v_out[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 128);
@@ -231,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       sh.cut[i] = -1;
     }
-    mbar_init(smem_addr(&sh.drained), 1);
+    mbar_init(smem_addr(&sh.drained), 2);
     sh.fail = 0;
     fence_mbar_init();
   }
@@ -425,6 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (mine) {
           tc::fence_smem_to_mma();
           mbar_arrive(smem_addr(&sh.q_full[x]));
+          if (p.split) mbar_arrive(smem_addr(&sh.q_full[1]));  // B's products take them too
         }
       }
 
@@ -435,64 +430,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m = -INFINITY, l = 0.0f;
       const int step = p.split ? 2 : 1;
       bool any = false;
-      for (int j = p.split ? x : 0; ok && j < p.n; j += step) {
+      for (int j = p.split ? (x ^ tiles_before) & 1 : 0; ok && j < p.n; j += step) {
         if (!(ok = warp_wait(sh, sh.s_full[x], s_phase))) break;
         s_phase ^= 1;
         tc::fence_after();
         const int slot = (tiles_before + j) & (INFO - 1);
         const int key0 = (p.kt0 + j) << 7;
-        // Two copies of the code, so that a tile that is seen whole pays nothing
-        // for the mask.  The scores are read twice, 32 columns at a time with the
-        // next ones on their way: for the maximum, then for the weights.  (All
-        // 128 in registers at once: 8 % slower, for spills.)
+        // Two copies of the code, so that a tile that is seen whole, of pages that
+        // are all there, pays nothing for the mask.  A thread's 128 scores stay in
+        // registers from the maximum to the weights: one stream of independent
+        // work (with the scores read twice, 32 at a time, the exponentials of a
+        // piece did not overlap the next's: 5 % slower).
         auto weigh = [&](auto edge) {
           constexpr bool MASK = decltype(edge)::value;
+          constexpr bool BLOCKS = FP8 || MASK;  // blocks differ in scale or presence
           const int mlo = lo - key0, mhi = hi - key0;  // columns seen
-          auto mask = [&](int col, uint32_t (&v)[32]) {
+          // What a block's scores are multiplied by (not 0, lest a masked score
+          // becomes NaN: a query of zeros, a scale of 0), what is added, and what
+          // its weights count in the sum.
+          auto factor = [&](int blk) {
+            return FP8 ? fmaxf(qs * sh.ks[slot][blk], 1.17549435e-38f) : fmaxf(qs, 1.17549435e-38f);
+          };
+          auto offset = [&](int blk) { return BLOCKS ? sh.lv[slot][blk] : 0.0f; };
+          uint32_t v[4][32];
+          float bm[8];  // the blocks' highest scores
+          auto highest = [&](int c) {
             if constexpr (MASK) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (col + i < mlo || col + i > mhi) v[i] = 0xff800000u;  // -infinity
+                if (32 * c + i < mlo || 32 * c + i > mhi) v[c][i] = 0xff800000u;  // -infinity
             }
-          };
-          // What a block's scores are multiplied by: not 0, lest a masked score
-          // becomes NaN (a query of zeros, a scale of 0).
-          auto factors = [&](int blk, float (&k)[4]) {
-            if constexpr (FP8) {
-              load4(&sh.ks[slot][blk], k);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) k[i] = fmaxf(qs * k[i], 1.17549435e-38f);
-            } else {
-              k[0] = k[1] = k[2] = k[3] = fmaxf(qs, 1.17549435e-38f);
-            }
-          };
-          uint32_t va[32], vb[32];
-          float mx = -INFINITY;
-          auto highest = [&](const uint32_t (&v)[32], float k0, float k1, float l0, float l1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // a block of 16 keys
-              const uint32_t* y = v + 16 * h;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* y = v[c] + 16 * h;
               const float a0 = max3(y[0], y[1], y[2]), a1 = max3(y[3], y[4], y[5]), a2 = max3(y[6], y[7], y[8]);
               const float a3 = max3(y[9], y[10], y[11]), a4 = max3(y[12], y[13], y[14]);
-              mx = fmaxf(mx, fmaf(fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15])), h ? k1 : k0, h ? l1 : l0));
+              bm[2 * c + h] = fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15]));
+              if constexpr (BLOCKS) bm[2 * c + h] = fmaf(bm[2 * c + h], factor(2 * c + h), offset(2 * c + h));
             }
           };
-          tc::ld32(s_tm, va);
+          tc::ld32(s_tm, v[0]);
+          tc::ld32(s_tm + 32, v[1]);
           tc::wait_ld();
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float k[4], lv[4];
-            factors(4 * c, k);
-            load4(&sh.lv[slot][4 * c], lv);
-            tc::ld32(s_tm + 64 * c + 32, vb);
-            mask(64 * c, va);
-            highest(va, k[0], k[1], lv[0], lv[1]);
-            tc::wait_ld();
-            tc::ld32(s_tm + ((64 * c + 64) & 127), va);
-            mask(64 * c + 32, vb);
-            highest(vb, k[2], k[3], lv[2], lv[3]);
-            tc::wait_ld();
-          }
+          tc::ld32(s_tm + 64, v[2]);
+          tc::ld32(s_tm + 96, v[3]);
+          highest(0);
+          highest(1);
+          tc::wait_ld();
+          highest(2);
+          highest(3);
+          float mx = max3(max3(bm[0], bm[1], bm[2]), max3(bm[3], bm[4], bm[5]), fmaxf(bm[6], bm[7]));
+          if constexpr (!BLOCKS) mx *= factor(0);
           const bool grow = mx > m + 8.0f;
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = fmaxf(m, mx);
@@ -501,69 +489,63 @@ __global__ void __launch_bounds__(THREADS, 1)
             m = mn;
             if (any) {  // the products so far
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                tc::ld32(o_tm + 32 * c, vb);
+              for (int c = 0; c < 8; ++c) {
+                uint32_t w[16];
+                tc::ld16(o_tm + 16 * c, w);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) vb[i] = __float_as_uint(as_f(vb[i]) * f);
-                tc::st32(o_tm + 32 * c, vb);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(as_f(w[i]) * f);
+                tc::st16(o_tm + 16 * c, w);
               }
             }
           }
           any = true;
           const float mu = m > -INFINITY ? m : 0.0f;
-          float sum = 0.0f;
-          auto weights = [&](const uint32_t (&v)[32], const float* k, const float* lv, const float* iv,
-                             uint32_t (&w)[16]) {
+          uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float d = lv[h] - mu;
-              const uint64_t k2 = pair(k[h], k[h]), d2 = pair(d, d);
-              uint64_t s0 = 0, s1 = 0;
+              const int blk = 2 * c + h;
+              const float k = factor(blk), d = offset(blk) - mu;
+              const uint64_t k2 = pair(k, k), d2 = pair(d, d);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float y0, y1;
-                unpair(fma2(pair(as_f(v[16 * h + 2 * i]), as_f(v[16 * h + 2 * i + 1])), k2, d2), y0, y1);
+                unpair(fma2(pair(as_f(v[c][16 * h + 2 * i]), as_f(v[c][16 * h + 2 * i + 1])), k2, d2), y0, y1);
                 y0 = ex2(y0);
                 y1 = ex2(y1);
                 const uint64_t y = pair(y0, y1);
+                const bool first = i < 2 && (FP8 || blk == 0);
                 if (i & 1)
-                  s1 = i == 1 ? y : add2(s1, y);
+                  s1 = first ? y : add2(s1, y);
                 else
-                  s0 = i == 0 ? y : add2(s0, y);
+                  s0 = first ? y : add2(s0, y);
                 w[8 * h + i] = pack_p<FP8>(y0, y1);
               }
-              float y0, y1;
-              unpair(add2(s0, s1), y0, y1);
-              sum = FP8 ? fmaf(y0 + y1, iv[h], sum) : sum + (y0 + y1);
+              if constexpr (FP8) {
+                float y0, y1;
+                unpair(add2(s0, s1), y0, y1);
+                l = fmaf(y0 + y1, sh.iv[slot][blk], l);
+              }
             }
-          };
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float k[4], lv[4], iv[4];
-            factors(4 * c, k);
-            load4(&sh.lv[slot][4 * c], lv);
-            if constexpr (FP8) load4(&sh.iv[slot][4 * c], iv);
-            uint32_t w[16];
-            tc::ld32(s_tm + 64 * c + 32, vb);
-            mask(64 * c, va);
-            weights(va, k, lv, iv, w);
-            tc::st16(s_tm + 32 * c, w);
-            tc::wait_ld();
-            if (c == 0) tc::ld32(s_tm + 64, va);
-            mask(64 * c + 32, vb);
-            weights(vb, k + 2, lv + 2, iv + 2, w);
-            tc::st16(s_tm + 32 * c + 16, w);
-            if (c == 0) tc::wait_ld();
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            // The second product may begin with half the weights.
-            if (lane == 0) mbar_arrive(smem_addr(c ? &sh.p_full[x] : &sh.p_half[x]));
+            tc::st16(s_tm + 16 * c, w);
+            if (c & 1) {
+              tc::wait_st();
+              tc::fence_before();
+              __syncwarp();
+              // The second product may begin with half the weights.
+              if (lane == 0) mbar_arrive(smem_addr(c == 1 ? &sh.p_half[x] : &sh.p_full[x]));
+            }
           }
-          l += sum;
+          if constexpr (!FP8) {
+            float y0, y1;
+            unpair(add2(s0, s1), y0, y1);
+            l += y0 + y1;
+          }
         };
-        if (key0 + TILE - 1 > hi_all || key0 < lo_all)
+        if (key0 + TILE - 1 > hi_all || key0 < lo_all || (!FP8 && !sh.plain[slot]))
           weigh(std::true_type{});
         else
           weigh(std::false_type{});
@@ -825,6 +807,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             sh.lv[info][lane] = live ? (FP8 ? log2f(z) : 0.0f) : -INFINITY;
             sh.iv[info][lane] = live && FP8 ? 1.0f / z : 1.0f;
           }
+          const unsigned there = __ballot_sync(0xffffffffu, at >= 0);
+          if (lane == 0) sh.plain[info] = (there & 0xffu) == 0xffu;
         }
         __syncwarp();
         if (lane == 0) mbar_expect_tx(bar, v ? (FP8 ? CODES : OPER) : C::KB);
@@ -839,78 +823,80 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int n = max(0, last_v - C::VR); n < last_v; ++n)
         mbar_wait(smem_addr(&sh.v_in[n % C::VR]), (n / C::VR) & 1, deadline);
     }
-  } else if (warp == 12) {
-    // ===== the products: one warp, of which one thread issues ==========================
+  } else if (warp == 12 || warp == 14) {
+    // ===== the products of tile A, of tile B: a warp each, of which one thread issues ===
+    // Issue blocks while the tensor core is busy, and the tensor core idles while
+    // its issuer waits on barriers (~60 cycles each, four a tile): with one warp
+    // for both tiles it idled a third of the time.
     constexpr uint32_t s_desc = FP8 ? tc::inst_desc_e4m3() : tc::inst_desc(true, false);
     constexpr uint32_t o_desc = tc::inst_desc(!FP8, true);
+    const int x = warp == 14;
     // Whatever steers the products is broadcast, so that it is uniform for the
     // compiler too.
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t s_at = __shfl_sync(0xffffffffu, tmem + 128 * x, 0), o_at = s_at + 256;
     const uint32_t q_lo = tc::desc_lo(q_smem, 16), k_lo = tc::desc_lo(k_smem, 16);
     const uint32_t v_lo = tc::desc_lo(v_smem, HALF);
-    uint32_t q_phase = 0, p_phase = 0;  // a bit a tile
+    uint32_t q_phase = 0, p_phase = 0;
     int t = 0;
     bool ok = true;
-    auto flip = [](uint32_t& bits, int x) { bits ^= 1u << x; };
-    auto k_ready = [&](int n) { return warp_wait(sh, sh.k_in[n % C::KR], (n / C::KR) & 1); };
-    // S_x = Q_q (K tile n)^T, and the tile's release.
-    auto scores = [&](int x, int q, int n, bool release) {
-      const uint32_t kt = k_lo + (uint32_t)(n % C::KR) * (C::KB >> 4), qt = q_lo + q * (OPER >> 4);
-      if (tc::one_thread()) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if constexpr (FP8)  // hi, then lo: 32 elements a step
-            tc::mma_ss<true>(tm + 128 * x, qt + ((k >> 2) * CODES + (k & 3) * 32 >> 4), kt + ((k & 3) * 32 >> 4),
-                             s_desc, k > 0);
-          else
-            tc::mma_ss<false>(tm + 128 * x, qt + ((k >> 2) * HALF + (k & 3) * 32 >> 4),
-                              kt + ((k >> 2) * HALF + (k & 3) * 32 >> 4), s_desc, k > 0);
-        }
-        tc::commit(smem_addr(&sh.s_full[x]));
-        if (release) tc::commit(smem_addr(&sh.k_out[n % C::KR]));
-      }
-      __syncwarp();
-    };
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
       cur += p.n;
       const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
       const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
-      // Step i is tile i & 1 (A, B) with key tile i / 2; split: key tile i.
-      const int steps = split ? tiles : 2 * tiles;
+      // Of a split item A takes the tiles of even number (counted over the CTA's
+      // whole share, so that a ring slot is always the same tile's: a phase that
+      // a warp neither used nor waited for could pass for the next one); both
+      // share A's queries, and a key tile has one user, which counts for both.
+      const int step = split ? 2 : 1, first = split ? (x ^ t) & 1 : 0;
+      const uint32_t qt = q_lo + (split ? 0 : x) * (OPER >> 4);
+      if (!(ok = warp_wait(sh, sh.q_full[x], q_phase))) break;
+      q_phase ^= 1;
 #pragma unroll 1
-      for (int i = -2; ok && i < steps; ++i) {
-        const int x = i & 1, j = split ? i : i >> 1;
-        if (i >= 0) {  // O_x += P_x V_j, the weights of keys 0-63 and 64-127 as they come
-          const int n = t + j, s = n % C::VR;
-          const uint32_t vt = v_lo + s * (OPER >> 4);
-          if (!(ok = warp_wait(sh, sh.v_full[s], (n / C::VR) & 1))) break;
-          const bool add = split ? i > 1 : j > 0;
+      for (int j = first - step; j < tiles; j += step) {
+        const int next = j + step;
+        const int nv = t + j, sv = nv % C::VR, nk = t + next, sk = nk % C::KR;
+        if (next < tiles && !(ok = warp_wait(sh, sh.k_in[sk], (nk / C::KR) & 1))) break;
+        if (j >= 0) {  // O += P V_j, the weights of keys 0-63 and 64-127 as they come
+          if (!(ok = warp_wait(sh, sh.v_full[sv], (nv / C::VR) & 1))) break;
+          const uint32_t vt = v_lo + sv * (OPER >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!(ok = warp_wait(sh, h ? sh.p_full[x] : sh.p_half[x], (p_phase >> x) & 1))) break;
+            if (!(ok = warp_wait(sh, h ? sh.p_full[x] : sh.p_half[x], p_phase))) break;
             tc::fence_after();
             if (tc::one_thread()) {
 #pragma unroll
               for (int k = 4 * h; k < 4 * h + 4; ++k)
-                tc::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * k, vt + k * (2048 >> 4), o_desc,
-                           k > 0 ? 1u : (uint32_t)add);
-              if (h && i + 2 >= steps) tc::commit(smem_addr(&sh.o_full[x]));
-              if (h && (split || x == 1)) tc::commit(smem_addr(&sh.v_out[s]));
+                tc::mma_ts(o_at, s_at + 8 * k, vt + k * (2048 >> 4), o_desc, k > 0 ? 1u : (uint32_t)(j > first));
+              if (h) {
+                tc::commit(smem_addr(&sh.v_out[sv]));
+                if (split) tc::commit(smem_addr(&sh.v_out[sv]));
+                if (next >= tiles) tc::commit(smem_addr(&sh.o_full[x]));
+              }
             }
             __syncwarp();
           }
           if (!ok) break;
-          flip(p_phase, x);
-        } else if (!split || i == -2) {  // the item's queries
-          if (!(ok = warp_wait(sh, sh.q_full[x], (q_phase >> x) & 1))) break;
-          flip(q_phase, x);
+          p_phase ^= 1;
         }
-        if (i + 2 < steps) {  // the scores two steps on
-          const int n = t + (split ? i + 2 : (i + 2) >> 1);
-          if (!(ok = k_ready(n))) break;
-          tc::fence_after();
-          scores(x, split ? 0 : x, n, split || x == 1);
+        if (next < tiles) {  // S = Q K_next^T
+          const uint32_t kt = k_lo + sk * (C::KB >> 4);
+          if (j < 0) tc::fence_after();
+          if (tc::one_thread()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if constexpr (FP8)  // hi, then lo: 32 elements a step
+                tc::mma_ss<true>(s_at, qt + ((k >> 2) * CODES + (k & 3) * 32 >> 4), kt + ((k & 3) * 32 >> 4),
+                                 s_desc, k > 0);
+              else
+                tc::mma_ss<false>(s_at, qt + ((k >> 2) * HALF + (k & 3) * 32 >> 4),
+                                  kt + ((k >> 2) * HALF + (k & 3) * 32 >> 4), s_desc, k > 0);
+            }
+            tc::commit(smem_addr(&sh.s_full[x]));
+            tc::commit(smem_addr(&sh.k_out[sk]));
+            if (split) tc::commit(smem_addr(&sh.k_out[sk]));
+          }
+          __syncwarp();
         }
       }
       t += tiles;
