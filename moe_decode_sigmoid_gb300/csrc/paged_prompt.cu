@@ -24,9 +24,9 @@
 // tiles of a prompt (they share the keys they load), or, where a sequence
 // brings no more than one tile, every other key tile of that one.
 //   warps 0-3, 4-7: softmax of A, of B; a thread has a row (TMEM lane)
-//   warp 13:        looks pages up and copies K and V tiles by TMA, a box a page
-//                   (16 to 128 keys), V's codes into a staging ring; a page that
-//                   is not there is a box beyond the cache, which fills with zeros
+//   warps 13, 15:   look pages up and copy K, V tiles by TMA, a box a page (16 to
+//                   128 keys), V's codes into a staging ring; a page that is not
+//                   there is a box beyond the cache, which fills with zeros
 //   warps 8-11:     widen V's codes to f16, and zero the rows of V that no query
 //                   of the item sees: whatever bits lie there must not meet a
 //                   zero weight
@@ -81,7 +81,6 @@ struct Shared {
   int qpre[MAX_SEQS + 1];            // items before each sequence
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
   alignas(16) float ks[INFO][8], lv[INFO][8], iv[INFO][8];  // a key tile's blocks (read four at a time)
-  int row[INFO][8];                  // their cache rows
   int plain[INFO];                   // all of them are there
 };
 
@@ -469,42 +468,12 @@ __global__ void __launch_bounds__(THREADS, 1)
               if constexpr (BLOCKS) bm[2 * c + h] = fmaf(bm[2 * c + h], factor(2 * c + h), offset(2 * c + h));
             }
           };
-          tc::ld32(s_tm, v[0]);
-          tc::ld32(s_tm + 32, v[1]);
-          tc::wait_ld();
-          tc::ld32(s_tm + 64, v[2]);
-          tc::ld32(s_tm + 96, v[3]);
-          highest(0);
-          highest(1);
-          tc::wait_ld();
-          highest(2);
-          highest(3);
-          float mx = max3(max3(bm[0], bm[1], bm[2]), max3(bm[3], bm[4], bm[5]), fmaxf(bm[6], bm[7]));
-          if constexpr (!BLOCKS) mx *= factor(0);
-          const bool grow = mx > m + 8.0f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = fmaxf(m, mx);
-            const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
-            l *= f;
-            m = mn;
-            if (any) {  // the products so far
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t w[16];
-                tc::ld16(o_tm + 16 * c, w);
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(as_f(w[i]) * f);
-                tc::st16(o_tm + 16 * c, w);
-              }
-            }
-          }
-          any = true;
-          const float mu = m > -INFINITY ? m : 0.0f;
+          uint32_t w[2][16];
           uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
+          float sum = 0.0f;
+          // The weights of 32 columns, relative to 2^m.
+          auto weights = [&](int c, uint32_t (&w)[16]) {
+            const float mu = m > -INFINITY ? m : 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int blk = 2 * c + h;
@@ -527,10 +496,50 @@ __global__ void __launch_bounds__(THREADS, 1)
               if constexpr (FP8) {
                 float y0, y1;
                 unpair(add2(s0, s1), y0, y1);
-                l = fmaf(y0 + y1, sh.iv[slot][blk], l);
+                sum = blk == 0 ? (y0 + y1) * sh.iv[slot][0] : fmaf(y0 + y1, sh.iv[slot][blk], sum);
               }
             }
-            tc::st16(s_tm + 16 * c, w);
+          };
+          tc::ld32(s_tm, v[0]);
+          tc::ld32(s_tm + 32, v[1]);
+          tc::wait_ld();
+          tc::ld32(s_tm + 64, v[2]);
+          tc::ld32(s_tm + 96, v[3]);
+          highest(0);
+          highest(1);
+          // The maximum moves only when it grows by more than 2^8 (or from
+          // nothing), so the exponentials start from the old one, before the new
+          // one is known, and are taken again in the few tiles where it moves.
+          weights(0, w[0]);
+          weights(1, w[1]);
+          tc::wait_ld();
+          highest(2);
+          highest(3);
+          float mx = max3(max3(bm[0], bm[1], bm[2]), max3(bm[3], bm[4], bm[5]), fmaxf(bm[6], bm[7]));
+          if constexpr (!BLOCKS) mx *= factor(0);
+          if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
+            const float mn = fmaxf(m, mx);
+            const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
+            l *= f;
+            m = mn;
+            if (any) {  // the products so far
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                tc::ld16(o_tm + 16 * c, w[0]);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[0][i] = __float_as_uint(as_f(w[0][i]) * f);
+                tc::st16(o_tm + 16 * c, w[0]);
+              }
+            }
+            weights(0, w[0]);
+            weights(1, w[1]);
+          }
+          any = true;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c >= 2) weights(c, w[c & 1]);
+            tc::st16(s_tm + 16 * c, w[c & 1]);
             if (c & 1) {
               tc::wait_st();
               tc::fence_before();
@@ -542,8 +551,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           if constexpr (!FP8) {
             float y0, y1;
             unpair(add2(s0, s1), y0, y1);
-            l += y0 + y1;
+            sum = y0 + y1;
           }
+          l += sum;
         };
         if (key0 + TILE - 1 > hi_all || key0 < lo_all || (!FP8 && !sh.plain[slot]))
           weigh(std::true_type{});
@@ -728,12 +738,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[s]));
       }
     }
-  } else if (warp == 13) {
-    // ===== K and V tiles, copied ======================================================
+  } else if (warp == 13 || warp == 15) {
+    // ===== K tiles, V tiles, copied: a warp each ======================================
+    const bool v = warp == 15;
     const int box_keys = min(1 << b.page_shift, TILE), boxes = TILE / box_keys;
     const int n_rows = b.n_pages << b.page_shift;
-    int t = 0;             // K tiles copied before this item, and V tiles
-    int last_k = 0, last_v = 0;
+    constexpr int SLOTS = 2;
+    static_assert(C::KR == SLOTS && C::VR == SLOTS, "one loop for both rings");
+    uint64_t *in = v ? sh.v_in : sh.k_in, *out = !v ? sh.k_out : FP8 ? sh.v_taken : sh.v_out;
+    const int bytes = FP8 ? CODES : OPER;
+    const uint32_t ring = !v ? k_smem : FP8 ? v_codes : v_smem;
+    const CUtensorMap* map = v ? &maps.v : &maps.k;
+    int t = 0;  // tiles copied
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
@@ -752,76 +768,62 @@ __global__ void __launch_bounds__(THREADS, 1)
       int row0 = -1, row1 = rows_of(0), row2 = rows_of(1);
       float ks0 = 0.0f, vs0 = 1.0f, ks1 = 0.0f, vs1 = 1.0f;
       auto scales = [&]() {
-        if (FP8 && row1 >= 0) {
+        if (FP8 && !v && row1 >= 0) {
           const size_t at = (size_t)(row1 >> 4) * b.nkv + p.kvh;
           ks1 = __ldg(a.k_scale + at);
           vs1 = __ldg(a.v_scale + at);
         }
       };
       scales();
-      // K_j of tile step i where j = i, V of the step `lead` before: K of the first
-      // tiles (one; two where A and B have a tile each), then V and K in turn.
-      const int lead = p.split ? 2 : 1;
 #pragma unroll 1
-      for (int i = 0; ok && i < 2 * (p.n + lead); ++i) {
-        const bool v = (i & 1) == 0;              // V first
-        const int tile = v ? (i >> 1) - lead : i >> 1;
-        if (tile < 0 || tile >= p.n) continue;
-        const int n = t + tile, info = n & (INFO - 1);
-        const int slot = v ? n % C::VR : n % C::KR, turn = v ? n / C::VR : n / C::KR;
-        if (!v && (tile & 3) == 0) {
+      for (int j = 0; j < p.n; ++j, ++t) {
+        if ((j & 3) == 0) {
           row0 = row1;
           ks0 = ks1;
           vs0 = vs1;
           row1 = row2;
           scales();
-          row2 = rows_of((tile >> 2) + 2);
+          row2 = rows_of((j >> 2) + 2);
         }
-        if (turn > 0) {
-          uint64_t& free = v ? (FP8 ? sh.v_taken[slot] : sh.v_out[slot]) : sh.k_out[slot];
-          if (!(ok = warp_wait(sh, free, (turn & 1) ^ 1))) break;
+        const int slot = t % SLOTS;
+        if (t >= SLOTS && !(ok = warp_wait(sh, out[slot], ((t / SLOTS) & 1) ^ 1))) break;
+        const uint32_t bar = smem_addr(&in[slot]), dst = ring + slot * bytes;
+        const int lane0 = 8 * (j & 3);  // the lanes with this tile's blocks
+#pragma unroll 1
+        for (int i = 0; i < boxes; ++i) {
+          int y = __shfl_sync(0xffffffffu, row0, lane0 + i * (box_keys >> 4));
+          if (y < 0) y = n_rows;
+          if (tc::one_thread()) {
+            tma_box(dst + i * box_keys * 128, map, p.kvh * HD, y, bar);
+            if constexpr (!FP8) tma_box(dst + HALF + i * box_keys * 128, map, p.kvh * HD + 64, y, bar);
+          }
+          __syncwarp();
         }
-        const uint32_t bar = smem_addr(v ? &sh.v_in[slot] : &sh.k_in[slot]);
-        const uint32_t dst = v ? (FP8 ? v_codes + slot * CODES : v_smem + slot * OPER) : k_smem + slot * C::KB;
-        const int blk = 8 * (tile & 3) + (lane & 7);  // the lane with this lane's block
-        int at = __shfl_sync(0xffffffffu, row0, blk);
-        if (v)
-          at = sh.row[info][lane & 7];
-        else if (lane < 8)
-          sh.row[info][lane] = at;
-        // Box i of the tile starts at its block i * box_keys / 16.
-        const int box = FP8 ? lane : lane >> 1, half = FP8 ? 0 : lane & 1;
-        int y = __shfl_sync(0xffffffffu, at, (box * (box_keys >> 4)) & 7);
-        if (y < 0) y = n_rows;
-        if (box < boxes)
-          tma_box(dst + half * HALF + box * box_keys * 128, v ? &maps.v : &maps.k, p.kvh * HD + 64 * half, y, bar);
         if (!v) {  // the tile's block table
+          const int blk = lane0 + (lane & 7), info = t & (INFO - 1);
+          const int at = __shfl_sync(0xffffffffu, row0, blk);
           const float k = FP8 ? __shfl_sync(0xffffffffu, ks0, blk) : 1.0f;
           // A scale of zero would take a block's weights out of the sum: 2^-100.
           const float z = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs0, blk), 7.8886090522101181e-31f) : 1.0f;
+          const int key = ((p.kt0 + j) << 7) + 16 * (lane & 7);
+          // A block that nothing sees may have any scale.
+          const bool live = at >= 0 && key <= see_hi && key + BLOCK - 1 >= see_lo;
+          const bool plain = __all_sync(0xffffffffu, at >= 0);
           if (lane < 8) {
-            const int key = ((p.kt0 + tile) << 7) + 16 * lane;
-            // A block that nothing sees may have any scale.
-            const bool live = at >= 0 && key <= see_hi && key + BLOCK - 1 >= see_lo;
             sh.ks[info][lane] = live ? k : 0.0f;
             sh.lv[info][lane] = live ? (FP8 ? log2f(z) : 0.0f) : -INFINITY;
             sh.iv[info][lane] = live && FP8 ? 1.0f / z : 1.0f;
+            if (lane == 0) sh.plain[info] = plain;
           }
-          const unsigned there = __ballot_sync(0xffffffffu, at >= 0);
-          if (lane == 0) sh.plain[info] = (there & 0xffu) == 0xffu;
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar, v ? (FP8 ? CODES : OPER) : C::KB);
-        (v ? last_v : last_k) = n + 1;
+        if (lane == 0) mbar_expect_tx(bar, bytes);
       }
-      t += p.n;
     }
     if (!ok) {  // nothing may land after the CTA has left
       const uint64_t deadline = globaltimer_ns() + 1000000000ull;
-      for (int n = max(0, last_k - C::KR); n < last_k; ++n)
-        mbar_wait(smem_addr(&sh.k_in[n % C::KR]), (n / C::KR) & 1, deadline);
-      for (int n = max(0, last_v - C::VR); n < last_v; ++n)
-        mbar_wait(smem_addr(&sh.v_in[n % C::VR]), (n / C::VR) & 1, deadline);
+      for (int n = max(0, t - SLOTS); n < t; ++n)
+        mbar_wait(smem_addr(&in[n % SLOTS]), (n / SLOTS) & 1, deadline);
     }
   } else if (warp == 12 || warp == 14) {
     // ===== the products of tile A, of tile B: a warp each, of which one thread issues ===
