@@ -82,6 +82,7 @@ struct Shared {
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
   alignas(16) float ks[INFO][8], lv[INFO][8], iv[INFO][8];  // a key tile's blocks (read four at a time)
   int plain[INFO];                   // all of them are there
+  float qs[2][TILE];                 // E4M3: what the query rows were divided by
 };
 
 static_assert(Cfg<true>::SMEM + sizeof(Shared) <= 227 * 1024, "fits");
@@ -165,6 +166,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// Where 16-byte chunk c of a 256-byte row lies in an operand tile.
+__device__ __forceinline__ uint32_t row_chunk(int r, int c) {
+  return (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // Waits for a phase, a second at most; a wait that runs out (in any warp) ends
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     total += sh.scan[w];
   }
   const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, PR_MIN_SHARE);
-  const int margin = share >> 4;
+  const int margin = min(share >> 4, PR_MARGIN);
   if (tid < n_items) {
     sh.pre[tid + 1] = pre + cnt;
     if (tid == 0) sh.pre[0] = 0;
@@ -363,64 +369,60 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item p = part(cur, it);
       cur += p.n;
       const int tok = tok_in_tile + (p.split ? 0 : x * tile_toks);
-      const bool live = tok < p.tokens;
       const int pos = p.pos0 + min(tok, p.tokens - 1);
       const int head = p.kvh * b.group + head_in_group;
 
-      // -- queries: this thread's row into the A operand's layout
-      float qs = a.scale_log2;
-      {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(
-            a.q + ((size_t)(p.q_row + (live ? tok : 0)) * nq + head) * HD);
-        const bool mine = !p.split || x == 0;
-        const uint32_t dst = q_smem + x * OPER + r * 128;
+      // -- queries into the A operand's layout: the warp's 32 rows, two at a time
+      if (!p.split || x == 0) {
+        const uint32_t dst = q_smem + x * OPER;
+        const int c = lane & 15;  // 16-byte chunk of the row
         uint4 w[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = *reinterpret_cast<const uint4*>(src + 16 * c);
-        if constexpr (FP8) {
-          float mx = 0.0f;
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 32 * (warp & 3) + 2 * i + (lane >> 4);
+          const int tk = (rr >> gshift) + x * tile_toks;
+          w[i] = tk < p.tokens ? *reinterpret_cast<const uint4*>(
+                                     a.q + ((size_t)(p.q_row + tk) * nq + p.kvh * b.group + (rr & (b.group - 1))) * HD + 8 * c)
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 32 * (warp & 3) + 2 * i + (lane >> 4);
+          if constexpr (FP8) {
+            float q[8] = {bf_lo(w[i].x), bf_hi(w[i].x), bf_lo(w[i].y), bf_hi(w[i].y),
+                          bf_lo(w[i].z), bf_hi(w[i].z), bf_lo(w[i].w), bf_hi(w[i].w)};
+            float mx = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mx = max3(mx, fabsf(bf_lo(v[j])), fabsf(bf_hi(v[j])));
-          }
-          // The power of two that brings it to (224, 448] = (0.875, 1.75] 2^8.
-          const uint32_t bits = __float_as_uint(mx);
-          const int e = min(max((int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 127);
-          // (NaN for a row with an infinity, which E4M3 would turn into 448.)
-          const float up = __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : (uint32_t)(127 + 8 - e) << 23);
-          qs *= __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+            for (int j = 0; j < 8; j += 2) mx = max3(mx, fabsf(q[j]), fabsf(q[j + 1]));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {  // 16 elements: a chunk of hi, a chunk of lo
-            uint32_t hi[4], lo[4];
+            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // The power of two that brings it to (224, 448] = (0.875, 1.75] 2^8
+            // (NaN for a row with an infinity, which E4M3 would turn into 448).
+            const uint32_t bits = __float_as_uint(mx);
+            const int e = min(max((int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 127);
+            const float up = __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : (uint32_t)(127 + 8 - e) << 23);
+            if (c == 0) sh.qs[x][rr] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t v0 = j < 2 ? (j ? w[2 * c].z : w[2 * c].x) : (j == 2 ? w[2 * c + 1].x : w[2 * c + 1].z);
-              const uint32_t v1 = j < 2 ? (j ? w[2 * c].w : w[2 * c].y) : (j == 2 ? w[2 * c + 1].y : w[2 * c + 1].w);
-              const float q[4] = {bf_lo(v0) * up, bf_hi(v0) * up, bf_lo(v1) * up, bf_hi(v1) * up};
-              const uint32_t h0 = f32x2_to_e4m3x2(q[0], q[1]), h1 = f32x2_to_e4m3x2(q[2], q[3]);
+            for (int j = 0; j < 2; ++j) {
+              const float q0 = q[4 * j] * up, q1 = q[4 * j + 1] * up, q2 = q[4 * j + 2] * up, q3 = q[4 * j + 3] * up;
+              const uint32_t h0 = f32x2_to_e4m3x2(q0, q1), h1 = f32x2_to_e4m3x2(q2, q3);
               const float2 g0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), g1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
               hi[j] = h0 | h1 << 16;
-              lo[j] = f32x2_to_e4m3x2(q[0] - g0.x, q[1] - g0.y) | f32x2_to_e4m3x2(q[2] - g1.x, q[3] - g1.y) << 16;
+              lo[j] = f32x2_to_e4m3x2(q0 - g0.x, q1 - g0.y) | f32x2_to_e4m3x2(q2 - g1.x, q3 - g1.y) << 16;
             }
-            if (mine) {
-              const uint32_t at = dst + ((c ^ (r & 7)) << 4);
-              sts128(at, hi[0], hi[1], hi[2], hi[3]);
-              sts128(at + CODES, lo[0], lo[1], lo[2], lo[3]);
-            }
+            const uint32_t at = dst + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + CODES), "r"(lo[0]), "r"(lo[1]) : "memory");
+          } else {
+            sts128(dst + row_chunk(rr, c), w[i].x, w[i].y, w[i].z, w[i].w);
           }
-        } else if (mine) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            sts128(dst + (c >> 3) * HALF + (((c & 7) ^ (r & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
         }
-        if (mine) {
-          tc::fence_smem_to_mma();
-          mbar_arrive(smem_addr(&sh.q_full[x]));
-          if (p.split) mbar_arrive(smem_addr(&sh.q_full[1]));  // B's products take them too
-        }
+        tc::fence_smem_to_mma();
+        mbar_arrive(smem_addr(&sh.q_full[x]));
+        if (p.split) mbar_arrive(smem_addr(&sh.q_full[1]));  // B's products take them too
       }
+      float qs = a.scale_log2;
 
       // -- the key tiles
       const int hi = pos, lo = a.window > 0 ? pos - a.window + 1 : 0;
@@ -433,46 +435,45 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!(ok = warp_wait(sh, sh.s_full[x], s_phase))) break;
         s_phase ^= 1;
         tc::fence_after();
+        if (FP8 && !any) qs *= sh.qs[p.split ? 0 : x][r];
         const int slot = (tiles_before + j) & (INFO - 1);
         const int key0 = (p.kt0 + j) << 7;
         // Two copies of the code, so that a tile that is seen whole, of pages that
-        // are all there, pays nothing for the mask.  A thread's 128 scores stay in
-        // registers from the maximum to the weights: one stream of independent
-        // work (with the scores read twice, 32 at a time, the exponentials of a
-        // piece did not overlap the next's: 5 % slower).
+        // are all there, pays nothing for the mask.
         auto weigh = [&](auto edge) {
           constexpr bool MASK = decltype(edge)::value;
           constexpr bool BLOCKS = FP8 || MASK;  // blocks differ in scale or presence
-          const int mlo = lo - key0, mhi = hi - key0;  // columns seen
           // What a block's scores are multiplied by (not 0, lest a masked score
-          // becomes NaN: a query of zeros, a scale of 0), what is added, and what
-          // its weights count in the sum.
+          // becomes NaN: a query of zeros, a scale of 0), and what is added.
           auto factor = [&](int blk) {
             return FP8 ? fmaxf(qs * sh.ks[slot][blk], 1.17549435e-38f) : fmaxf(qs, 1.17549435e-38f);
           };
           auto offset = [&](int blk) { return BLOCKS ? sh.lv[slot][blk] : 0.0f; };
-          uint32_t v[4][32];
-          float bm[8];  // the blocks' highest scores
-          auto highest = [&](int c) {
+          // Columns 32c .. of the row: not seen is -infinity; the highest of each block.
+          auto mask = [&](int c, uint32_t (&v)[32]) {
             if constexpr (MASK) {
+              const int mlo = lo - key0 - 32 * c, mhi = hi - key0 - 32 * c;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (32 * c + i < mlo || 32 * c + i > mhi) v[c][i] = 0xff800000u;  // -infinity
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t* y = v[c] + 16 * h;
-              const float a0 = max3(y[0], y[1], y[2]), a1 = max3(y[3], y[4], y[5]), a2 = max3(y[6], y[7], y[8]);
-              const float a3 = max3(y[9], y[10], y[11]), a4 = max3(y[12], y[13], y[14]);
-              bm[2 * c + h] = fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15]));
-              if constexpr (BLOCKS) bm[2 * c + h] = fmaf(bm[2 * c + h], factor(2 * c + h), offset(2 * c + h));
+                if (i < mlo || i > mhi) v[i] = 0xff800000u;
             }
           };
-          uint32_t w[2][16];
+          auto highest = [&](int c, const uint32_t (&v)[32]) {
+            float bm[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* y = v + 16 * h;
+              const float a0 = max3(y[0], y[1], y[2]), a1 = max3(y[3], y[4], y[5]), a2 = max3(y[6], y[7], y[8]);
+              const float a3 = max3(y[9], y[10], y[11]), a4 = max3(y[12], y[13], y[14]);
+              bm[h] = fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15]));
+              if constexpr (BLOCKS) bm[h] = fmaf(bm[h], factor(2 * c + h), offset(2 * c + h));
+            }
+            return fmaxf(bm[0], bm[1]);
+          };
+          // The weights of 32 columns, relative to 2^m.
           uint64_t s0 = 0, s1 = 0;
           float sum = 0.0f;
-          // The weights of 32 columns, relative to 2^m.
-          auto weights = [&](int c, uint32_t (&w)[16]) {
+          auto weights = [&](int c, const uint32_t (&v)[32], uint32_t (&w)[16]) {
             const float mu = m > -INFINITY ? m : 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float y0, y1;
-                unpair(fma2(pair(as_f(v[c][16 * h + 2 * i]), as_f(v[c][16 * h + 2 * i + 1])), k2, d2), y0, y1);
+                unpair(fma2(pair(as_f(v[16 * h + 2 * i]), as_f(v[16 * h + 2 * i + 1])), k2, d2), y0, y1);
                 y0 = ex2(y0);
                 y1 = ex2(y1);
                 const uint64_t y = pair(y0, y1);
@@ -500,22 +501,26 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           };
-          tc::ld32(s_tm, v[0]);
-          tc::ld32(s_tm + 32, v[1]);
-          tc::wait_ld();
-          tc::ld32(s_tm + 64, v[2]);
-          tc::ld32(s_tm + 96, v[3]);
-          highest(0);
-          highest(1);
           // The maximum moves only when it grows by more than 2^8 (or from
-          // nothing), so the exponentials start from the old one, before the new
-          // one is known, and are taken again in the few tiles where it moves.
-          weights(0, w[0]);
-          weights(1, w[1]);
+          // nothing), so the first half's exponentials start from the old one,
+          // before the new one is known, and are taken again, from scores still in
+          // TMEM, in the few tiles where it moves.
+          uint32_t va[32], vb[32], vc[32], w0[16], w1[16];
+          tc::ld32(s_tm, va);
+          tc::ld32(s_tm + 32, vb);
           tc::wait_ld();
-          highest(2);
-          highest(3);
-          float mx = max3(max3(bm[0], bm[1], bm[2]), max3(bm[3], bm[4], bm[5]), fmaxf(bm[6], bm[7]));
+          tc::ld32(s_tm + 64, vc);
+          mask(0, va);
+          float mx = highest(0, va);
+          weights(0, va, w0);
+          tc::ld32(s_tm + 96, va);
+          mask(1, vb);
+          mx = fmaxf(mx, highest(1, vb));
+          weights(1, vb, w1);
+          tc::wait_ld();
+          mask(2, vc);
+          mask(3, va);
+          mx = max3(mx, highest(2, vc), highest(3, va));
           if constexpr (!BLOCKS) mx *= factor(0);
           if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
             const float mn = fmaxf(m, mx);
@@ -525,29 +530,37 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (any) {  // the products so far
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
-                tc::ld16(o_tm + 16 * c, w[0]);
+                tc::ld16(o_tm + 16 * c, w0);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[0][i] = __float_as_uint(as_f(w[0][i]) * f);
-                tc::st16(o_tm + 16 * c, w[0]);
+                for (int i = 0; i < 16; ++i) w0[i] = __float_as_uint(as_f(w0[i]) * f);
+                tc::st16(o_tm + 16 * c, w0);
               }
             }
-            weights(0, w[0]);
-            weights(1, w[1]);
+            tc::ld32(s_tm, vb);
+            tc::wait_ld();
+            mask(0, vb);
+            weights(0, vb, w0);
+            tc::ld32(s_tm + 32, vb);
+            tc::wait_ld();
+            mask(1, vb);
+            weights(1, vb, w1);
           }
           any = true;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c >= 2) weights(c, w[c & 1]);
-            tc::st16(s_tm + 16 * c, w[c & 1]);
-            if (c & 1) {
-              tc::wait_st();
-              tc::fence_before();
-              __syncwarp();
-              // The second product may begin with half the weights.
-              if (lane == 0) mbar_arrive(smem_addr(c == 1 ? &sh.p_half[x] : &sh.p_full[x]));
-            }
-          }
+          auto hand_over = [&](uint64_t& bar) {
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&bar));
+          };
+          tc::st16(s_tm, w0);
+          tc::st16(s_tm + 16, w1);
+          hand_over(sh.p_half[x]);  // the second product may begin
+          weights(2, vc, w0);
+          tc::st16(s_tm + 32, w0);
+          weights(3, va, w1);
+          tc::st16(s_tm + 48, w1);
+          hand_over(sh.p_full[x]);
           if constexpr (!FP8) {
             float y0, y1;
             unpair(add2(s0, s1), y0, y1);
@@ -572,7 +585,31 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int cut0 = (p.row0 + margin) / share + 1, cut1 = (p.row0 + p.all - margin - 1) / share;
       const bool whole = p.all <= PR_WHOLE || cut0 > cut1;
       const int c0 = cut0 - 1, c1 = cut1;
-      uint16_t* out = a.out + ((size_t)(p.q_row + tok) * nq + head) * HD;
+      // A finished row goes out by way of the query tile's place, which is free:
+      // a thread writes chunks of its row there, and the warp takes its 32 rows
+      // out two at a time, whole lines instead of 16 bytes of 32 rows.
+      const uint32_t stage = q_smem + x * OPER;
+      auto put = [&](int c, const float* o, float f) {  // 8 columns
+        sts128(stage + row_chunk(r, c), pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
+               pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
+      };
+      auto send = [&](int chunks, int first) {  // `chunks` (16 or 8) of the rows' chunks
+        __syncwarp();
+        const int per = 32 / chunks, c = first + (lane & (chunks - 1));
+#pragma unroll 4
+        for (int i = 0; i < 32; i += per) {
+          const int rr = 32 * (warp & 3) + i + lane / chunks;
+          const int tk = (rr >> gshift) + (p.split ? 0 : x * tile_toks);
+          uint4 w;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(stage + row_chunk(rr, c)));
+          if (tk < p.tokens)
+            *reinterpret_cast<uint4*>(
+                a.out + ((size_t)(p.q_row + tk) * nq + p.kvh * b.group + (rr & (b.group - 1))) * HD + 8 * c) = w;
+        }
+        __syncwarp();
+      };
       if (whole && !p.split) {
         const float inv = row_factor(a, head, m, l);
 #pragma unroll 1
@@ -580,16 +617,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
           tc::wait_ld();
-          if (live) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
-                  make_uint4(pack_bf16(as_f(v[8 * i]) * inv, as_f(v[8 * i + 1]) * inv),
-                             pack_bf16(as_f(v[8 * i + 2]) * inv, as_f(v[8 * i + 3]) * inv),
-                             pack_bf16(as_f(v[8 * i + 4]) * inv, as_f(v[8 * i + 5]) * inv),
-                             pack_bf16(as_f(v[8 * i + 6]) * inv, as_f(v[8 * i + 7]) * inv));
-          }
+          for (int i = 0; i < 4; ++i) put(4 * c + i, reinterpret_cast<const float*>(v) + 8 * i, inv);
         }
+        send(16, 0);
         continue;
       }
       // Partial: maxima, sums and unscaled outputs of this tile, [4 columns][row].
@@ -663,16 +694,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             o[4 * i + 3] = fmaf(w[i].w, f, o[4 * i + 3]);
           }
         }
-        if (live) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(out + 64 * c + 8 * i) =
-                make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                           pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                           pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                           pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-        }
+        for (int i = 0; i < 8; ++i) put(8 * c + i, o + 8 * i, inv);
       }
+      if (p.split)
+        send(8, 8 * x);
+      else
+        send(16, 0);
       // Slots that a later item of this CTA writes are read by now.
       named_sync(1, 256);
     }
@@ -789,7 +817,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (t >= SLOTS && !(ok = warp_wait(sh, out[slot], ((t / SLOTS) & 1) ^ 1))) break;
         const uint32_t bar = smem_addr(&in[slot]), dst = ring + slot * bytes;
         const int lane0 = 8 * (j & 3);  // the lanes with this tile's blocks
-#pragma unroll 1
+#pragma unroll 4
         for (int i = 0; i < boxes; ++i) {
           int y = __shfl_sync(0xffffffffu, row0, lane0 + i * (box_keys >> 4));
           if (y < 0) y = n_rows;

@@ -24,8 +24,9 @@ constexpr int DEC_MIN_SHARE = 16, DEC_WHOLE = 64;
 // A slot of the prompt kernel: two tiles of 128 maxima, 128 sums and 128 x 128
 // outputs.
 constexpr int PR_TILE = 128 * (2 + HD), PR_SLOT = 2 * PR_TILE;
-// Fewest key tiles in a CTA's share, and the longest item that is never cut.
-constexpr int PR_MIN_SHARE = 4, PR_WHOLE = 6;
+// Fewest key tiles in a CTA's share, the longest item that is never cut, and how
+// far a cut moves to an item's end at most: what a join costs, in tiles.
+constexpr int PR_MIN_SHARE = 4, PR_WHOLE = 6, PR_MARGIN = 3;
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
   return WS_HEAD + sizeof(float) * 2 * MAX_CTAS * (size_t)PR_SLOT;
