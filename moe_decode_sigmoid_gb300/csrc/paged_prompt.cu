@@ -62,6 +62,7 @@ template <bool FP8>
 struct Cfg {
   static constexpr int KB = FP8 ? CODES : OPER;  // bytes of a K tile
   static constexpr int KR = 2;                   // K tiles
+  static constexpr int KS = FP8 ? 4 : 2;         // of a split item: E4M3 has two more in tile B's queries' place
   static constexpr int VR = 2;                   // V tiles as operands, and as codes
   // Warps that hand a V tile over: all four widen, one looks after bf16's edges.
   static constexpr int HANDS = FP8 ? 4 : 1;
@@ -69,10 +70,10 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t k_in[2], k_out[2];        // K tiles: copied, used
+  uint64_t k_in[4], k_out[4];        // K tiles: copied, used
   uint64_t v_in[2], v_taken[2];      // V tiles: copied; codes read
   uint64_t v_full[2], v_out[2];      // V operands: ready, used
-  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drained;
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], b_free, drained;
   uint32_t tmem;
   int fail, last, cut[2], first;
   int scan[16];
@@ -168,6 +169,27 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// How often a ring's slots have been used, as parities, over items whose number
+// of slots may differ: tile j of an item uses slot j % slots.  Every warp counts
+// every slot, its own use or not.
+struct Turns {
+  uint32_t parity = 0, used = 0;  // a bit a slot
+  // Parity of the phase in which tile j of the current item is in its slot.
+  __device__ __forceinline__ uint32_t of(int slot, int j, int shift) const {
+    return ((parity >> slot) ^ (uint32_t)(j >> shift)) & 1u;
+  }
+  __device__ __forceinline__ bool fresh(int slot, int j, int shift) const {
+    return (j >> shift) == 0 && ((used >> slot) & 1u) == 0;
+  }
+  __device__ __forceinline__ void item(int n, int shift) {  // n tiles in 1 << shift slots
+    for (int s = 0; s < (1 << shift); ++s) {
+      const int uses = (n - s + (1 << shift) - 1) >> shift;
+      parity ^= (uint32_t)(uses & 1) << s;
+      used |= (uint32_t)(uses > 0) << s;
+    }
+  }
+};
+
 // Where 16-byte chunk c of a 256-byte row lies in an operand tile.
 __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
   return (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
@@ -212,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t v_codes = v_smem + C::VR * OPER;
 
   if (tid == 0) {
-    for (int i = 0; i < C::KR; ++i) {
+    for (int i = 0; i < C::KS; ++i) {
       mbar_init(smem_addr(&sh.k_in[i]), 1);
       mbar_init(smem_addr(&sh.k_out[i]), 2);
     }
@@ -230,6 +252,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       sh.cut[i] = -1;
     }
+    mbar_init(smem_addr(&sh.b_free), 4);
     mbar_init(smem_addr(&sh.drained), 2);
     sh.fail = 0;
     fence_mbar_init();
@@ -422,6 +445,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_arrive(smem_addr(&sh.q_full[x]));
         if (p.split) mbar_arrive(smem_addr(&sh.q_full[1]));  // B's products take them too
       }
+      if (C::KS > 2 && p.split && x == 1) {  // B's queries' place is free for keys
+        tc::fence_smem_to_mma();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.b_free));
+      }
       float qs = a.scale_log2;
 
       // -- the key tiles
@@ -431,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m = -INFINITY, l = 0.0f;
       const int step = p.split ? 2 : 1;
       bool any = false;
-      for (int j = p.split ? (x ^ tiles_before) & 1 : 0; ok && j < p.n; j += step) {
+      for (int j = p.split ? x : 0; ok && j < p.n; j += step) {
         if (!(ok = warp_wait(sh, sh.s_full[x], s_phase))) break;
         s_phase ^= 1;
         tc::fence_after();
@@ -588,7 +616,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // A finished row goes out by way of the query tile's place, which is free:
       // a thread writes chunks of its row there, and the warp takes its 32 rows
       // out two at a time, whole lines instead of 16 bytes of 32 rows.
-      const uint32_t stage = q_smem + x * OPER;
+      // (A split item's two halves of the columns share A's: B's may hold keys.)
+      const uint32_t stage = q_smem + (p.split ? 0 : x * OPER);
       auto put = [&](int c, const float* o, float f) {  // 8 columns
         sts128(stage + row_chunk(r, c), pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
                pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
@@ -707,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp < 12) {
     // ===== V tiles from copies to operands ==========================================
     const int w4 = warp - 8;
-    int t = 0;  // tiles handed over
+    Turns turns;
     bool ok = w4 < C::HANDS;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
@@ -715,9 +744,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int see_hi = p.pos0 + p.tokens - 1;
       const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
 #pragma unroll 1
-      for (int j = 0; j < p.n; ++j, ++t) {
-        const int s = t % C::VR, key0 = (p.kt0 + j) << 7;
-        const uint32_t phase = (t / C::VR) & 1, dst = v_smem + s * OPER;
+      for (int j = 0; j < p.n; ++j) {
+        const int s = j & 1, key0 = (p.kt0 + j) << 7;
+        const uint32_t phase = turns.of(s, j, 1), dst = v_smem + s * OPER;
         const bool edge = key0 < see_lo || key0 + TILE - 1 > see_hi;
         if (!(ok = warp_wait(sh, sh.v_in[s], phase))) break;
         if constexpr (FP8) {
@@ -738,7 +767,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.v_taken[s]));
-          if (t >= C::VR && !(ok = warp_wait(sh, sh.v_out[s], phase ^ 1))) break;
+          if (!turns.fresh(s, j, 1) && !(ok = warp_wait(sh, sh.v_out[s], phase ^ 1))) break;
           // Operand chunks 2c and 2c + 1; the upper lanes store the odd one first,
           // so that the eight lanes of a phase fall into distinct banks.
           const int c = lane & 7, odd = (lane >> 2) & 1;
@@ -765,19 +794,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[s]));
       }
+      turns.item(p.n, 1);
     }
   } else if (warp == 13 || warp == 15) {
     // ===== K tiles, V tiles, copied: a warp each ======================================
     const bool v = warp == 15;
     const int box_keys = min(1 << b.page_shift, TILE), boxes = TILE / box_keys;
     const int n_rows = b.n_pages << b.page_shift;
-    constexpr int SLOTS = 2;
-    static_assert(C::KR == SLOTS && C::VR == SLOTS, "one loop for both rings");
+    static_assert(C::KR == 2 && C::VR == 2, "a shift of 1");
     uint64_t *in = v ? sh.v_in : sh.k_in, *out = !v ? sh.k_out : FP8 ? sh.v_taken : sh.v_out;
     const int bytes = FP8 ? CODES : OPER;
     const uint32_t ring = !v ? k_smem : FP8 ? v_codes : v_smem;
     const CUtensorMap* map = v ? &maps.v : &maps.k;
     int t = 0;  // tiles copied
+    Turns turns;
+    uint32_t flying = 0, flying_parity = 0;  // the slots' last copies
+    uint32_t b_phase = 0;
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
@@ -803,6 +835,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       scales();
+      const int shift = !v && p.split && C::KS == 4 ? 2 : 1;
 #pragma unroll 1
       for (int j = 0; j < p.n; ++j, ++t) {
         if ((j & 3) == 0) {
@@ -813,9 +846,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           scales();
           row2 = rows_of((j >> 2) + 2);
         }
-        const int slot = t % SLOTS;
-        if (t >= SLOTS && !(ok = warp_wait(sh, out[slot], ((t / SLOTS) & 1) ^ 1))) break;
-        const uint32_t bar = smem_addr(&in[slot]), dst = ring + slot * bytes;
+        const int slot = j & ((1 << shift) - 1);
+        const uint32_t phase = turns.of(slot, j, shift);
+        if (shift == 2 && j == min(2, p.n - 1)) {  // tile B is through with its last item's outputs
+          if (!(ok = warp_wait(sh, sh.b_free, b_phase))) break;
+          b_phase ^= 1;
+        }
+        if (!turns.fresh(slot, j, shift) && !(ok = warp_wait(sh, out[slot], phase ^ 1))) break;
+        const uint32_t bar = smem_addr(&in[slot]);
+        const uint32_t dst = slot < 2 ? ring + slot * bytes : q_smem + OPER + (slot - 2) * bytes;
         const int lane0 = 8 * (j & 3);  // the lanes with this tile's blocks
 #pragma unroll 4
         for (int i = 0; i < boxes; ++i) {
@@ -846,12 +885,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         if (lane == 0) mbar_expect_tx(bar, bytes);
+        flying |= 1u << slot;
+        flying_parity = (flying_parity & ~(1u << slot)) | phase << slot;
       }
+      turns.item(p.n, shift);
     }
     if (!ok) {  // nothing may land after the CTA has left
       const uint64_t deadline = globaltimer_ns() + 1000000000ull;
-      for (int n = max(0, t - SLOTS); n < t; ++n)
-        mbar_wait(smem_addr(&in[n % SLOTS]), (n / SLOTS) & 1, deadline);
+      for (int s = 0; s < C::KS; ++s)
+        if ((flying >> s) & 1u) mbar_wait(smem_addr(&in[s]), (flying_parity >> s) & 1u, deadline);
     }
   } else if (warp == 12 || warp == 14) {
     // ===== the products of tile A, of tile B: a warp each, of which one thread issues ===
@@ -867,28 +909,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t q_lo = tc::desc_lo(q_smem, 16), k_lo = tc::desc_lo(k_smem, 16);
     const uint32_t v_lo = tc::desc_lo(v_smem, HALF);
     uint32_t q_phase = 0, p_phase = 0;
-    int t = 0;
+    Turns k_turns, v_turns;
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
       cur += p.n;
       const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
       const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
-      // Of a split item A takes the tiles of even number (counted over the CTA's
-      // whole share, so that a ring slot is always the same tile's: a phase that
-      // a warp neither used nor waited for could pass for the next one); both
-      // share A's queries, and a key tile has one user, which counts for both.
-      const int step = split ? 2 : 1, first = split ? (x ^ t) & 1 : 0;
+      // Of a split item A has the even key tiles and B the odd ones (a ring slot
+      // is then one warp's throughout the item); both share A's queries, and a
+      // key tile has one user, which counts for both.
+      const int step = split ? 2 : 1, first = split ? x : 0, shift = split && C::KS == 4 ? 2 : 1;
       const uint32_t qt = q_lo + (split ? 0 : x) * (OPER >> 4);
       if (!(ok = warp_wait(sh, sh.q_full[x], q_phase))) break;
       q_phase ^= 1;
 #pragma unroll 1
       for (int j = first - step; j < tiles; j += step) {
         const int next = j + step;
-        const int nv = t + j, sv = nv % C::VR, nk = t + next, sk = nk % C::KR;
-        if (next < tiles && !(ok = warp_wait(sh, sh.k_in[sk], (nk / C::KR) & 1))) break;
+        const int sv = j & 1, sk = next & ((1 << shift) - 1);
         if (j >= 0) {  // O += P V_j, the weights of keys 0-63 and 64-127 as they come
-          if (!(ok = warp_wait(sh, sh.v_full[sv], (nv / C::VR) & 1))) break;
+          if (!(ok = warp_wait(sh, sh.v_full[sv], v_turns.of(sv, j, 1)))) break;
           const uint32_t vt = v_lo + sv * (OPER >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -910,8 +950,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           p_phase ^= 1;
         }
         if (next < tiles) {  // S = Q K_next^T
-          const uint32_t kt = k_lo + sk * (C::KB >> 4);
-          if (j < 0) tc::fence_after();
+          const uint32_t kt = sk < 2 ? k_lo + sk * (C::KB >> 4) : q_lo + (OPER >> 4) + (sk - 2) * (C::KB >> 4);
+          if (!(ok = warp_wait(sh, sh.k_in[sk], k_turns.of(sk, next, shift)))) break;
+          tc::fence_after();
           if (tc::one_thread()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -929,7 +970,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
       }
-      t += tiles;
+      k_turns.item(tiles, shift);
+      v_turns.item(tiles, 1);
     }
     // Every product is complete before the TMEM is given back.
     if (tc::one_thread()) tc::commit(smem_addr(&sh.drained));
