@@ -399,18 +399,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!p.split || x == 0) {
         const uint32_t dst = q_smem + x * OPER;
         const int c = lane & 15;  // 16-byte chunk of the row
-        uint4 w[16];
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rr = 32 * (warp & 3) + 2 * i + (lane >> 4);
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
           const int tk = (rr >> gshift) + x * tile_toks;
           w[i] = tk < p.tokens ? *reinterpret_cast<const uint4*>(
                                      a.q + ((size_t)(p.q_row + tk) * nq + p.kvh * b.group + (rr & (b.group - 1))) * HD + 8 * c)
                                : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rr = 32 * (warp & 3) + 2 * i + (lane >> 4);
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
           if constexpr (FP8) {
             float q[8] = {bf_lo(w[i].x), bf_hi(w[i].x), bf_lo(w[i].y), bf_hi(w[i].y),
                           bf_lo(w[i].z), bf_hi(w[i].z), bf_lo(w[i].w), bf_hi(w[i].w)};
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else {
             sts128(dst + row_chunk(rr, c), w[i].x, w[i].y, w[i].z, w[i].w);
           }
+        }
         }
         tc::fence_smem_to_mma();
         mbar_arrive(smem_addr(&sh.q_full[x]));
@@ -479,8 +482,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           auto offset = [&](int blk) { return BLOCKS ? sh.lv[slot][blk] : 0.0f; };
           // Columns 32c .. of the row: not seen is -infinity; the highest of each block.
           auto mask = [&](int c, uint32_t (&v)[32]) {
-            if constexpr (MASK) {
-              const int mlo = lo - key0 - 32 * c, mhi = hi - key0 - 32 * c;
+            const int k0 = key0 + 32 * c;
+            if (MASK && (k0 < lo_all || k0 + 31 > hi_all)) {
+              const int mlo = lo - k0, mhi = hi - k0;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i < mlo || i > mhi) v[i] = 0xff800000u;
@@ -846,27 +850,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           scales();
           row2 = rows_of((j >> 2) + 2);
         }
-        const int slot = j & ((1 << shift) - 1);
-        const uint32_t phase = turns.of(slot, j, shift);
-        if (shift == 2 && j == min(2, p.n - 1)) {  // tile B is through with its last item's outputs
-          if (!(ok = warp_wait(sh, sh.b_free, b_phase))) break;
-          b_phase ^= 1;
-        }
-        if (!turns.fresh(slot, j, shift) && !(ok = warp_wait(sh, out[slot], phase ^ 1))) break;
-        const uint32_t bar = smem_addr(&in[slot]);
-        const uint32_t dst = slot < 2 ? ring + slot * bytes : q_smem + OPER + (slot - 2) * bytes;
         const int lane0 = 8 * (j & 3);  // the lanes with this tile's blocks
-#pragma unroll 4
-        for (int i = 0; i < boxes; ++i) {
-          int y = __shfl_sync(0xffffffffu, row0, lane0 + i * (box_keys >> 4));
-          if (y < 0) y = n_rows;
-          if (tc::one_thread()) {
-            tma_box(dst + i * box_keys * 128, map, p.kvh * HD, y, bar);
-            if constexpr (!FP8) tma_box(dst + HALF + i * box_keys * 128, map, p.kvh * HD + 64, y, bar);
-          }
-          __syncwarp();
+        // All that can be done before the slot is free: the boxes' rows (a shuffle,
+        // an election and a barrier for each copy took 200 cycles apiece) and the
+        // tile's block table.
+        int y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = __shfl_sync(0xffffffffu, row0, lane0 + ((i * (box_keys >> 4)) & 7));
+          y[i] = y[i] < 0 ? n_rows : y[i];
         }
-        if (!v) {  // the tile's block table
+        if (!v) {
           const int blk = lane0 + (lane & 7), info = t & (INFO - 1);
           const int at = __shfl_sync(0xffffffffu, row0, blk);
           const float k = FP8 ? __shfl_sync(0xffffffffu, ks0, blk) : 1.0f;
@@ -884,7 +878,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         }
-        if (lane == 0) mbar_expect_tx(bar, bytes);
+        const int slot = j & ((1 << shift) - 1);
+        const uint32_t phase = turns.of(slot, j, shift);
+        if (shift == 2 && j == min(2, p.n - 1)) {  // tile B is through with its last item's outputs
+          if (!(ok = warp_wait(sh, sh.b_free, b_phase))) break;
+          b_phase ^= 1;
+        }
+        if (!turns.fresh(slot, j, shift) && !(ok = warp_wait(sh, out[slot], phase ^ 1))) break;
+        const uint32_t bar = smem_addr(&in[slot]);
+        const uint32_t dst = slot < 2 ? ring + slot * bytes : q_smem + OPER + (slot - 2) * bytes;
+        if (tc::one_thread()) {
+          mbar_expect_tx(bar, bytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < boxes) {
+              tma_box(dst + i * box_keys * 128, map, p.kvh * HD, y[i], bar);
+              if constexpr (!FP8) tma_box(dst + HALF + i * box_keys * 128, map, p.kvh * HD + 64, y[i], bar);
+            }
+        }
+        __syncwarp();
         flying |= 1u << slot;
         flying_parity = (flying_parity & ~(1u << slot)) | phase << slot;
       }
