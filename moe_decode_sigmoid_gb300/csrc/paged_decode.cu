@@ -24,13 +24,12 @@
 // two or three of them on the way at any time, ~190 KiB an SM, with no barrier
 // between warps.  (With the granule on its way in registers instead, 64 KiB an
 // SM, 32 x 100K E4M3 took 440 us, 5.0 TB/s.)
-// Work: the (sequence, KV head) rows' 16-key granules laid end to end and cut
+// Work: the (sequence, KV head) rows of 16-key granules laid end to end and cut
 // into equal shares, one per CTA (one per SM); a share's warps take its
 // granules in turn.  A row cut between CTAs leaves partial results in the
 // workspace, and the CTA that arrives last joins them in their order, so the
-// bits do not depend on timing.  Short rows are not cut (the cut moves to their
-// nearer end): a join costs microseconds.  The lengths are on the device: every
-// CTA computes the cuts itself, by a scan over the sequences.
+// bits do not depend on timing.  The lengths are on the device: every CTA
+// computes the cuts itself, by a scan over the sequences.
 #include "nv_util.cuh"
 #include "paged.cuh"
 #include "paged_work.cuh"
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   constexpr int WARPS = Cfg<FP8>::WARPS, THREADS = Cfg<FP8>::THREADS, SLOTS = Cfg<FP8>::SLOTS;
   constexpr int ROW = Cfg<FP8>::ROW, SLOT = Cfg<FP8>::SLOT;
   extern __shared__ __align__(128) float s_o[];  // the rings; then [WARPS][DEC_O]
-  __shared__ int s_pre[MAX_SEQS + 1];            // granules (of all heads) before each sequence
+  __shared__ int s_pre[MAX_SEQS + 1];            // weight (of all heads) before each sequence
   __shared__ int4 s_seq[MAX_SEQS];               // {position, row, first granule, granules}
   __shared__ int s_scan[MAX_SEQS / 32];
   __shared__ float s_m[WARPS * 8], s_l[WARPS * 8];
@@ -111,8 +110,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   const int nq = b.nkv * b.group;
 
   // ---- the cuts ---------------------------------------------------------------
-  // Lengths are below 2^23 tokens, so 256 sequences of 8 heads stay below 2^31
-  // granules.
+  // Lengths are below 2^23 tokens, so 256 sequences of 8 heads weigh below 2^31.
   int cnt = 0, pre = 0;
   int4 info = make_int4(-1, -1, 0, 0);
   if (tid < MAX_SEQS) {
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       if (q.n > 0) {
         info = make_int4(pos, q.q0, lo >> 4, pos >= 0 ? (pos >> 4) + 1 - (lo >> 4) : 0);
-        cnt = info.w * b.nkv;
+        cnt = DecCut::weight(info.w) * b.nkv;
       }
       s_seq[tid] = info;
     }
@@ -143,18 +141,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     if (w == warp) pre += total;
     total += s_scan[w];
   }
-  const int share = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), DEC_MIN_SHARE);
-  const int margin = share >> 4;
+  const DecCut cuts(total, gridDim.x);
   if (tid < MAX_SEQS && tid < b.n_seqs) {
     s_pre[tid + 1] = pre + cnt;
     if (tid == 0) s_pre[0] = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const long long x = (long long)share * (blockIdx.x + k);
-      if (pre <= x && x < pre + cnt) {  // this sequence holds the cut: move it to a near row end
-        const int off = (int)(x - pre) % info.w, rest = info.w - off;
-        const int near = min(off, rest);
-        s_cut[k] = (int)x + (info.w <= DEC_WHOLE || near <= margin ? (off <= rest ? -off : rest) : 0);
+      const long long x = (long long)cuts.share * (blockIdx.x + k);
+      if (pre <= x && x < pre + cnt) {  // this sequence holds the cut
+        s_cut[k] = cuts.at((int)x, pre, info.w);
         if (k == 0) s_first = tid;
       }
     }
@@ -176,9 +171,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   while (cur < end) {
     while (cur >= s_pre[s + 1]) ++s;
     const int4 sq = s_seq[s];
-    const int rel = cur - s_pre[s];
-    const int kvh = rel / sq.w, off = rel - kvh * sq.w;
-    const int n = min(sq.w - off, end - cur);  // granules of this segment
+    const int weight = DecCut::weight(sq.w), kvh = (cur - s_pre[s]) / weight;
+    const int row0 = s_pre[s] + kvh * weight;
+    int off, to;
+    cuts.part(cur, end, row0, sq.w, off, to);
+    const int n = to - off;                    // granules of this segment
     const int first_key = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
     const int g0 = sq.z + off;                 // the first of them
 
@@ -431,11 +428,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         *reinterpret_cast<float2*>(s_o + warp * DEC_O + ((2 * j + e) * 8 + g) * 8 + 2 * t) =
             make_float2(o[j][2 * e], o[j][2 * e + 1]);
     __syncthreads();
-    // The cuts inside the row (none: it is whole here), the CTAs that share it.
-    const int row0 = cur - off;
-    const int cut0 = (row0 + margin) / share + 1, cut1 = (row0 + sq.w - margin - 1) / share;
-    const bool whole = sq.w <= DEC_WHOLE || cut0 > cut1;
-    const int c0 = cut0 - 1, c1 = cut1;
+    int c0, c1;
+    const bool whole = !cuts.shared(row0, sq.w, c0, c1);
     float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0);
     for (int i = tid; i < 512; i += THREADS) {  // (tile j, lane row, head): elements d, d + 1
       const int h = i & 7, r = i >> 3, j = r >> 3, gg = r & 7;
@@ -508,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       }
     }
     __syncthreads();  // the shared buffers are free
-    cur += n;
+    cur = min(end, row0 + weight);
   }
 }
 

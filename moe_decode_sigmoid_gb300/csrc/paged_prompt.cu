@@ -34,9 +34,9 @@
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each; P takes its S's place.  O is
 // rescaled only when a row's maximum grows by more than 2^8.
 //
-// Work: items (tile pair of a sequence, KV head) of so many key tiles, laid end
-// to end and cut into equal shares, as the next-token kernel cuts its rows; cut
-// items are joined through the workspace by the CTA that arrives last.
+// Work: items (tile pair of a sequence, KV head) of so many key tiles, cut as the
+// next-token kernel's rows; cut items are joined through the workspace by the
+// CTA that arrives last.
 #include <type_traits>
 
 #include "nv_util.cuh"
@@ -77,7 +77,7 @@ struct Shared {
   uint32_t tmem;
   int fail, last, cut[2], first;
   int scan[16];
-  int pre[MAX_ITEMS + 1];            // key tiles (of all heads) before each item
+  int pre[MAX_ITEMS + 1];            // weight (of all heads) before each item
   int4 item[MAX_ITEMS];              // {sequence, pair, first key tile, key tiles}
   int qpre[MAX_SEQS + 1];            // items before each sequence
   int4 seq[MAX_SEQS];                // {first row, rows, first position, -}
@@ -101,6 +101,7 @@ struct Item {
   int tokens, pos0;      // tokens of the item, position of the first
   int q_row;             // its row of q / out
   int row0, all;         // where the whole item begins, its key tiles
+  int next;              // where the share goes on
   bool split;            // one tile: A and B have every other key tile
 };
 
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int k0 = (a.window > 0 ? max(0, first - a.window + 1) : 0) >> 7;
     info = make_int4(lo, pair, k0, last >= 0 ? (last >> 7) + 1 - k0 : 0);
     sh.item[tid] = info;
-    cnt = info.w * b.nkv;
+    cnt = PrCut::weight(info.w) * b.nkv;
   }
   pre = cnt;
 #pragma unroll
@@ -317,18 +318,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (w == warp) pre += total;
     total += sh.scan[w];
   }
-  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, PR_MIN_SHARE);
-  const int margin = min(share >> 4, PR_MARGIN);
+  const PrCut cuts(total, gridDim.x);
   if (tid < n_items) {
     sh.pre[tid + 1] = pre + cnt;
     if (tid == 0) sh.pre[0] = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const long long x = (long long)share * (blockIdx.x + k);
-      if (pre <= x && x < pre + cnt) {  // this item holds the cut: move it to a near end
-        const int off = (int)(x - pre) % info.w, rest = info.w - off;
-        const int near = min(off, rest);
-        sh.cut[k] = (int)x + (info.w <= PR_WHOLE || near <= margin ? (off <= rest ? -off : rest) : 0);
+      const long long x = (long long)cuts.share * (blockIdx.x + k);
+      if (pre <= x && x < pre + cnt) {  // this item holds the cut
+        sh.cut[k] = cuts.at((int)x, pre, info.w);
         if (k == 0) sh.first = tid;
       }
     }
@@ -352,22 +350,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int4 e = sh.item[it];
     const int4 sq = sh.seq[e.x];
     Item p;
-    int off = cur - sh.pre[it];
+    const int weight = PrCut::weight(e.w);
+    p.row0 = sh.pre[it];
     p.kvh = 0;
-    while (off >= e.w) {
-      off -= e.w;
+    while (cur >= p.row0 + weight) {
+      p.row0 += weight;
       ++p.kvh;
     }
+    int from, to;
+    cuts.part(cur, end, p.row0, e.w, from, to);
+    p.next = min(end, p.row0 + weight);
     p.seq = e.x;
-    p.kt0 = e.z + off;
-    p.n = min(e.w - off, end - cur);
+    p.kt0 = e.z + from;
+    p.n = to - from;
+    p.all = e.w;
     const int tok0 = e.y * 2 * tile_toks;
     p.tokens = min(sq.y - tok0, 2 * tile_toks);
     p.pos0 = sq.z + tok0;
     p.q_row = sq.x + tok0;
     p.split = p.tokens <= tile_toks;
-    p.row0 = cur - off;
-    p.all = e.w;
     return p;
   };
 
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int cur = begin, it = sh.first; cur < end;) {
       const Item p = part(cur, it);
-      cur += p.n;
+      cur = p.next;
       const int tok = tok_in_tile + (p.split ? 0 : x * tile_toks);
       const int pos = p.pos0 + min(tok, p.tokens - 1);
       const int head = p.kvh * b.group + head_in_group;
@@ -613,10 +614,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         o_phase ^= 1;
         tc::fence_after();
       }
-      // The cuts inside the item (none: it is whole here), the CTAs that share it.
-      const int cut0 = (p.row0 + margin) / share + 1, cut1 = (p.row0 + p.all - margin - 1) / share;
-      const bool whole = p.all <= PR_WHOLE || cut0 > cut1;
-      const int c0 = cut0 - 1, c1 = cut1;
+      int c0, c1;  // the CTAs that share the item
+      const bool whole = !cuts.shared(p.row0, p.all, c0, c1);
       // A finished row goes out by way of the query tile's place, which is free:
       // a thread writes chunks of its row there, and the warp takes its 32 rows
       // out two at a time, whole lines instead of 16 bytes of 32 rows.
@@ -744,7 +743,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = w4 < C::HANDS;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
-      cur += p.n;
+      cur = p.next;
       const int see_hi = p.pos0 + p.tokens - 1;
       const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
 #pragma unroll 1
@@ -817,7 +816,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
-      cur += p.n;
+      cur = p.next;
       // Keys some query of the item sees.
       const int see_hi = p.pos0 + p.tokens - 1;
       const int see_lo = a.window > 0 ? max(0, p.pos0 - a.window + 1) : 0;
@@ -925,7 +924,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
-      cur += p.n;
+      cur = p.next;
       const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
       const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
       // Of a split item A has the even key tiles and B the odd ones (a ring slot

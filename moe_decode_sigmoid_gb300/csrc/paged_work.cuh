@@ -16,17 +16,46 @@ constexpr int MAX_CTAS = 160;  // CTAs of an attention launch (one per SM; GB300
 constexpr size_t WS_HEAD = 4096, WS_ERROR = WS_HEAD - 4;
 static_assert(MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
 
+// The cut.  A row (next tokens: a sequence and KV head; prompts: an item, a tile
+// pair and KV head) weighs its key granules (tiles) and what it costs besides,
+// START of them: its queries, its first keys, its outputs.  The rows' weights are
+// laid end to end and cut into equal shares, one per CTA.  A cut near a row's end
+// moves to it (a join costs microseconds, MARGIN granules), and a row of at most
+// WHOLE is not cut at all.
+template <int START, int WHOLE, int MARGIN>
+struct Cut {
+  int share, margin;
+  __device__ __forceinline__ Cut(int total, int ctas)
+      : share(max((total + ctas - 1) / ctas, START + 1)), margin(min(share >> 4, MARGIN)) {}
+  static __device__ __forceinline__ int weight(int n) { return n > 0 ? n + START : 0; }
+  // Where a cut at place x falls, in a run of rows of n granules each from `first`.
+  __device__ __forceinline__ int at(int x, int first, int n) const {
+    const int w = weight(n), off = (x - first) % w, rest = w - off;
+    if (n <= WHOLE) return off <= rest ? x - off : x + rest;
+    return off <= START + margin ? x - off : rest <= margin ? x + rest : x;
+  }
+  // The granules [from, to) of the row at row0 that the share cur .. end - 1 has.
+  __device__ __forceinline__ void part(int cur, int end, int row0, int n, int& from, int& to) const {
+    from = cur == row0 ? 0 : cur - row0 - START;
+    to = end >= row0 + weight(n) ? n : end - row0 - START;
+  }
+  // The CTAs c0 .. c1 that share the row at row0; false if one has it whole.
+  __device__ __forceinline__ bool shared(int row0, int n, int& c0, int& c1) const {
+    const int i0 = (row0 + START + margin) / share + 1, i1 = (row0 + weight(n) - margin - 1) / share;
+    c0 = i0 - 1;
+    c1 = i1;
+    return n > WHOLE && i0 <= i1;
+  }
+};
+
 // A slot of the next-token kernel: 8 maxima, 8 sums, 128 x 8 outputs.
 constexpr int DEC_ML = 16, DEC_O = HD * 8, DEC_SLOT = DEC_ML + DEC_O;
-// Fewest granules in a CTA's share, and the longest row that is never cut.
-constexpr int DEC_MIN_SHARE = 16, DEC_WHOLE = 64;
+using DecCut = Cut<16, 64, 32>;
 
 // A slot of the prompt kernel: two tiles of 128 maxima, 128 sums and 128 x 128
 // outputs.
 constexpr int PR_TILE = 128 * (2 + HD), PR_SLOT = 2 * PR_TILE;
-// Fewest key tiles in a CTA's share, the longest item that is never cut, and how
-// far a cut moves to an item's end at most: what a join costs, in tiles.
-constexpr int PR_MIN_SHARE = 4, PR_WHOLE = 6, PR_MARGIN = 3;
+using PrCut = Cut<3, 6, 3>;
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
   return WS_HEAD + sizeof(float) * 2 * MAX_CTAS * (size_t)PR_SLOT;
