@@ -495,51 +495,61 @@ class PagedBatch:
         self._pointers = (_arg(f, "q_start", q_start, _I32T, (n + 1,), dev),
                           _arg(f, "kv_len", kv_len, _I32T, (n,), dev),
                           _arg(f, "page_table", page_table, _I32T, (n, max_pages), dev))
-        self._struct = None
+        self._for = (0, None)  # the C struct for caches of so many pages
 
     def _ref(self, n_pages):
-        """The C struct for a cache of n_pages pages."""
-        st = self._struct
-        if st is None or st.n_pages != n_pages:
-            st = self._struct = _PagedBatchStruct(*self._fields, n_pages, *self._pointers)
-        return st
+        """The C struct, by reference, for caches of n_pages pages."""
+        pages, ref = self._for
+        if pages != n_pages:
+            ref = ctypes.byref(_PagedBatchStruct(*self._fields, n_pages, *self._pointers))
+            self._for = (n_pages, ref)
+        return ref
 
 
-def _paged(where, name, rows, batch, k_cache, d):
+def _paged(where, name, rows, batch, k_cache, hd, nkv):
     """(rows, device, pages, C struct) of a paged call after checking its batch
     and device; rows [n_tokens, ...] on the current CUDA device."""
-    if not isinstance(batch, PagedBatch):
+    if type(batch) is not PagedBatch:
         raise FlintError(FLINT_ERR_INVALID_ARG, "%s: batch must be a PagedBatch, got %s" %
                          (where, type(batch).__name__))
     dev = batch.device
     if not (isinstance(rows, torch.Tensor) and rows.device == dev and rows.dim() >= 2 and
             1 <= rows.shape[0] <= PAGED_MAX_TOKENS):
         _bad(where, name, "of 1 to %d token rows on %s" % (PAGED_MAX_TOKENS, dev), rows)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         _on_current_device(where, name, rows)
     if not (isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 and k_cache.shape[0] >= 1):
-        _bad(where, "k_cache", "a [pages, %d, %d, %d] tensor" % (batch.page_size, d.n_kv_heads,
-                                                                d.head_dim), k_cache)
+        _bad(where, "k_cache", "a [pages, %d, %d, %d] tensor" % (batch.page_size, nkv, hd), k_cache)
     pages = k_cache.shape[0]
     return rows.shape[0], dev, pages, batch._ref(pages)
 
 
+def _heads(dims):
+    """(query heads, KV heads, head size, C struct by reference) of a call."""
+    if dims is None:
+        return N_Q_HEADS, N_KV_HEADS, HEAD_DIM, _ATTN_DIMS_REF
+    return dims.n_q_heads, dims.n_kv_heads, dims.head_dim, ctypes.byref(dims)
+
+
+_ATTN_DIMS_REF = ctypes.byref(ATTN_DIMS)
+
+
 def _append(f, qkv, q_norm, k_norm, batch, q_out, k_cache, v_cache, scales, dtype, rope_theta, eps,
             stream, dims):
-    d = ATTN_DIMS if dims is None else dims
-    nq, nkv, hd = d.n_q_heads, d.n_kv_heads, d.head_dim
-    T, dev, pages, st = _paged(f, "qkv", qkv, batch, k_cache, d)
+    nq, nkv, hd, d = _heads(dims)
+    T, dev, pages, b = _paged(f, "qkv", qkv, batch, k_cache, hd, nkv)
     cache = (pages, batch.page_size, nkv, hd)
-    blocks = (pages, batch.page_size // KV_BLOCK, nkv)
     args = (_arg(f, "qkv", qkv, _BF16, (T, (nq + 2 * nkv) * hd), dev),
             _arg(f, "q_norm", q_norm, _BF16, (hd,), dev),
-            _arg(f, "k_norm", k_norm, _BF16, (hd,), dev))
-    outs = (_arg(f, "q_out", q_out, _BF16, (T, nq, hd), dev),
+            _arg(f, "k_norm", k_norm, _BF16, (hd,), dev), rope_theta, eps,
+            _arg(f, "q_out", q_out, _BF16, (T, nq, hd), dev),
             _arg(f, "k_cache", k_cache, dtype, cache, dev),
             _arg(f, "v_cache", v_cache, dtype, cache, dev))
-    outs += tuple(_arg(f, n, t, _F32, blocks, dev) for n, t in scales)
-    _check(getattr(lib(), f)(ctypes.byref(d), ctypes.byref(st), T, *args, float(rope_theta),
-                             float(eps), *outs, _stream(stream)), f)
+    if scales:
+        blocks = (pages, batch.page_size // KV_BLOCK, nkv)
+        args += (_arg(f, "k_scale", scales[0], _F32, blocks, dev),
+                 _arg(f, "v_scale", scales[1], _F32, blocks, dev))
+    _check(getattr(_lib or lib(), f)(d, b, T, *args, _stream(stream)), f)
 
 
 def flint_qk_norm_rope_kv_paged_bf16(qkv, q_norm, k_norm, batch: PagedBatch, q_out, k_cache,
@@ -550,7 +560,7 @@ def flint_qk_norm_rope_kv_paged_bf16(qkv, q_norm, k_norm, batch: PagedBatch, q_o
     [T, nq, 128], keys and values to k_cache / v_cache [pages, page_size, nkv,
     128] (bf16) at the rows the batch's page table gives."""
     _append("flint_qk_norm_rope_kv_paged_bf16", qkv, q_norm, k_norm, batch, q_out, k_cache,
-            v_cache, (), _BF16, rope_theta, eps, stream, dims)
+            v_cache, None, _BF16, rope_theta, eps, stream, dims)
 
 
 def flint_qk_norm_rope_kv_paged_fp8(qkv, q_norm, k_norm, batch: PagedBatch, q_out, k_cache,
@@ -560,7 +570,7 @@ def flint_qk_norm_rope_kv_paged_fp8(qkv, q_norm, k_norm, batch: PagedBatch, q_ou
     [pages, page_size, nkv, 128] and fp32 power-of-two scales
     [pages, page_size / 16, nkv] per 16-token block and head."""
     _append("flint_qk_norm_rope_kv_paged_fp8", qkv, q_norm, k_norm, batch, q_out, k_cache, v_cache,
-            (("k_scale", k_scale), ("v_scale", v_scale)), _U8, rope_theta, eps, stream, dims)
+            (k_scale, v_scale), _U8, rope_theta, eps, stream, dims)
 
 
 def flint_attn_workspace_bytes(dims: AttnDims | None = None) -> int:
@@ -579,21 +589,22 @@ def flint_attn_get_device_status(workspace: torch.Tensor, stream=None) -> int:
 
 def _attend(f, q, k_cache, v_cache, scales, dtype, batch, out, workspace, sinks, window,
             softmax_scale, stream, dims):
-    d = ATTN_DIMS if dims is None else dims
-    nq, nkv, hd = d.n_q_heads, d.n_kv_heads, d.head_dim
-    T, dev, pages, st = _paged(f, "q", q, batch, k_cache, d)
-    cache = (pages, batch.page_size, nkv, hd)
-    blocks = (pages, batch.page_size // KV_BLOCK, nkv)
-    args = (_arg(f, "q", q, _BF16, (T, nq, hd), dev),
+    nq, nkv, hd, d = _heads(dims)
+    T, dev, pages, b = _paged(f, "q", q, batch, k_cache, hd, nkv)
+    cache, rows = (pages, batch.page_size, nkv, hd), (T, nq, hd)
+    args = (_arg(f, "q", q, _BF16, rows, dev),
             _arg(f, "k_cache", k_cache, dtype, cache, dev),
             _arg(f, "v_cache", v_cache, dtype, cache, dev))
-    args += tuple(_arg(f, n, t, _F32, blocks, dev) for n, t in scales)
-    args += (_arg(f, "sinks", sinks, _F32, (nq,), dev, optional=True),)
-    o = _arg(f, "out", out, _BF16, (T, nq, hd), dev)
+    if scales:
+        blocks = (pages, batch.page_size // KV_BLOCK, nkv)
+        args += (_arg(f, "k_scale", scales[0], _F32, blocks, dev),
+                 _arg(f, "v_scale", scales[1], _F32, blocks, dev))
     wp, wb = _ws_arg(f, workspace, dev)
-    scale = hd ** -0.5 if softmax_scale is None else float(softmax_scale)
-    _check(getattr(lib(), f)(ctypes.byref(d), ctypes.byref(st), T, *args, scale, int(window), o, wp,
-                             wb, _stream(stream)), f)
+    _check(getattr(_lib or lib(), f)(
+        d, b, T, *args,
+        None if sinks is None else _arg(f, "sinks", sinks, _F32, (nq,), dev),
+        hd ** -0.5 if softmax_scale is None else softmax_scale, window,
+        _arg(f, "out", out, _BF16, rows, dev), wp, wb, _stream(stream)), f)
 
 
 def flint_attn_paged_bf16(q, k_cache, v_cache, batch: PagedBatch, out, workspace, sinks=None,
@@ -604,7 +615,7 @@ def flint_attn_paged_bf16(q, k_cache, v_cache, batch: PagedBatch, out, workspace
     positions (0: all), with optional learned sinks fp32 [nq] in the softmax's
     denominator, into out [T, nq, 128].  softmax_scale defaults to 128 ** -0.5;
     workspace: new_attn_workspace()."""
-    _attend("flint_attn_paged_bf16", q, k_cache, v_cache, (), _BF16, batch, out, workspace, sinks,
+    _attend("flint_attn_paged_bf16", q, k_cache, v_cache, None, _BF16, batch, out, workspace, sinks,
             window, softmax_scale, stream, dims)
 
 
@@ -613,9 +624,8 @@ def flint_attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, batch: PagedBatc
                          stream=None, dims: AttnDims | None = None):
     """flint_attn_paged_bf16 over an E4M3 cache (uint8 codes and fp32 scales as
     flint_qk_norm_rope_kv_paged_fp8 writes them)."""
-    _attend("flint_attn_paged_fp8", q, k_cache, v_cache,
-            (("k_scale", k_scale), ("v_scale", v_scale)), _U8, batch, out, workspace, sinks, window,
-            softmax_scale, stream, dims)
+    _attend("flint_attn_paged_fp8", q, k_cache, v_cache, (k_scale, v_scale), _U8, batch, out,
+            workspace, sinks, window, softmax_scale, stream, dims)
 
 
 # ---------------------------------------------------------------- conveniences
