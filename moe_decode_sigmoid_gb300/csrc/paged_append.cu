@@ -19,6 +19,8 @@
 // the host does not know them.  A head's row belongs to 16 lanes, and a lane
 // loads five of its up to ten rows before it uses the first: two round trips to
 // memory instead of ten, with room for four CTAs on an SM.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace flint {
@@ -94,6 +96,7 @@ __global__ void __launch_bounds__(THREADS, 4) paged_append_kernel(const __grid_c
   __shared__ int s_blk, s_which;
   __shared__ __align__(16) float s_cos[BLOCK][HD / 2];  // read four at a time
   __shared__ __align__(16) float s_sin[BLOCK][HD / 2];
+  __shared__ float2 s_step[4][HD / 2];           // turns by 1, 2, 4 and 8 tokens
   __shared__ int s_amax[2];  // of the new keys and values, as bits
   pdl_wait();  // the projection rows come from the preceding kernel
   pdl_trigger();
@@ -138,24 +141,10 @@ __global__ void __launch_bounds__(THREADS, 4) paged_append_kernel(const __grid_c
   const int nq = b.nkv * b.group;
 
   // Row i: token i % n of head i / n, the key, the value, then the queries.
-  // This lane's rows are hw, hw + 16, ...
+  // This lane's rows are hw, hw + 16, ...: in a whole block all of one token.
   const int hw = tid >> 4, l = tid & 15, rows = n * (b.group + 2);
   const int recip = (65536 + n - 1) / n;  // i / n for i < 160
   auto head_of = [&](int i) { return (i * recip) >> 16; };
-  auto src_of = [&](int i) {
-    const int j = head_of(i), tok = i - j * n;
-    const int head = j == 0 ? nq + kvh : j == 1 ? nq + b.nkv + kvh : kvh * b.group + j - 2;
-    return a.qkv + ((size_t)(t0 + tok) * (nq + 2 * b.nkv) + head) * HD + 4 * l;
-  };
-  Row raw[BATCH];
-  auto load_batch = [&](int first) {
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int i = hw + ROWS * (first + k);
-      raw[k] = i < rows ? load_row(src_of(i)) : Row{make_uint2(0u, 0u), make_uint2(0u, 0u)};
-    }
-  };
-  load_batch(0);
   const Row k_gain = load_row(a.k_norm + 4 * l), q_gain = load_row(a.q_norm + 4 * l);
   // Blocks divide pages, so one look-up serves the block.
   const int row0 = base >= 0 ? cache_row(b, s, base) : -1;
@@ -166,100 +155,143 @@ __global__ void __launch_bounds__(THREADS, 4) paged_append_kernel(const __grid_c
     old_k = a.k_scale[sc];
     old_v = a.v_scale[sc];
   }
-
-  // The first token's angles in fp64 (a position of 2^18 times a frequency near
-  // 1 would leave an fp32 angle 0.03 rad off), reduced to [-pi, pi]; the others
-  // turn on from there by at most 15 steps, whose angles fp32 holds to 2^-21.
-  // (fp64 for all of them: at two operations a clock and SM it took longer than
-  // the block's bytes.)
-  if (a.rope) {
-    constexpr double INV_TWO_PI = 0.15915494309189535;  // 1 / (2 pi)
-    constexpr double TWO_PI_HI = 6.283185307179586;     // 2 pi = HI + LO
-    constexpr double TWO_PI_LO = 2.4492935982947064e-16;
-    if (tid < HD / 2) {
-      const double ang = (double)lo * a.inv_freq[tid];
-      const double k = rint(ang * INV_TWO_PI);
-      const double r = fma(-k, TWO_PI_LO, fma(-k, TWO_PI_HI, ang));
-      float sn, cs;
-      sincosf((float)r, &sn, &cs);
-      s_cos[0][tid] = cs;
-      s_sin[0][tid] = sn;
-    }
-    if (n > 1) {
-      __syncthreads();
-      for (int i = tid + HD / 2; i < n * (HD / 2); i += THREADS) {
-        const int tok = i >> 6, e = i & 63;
-        float sn, cs;
-        sincosf((float)tok * (float)a.inv_freq[e], &sn, &cs);
-        const float c0 = s_cos[0][e], s0 = s_sin[0][e];
-        s_cos[tok][e] = c0 * cs - s0 * sn;
-        s_sin[tok][e] = s0 * cs + c0 * sn;
-      }
-    }
-  }
-  __syncthreads();
-
-  // Norm and rotation of a row.
-  auto turned = [&](const Row& w, const Row& gain, int tok, float (&x)[8]) {
-    widen(w, x);
-    float ss = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(ss / (float)HD + a.eps);
-    float g[8];
-    widen(gain, g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
-    if (a.rope) {
-      const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[tok][4 * l]);
-      const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[tok][4 * l]);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = x[j], hi = x[4 + j];
-        x[j] = lo * c[j] - hi * sn[j];
-        x[4 + j] = hi * c[j] + lo * sn[j];
-      }
-    }
-  };
-
   // The keys are among the lanes' first rows, the values among the first two;
   // E4M3 keeps them until the block's scale is known.
   float key[8];
   Row val[2];
+
+  auto rows_of = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;  // n is 16: no index arithmetic
+    const uint16_t* tok_row = a.qkv + (size_t)(t0 + hw) * (nq + 2 * b.nkv) * HD + 4 * l;
+    auto src_of = [&](int k) {
+      const int i = hw + ROWS * k, j = WHOLE ? k : head_of(i);
+      const int head = j == 0 ? nq + kvh : j == 1 ? nq + b.nkv + kvh : kvh * b.group + j - 2;
+      if constexpr (WHOLE) return tok_row + head * HD;
+      return a.qkv + ((size_t)(t0 + i - j * n) * (nq + 2 * b.nkv) + head) * HD + 4 * l;
+    };
+    Row raw[BATCH];
+    auto load_batch = [&](int first) {
 #pragma unroll
-  for (int k = 0; k < MOST; ++k) {
-    const int i = hw + ROWS * k;
-    if (!__any_sync(0xffffffffu, i < rows)) break;  // shuffles need the whole warp
-    if (k == BATCH) load_batch(BATCH);
-    const bool live = i < rows;
-    const int j = live ? head_of(i) : 2, tok = live ? i - j * n : 0;
-    const Row w = raw[k % BATCH];
-    float x[8];
-    turned(w, j == 0 ? k_gain : q_gain, tok, x);
-    if (k < 2 && __any_sync(0xffffffffu, j < 2)) {
-      if constexpr (FP8) {
-        float v[8];
-        widen(w, v);
-        val[k] = w;
+      for (int k = 0; k < BATCH; ++k)
+        raw[k] = hw + ROWS * (first + k) < rows ? load_row(src_of(first + k))
+                                                : Row{make_uint2(0u, 0u), make_uint2(0u, 0u)};
+    };
+    load_batch(0);
+    // The first token's angles in fp64 (a position of 2^18 times a frequency near
+    // 1 would leave an fp32 angle 0.03 rad off), reduced to [-pi, pi]; the others
+    // turn on from there by steps of 1, 2, 4 and 8 tokens, whose angles fp32 holds
+    // to 2^-21, at most four products after one another.  So a thread takes one
+    // or two sines instead of four, and fp64, at two operations a clock and SM,
+    // stays off the other tokens.
+    if (a.rope) {
+      constexpr double INV_TWO_PI = 0.15915494309189535;  // 1 / (2 pi)
+      constexpr double TWO_PI_HI = 6.283185307179586;     // 2 pi = HI + LO
+      constexpr double TWO_PI_LO = 2.4492935982947064e-16;
+      const int e = tid & 63, part = tid >> 6;  // frequency; bit of the step, then four tokens
+      if (n > 1) {
+        const float ang = (float)(1 << part) * (float)a.inv_freq[e];
+        float sn, cs;
+        sincosf(ang, &sn, &cs);
+        s_step[part][e] = make_float2(cs, sn);
+      }
+      if (tid < HD / 2) {
+        const double ang = (double)lo * a.inv_freq[tid];
+        const double k = rint(ang * INV_TWO_PI);
+        const double r = fma(-k, TWO_PI_LO, fma(-k, TWO_PI_HI, ang));
+        float sn, cs;
+        sincosf((float)r, &sn, &cs);
+        s_cos[0][tid] = cs;
+        s_sin[0][tid] = sn;
+      }
+      if (n > 1) {
+        __syncthreads();
+        auto on = [&](float2 x, int bit) {
+          const float2 y = s_step[bit][e];
+          return make_float2(x.x * y.x - x.y * y.y, x.y * y.x + x.x * y.y);
+        };
+        float2 at[4];
+        at[0] = make_float2(s_cos[0][e], s_sin[0][e]);
+        if (part & 1) at[0] = on(at[0], 2);
+        if (part & 2) at[0] = on(at[0], 3);
+        at[1] = on(at[0], 0);
+        at[2] = on(at[0], 1);
+        at[3] = on(at[2], 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (k == 0) key[e] = x[e];
-          if (j == 1) x[e] = v[e];
-        }
-        const float m = finite_max(x);
-        if (j < 2 && l == 0) atomicMax(&s_amax[j], __float_as_int(m));
-      } else if (j < 2 && row0 >= 0) {
-        store_row(static_cast<uint16_t*>(j ? a.v_cache : a.k_cache) +
-                      ((size_t)(row0 + kept + tok) * b.nkv + kvh) * HD + 4 * l,
-                  j ? w : narrow(x));  // a value as it came, bit for bit
+        for (int i = 0; i < 4; ++i)
+          if (part || i) {  // the first is there, and others read it
+            s_cos[4 * part + i][e] = at[i].x;
+            s_sin[4 * part + i][e] = at[i].y;
+          }
       }
     }
-    if (live && j >= 2)
-      store_row(a.q_out + ((size_t)(t0 + tok) * nq + kvh * b.group + j - 2) * HD + 4 * l, narrow(x));
-  }
+    __syncthreads();
+
+    float4 c4, s4;  // the token's turn
+    auto turn_of = [&](int tok) {
+      c4 = *reinterpret_cast<const float4*>(&s_cos[tok][4 * l]);
+      s4 = *reinterpret_cast<const float4*>(&s_sin[tok][4 * l]);
+    };
+    if (WHOLE) turn_of(hw);
+    // Norm and rotation of a row.
+    auto turned = [&](const Row& w, const Row& gain, float (&x)[8]) {
+      widen(w, x);
+      float ss = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss / (float)HD + a.eps);
+      float g[8];
+      widen(gain, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
+      if (a.rope) {
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = x[j], hi = x[4 + j];
+          x[j] = lo * c[j] - hi * sn[j];
+          x[4 + j] = hi * c[j] + lo * sn[j];
+        }
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      const int i = hw + ROWS * k;
+      if (WHOLE ? k >= b.group + 2 : !__any_sync(0xffffffffu, i < rows)) break;  // shuffles need the whole warp
+      if (k == BATCH) load_batch(BATCH);
+      const bool live = WHOLE || i < rows;
+      const int j = WHOLE ? k : live ? head_of(i) : 2, tok = WHOLE ? hw : live ? i - j * n : 0;
+      const Row w = raw[k % BATCH];
+      float x[8];
+      if (!WHOLE) turn_of(tok);
+      if (!WHOLE || k != 1) turned(w, j == 0 ? k_gain : q_gain, x);
+      if (k < 2 && (WHOLE || __any_sync(0xffffffffu, j < 2))) {
+        if constexpr (FP8) {
+          float v[8];
+          widen(w, v);
+          val[k] = w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (k == 0) key[e] = x[e];
+            if (j == 1) x[e] = v[e];
+          }
+          const float m = finite_max(x);
+          if (j < 2 && l == 0) atomicMax(&s_amax[j], __float_as_int(m));
+        } else if (j < 2 && row0 >= 0) {
+          store_row(static_cast<uint16_t*>(j ? a.v_cache : a.k_cache) +
+                        ((size_t)(row0 + kept + tok) * b.nkv + kvh) * HD + 4 * l,
+                    j ? w : narrow(x));  // a value as it came, bit for bit
+        }
+      }
+      if (live && j >= 2)
+        store_row(a.q_out + ((size_t)(t0 + tok) * nq + kvh * b.group + j - 2) * HD + 4 * l, narrow(x));
+    }
+  };
+  if (n == BLOCK)
+    rows_of(std::true_type{});
+  else
+    rows_of(std::false_type{});
   if constexpr (FP8) {
     __syncthreads();
     if (row0 < 0) return;
