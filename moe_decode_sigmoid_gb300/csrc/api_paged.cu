@@ -159,8 +159,8 @@ flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.window = window;
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
-  return cuda_status(a.b.max_q == 1 ? launch_paged_decode(a, fp8, sms, stream)
-                                    : launch_paged_prompt(a, fp8, sms, stream));
+  return cuda_status(a.b.max_q * a.b.group <= pg::DEC_ROWS ? launch_paged_decode(a, fp8, sms, stream)
+                                                           : launch_paged_prompt(a, fp8, sms, stream));
 }
 
 }  // namespace

@@ -14,6 +14,7 @@ constexpr int MAX_SEQS = 256;
 constexpr int MAX_TOKENS = 8192;
 constexpr int MAX_KV_HEADS = 8;
 constexpr int MAX_GROUP = 8;       // query heads per KV head
+constexpr int DEC_ROWS = 16;       // query rows (tokens x group) a KV head has at most in the next-token kernel
 }  // namespace pg
 
 // The batch a call works on (flint_paged_batch, the call's rows and the head
@@ -57,7 +58,7 @@ struct PagedAttnArgs {
   uint16_t* out;           // [n_tokens, nq, HD] bf16
   void* ws;
 };
-// One row a sequence (max_q 1), and any number.
+// A few rows a sequence (max_q * group at most DEC_ROWS), and any number.
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream);
 

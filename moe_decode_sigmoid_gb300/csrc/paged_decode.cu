@@ -39,15 +39,17 @@ namespace {
 
 using namespace pg;
 
-template <bool FP8>
+// NT: groups of 8 rows.
+template <bool FP8, int NT>
 struct Cfg {
-  static constexpr int WARPS = FP8 ? 16 : 8;
-  static constexpr int SLOTS = 3;                    // granules of a warp's ring
+  static constexpr int WARPS = FP8 && NT == 1 ? 16 : 8;
+  static constexpr int SLOTS = FP8 && NT > 1 ? 6 : 3;  // granules of a warp's ring
   static constexpr int THREADS = WARPS * 32;
   static constexpr int ROW = FP8 ? HD : 2 * HD;      // bytes of a head's key
   static constexpr int SLOT = 2 * BLOCK * ROW;       // bytes of a granule: keys, then values
   static constexpr int SMEM = WARPS * SLOTS * SLOT;  // the warps' results reuse it
-  static_assert(SMEM >= WARPS * DEC_O * 4, "the joint buffer fits");
+  static constexpr int O = NT * DEC_O, ML = NT * DEC_ML;  // floats of a warp's outputs, of maxima and sums
+  static_assert(SMEM >= WARPS * O * 4, "the warps' outputs fit");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
@@ -90,39 +92,43 @@ struct Batch {
 
 }  // namespace
 
-template <bool FP8>
-__global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int WARPS = Cfg<FP8>::WARPS, THREADS = Cfg<FP8>::THREADS, SLOTS = Cfg<FP8>::SLOTS;
-  constexpr int ROW = Cfg<FP8>::ROW, SLOT = Cfg<FP8>::SLOT;
-  extern __shared__ __align__(128) float s_o[];  // the rings; then [WARPS][DEC_O]
+  using C = Cfg<FP8, NT>;
+  constexpr int WARPS = C::WARPS, THREADS = C::THREADS, SLOTS = C::SLOTS;
+  constexpr int ROW = C::ROW, SLOT = C::SLOT, ROWS = 8 * NT;
+  extern __shared__ __align__(128) float s_o[];  // the rings; then [WARPS][O]
   __shared__ int s_pre[MAX_SEQS + 1];            // weight (of all heads) before each sequence
   __shared__ int4 s_seq[MAX_SEQS];               // {position, row, first granule, granules}
   __shared__ int s_scan[MAX_SEQS / 32];
-  __shared__ float s_m[WARPS * 8], s_l[WARPS * 8];
-  __shared__ float s_jm[MAX_CTAS * 8], s_jl[MAX_CTAS * 8];
+  __shared__ int s_new[MAX_SEQS];                // rows of the sequence
+  // Parts that are joined (the warps', the CTAs'): maxima, sums, factors; the rows' joint ones.
+  constexpr int PARTS = WARPS > JOIN_MOST ? WARPS : JOIN_MOST;
+  __shared__ float s_m[PARTS * ROWS], s_l[PARTS * ROWS], s_mm[ROWS], s_ll[ROWS];
+  __shared__ __align__(16) float s_f[PARTS * ROWS];  // read four at a time
   __shared__ int s_cut[2], s_first, s_last;
   pdl_wait();
   pdl_trigger();
   const PagedView& b = a.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int nq = b.nkv * b.group;
+  const int nq = b.nkv * b.group, gshift = 31 - __clz(b.group);  // group is a power of two
 
   // ---- the cuts ---------------------------------------------------------------
   // Lengths are below 2^23 tokens, so 256 sequences of 8 heads weigh below 2^31.
-  int cnt = 0, pre = 0;
+  int cnt = 0, pre = 0, rows = 0;
   int4 info = make_int4(-1, -1, 0, 0);
   if (tid < MAX_SEQS) {
     if (tid < b.n_seqs) {
       const Seq q = load_seq(b, tid);
-      const int pos = q.first;  // one row a sequence
-      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      const int lo = a.window > 0 ? max(0, q.first - a.window + 1) : 0;
       if (q.n > 0) {
-        info = make_int4(pos, q.q0, lo >> 4, pos >= 0 ? (pos >> 4) + 1 - (lo >> 4) : 0);
+        info = make_int4(q.first, q.q0, lo >> 4, q.len > 0 ? ((q.len - 1) >> 4) + 1 - (lo >> 4) : 0);
         cnt = DecCut::weight(info.w) * b.nkv;
       }
       s_seq[tid] = info;
+      s_new[tid] = rows = q.n;
     }
     pre = cnt;
 #pragma unroll
@@ -153,10 +159,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         if (k == 0) s_first = tid;
       }
     }
-    // A row that sees nothing: zeros.
+    // Rows that see nothing: zeros.
     if (info.w == 0 && info.y >= 0 && tid % gridDim.x == blockIdx.x) {
       uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)info.y * nq * HD);
-      for (int i = 0; i < nq * HD / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < rows * nq * HD / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   __syncthreads();
@@ -176,19 +182,25 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     int off, to;
     cuts.part(cur, end, row0, sq.w, off, to);
     const int n = to - off;                    // granules of this segment
-    const int first_key = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
     const int g0 = sq.z + off;                 // the first of them
+    // Row r is token r / group, head r % group; the keys that all rows see and
+    // that some row does.
+    const int n_new = s_new[s], pos_last = sq.x + n_new - 1;
+    const int some_lo = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
+    const int all_lo = a.window > 0 ? max(0, pos_last - a.window + 1) : 0;
 
     // The queries' words, to arrive while the granules are looked up.
-    uint4 qw[4];
-    {
+    uint4 qw[NT][4];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int r = 8 * u + g, tok = r >> gshift;
       const uint8_t* src = reinterpret_cast<const uint8_t*>(
-          a.q + ((size_t)sq.y * nq + kvh * b.group + g) * HD);
+          a.q + ((size_t)(sq.y + tok) * nq + kvh * b.group + (r & (b.group - 1))) * HD);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // E4M3: elements 16t .. 16t + 15 and 64 + 16t ..; bf16: 32i + 8t .. + 7
         const int at = FP8 ? (i >> 1) * 128 + 32 * t + (i & 1) * 16 : 64 * i + 16 * t;
-        qw[i] = g < b.group ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
+        qw[u][i] = tok < n_new ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
 
@@ -236,44 +248,54 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     // ---- the group's queries as A fragments -----------------------------------
     // E4M3: f16, each head scaled by a power of two so that its largest element
     // lies in [2^14, 2^15): a bf16 element is then exact down to 2^-31 of it.
-    uint32_t qa[8][2];
-    float qs = a.scale_log2;
-    if constexpr (FP8) {
-      float mx = 0.0f;
+    uint32_t qa[NT][8][2];
+    float qs[NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
+    for (int u = 0; u < NT; ++u) {
+      qs[u] = a.scale_log2;
+      if constexpr (FP8) {
+        float mx = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(x[j])), fabsf(bf_hi(x[j]))));
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
-      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-      qs *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x[4] = {qw[u][i].x, qw[u][i].y, qw[u][i].z, qw[u][i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
+          for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(x[j])), fabsf(bf_hi(x[j]))));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        qs[u] *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qa[2 * i + (j >> 1)][j & 1] = nvu::f16x2_of(bf_lo(x[j]) * up, bf_hi(x[j]) * up);
-      }
-    } else {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x[4] = {qw[u][i].x, qw[u][i].y, qw[u][i].z, qw[u][i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        qa[2 * i][0] = qw[i].x;
-        qa[2 * i][1] = qw[i].y;
-        qa[2 * i + 1][0] = qw[i].z;
-        qa[2 * i + 1][1] = qw[i].w;
+          for (int j = 0; j < 4; ++j)
+            qa[u][2 * i + (j >> 1)][j & 1] = nvu::f16x2_of(bf_lo(x[j]) * up, bf_hi(x[j]) * up);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qa[u][2 * i][0] = qw[u][i].x;
+          qa[u][2 * i][1] = qw[u][i].y;
+          qa[u][2 * i + 1][0] = qw[u][i].z;
+          qa[u][2 * i + 1][1] = qw[u][i].w;
+        }
       }
     }
+    // Rows g and g + 8 of the fragments of row groups 2v and 2v + 1.
+    auto q_frag = [&](int v, int k, int half, int word) { return 2 * v + half < NT ? qa[2 * v + half][k][word] : 0u; };
 
-    float o[8][4];
+    float o[NT][8][4], m[NT], l[NT];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int u = 0; u < NT; ++u) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[u][j][i] = 0.0f;
+      m[u] = -INFINITY;
+      l[u] = 0.0f;
+    }
 
     for (int it = 0; it < mine_n; ++it) {
       issue(it + SLOTS - 1);
@@ -283,9 +305,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       const bool behind = (it >> 5) != (min(it + SLOTS - 1, mine_n - 1) >> 5);
       const int row = __shfl_sync(0xffffffffu, behind ? old.row : now.row, it & 31);
       if (row < 0) continue;
-      float f = qs, lv = 0.0f, iv = 1.0f;
+      float scale = 1.0f, lv = 0.0f, iv = 1.0f;
       if constexpr (FP8) {
-        f *= __shfl_sync(0xffffffffu, behind ? old.ks : now.ks, it & 31);
+        scale = __shfl_sync(0xffffffffu, behind ? old.ks : now.ks, it & 31);
         // A scale of zero would take a block's weights out of the sum: 2^-100.
         const float vs = fmaxf(__shfl_sync(0xffffffffu, behind ? old.vs : now.vs, it & 31),
                                7.8886090522101181e-31f);
@@ -294,9 +316,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
       }
       const uint32_t ks = ring + (it % SLOTS) * SLOT, vsm = ks + BLOCK * ROW;
       const int key0 = (g0 + warp + WARPS * it) << 4;
-      const bool cut = key0 < first_key || key0 + 15 > sq.x;  // a granule cut by the mask
+      const bool cut = key0 < all_lo || key0 + 15 > sq.x;  // a granule cut by a row's mask
 
-      float c[2][4] = {};
+      float c[(NT + 1) / 2][2][4] = {};  // rows g and g + 8 of two row groups
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         const uint32_t kr = ks + (8 * nt + g) * ROW;
@@ -306,57 +328,89 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           if constexpr (FP8) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              nvu::mma_f16(c[nt], qa[4 * i + j][0], 0u, qa[4 * i + j][1], 0u,
-                           e4m3x2_to_f16x2(x[j] & 0xffffu), e4m3x2_to_f16x2(x[j] >> 16));
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t k0 = e4m3x2_to_f16x2(x[j] & 0xffffu), k1 = e4m3x2_to_f16x2(x[j] >> 16);
+#pragma unroll
+              for (int v = 0; v < (NT + 1) / 2; ++v)
+                nvu::mma_f16(c[v][nt], q_frag(v, 4 * i + j, 0, 0), q_frag(v, 4 * i + j, 1, 0),
+                             q_frag(v, 4 * i + j, 0, 1), q_frag(v, 4 * i + j, 1, 1), k0, k1);
+            }
           } else {
-            mma_bf16(c[nt], qa[2 * i][0], 0u, qa[2 * i][1], 0u, w.x, w.y);
-            mma_bf16(c[nt], qa[2 * i + 1][0], 0u, qa[2 * i + 1][1], 0u, w.z, w.w);
+#pragma unroll
+            for (int v = 0; v < (NT + 1) / 2; ++v) {
+              mma_bf16(c[v][nt], q_frag(v, 2 * i, 0, 0), q_frag(v, 2 * i, 1, 0), q_frag(v, 2 * i, 0, 1),
+                       q_frag(v, 2 * i, 1, 1), w.x, w.y);
+              mma_bf16(c[v][nt], q_frag(v, 2 * i + 1, 0, 0), q_frag(v, 2 * i + 1, 1, 0),
+                       q_frag(v, 2 * i + 1, 0, 1), q_frag(v, 2 * i + 1, 1, 1), w.z, w.w);
+            }
           }
         }
       }
-      float p[4];
-      p[0] = fmaf(c[0][0], f, lv);
-      p[1] = fmaf(c[0][1], f, lv);
-      p[2] = fmaf(c[1][0], f, lv);
-      p[3] = fmaf(c[1][1], f, lv);
+      float p[NT][4], mx[NT];
+      bool grows = false;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        const float f = qs[u] * scale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[u][i] = fmaf(c[u >> 1][i >> 1][2 * (u & 1) + (i & 1)], f, lv);
+      }
       uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
       if (cut) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
-          if (key < first_key || key > sq.x) {
-            p[i] = -INFINITY;
-            seen[i] = 0u;  // whatever bits the cache holds there must not meet a zero weight
+          // Whatever bits the cache holds where no row sees must not meet a zero weight.
+          if (key < some_lo || key > pos_last) seen[i] = 0u;
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int pos = sq.x + min((8 * u + g) >> gshift, n_new - 1);
+            if (key > pos || (a.window > 0 && key <= pos - a.window)) p[u][i] = -INFINITY;
           }
         }
       }
-      float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        mx[u] = fmaxf(fmaxf(p[u][0], p[u][1]), fmaxf(p[u][2], p[u][3]));
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+        grows |= mx[u] > m[u] + 8.0f;
+      }
       // The maximum moves only when it grows by more than 2^8 (or from
       // nothing): weights stay below 2^8, and the outputs are rarely scaled.
-      if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
-        const float mn = fmaxf(m, mx);
-        const float r = m > -INFINITY ? ex2(m - mn) : 0.0f;
-        l *= r;
-        m = mn;
-        const float r0 = __shfl_sync(0xffffffffu, r, 8 * t), r1 = __shfl_sync(0xffffffffu, r, 8 * t + 4);
+      if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j][0] *= r0;
-          o[j][1] *= r1;
-          o[j][2] *= r0;
-          o[j][3] *= r1;
+        for (int u = 0; u < NT; ++u) {
+          const float mn = fmaxf(m[u], mx[u]);
+          const float r = m[u] > -INFINITY ? ex2(m[u] - mn) : 0.0f;
+          l[u] *= r;
+          m[u] = mn;
+          const float r0 = __shfl_sync(0xffffffffu, r, 8 * t), r1 = __shfl_sync(0xffffffffu, r, 8 * t + 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[u][j][0] *= r0;
+            o[u][j][1] *= r1;
+            o[u][j][2] *= r0;
+            o[u][j][3] *= r1;
+          }
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m);
-      l = fmaf((p[0] + p[1]) + (p[2] + p[3]), iv, l);
+      for (int u = 0; u < NT; ++u) {
+        // A row that has seen nothing yet, its granule cut for another: weights 0.
+        const float mu = m[u] > -INFINITY ? m[u] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[u][i] = ex2(p[u][i] - mu);
+        l[u] = fmaf((p[u][0] + p[u][1]) + (p[u][2] + p[u][3]), iv, l[u]);
+      }
       // Keys 2t, 2t + 1, 2t + 8, 2t + 9; chunk pi(g) of each.
       const int vc = (g >> 1) | ((g & 1) << 2);
       if constexpr (FP8) {
-        const uint32_t b0 = nvu::f16x2_of(p[0], p[1]), b1 = nvu::f16x2_of(p[2], p[3]);
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          pb[u][0] = nvu::f16x2_of(p[u][0], p[u][1]);
+          pb[u][1] = nvu::f16x2_of(p[u][2], p[u][3]);
+        }
         uint4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -375,14 +429,19 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
         for (int j = 0; j < 8; ++j) {  // elements 16 pi(g) + 2j, + 1
           const uint32_t x = __byte_perm(x0[j >> 1], x1[j >> 1], j & 1 ? 0x7362 : 0x5140);
           const uint32_t y = __byte_perm(y0[j >> 1], y1[j >> 1], j & 1 ? 0x7362 : 0x5140);
-          nvu::mma_f16(o[j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                       e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), b0, b1);
+          const uint32_t a0 = e4m3x2_to_f16x2(x & 0xffffu), a1 = e4m3x2_to_f16x2(x >> 16);
+          const uint32_t a2 = e4m3x2_to_f16x2(y & 0xffffu), a3 = e4m3x2_to_f16x2(y >> 16);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) nvu::mma_f16(o[u][j], a0, a1, a2, a3, pb[u][0], pb[u][1]);
         }
       } else {
         // A weight as a bf16 pair hi + lo: 16 significant bits.
-        uint32_t h0, l0, h1, l1;
-        split_bf2(p[0], p[1], h0, l0);
-        split_bf2(p[2], p[3], h1, l1);
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          split_bf2(p[u][0], p[u][1], ph[u][0], pl[u][0]);
+          split_bf2(p[u][2], p[u][3], ph[u][1], pl[u][1]);
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint4 w[4];
@@ -403,8 +462,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
           for (int j = 0; j < 4; ++j) {  // elements 64 half + 8 pi(g) + 2j, + 1
             const uint32_t a0 = __byte_perm(x0[j], x1[j], 0x5410), a1 = __byte_perm(x0[j], x1[j], 0x7632);
             const uint32_t a2 = __byte_perm(y0[j], y1[j], 0x5410), a3 = __byte_perm(y0[j], y1[j], 0x7632);
-            mma_bf16(o[4 * half + j], a0, a1, a2, a3, h0, h1);
-            mma_bf16(o[4 * half + j], a0, a1, a2, a3, l0, l1);
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+              mma_bf16(o[u][4 * half + j], a0, a1, a2, a3, ph[u][0], ph[u][1]);
+              mma_bf16(o[u][4 * half + j], a0, a1, a2, a3, pl[u][0], pl[u][1]);
+            }
           }
         }
       }
@@ -414,91 +476,114 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
     __syncthreads();  // the rings are done with: their memory takes the results
 
     // ---- the warps' results ---------------------------------------------------
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (t == 0) {
-      s_m[warp * 8 + g] = m;
-      s_l[warp * 8 + g] = l;
+    // Output element e of tile j and lane row g, row 8u + h: at ((16u + 2j + e) * 8 + g) * 8 + h.
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+      if (t == 0) {
+        s_m[warp * ROWS + 8 * u + g] = m[u];
+        s_l[warp * ROWS + 8 * u + g] = l[u];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(s_o + warp * C::O + ((16 * u + 2 * j + e) * 8 + g) * 8 + 2 * t) =
+              make_float2(o[u][j][2 * e], o[u][j][2 * e + 1]);
     }
-    // Output element e of tile j and lane row g, head h at ((2j + e) * 8 + g) * 8 + h.
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float2*>(s_o + warp * DEC_O + ((2 * j + e) * 8 + g) * 8 + 2 * t) =
-            make_float2(o[j][2 * e], o[j][2 * e + 1]);
     __syncthreads();
+    // Factors of n parts and the rows' joint maxima and sums.
+    auto weigh = [&](int n) {
+      for (int i = tid; i < n * ROWS; i += THREADS) {
+        const int r = i % ROWS;
+        float mm = -INFINITY;
+        for (int w = 0; w < n; ++w) mm = fmaxf(mm, s_m[w * ROWS + r]);
+        s_f[i] = s_m[i] > -INFINITY ? ex2(s_m[i] - mm) : 0.0f;
+      }
+      __syncthreads();
+      if (tid < ROWS) {
+        float mm = -INFINITY, ll = 0.0f;
+        for (int w = 0; w < n; ++w) {
+          mm = fmaxf(mm, s_m[w * ROWS + tid]);
+          ll = fmaf(s_l[w * ROWS + tid], s_f[w * ROWS + tid], ll);
+        }
+        s_mm[tid] = mm;
+        s_ll[tid] = ll;
+      }
+      __syncthreads();
+    };
+    // Four rows' values of an element, item i of the layout above.
+    auto rows_of = [&](int i) { return 8 * (i >> 8) + 4 * (i & 1); };
+    auto add = [&](float4& x, const float4& v, int w, int i) {
+      const float4 f = *reinterpret_cast<const float4*>(&s_f[w * ROWS + rows_of(i)]);
+      x.x = fmaf(v.x, f.x, x.x);
+      x.y = fmaf(v.y, f.y, x.y);
+      x.z = fmaf(v.z, f.z, x.z);
+      x.w = fmaf(v.w, f.w, x.w);
+    };
+    // Finished: lanes l and l ^ 16 hold the elements d and d + 1, and take two rows each.
+    auto finish = [&](int i, const float4& x) {
+      const bool e = (i >> 4) & 1;
+      const float y0 = __shfl_xor_sync(0xffffffffu, e ? x.x : x.z, 16);
+      const float y1 = __shfl_xor_sync(0xffffffffu, e ? x.y : x.w, 16);
+      const int gg = (i >> 1) & 7, j = (i >> 5) & 7, pg = (gg >> 1) | ((gg & 1) << 2);
+      const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = rows_of(i) + 2 * e + k, tok = r >> gshift, head = kvh * b.group + (r & (b.group - 1));
+        const float mine = k ? (e ? x.w : x.y) : (e ? x.z : x.x), other = k ? y1 : y0;
+        if (tok < n_new)
+          store2(a, sq.y + tok, head, d, e ? other : mine, e ? mine : other, row_factor(a, head, s_mm[r], s_ll[r]));
+      }
+    };
+    weigh(WARPS);
     int c0, c1;
     const bool whole = !cuts.shared(row0, sq.w, c0, c1);
-    float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0);
-    for (int i = tid; i < 512; i += THREADS) {  // (tile j, lane row, head): elements d, d + 1
-      const int h = i & 7, r = i >> 3, j = r >> 3, gg = r & 7;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w * 8 + h]);
-      float ll = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float mw = s_m[w * 8 + h], f = mw > -INFINITY ? ex2(mw - mm) : 0.0f;
-        const float* src = s_o + w * DEC_O + (16 * j + gg) * 8 + h;
-        ll = fmaf(s_l[w * 8 + h], f, ll);
-        o0 = fmaf(src[0], f, o0);
-        o1 = fmaf(src[64], f, o1);
+    float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0, NT);
+    auto store_ml = [&](float* to) {
+      if (tid < ROWS) {
+        __stcg(to + tid, s_mm[tid]);
+        __stcg(to + ROWS + tid, s_ll[tid]);
       }
-      if (whole) {
-        const int pg = (gg >> 1) | ((gg & 1) << 2);
-        const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
-        if (h < b.group) store2(a, sq.y, kvh * b.group + h, d, o0, o1, row_factor(a, kvh * b.group + h, mm, ll));
-      } else {
-        __stcg(slot + DEC_ML + (16 * j + gg) * 8 + h, o0);
-        __stcg(slot + DEC_ML + (16 * j + gg) * 8 + h + 64, o1);
-        if (r == 0) {
-          __stcg(slot + h, mm);
-          __stcg(slot + 8 + h, ll);
-        }
-      }
+    };
+    for (int i = tid; i < 256 * NT; i += THREADS) {
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) add(x, *reinterpret_cast<const float4*>(s_o + w * C::O + 4 * i), w, i);
+      if (whole)
+        finish(i, x);
+      else
+        __stcg(reinterpret_cast<float4*>(slot + C::ML) + i, x);
     }
     if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t* ticket = ws_tickets(a.ws) + c0;
-        const bool last = atomicAdd(ticket, 1u) == (uint32_t)(c1 - c0);
-        if (last) *ticket = 0u;  // ready for the next call
+      store_ml(slot);
+      for (Join jn(blockIdx.x, c0, c1);; jn.up()) {
         __threadfence();
-        s_last = last;
-      }
-      __syncthreads();
-      if (s_last) {
-        const int segs = c1 - c0 + 1;
-        for (int i = tid; i < segs * 8; i += THREADS) {
-          const float* src = dec_slot(a.ws, c0 + (i >> 3), i < 8);
-          s_jm[i] = __ldcg(src + (i & 7));
-          s_jl[i] = __ldcg(src + 8 + (i & 7));
+        __syncthreads();
+        if (tid == 0) s_last = jn.arrive(a.ws);
+        __syncthreads();
+        if (!s_last) break;
+        for (int i = tid; i < jn.n * ROWS; i += THREADS) {
+          const float* src = dec_slot(a.ws, jn.cta(i / ROWS), jn.begins(i / ROWS), NT);
+          s_m[i] = __ldcg(src + i % ROWS);
+          s_l[i] = __ldcg(src + ROWS + i % ROWS);
         }
         __syncthreads();
-        const int h = tid & 7;
-        float mm = -INFINITY, ll = 0.0f;
-        for (int i = 0; i < segs; ++i) mm = fmaxf(mm, s_jm[i * 8 + h]);
-        for (int i = 0; i < segs; ++i) {
-          const float mw = s_jm[i * 8 + h], f = mw > -INFINITY ? ex2(mw - mm) : 0.0f;
-          ll = fmaf(s_jl[i * 8 + h], f, ll);
+        weigh(jn.n);
+        float* to = dec_slot(a.ws, jn.first, jn.begins(0), NT);
+        for (int i = tid; i < 256 * NT; i += THREADS) {
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll JOIN
+          for (int k = 0; k < jn.n; ++k)
+            add(x, __ldcg(reinterpret_cast<const float4*>(dec_slot(a.ws, jn.cta(k), jn.begins(k), NT) + C::ML) + i), k, i);
+          if (jn.top)
+            finish(i, x);
+          else
+            __stcg(reinterpret_cast<float4*>(to + C::ML) + i, x);
         }
-        for (int i = tid; i < 512; i += THREADS) {
-          const int r = i >> 3, j = r >> 3, gg = r & 7;
-          const int at = DEC_ML + (16 * j + gg) * 8 + h;
-          float o0 = 0.0f, o1 = 0.0f;
-#pragma unroll 8
-          for (int k = 0; k < segs; ++k) {
-            const float* src = dec_slot(a.ws, c0 + k, k == 0) + at;
-            const float mw = s_jm[k * 8 + h], f = mw > -INFINITY ? ex2(mw - mm) : 0.0f;
-            o0 = fmaf(__ldcg(src), f, o0);
-            o1 = fmaf(__ldcg(src + 64), f, o1);
-          }
-          const int pg = (gg >> 1) | ((gg & 1) << 2);
-        const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
-          if (h < b.group) store2(a, sq.y, kvh * b.group + h, d, o0, o1, row_factor(a, kvh * b.group + h, mm, ll));
-        }
+        if (jn.top) break;
+        store_ml(to);
       }
     }
     __syncthreads();  // the shared buffers are free
@@ -506,24 +591,30 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1)
   }
 }
 
-cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
-  static std::atomic<uint64_t> done[2];
-  const int smem = fp8 ? Cfg<true>::SMEM : Cfg<false>::SMEM;
-  const cudaError_t e = fp8 ? set_smem_limit_once(paged_decode_kernel<true>, smem, done[1])
-                            : set_smem_limit_once(paged_decode_kernel<false>, smem, done[0]);
+namespace {
+template <bool FP8, int NT>
+cudaError_t launch(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done;
+  using C = Cfg<FP8, NT>;
+  const cudaError_t e = set_smem_limit_once(paged_decode_kernel<FP8, NT>, C::SMEM, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < MAX_CTAS ? sms : MAX_CTAS, 1, 1);
-  cfg.blockDim = dim3(fp8 ? Cfg<true>::THREADS : Cfg<false>::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return fp8 ? cudaLaunchKernelEx(&cfg, paged_decode_kernel<true>, a)
-             : cudaLaunchKernelEx(&cfg, paged_decode_kernel<false>, a);
+  return cudaLaunchKernelEx(&cfg, paged_decode_kernel<FP8, NT>, a);
+}
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
+  if (a.b.max_q * a.b.group <= 8) return fp8 ? launch<true, 1>(a, sms, stream) : launch<false, 1>(a, sms, stream);
+  return fp8 ? launch<true, 2>(a, sms, stream) : launch<false, 2>(a, sms, stream);
 }
 
 size_t paged_attn_workspace_bytes() { return attn_ws_bytes(); }

@@ -621,16 +621,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       // out two at a time, whole lines instead of 16 bytes of 32 rows.
       // (A split item's two halves of the columns share A's: B's may hold keys.)
       const uint32_t stage = q_smem + (p.split ? 0 : x * OPER);
-      auto put = [&](int c, const float* o, float f) {  // 8 columns
-        sts128(stage + row_chunk(r, c), pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
+      auto put = [&](int row, int c, const float* o, float f) {  // 8 columns
+        sts128(stage + row_chunk(row, c), pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
                pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
       };
-      auto send = [&](int chunks, int first) {  // `chunks` (16 or 8) of the rows' chunks
+      auto send = [&](int row, int chunks, int first) {  // `chunks` (a power of two) of 32 rows' chunks
         __syncwarp();
         const int per = 32 / chunks, c = first + (lane & (chunks - 1));
 #pragma unroll 4
         for (int i = 0; i < 32; i += per) {
-          const int rr = 32 * (warp & 3) + i + lane / chunks;
+          const int rr = row + i + lane / chunks;
           const int tk = (rr >> gshift) + (p.split ? 0 : x * tile_toks);
           uint4 w;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -650,13 +650,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::ld32(o_tm + 32 * c, v);
           tc::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put(4 * c + i, reinterpret_cast<const float*>(v) + 8 * i, inv);
+          for (int i = 0; i < 4; ++i) put(r, 4 * c + i, reinterpret_cast<const float*>(v) + 8 * i, inv);
         }
-        send(16, 0);
+        send(r & ~31, 16, 0);
         continue;
       }
-      // Partial: maxima, sums and unscaled outputs of this tile, [4 columns][row].
-      {
+      // Partial: maxima, sums and unscaled outputs of this tile, [4 columns][row],
+      // of the warps that have a row.
+      if (__any_sync(0xffffffffu, tok < p.tokens)) {
         float* slot = pr_slot(a.ws, blockIdx.x, whole || (int)blockIdx.x == c0, x);
         __stcg(slot + r, m);
         __stcg(slot + TILE + r, any ? l : 0.0f);
@@ -673,66 +674,80 @@ __global__ void __launch_bounds__(THREADS, 1)
                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
       }
-      __threadfence();
-      named_sync(1, 256);
-      if (!whole) {
-        if (tid == 0) {
-          uint32_t* ticket = ws_tickets(a.ws) + c0;
-          const bool last = atomicAdd(ticket, 1u) == (uint32_t)(c1 - c0);
-          if (last) *ticket = 0u;  // ready for the next call
-          __threadfence();
-          sh.last = last;
-        }
+      // Join, in the order of the keys: a pair's warps have their own rows; a split
+      // tile's 32-row blocks (a power of two of them) are shared by all eight warps,
+      // a part of the columns each.
+      const int rows = p.tokens << gshift;
+      const int blocks = !p.split ? 8 : rows <= 32 ? 1 : rows <= 64 ? 2 : 4, share = 4 * blocks;
+      const int row = !p.split ? r : 32 * (warp & (blocks - 1)) + lane, col = (warp / blocks) * share;  // of 32
+      const int h0 = p.split ? 0 : x, row_tok = (row >> gshift) + h0 * tile_toks;
+      const int row_head = p.kvh * b.group + (row & (b.group - 1));
+      int halves = p.split ? 2 : 1;
+      Join jn(blockIdx.x, whole ? (int)blockIdx.x : c0, whole ? (int)blockIdx.x : c1);
+      for (;; jn.up(), halves = 1) {
+        __threadfence();
         named_sync(1, 256);
-        const bool last = sh.last != 0;
-        named_sync(1, 256);  // sh.last is read before the next item sets it
-        if (!last) continue;
-      }
-      // Join, in the order of the keys' shares: a pair's tile each (64 columns at
-      // a time); of a split tile the two halves of the columns.
-      const int halves = p.split ? 2 : 1, parts = (whole ? 1 : c1 - c0 + 1) * halves;
-      auto slot_of = [&](int q) {
-        const int k = p.split ? q >> 1 : q, h = p.split ? q & 1 : x;
-        return pr_slot(a.ws, whole ? blockIdx.x : c0 + k, whole || k == 0, h);
-      };
-      float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-      for (int q = 0; q < parts; ++q) mm = fmaxf(mm, __ldcg(slot_of(q) + r));
-#pragma unroll 4
-      for (int q = 0; q < parts; ++q) {
-        const float* s = slot_of(q);
-        const float mk = __ldcg(s + r), lk = __ldcg(s + TILE + r);
-        ll = fmaf(lk, mk > -INFINITY ? ex2(mk - mm) : 0.0f, ll);
-      }
-      const float inv = row_factor(a, head, mm, ll);
-#pragma unroll 1
-      for (int c = p.split ? x : 0; c < (p.split ? x + 1 : 2); ++c) {
-        float o[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
-#pragma unroll 1
-        for (int q = 0; q < parts; ++q) {
-          const float* s = slot_of(q);
-          const float4* o4 = reinterpret_cast<const float4*>(s + 2 * TILE) + 16 * c * TILE + r;
-          float4 w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = __ldcg(o4 + i * TILE);
-          const float mk = __ldcg(s + r), f = mk > -INFINITY ? ex2(mk - mm) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            o[4 * i] = fmaf(w[i].x, f, o[4 * i]);
-            o[4 * i + 1] = fmaf(w[i].y, f, o[4 * i + 1]);
-            o[4 * i + 2] = fmaf(w[i].z, f, o[4 * i + 2]);
-            o[4 * i + 3] = fmaf(w[i].w, f, o[4 * i + 3]);
-          }
+        if (!whole) {
+          if (tid == 0) sh.last = jn.arrive(a.ws);
+          named_sync(1, 256);
+          const bool last = sh.last != 0;
+          named_sync(1, 256);  // sh.last is read before it is set again
+          if (!last) break;
         }
+        const int parts = jn.n * halves;
+        auto slot_of = [&](int q) {
+          const int k = halves == 2 ? q >> 1 : q, h = halves == 2 ? q & 1 : h0;
+          return pr_slot(a.ws, jn.cta(k), jn.begins(k), h);
+        };
+        float* to = slot_of(0);
+        const bool live = __any_sync(0xffffffffu, row_tok < p.tokens);
+        float mm = -INFINITY, ll = 0.0f;
+        if (live) {
+#pragma unroll 4
+          for (int q = 0; q < parts; ++q) mm = fmaxf(mm, __ldcg(slot_of(q) + row));
+#pragma unroll 4
+          for (int q = 0; q < parts; ++q) {
+            const float* s = slot_of(q);
+            const float mk = __ldcg(s + row), lk = __ldcg(s + TILE + row);
+            ll = fmaf(lk, mk > -INFINITY ? ex2(mk - mm) : 0.0f, ll);
+          }
+          const float inv = row_factor(a, row_head, mm, ll);
+#pragma unroll 1
+          for (int c = col; c < col + share; c += 4) {  // 16 columns at a time
+            float o[16] = {};
+#pragma unroll 4
+            for (int q = 0; q < parts; ++q) {
+              const float* s = slot_of(q);
+              const float4* o4 = reinterpret_cast<const float4*>(s + 2 * TILE) + c * TILE + row;
+              const float mk = __ldcg(s + row), f = mk > -INFINITY ? ex2(mk - mm) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) put(8 * c + i, o + 8 * i, inv);
+              for (int i = 0; i < 4; ++i) {
+                const float4 w = __ldcg(o4 + i * TILE);
+                o[4 * i] = fmaf(w.x, f, o[4 * i]);
+                o[4 * i + 1] = fmaf(w.y, f, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(w.z, f, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(w.w, f, o[4 * i + 3]);
+              }
+            }
+            if (jn.top) {
+              put(row, c >> 1, o, inv);
+              put(row, (c >> 1) + 1, o + 8, inv);
+            } else {  // in place: no other thread reads these
+              float4* o4 = reinterpret_cast<float4*>(to + 2 * TILE) + c * TILE + row;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                __stcg(o4 + i * TILE, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+            }
+          }
+          if (jn.top) send(row & ~31, share >> 1, col >> 1);
+        }
+        if (jn.top) break;
+        named_sync(1, 256);  // the maxima and sums have been read
+        if (live && col == 0) {
+          __stcg(to + row, mm);
+          __stcg(to + TILE + row, ll);
+        }
       }
-      if (p.split)
-        send(8, 8 * x);
-      else
-        send(16, 0);
       // Slots that a later item of this CTA writes are read by now.
       named_sync(1, 256);
     }

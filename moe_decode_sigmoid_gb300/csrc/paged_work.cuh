@@ -10,11 +10,11 @@ namespace pg {
 
 constexpr int MAX_CTAS = 160;  // CTAs of an attention launch (one per SM; GB300 has 152)
 
-// Workspace: a ticket per CTA and an error word, then two slots per CTA: one
+// Workspace: three tickets per CTA and an error word, then two slots per CTA: one
 // for a row (or item) that began in an earlier CTA's share and one for one that
 // goes on in the next one's.
 constexpr size_t WS_HEAD = 4096, WS_ERROR = WS_HEAD - 4;
-static_assert(MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
+static_assert(3 * MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
 
 // The cut.  A row (next tokens: a sequence and KV head; prompts: an item, a tile
 // pair and KV head) weighs its key granules (tiles) and what it costs besides,
@@ -48,7 +48,8 @@ struct Cut {
   }
 };
 
-// A slot of the next-token kernel: 8 maxima, 8 sums, 128 x 8 outputs.
+// A slot of the next-token kernel, for each group of 8 rows (DEC_ROWS at most): 8
+// maxima, 8 sums, 128 x 8 outputs.
 constexpr int DEC_ML = 16, DEC_O = HD * 8, DEC_SLOT = DEC_ML + DEC_O;
 using DecCut = Cut<16, 64, 32>;
 
@@ -56,18 +57,51 @@ using DecCut = Cut<16, 64, 32>;
 // outputs.
 constexpr int PR_TILE = 128 * (2 + HD), PR_SLOT = 2 * PR_TILE;
 using PrCut = Cut<3, 6, 3>;
+static_assert(DEC_ROWS / 8 * DEC_SLOT <= PR_SLOT, "a workspace for either");
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
   return WS_HEAD + sizeof(float) * 2 * MAX_CTAS * (size_t)PR_SLOT;
 }
 
-__device__ __forceinline__ uint32_t* ws_tickets(void* ws) { return static_cast<uint32_t*>(ws); }
+// The join of the partial results of the CTAs c0 .. c1 that share a row, always in
+// the order of its keys: groups of JOIN neighbours first, each by the one of them
+// that arrives last, then the groups' results, by the group that arrives last.
+// (All of 38 by one CTA: its reads alone took 17 us for 32 rows of 1 x 30K tokens.)
+constexpr int JOIN = 8, JOIN_MOST = (MAX_CTAS + JOIN - 1) / JOIN;
+struct Join {
+  int c0, c1, first, n, stride, kind;
+  bool top;  // what this join makes is the row's result
+  __device__ __forceinline__ Join(int cta, int c0, int c1)
+      : c0(c0), c1(c1), first(c0 + (cta - c0) / JOIN * JOIN), stride(1) {
+    n = min(JOIN, c1 - first + 1);
+    top = c1 - c0 < JOIN;
+    // A CTA may be the first of a row and of a later group of the row before.
+    kind = top ? 0 : first == c0 ? 1 : 2;
+  }
+  __device__ __forceinline__ void up() {
+    first = c0;
+    n = (c1 - c0) / JOIN + 1;
+    stride = JOIN;
+    kind = 0;
+    top = true;
+  }
+  __device__ __forceinline__ int cta(int k) const { return first + k * stride; }
+  __device__ __forceinline__ bool begins(int k) const { return cta(k) == c0; }
+  // One thread of the CTA, all of its results written before: is it the last?
+  __device__ __forceinline__ bool arrive(void* ws) const {
+    uint32_t* ticket = static_cast<uint32_t*>(ws) + kind * MAX_CTAS + first;
+    const bool last = atomicAdd(ticket, 1u) == (uint32_t)(n - 1);
+    if (last) *ticket = 0u;  // ready for the next call
+    __threadfence();
+    return last;
+  }
+};
 __device__ __forceinline__ void ws_error(void* ws) {
   atomicCAS(reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + WS_ERROR), DEV_OK, DEV_TIMEOUT);
 }
-__device__ __forceinline__ float* dec_slot(void* ws, int cta, bool begins) {
+__device__ __forceinline__ float* dec_slot(void* ws, int cta, bool begins, int groups) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEAD) +
-         (size_t)(2 * cta + (begins ? 1 : 0)) * DEC_SLOT;
+         (size_t)(2 * cta + (begins ? 1 : 0)) * groups * DEC_SLOT;
 }
 __device__ __forceinline__ float* pr_slot(void* ws, int cta, bool begins, int tile) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEAD) +
