@@ -84,6 +84,10 @@ __device__ __forceinline__ void store2(const PagedAttnArgs& a, int row, int head
 // the four of the values, fall into distinct banks.
 __device__ __forceinline__ int mix(int r) { return ((r & 1) << 2) | ((r >> 1) & 3); }
 
+// The maximum of a row that has seen no key: finite, so that a masked score,
+// -infinity, has the weight 0 against it too.
+constexpr float LOWEST = -3.402823466e38f;
+
 // Where the warp's granules lie: lane l holds granule 32 * batch + l.
 struct Batch {
   int row;        // cache row of its first key; -1: its page is not there
@@ -183,14 +187,12 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     cuts.part(cur, end, row0, sq.w, off, to);
     const int n = to - off;                    // granules of this segment
     const int g0 = sq.z + off;                 // the first of them
-    // Row r is token r / group, head r % group; the keys that all rows see and
-    // that some row does.
-    const int n_new = s_new[s], pos_last = sq.x + n_new - 1;
-    const int some_lo = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
-    const int all_lo = a.window > 0 ? max(0, pos_last - a.window + 1) : 0;
+    // Row r is token r / group, head r % group; the first key that all rows see.
+    const int all_lo = a.window > 0 ? max(0, sq.x + s_new[s] - a.window) : 0;
 
     // The queries' words, to arrive while the granules are looked up.
     uint4 qw[NT][4];
+    const int n_new = s_new[s];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int r = 8 * u + g, tok = r >> gshift;
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[u][j][i] = 0.0f;
-      m[u] = -INFINITY;
+      m[u] = LOWEST;
       l[u] = 0.0f;
     }
 
@@ -356,6 +358,8 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       }
       uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
       if (cut) {
+        const int n_new = s_new[s], pos_last = sq.x + n_new - 1;
+        const int some_lo = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
@@ -380,8 +384,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-          const float mn = fmaxf(m[u], mx[u]);
-          const float r = m[u] > -INFINITY ? ex2(m[u] - mn) : 0.0f;
+          const float mn = fmaxf(m[u], mx[u]), r = ex2(m[u] - mn);
           l[u] *= r;
           m[u] = mn;
           const float r0 = __shfl_sync(0xffffffffu, r, 8 * t), r1 = __shfl_sync(0xffffffffu, r, 8 * t + 4);
@@ -396,10 +399,8 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       }
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        // A row that has seen nothing yet, its granule cut for another: weights 0.
-        const float mu = m[u] > -INFINITY ? m[u] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[u][i] = ex2(p[u][i] - mu);
+        for (int i = 0; i < 4; ++i) p[u][i] = ex2(p[u][i] - m[u]);
         l[u] = fmaf((p[u][0] + p[u][1]) + (p[u][2] + p[u][3]), iv, l[u]);
       }
       // Keys 2t, 2t + 1, 2t + 8, 2t + 9; chunk pi(g) of each.
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
       l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
       if (t == 0) {
-        s_m[warp * ROWS + 8 * u + g] = m[u];
+        s_m[warp * ROWS + 8 * u + g] = m[u] > LOWEST ? m[u] : -INFINITY;
         s_l[warp * ROWS + 8 * u + g] = l[u];
       }
 #pragma unroll
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       for (int k = 0; k < 2; ++k) {
         const int r = rows_of(i) + 2 * e + k, tok = r >> gshift, head = kvh * b.group + (r & (b.group - 1));
         const float mine = k ? (e ? x.w : x.y) : (e ? x.z : x.x), other = k ? y1 : y0;
-        if (tok < n_new)
+        if (tok < s_new[s])
           store2(a, sq.y + tok, head, d, e ? other : mine, e ? mine : other, row_factor(a, head, s_mm[r], s_ll[r]));
       }
     };
