@@ -42,14 +42,19 @@ using namespace pg;
 // NT: groups of 8 rows.
 template <bool FP8, int NT>
 struct Cfg {
-  static constexpr int WARPS = FP8 && NT == 1 ? 16 : 8;
-  static constexpr int SLOTS = FP8 && NT > 1 ? 6 : 3;  // granules of a warp's ring
+  // (E4M3, 32 x 100K: 16 warps of 3 slots 355 us, 12 of 4 342, 8 of 6 416: what a
+  // warp holds in registers against warps that hide each other's latency.)
+  static constexpr int WARPS = FP8 && NT == 1 ? 12 : 8;
+  static constexpr int SLOTS = FP8 ? (NT > 1 ? 6 : 4) : 3;  // granules of a warp's ring
   static constexpr int THREADS = WARPS * 32;
   static constexpr int ROW = FP8 ? HD : 2 * HD;      // bytes of a head's key
   static constexpr int SLOT = 2 * BLOCK * ROW;       // bytes of a granule: keys, then values
-  static constexpr int SMEM = WARPS * SLOTS * SLOT;  // the warps' results reuse it
+  static constexpr int SMEM = WARPS * SLOTS * SLOT;
   static constexpr int O = NT * DEC_O, ML = NT * DEC_ML;  // floats of a warp's outputs, of maxima and sums
-  static_assert(SMEM >= WARPS * O * 4, "the warps' outputs fit");
+  // A warp's outputs take the last slots of its ring; the others' granules of the
+  // next segment are on their way by then.
+  static constexpr int PRE = SLOTS - (O * 4 + SLOT - 1) / SLOT;
+  static_assert(PRE >= 1 && PRE < SLOTS, "room for both");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
@@ -94,15 +99,23 @@ struct Batch {
   float ks, vs;   // E4M3: scales of its keys and values
 };
 
+// A share's part of a row.
+struct Segment {
+  int seq, kvh, row0;  // where the whole row begins
+  int n, g0;           // granules, the first of them
+  int next;            // where the share goes on
+};
+
 }  // namespace
 
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
   using C = Cfg<FP8, NT>;
+  using Cuts = DecCut<FP8>;
   constexpr int WARPS = C::WARPS, THREADS = C::THREADS, SLOTS = C::SLOTS;
   constexpr int ROW = C::ROW, SLOT = C::SLOT, ROWS = 8 * NT;
-  extern __shared__ __align__(128) float s_o[];  // the rings; then [WARPS][O]
+  extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_pre[MAX_SEQS + 1];            // weight (of all heads) before each sequence
   __shared__ int4 s_seq[MAX_SEQS];               // {position, row, first granule, granules}
   __shared__ int s_scan[MAX_SEQS / 32];
@@ -129,7 +142,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       const int lo = a.window > 0 ? max(0, q.first - a.window + 1) : 0;
       if (q.n > 0) {
         info = make_int4(q.first, q.q0, lo >> 4, q.len > 0 ? ((q.len - 1) >> 4) + 1 - (lo >> 4) : 0);
-        cnt = DecCut::weight(info.w) * b.nkv;
+        cnt = Cuts::weight(info.w) * b.nkv;
       }
       s_seq[tid] = info;
       s_new[tid] = rows = q.n;
@@ -151,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     if (w == warp) pre += total;
     total += s_scan[w];
   }
-  const DecCut cuts(total, gridDim.x);
+  const Cuts cuts(total, gridDim.x);
   if (tid < MAX_SEQS && tid < b.n_seqs) {
     s_pre[tid + 1] = pre + cnt;
     if (tid == 0) s_pre[0] = 0;
@@ -170,34 +183,75 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     }
   }
   __syncthreads();
-  int cur = s_cut[0];
+  const int cur = s_cut[0];
   const int end = s_cut[1] < 0 ? total : s_cut[1];
   if (cur < 0 || cur >= end) return;
-  int s = s_first;
 
   const size_t tok_bytes = (size_t)b.nkv * ROW;  // one token row of a cache
-  const uint32_t ring = smem_addr(s_o) + warp * SLOTS * SLOT;
+  const uint32_t ring = smem_addr(s_ring) + warp * SLOTS * SLOT;
+  auto outputs = [&](int w) {  // of warp w
+    return reinterpret_cast<float*>(s_ring + (w * SLOTS + C::PRE) * SLOT);
+  };
 
-  while (cur < end) {
+  auto segment = [&](int cur, int s) {
     while (cur >= s_pre[s + 1]) ++s;
     const int4 sq = s_seq[s];
-    const int weight = DecCut::weight(sq.w), kvh = (cur - s_pre[s]) / weight;
+    const int weight = Cuts::weight(sq.w), kvh = (cur - s_pre[s]) / weight;
     const int row0 = s_pre[s] + kvh * weight;
     int off, to;
     cuts.part(cur, end, row0, sq.w, off, to);
-    const int n = to - off;                    // granules of this segment
-    const int g0 = sq.z + off;                 // the first of them
-    // Row r is token r / group, head r % group; the first key that all rows see.
-    const int all_lo = a.window > 0 ? max(0, sq.x + s_new[s] - a.window) : 0;
-
-    // The queries' words, to arrive while the granules are looked up.
-    uint4 qw[NT][4];
-    const int n_new = s_new[s];
+    return Segment{s, kvh, row0, to - off, sq.z + off, min(end, row0 + weight)};
+  };
+  uint4 qw[NT][4];
+  Batch now{-1, 0.0f, 0.0f}, old{-1, 0.0f, 0.0f};
+  auto mine_of = [&](const Segment& sg) { return sg.n > warp ? (sg.n - warp + WARPS - 1) / WARPS : 0; };
+  // (Looked up a batch ahead, 8 and 16 granules before its use, the long E4M3 cases
+  // took 8 % longer: registers and branches in the loop.)
+  auto look_up = [&](const Segment& sg, int batch) {
+    const int i = warp + WARPS * (32 * batch + lane);
+    old = now;
+    now.row = -1;
+    if (i < sg.n) {
+      now.row = cache_row(b, sg.seq, (sg.g0 + i) << 4);
+      if (FP8 && now.row >= 0) {
+        const size_t at = (size_t)(now.row >> 4) * b.nkv + sg.kvh;
+        now.ks = __ldg(a.k_scale + at);
+        now.vs = __ldg(a.v_scale + at);
+      }
+    }
+  };
+  // Granule i of the warp on its way into slot i % SLOTS.
+  const int cr = FP8 ? lane >> 3 : lane >> 4, cc = FP8 ? lane & 7 : lane & 15;
+  const size_t src0 = (size_t)cr * tok_bytes + 16 * cc;
+  auto issue = [&](const Segment& sg, int i) {
+    if (i < mine_of(sg)) {
+      if ((i & 31) == 0) look_up(sg, i >> 5);
+      const int row = __shfl_sync(0xffffffffu, now.row, i & 31);
+      if (row >= 0) {
+        constexpr int STEP = FP8 ? 4 : 2;  // rows a warp copies at a time
+        const size_t at = (size_t)row * tok_bytes + (size_t)sg.kvh * ROW + src0;
+        const uint8_t* k = static_cast<const uint8_t*>(a.k_cache) + at;
+        const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
+        const uint32_t dst = ring + (i % SLOTS) * SLOT + cr * ROW;
+#pragma unroll
+        for (int j = 0; j < BLOCK / STEP; ++j) {
+          const int c = cc ^ mix(cr + STEP * j);
+          cp_async16(dst + j * STEP * ROW + 16 * c, k + (size_t)(STEP * j) * tok_bytes);
+          cp_async16(dst + BLOCK * ROW + j * STEP * ROW + 16 * c, v + (size_t)(STEP * j) * tok_bytes);
+        }
+      }
+    }
+    cp_commit();
+  };
+  // The queries' words, to arrive while the granules are looked up, and the first
+  // granules.  Row r is token r / group, head r % group.
+  auto begin = [&](const Segment& sg) {
+    const int n_new = s_new[sg.seq], row = s_seq[sg.seq].y;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int r = 8 * u + g, tok = r >> gshift;
       const uint8_t* src = reinterpret_cast<const uint8_t*>(
-          a.q + ((size_t)(sq.y + tok) * nq + kvh * b.group + (r & (b.group - 1))) * HD);
+          a.q + ((size_t)(row + tok) * nq + sg.kvh * b.group + (r & (b.group - 1))) * HD);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // E4M3: elements 16t .. 16t + 15 and 64 + 16t ..; bf16: 32i + 8t .. + 7
@@ -205,47 +259,18 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         qw[u][i] = tok < n_new ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
+#pragma unroll 1
+    for (int i = 0; i < C::PRE; ++i) issue(sg, i);
+  };
 
-    const int mine_n = n > warp ? (n - warp + WARPS - 1) / WARPS : 0;
-    Batch now{-1, 0.0f, 0.0f}, old{-1, 0.0f, 0.0f};
-    auto look_up = [&](int batch) {
-      const int i = warp + WARPS * (32 * batch + lane);
-      old = now;
-      now.row = -1;
-      if (i < n) {
-        now.row = cache_row(b, s, (g0 + i) << 4);
-        if (FP8 && now.row >= 0) {
-          const size_t at = (size_t)(now.row >> 4) * b.nkv + kvh;
-          now.ks = __ldg(a.k_scale + at);
-          now.vs = __ldg(a.v_scale + at);
-        }
-      }
-    };
-    // Granule i of the warp on its way into slot i % SLOTS.
-    const int cr = FP8 ? lane >> 3 : lane >> 4, cc = FP8 ? lane & 7 : lane & 15;
-    const size_t src0 = (size_t)cr * tok_bytes + (size_t)kvh * ROW + 16 * cc;
-    auto issue = [&](int i) {
-      if (i < mine_n) {
-        if ((i & 31) == 0) look_up(i >> 5);
-        const int row = __shfl_sync(0xffffffffu, now.row, i & 31);
-        if (row >= 0) {
-          constexpr int STEP = FP8 ? 4 : 2;  // rows a warp copies at a time
-          const size_t at = (size_t)row * tok_bytes + src0;
-          const uint8_t* k = static_cast<const uint8_t*>(a.k_cache) + at;
-          const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
-          const uint32_t dst = ring + (i % SLOTS) * SLOT + cr * ROW;
-#pragma unroll
-          for (int j = 0; j < BLOCK / STEP; ++j) {
-            const int c = cc ^ mix(cr + STEP * j);
-            cp_async16(dst + j * STEP * ROW + 16 * c, k + (size_t)(STEP * j) * tok_bytes);
-            cp_async16(dst + BLOCK * ROW + j * STEP * ROW + 16 * c, v + (size_t)(STEP * j) * tok_bytes);
-          }
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) issue(i);
+  Segment sg = segment(cur, s_first);
+  begin(sg);
+  for (;;) {
+    const int4 sq = s_seq[sg.seq];
+    const int mine_n = mine_of(sg);
+    const int all_lo = a.window > 0 ? max(0, sq.x + s_new[sg.seq] - a.window) : 0;  // first key that all rows see
+#pragma unroll 1
+    for (int i = C::PRE; i < SLOTS - 1; ++i) issue(sg, i);
 
     // ---- the group's queries as A fragments -----------------------------------
     // E4M3: f16, each head scaled by a power of two so that its largest element
@@ -300,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     }
 
     for (int it = 0; it < mine_n; ++it) {
-      issue(it + SLOTS - 1);
+      issue(sg, it + SLOTS - 1);
       cp_wait<SLOTS - 1>();
       __syncwarp();  // the other lanes' copies of granule `it` too
       // The batch of granule `it`: the issue may already be in the next one.
@@ -317,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         iv = 1.0f / vs;
       }
       const uint32_t ks = ring + (it % SLOTS) * SLOT, vsm = ks + BLOCK * ROW;
-      const int key0 = (g0 + warp + WARPS * it) << 4;
+      const int key0 = (sg.g0 + warp + WARPS * it) << 4;
       const bool cut = key0 < all_lo || key0 + 15 > sq.x;  // a granule cut by a row's mask
 
       float c[(NT + 1) / 2][2][4] = {};  // rows g and g + 8 of two row groups
@@ -358,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       }
       uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
       if (cut) {
-        const int n_new = s_new[s], pos_last = sq.x + n_new - 1;
+        const int n_new = s_new[sg.seq], pos_last = sq.x + n_new - 1;
         const int some_lo = a.window > 0 ? max(0, sq.x - a.window + 1) : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -474,7 +499,6 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       __syncwarp();  // the slot is free for granule it + SLOTS
     }
     cp_wait<0>();
-    __syncthreads();  // the rings are done with: their memory takes the results
 
     // ---- the warps' results ---------------------------------------------------
     // Output element e of tile j and lane row g, row 8u + h: at ((16u + 2j + e) * 8 + g) * 8 + h.
@@ -490,8 +514,15 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float2*>(s_o + warp * C::O + ((16 * u + 2 * j + e) * 8 + g) * 8 + 2 * t) =
+          *reinterpret_cast<float2*>(outputs(warp) + ((16 * u + 2 * j + e) * 8 + g) * 8 + 2 * t) =
               make_float2(o[u][j][2 * e], o[u][j][2 * e + 1]);
+    }
+    // The next segment's first granules travel while this one's results are joined.
+    const bool more = sg.next < end;
+    Segment following = sg;
+    if (more) {
+      following = segment(sg.next, sg.seq);
+      begin(following);
     }
     __syncthreads();
     // Factors of n parts and the rows' joint maxima and sums.
@@ -532,15 +563,15 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       const int d = FP8 ? 16 * pg + 2 * j : 64 * (j >> 2) + 8 * pg + 2 * (j & 3);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = rows_of(i) + 2 * e + k, tok = r >> gshift, head = kvh * b.group + (r & (b.group - 1));
+        const int r = rows_of(i) + 2 * e + k, tok = r >> gshift, head = sg.kvh * b.group + (r & (b.group - 1));
         const float mine = k ? (e ? x.w : x.y) : (e ? x.z : x.x), other = k ? y1 : y0;
-        if (tok < s_new[s])
+        if (tok < s_new[sg.seq])
           store2(a, sq.y + tok, head, d, e ? other : mine, e ? mine : other, row_factor(a, head, s_mm[r], s_ll[r]));
       }
     };
     weigh(WARPS);
     int c0, c1;
-    const bool whole = !cuts.shared(row0, sq.w, c0, c1);
+    const bool whole = !cuts.shared(sg.row0, sq.w, c0, c1);
     float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0, NT);
     auto store_ml = [&](float* to) {
       if (tid < ROWS) {
@@ -551,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     for (int i = tid; i < 256 * NT; i += THREADS) {
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) add(x, *reinterpret_cast<const float4*>(s_o + w * C::O + 4 * i), w, i);
+      for (int w = 0; w < WARPS; ++w) add(x, *reinterpret_cast<const float4*>(outputs(w) + 4 * i), w, i);
       if (whole)
         finish(i, x);
       else
@@ -587,8 +618,9 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         store_ml(to);
       }
     }
+    if (!more) break;
     __syncthreads();  // the shared buffers are free
-    cur = min(end, row0 + weight);
+    sg = following;
   }
 }
 

@@ -51,7 +51,8 @@ struct Cut {
 // A slot of the next-token kernel, for each group of 8 rows (DEC_ROWS at most): 8
 // maxima, 8 sums, 128 x 8 outputs.
 constexpr int DEC_ML = 16, DEC_O = HD * 8, DEC_SLOT = DEC_ML + DEC_O;
-using DecCut = Cut<16, 64, 32>;
+template <bool FP8>
+using DecCut = Cut<FP8 ? 64 : 40, 64, 32>;
 
 // A slot of the prompt kernel: two tiles of 128 maxima, 128 sums and 128 x 128
 // outputs.
