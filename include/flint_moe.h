@@ -362,7 +362,8 @@ flint_status flint_qk_norm_rope_kv_bf16(const flint_attn_dims* dims, int32_t bat
  * the call's kernels run.
  *   n_seqs     sequences, 1 .. FLINT_PAGED_MAX_SEQS
  *   max_q_len  >= 1: an upper bound of the new tokens of any one sequence.  It
- *              chooses the attention kernel (1: next tokens; more: drafts and
+ *              chooses the attention kernel (up to 16 query rows a KV head, i.e.
+ *              max_q_len * nq / nkv <= 16: next tokens and short drafts; more:
  *              prompts); the appends ignore it
  *   page_size  tokens per page: a power of two, 16 .. 1024
  *   max_pages  columns of page_table (>= 1; max_pages * page_size <= 2^23)
@@ -451,18 +452,23 @@ flint_status flint_attn_get_device_status(const void* workspace, cudaStream_t st
  *   softmax_scale >= 0, finite; window >= 0
  *   out_bf16 [n_tokens, nq, D]
  *   workspace (16-byte aligned) as flint_attn_workspace_bytes says
- * Cache rows that no new row of a call may see do not matter, whatever bits
- * they hold.  Scores, the running maximum, sums and outputs are fp32; each
- * output is rounded to bf16 once.  Results do not depend on timing: the same
- * call gives the same bits.  Errors as the appends', and FLINT_ERR_WORKSPACE
- * for a NULL, misaligned or too small workspace. */
+ * Cache rows that no new row of a sequence may see do not matter, whatever bits
+ * they hold; an infinity or NaN in a value that one of its new rows sees may
+ * reach its other new rows of the same call.  Scores, the running maximum, sums
+ * and outputs are fp32; each output is rounded to bf16 once.  A weight e_j meets
+ * V with 16 significant bits (up to 16 query rows a KV head) or 8 (prompts).
+ * Results do not depend on timing: the same call gives the same bits.  Errors as
+ * the appends', and FLINT_ERR_WORKSPACE for a NULL, misaligned or too small
+ * workspace. */
 flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_paged_batch* batch,
                                    int32_t n_tokens, const void* q_bf16, const void* k_cache_bf16,
                                    const void* v_cache_bf16, const float* sinks,
                                    float softmax_scale, int32_t window, void* out_bf16,
                                    void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* The same over an E4M3 cache with its scales. */
+/* The same over an E4M3 cache with its scales.  A weight meets the codes with 11
+ * significant bits, and no finer than 2^-24 of the row's largest weight times
+ * scale; over prompts a query's elements count to 2^-18 of its largest. */
 flint_status flint_attn_paged_fp8(const flint_attn_dims* dims, const flint_paged_batch* batch,
                                   int32_t n_tokens, const void* q_bf16,
                                   const uint8_t* k_cache_e4m3, const uint8_t* v_cache_e4m3,

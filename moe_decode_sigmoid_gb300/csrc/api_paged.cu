@@ -2,6 +2,8 @@
 // append with Q/K norm and rotary embedding, and the attention over the cache.
 // Host-side argument checks, argument blocks and launches; nothing here
 // allocates, and only flint_attn_get_device_status synchronises.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "flint_moe.h"
@@ -155,8 +157,10 @@ flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.sinks = sinks;
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.window = window;
+  a.scale_log2 = std::fmin(softmax_scale * 1.4426950408889634f, FLT_MAX);
+  // Positions lie within -MAX_TOKENS .. MAX_LENGTH: a wider window sees no more,
+  // and position - window stays within 32 bits.
+  a.window = (int)std::min<long long>(window, 2 * MAX_LENGTH);
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
   return cuda_status(a.b.max_q * a.b.group <= pg::DEC_ROWS ? launch_paged_decode(a, fp8, sms, stream)

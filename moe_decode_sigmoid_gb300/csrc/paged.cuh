@@ -54,11 +54,5 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h2) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 }  // namespace pg
 }  // namespace flint

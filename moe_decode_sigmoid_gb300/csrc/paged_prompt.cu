@@ -118,6 +118,19 @@ __device__ __forceinline__ float max3(A a, B b, C c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(as_f(a)), "f"(as_f(b)), "f"(as_f(c)));
   return r;
 }
+// The same, and pair(), of registers that a TMEM load filled: volatile, so that
+// they stay behind the wait for it.
+template <class A, class B, class C>
+__device__ __forceinline__ float max3_tm(A a, B b, C c) {
+  float r;
+  asm volatile("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(as_f(a)), "f"(as_f(b)), "f"(as_f(c)));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_tm(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -258,6 +271,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     sh.fail = 0;
     fence_mbar_init();
   }
+  // (No other kernel that uses TMEM finds room beside this one's shared memory, so
+  // none that this launch waits for is held up by the allocation.)
   if (warp == 12) tc::alloc512(smem_addr(&sh.tmem));
   pdl_wait();
   pdl_trigger();
@@ -486,6 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int k0 = key0 + 32 * c;
             if (MASK && (k0 < lo_all || k0 + 31 > hi_all)) {
               const int mlo = lo - k0, mhi = hi - k0;
+              tc::arrived(v);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i < mlo || i > mhi) v[i] = 0xff800000u;
@@ -496,9 +512,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t* y = v + 16 * h;
-              const float a0 = max3(y[0], y[1], y[2]), a1 = max3(y[3], y[4], y[5]), a2 = max3(y[6], y[7], y[8]);
-              const float a3 = max3(y[9], y[10], y[11]), a4 = max3(y[12], y[13], y[14]);
-              bm[h] = fmaxf(max3(a0, a1, a2), max3(a3, a4, y[15]));
+              const float a0 = max3_tm(y[0], y[1], y[2]), a1 = max3_tm(y[3], y[4], y[5]);
+              const float a2 = max3_tm(y[6], y[7], y[8]), a3 = max3_tm(y[9], y[10], y[11]);
+              const float a4 = max3_tm(y[12], y[13], y[14]), a5 = max3_tm(a3, a4, y[15]);
+              bm[h] = fmaxf(max3(a0, a1, a2), a5);
               if constexpr (BLOCKS) bm[h] = fmaf(bm[h], factor(2 * c + h), offset(2 * c + h));
             }
             return fmaxf(bm[0], bm[1]);
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float y0, y1;
-                unpair(fma2(pair(as_f(v[16 * h + 2 * i]), as_f(v[16 * h + 2 * i + 1])), k2, d2), y0, y1);
+                unpair(fma2(pair_tm(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]), k2, d2), y0, y1);
                 y0 = ex2(y0);
                 y1 = ex2(y1);
                 const uint64_t y = pair(y0, y1);
@@ -565,6 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int c = 0; c < 8; ++c) {
                 tc::ld16(o_tm + 16 * c, w0);
                 tc::wait_ld();
+                tc::arrived(w0);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w0[i] = __float_as_uint(as_f(w0[i]) * f);
                 tc::st16(o_tm + 16 * c, w0);
@@ -649,6 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
           tc::wait_ld();
+          tc::arrived(v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) put(r, 4 * c + i, reinterpret_cast<const float*>(v) + 8 * i, inv);
         }
@@ -667,6 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t v[32];
           tc::ld32(o_tm + 32 * c, v);
           tc::wait_ld();
+          tc::arrived(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(o4 + (8 * c + i) * TILE + r,

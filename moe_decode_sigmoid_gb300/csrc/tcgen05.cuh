@@ -128,8 +128,14 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 // All of the thread's TMEM loads have arrived.  The registers are not operands
 // of the wait: tied to it they were copied, one instruction each, half as many
-// as the whole softmax.  What uses them follows in program order.
+// as the whole softmax.  Whatever uses them first is volatile itself, which keeps
+// it behind this, or goes through arrived().
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void arrived(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace tc
