@@ -18,7 +18,12 @@
 // between CTAs.  It finds its block by a scan of the sequences' block counts:
 // the host does not know them.  A head's row belongs to 16 lanes, and a lane
 // loads five of its up to ten rows before it uses the first: two round trips to
-// memory instead of ten, with room for four CTAs on an SM.
+// memory instead of ten, with room for four CTAs on an SM.  A whole block (16
+// tokens) has one token a lane and no index arithmetic: 33 -> 28 us for 5.5K
+// tokens into E4M3, and the angles from steps of 1, 2, 4 and 8 tokens instead of
+// a sine each: 25 us, 4.2 TB/s (its bytes at the copy rate: 16 us).  2.2K tokens
+// into bf16: 10.5 us, 4.1 TB/s.  What is left is latency: half the warps an SM
+// has room for, waiting on shared memory, shuffles and their rows in turn.
 #include <type_traits>
 
 #include "paged.cuh"

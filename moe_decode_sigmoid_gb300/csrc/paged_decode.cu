@@ -1,7 +1,8 @@
-// paged_decode.cu — attention of next tokens (one query row a sequence) over a
-// paged KV cache, bf16 or E4M3 with a scale per 16-token block and KV head.
+// paged_decode.cu — attention of next tokens and short drafts (up to 16 query rows,
+// tokens x the `group` heads that share a KV head) over a paged KV cache, bf16 or
+// E4M3 with a scale per 16-token block and KV head.
 //
-// For a row and the `group` query heads that share KV head g: scores s_j =
+// For a query row, and the keys of its KV head: scores s_j =
 // scale q.k_j, o = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^sink), in one pass
 // over the keys with a running maximum m, sum l and output o (2^x throughout,
 // the scale carrying log2 e).  E4M3: k_j = kc_j ks and v_j = vc_j vs with one
@@ -13,23 +14,31 @@
 // Bound: the cache bytes.  16 (E4M3) or 8 (bf16) operations a byte at 8 query
 // heads a KV head are far below the tensor cores' ridge but above the CUDA
 // cores', so both products run on mma.sync m16n8k16:
-//   S = Q K^T:     A = 8 query heads (rows 8..15 zero), B = 8 keys a tile
+//   S = Q K^T:     A = 8 or 16 query rows (of 8, the upper half is zero), B = 8 keys
 //   O^T = V^T P^T: A = V^T (16 elements x 16 keys), B = P^T: the score tile's
 //                  accumulator registers are its operand registers.
+// 16 rows is where it ends: an SM quarter issues such a product every 16 cycles or
+// so, and 32 rows of E4M3 (64 products a granule) ran at 3.7 TB/s, the tcgen05
+// kernel at 5.0.  At 16 rows (8 x 30K, 2 drafts) 62 us here, 84 there.
 // The order of the 128 elements inside a dot product and of the outputs is
 // free, so a lane's 16-byte shared-memory loads are its operand words, and only
 // V's keys have to be paired (one byte permute per two codes).  What a
 // streaming kernel lives on is loads in flight: every warp copies its granules
 // (16 keys: 4 KiB of codes, 8 KiB of bf16) into a ring of its own with cp.async,
-// two or three of them on the way at any time, ~190 KiB an SM, with no barrier
+// two to five of them on the way at any time, ~190 KiB an SM, with no barrier
 // between warps.  (With the granule on its way in registers instead, 64 KiB an
 // SM, 32 x 100K E4M3 took 440 us, 5.0 TB/s.)
 // Work: the (sequence, KV head) rows of 16-key granules laid end to end and cut
 // into equal shares, one per CTA (one per SM); a share's warps take its
-// granules in turn.  A row cut between CTAs leaves partial results in the
-// workspace, and the CTA that arrives last joins them in their order, so the
-// bits do not depend on timing.  The lengths are on the device: every CTA
-// computes the cuts itself, by a scan over the sequences.
+// granules in turn, and start on the next row's while this row's results are put
+// together.  A row cut between CTAs leaves partial results in the workspace, and
+// the CTAs that arrive last join them in the order of the keys, so the bits do not
+// depend on timing.  The lengths are on the device: every CTA computes the cuts
+// itself, by a scan over the sequences.
+// Measured: 8 x 100K bf16 246-256 us, 6.4-6.7 TB/s; 32 x 100K E4M3 335-340 us, 6.5
+// (the copy rate: 6.7).  A single 100K E4M3 sequence: 31 us against 15 of bytes;
+// the rest is the launch, three dependent look-ups before the first key (~3 us),
+// and the joins (two tickets and reads through L2, ~4 us).
 #include "nv_util.cuh"
 #include "paged.cuh"
 #include "paged_work.cuh"

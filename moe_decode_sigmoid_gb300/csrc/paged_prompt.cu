@@ -36,7 +36,18 @@
 //
 // Work: items (tile pair of a sequence, KV head) of so many key tiles, cut as the
 // next-token kernel's rows; cut items are joined through the workspace by the
-// CTA that arrives last.
+// CTAs that arrive last.
+//
+// Measured: a chunk of 2048 tokens over 8192, 32 / 4 heads, 211 us in bf16, 1.14
+// PFLOP/s (of 1.92 measured for a plain product), 229 us in E4M3; four drafted
+// tokens for 8 sequences of 30K E4M3 58 us (25 of bytes).  A step of two tiles takes
+// 3200-3600 cycles where its products need 2056 and its softmax alone ~1750: the
+// chain scores -> softmax -> product of each tile, half hidden by the other tile, and
+// an item's start and end (~6 us: queries, first keys, first maximum, outputs).
+// Tried, and not faster: all 128 scores of a row in registers, tokens that keep the
+// two product warps in turn (2-4 %, not kept for their waits), the next item's
+// queries loaded ahead (into registers: 6 % slower; into L2: no change), the halves
+// of a split item joined through shared memory (slower: registers).
 #include <type_traits>
 
 #include "nv_util.cuh"

@@ -21,7 +21,9 @@ static_assert(3 * MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
 // START of them: its queries, its first keys, its outputs.  The rows' weights are
 // laid end to end and cut into equal shares, one per CTA.  A cut near a row's end
 // moves to it (a join costs microseconds, MARGIN granules), and a row of at most
-// WHOLE is not cut at all.
+// WHOLE is not cut at all.  START, measured: next tokens, 8 x 30K E4M3 61, 59, 58 us
+// at 24, 40, 64, but 128 ragged sequences of 2K 47.8, 48.4, 50.5; prompts, windows
+// of 513 (WHOLE 6) 45 us at 3, 49 at 6, and with WHOLE 4 50 us.
 template <int START, int WHOLE, int MARGIN>
 struct Cut {
   int share, margin;
