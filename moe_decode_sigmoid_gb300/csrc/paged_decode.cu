@@ -110,9 +110,10 @@ struct Batch {
 
 // A share's part of a row.
 struct Segment {
-  int seq, kvh, row0;  // where the whole row begins
-  int n, g0;           // granules, the first of them
-  int next;            // where the share goes on
+  int seq, kvh;
+  int n, g0;   // granules, the first of them
+  int c0, c1;  // the CTAs that share the row
+  int next;    // where the share goes on
 };
 
 }  // namespace
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
   constexpr int PARTS = WARPS > JOIN_MOST ? WARPS : JOIN_MOST;
   __shared__ float s_m[PARTS * ROWS], s_l[PARTS * ROWS], s_mm[ROWS], s_ll[ROWS];
   __shared__ __align__(16) float s_f[PARTS * ROWS];  // read four at a time
-  __shared__ int s_cut[2], s_first, s_last;
+  __shared__ int s_cut[2], s_first, s_last, s_parts;
   pdl_wait();
   pdl_trigger();
   const PagedView& b = a.b;
@@ -156,33 +157,53 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       s_seq[tid] = info;
       s_new[tid] = rows = q.n;
     }
+  }
+  // Exclusive sums over the sequences, and the total; returns how many are nonzero.
+  int total;
+  auto scan = [&]() {
     pre = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, pre, o);
       if (lane >= o) pre += v;
     }
-    if (lane == 31) s_scan[warp] = pre;
+    if (lane == 31 && warp < MAX_SEQS / 32) s_scan[warp] = pre;
     pre -= cnt;
-  }
-  if (tid < 2) s_cut[tid] = -1;
-  __syncthreads();
-  int total = 0;
+    const int some = __syncthreads_count(cnt > 0);
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < MAX_SEQS / 32; ++w) {
-    if (w == warp) pre += total;
-    total += s_scan[w];
-  }
+    for (int w = 0; w < MAX_SEQS / 32; ++w) {
+      if (w == warp) pre += total;
+      total += s_scan[w];
+    }
+    return some;
+  };
+  if (tid < 2) s_cut[tid] = -1;
+  const int n_rows = scan() * b.nkv;
   const Cuts cuts(total, gridDim.x);
+  const int size = Cuts::deal(total, n_rows, gridDim.x);
+  if (size > 0) {  // few short rows
+    cnt = Cuts::parts(info.w, size) * b.nkv;
+    __syncthreads();  // s_scan has been read
+    scan();
+  }
   if (tid < MAX_SEQS && tid < b.n_seqs) {
     s_pre[tid + 1] = pre + cnt;
     if (tid == 0) s_pre[0] = 0;
+    if (size > 0) {
+      if (pre <= (int)blockIdx.x && (int)blockIdx.x < pre + cnt) {
+        s_cut[0] = pre;
+        s_first = tid;
+        s_parts = cnt / b.nkv;
+      }
+    } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const long long x = (long long)cuts.share * (blockIdx.x + k);
-      if (pre <= x && x < pre + cnt) {  // this sequence holds the cut
-        s_cut[k] = cuts.at((int)x, pre, info.w);
-        if (k == 0) s_first = tid;
+      for (int k = 0; k < 2; ++k) {
+        const long long x = (long long)cuts.share * (blockIdx.x + k);
+        if (pre <= x && x < pre + cnt) {  // this sequence holds the cut
+          s_cut[k] = cuts.at((int)x, pre, info.w);
+          if (k == 0) s_first = tid;
+        }
       }
     }
     // Rows that see nothing: zeros.
@@ -203,13 +224,21 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
   };
 
   auto segment = [&](int cur, int s) {
+    if (size > 0) {  // all that this CTA has
+      const int4 sq = s_seq[s];
+      const int at = (int)blockIdx.x - cur, parts = s_parts, kvh = at / parts, part = at - kvh * parts;
+      const int off = sq.w * part / parts, to = sq.w * (part + 1) / parts, c0 = (int)blockIdx.x - part;
+      return Segment{s, kvh, to - off, sq.z + off, c0, c0 + parts - 1, end};
+    }
     while (cur >= s_pre[s + 1]) ++s;
     const int4 sq = s_seq[s];
     const int weight = Cuts::weight(sq.w), kvh = (cur - s_pre[s]) / weight;
     const int row0 = s_pre[s] + kvh * weight;
     int off, to;
     cuts.part(cur, end, row0, sq.w, off, to);
-    return Segment{s, kvh, row0, to - off, sq.z + off, min(end, row0 + weight)};
+    int c0, c1;
+    if (!cuts.shared(row0, sq.w, c0, c1)) c0 = c1 = blockIdx.x;
+    return Segment{s, kvh, to - off, sq.z + off, c0, c1, min(end, row0 + weight)};
   };
   uint4 qw[NT][4];
   Batch now{-1, 0.0f, 0.0f}, old{-1, 0.0f, 0.0f};
@@ -579,9 +608,8 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       }
     };
     weigh(WARPS);
-    int c0, c1;
-    const bool whole = !cuts.shared(sg.row0, sq.w, c0, c1);
-    float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == c0, NT);
+    const bool whole = sg.c0 == sg.c1;
+    float* slot = dec_slot(a.ws, blockIdx.x, (int)blockIdx.x == sg.c0, NT);
     auto store_ml = [&](float* to) {
       if (tid < ROWS) {
         __stcg(to + tid, s_mm[tid]);
@@ -599,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
     }
     if (!whole) {
       store_ml(slot);
-      for (Join jn(blockIdx.x, c0, c1);; jn.up()) {
+      for (Join jn(blockIdx.x, sg.c0, sg.c1);; jn.up()) {
         __threadfence();
         __syncthreads();
         if (tid == 0) s_last = jn.arrive(a.ws);

@@ -24,7 +24,7 @@ static_assert(3 * MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
 // WHOLE is not cut at all.  START, measured: next tokens, 8 x 30K E4M3 61, 59, 58 us
 // at 24, 40, 64, but 128 ragged sequences of 2K 47.8, 48.4, 50.5; prompts, windows
 // of 513 (WHOLE 6) 45 us at 3, 49 at 6, and with WHOLE 4 50 us.
-template <int START, int WHOLE, int MARGIN>
+template <int START, int WHOLE, int MARGIN, int LEAST = 0>
 struct Cut {
   int share, margin;
   __device__ __forceinline__ Cut(int total, int ctas)
@@ -48,13 +48,25 @@ struct Cut {
     c1 = i1;
     return n > WHOLE && i0 <= i1;
   }
+  // Few short rows are dealt out instead, a part of one row a CTA: of R rows of N
+  // granules in all, none cut into parts of less than N / (ctas - R), there are at
+  // most ctas parts; that is less work a CTA than an equal share, N / ctas + START
+  // R / ctas, if N < START (ctas - R).  Returns the parts' size, 0 for shares.
+  static __device__ __forceinline__ int deal(int total, int rows, int ctas) {
+    const int n = total - START * rows, rest = ctas - rows;
+    if (rest <= 0 || (long long)n > (long long)START * rest) return 0;
+    return max((n + rest - 1) / rest, LEAST);
+  }
+  static __device__ __forceinline__ int parts(int n, int size) {
+    return n <= 0 ? 0 : n <= LEAST + LEAST / 2 ? 1 : (n + size - 1) / size;
+  }
 };
 
 // A slot of the next-token kernel, for each group of 8 rows (DEC_ROWS at most): 8
 // maxima, 8 sums, 128 x 8 outputs.
 constexpr int DEC_ML = 16, DEC_O = HD * 8, DEC_SLOT = DEC_ML + DEC_O;
 template <bool FP8>
-using DecCut = Cut<FP8 ? 64 : 40, 64, 32>;
+using DecCut = Cut<FP8 ? 64 : 40, 64, 32, FP8 ? 24 : 16>;
 
 // A slot of the prompt kernel: two tiles of 128 maxima, 128 sums and 128 x 128
 // outputs.
