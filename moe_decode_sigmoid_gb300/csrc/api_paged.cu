@@ -163,7 +163,7 @@ flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.window = (int)std::min<long long>(window, 2 * MAX_LENGTH);
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
-  return cuda_status(a.b.max_q * a.b.group <= pg::DEC_ROWS ? launch_paged_decode(a, fp8, sms, stream)
+  return cuda_status(a.b.max_q <= pg::DEC_ROWS / a.b.group ? launch_paged_decode(a, fp8, sms, stream)
                                                            : launch_paged_prompt(a, fp8, sms, stream));
 }
 

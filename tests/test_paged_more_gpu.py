@@ -135,3 +135,22 @@ def test_draft_rows_equal_next_tokens_one_by_one(m, ws, fmt, q):
                                    c.scaled(c.vs), b, out, ws, dims=dims)
         at = [i, q + i]
         assert ((out.double() - ref[at]).abs() <= tol[at]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_q", [1 << 29, (1 << 31) - 1])
+def test_any_bound_on_new_tokens(m, ws, fmt, max_q):
+    c = Case(380, fmt, [20, 1], [300, 90])
+    c.check(c.attend(m, ws, max_q=max_q))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,total", [
+    ([1] * 3, [1000, 24, 37]), ([1] * 5, [2000, 0, 600, 16, 401]), ([1] * 30, [700] * 30),
+    ([1] * 37, [600 + 7 * i for i in range(37)]), ([1] * 38, [600 + 7 * i for i in range(38)]),
+    ([2, 1], [9000, 400])])
+def test_few_short_rows_are_dealt_out(m, ws, fmt, new, total):
+    """Calls of so few rows that a CTA gets a part of one, up to as many rows as CTAs."""
+    c = Case(390 + len(new), fmt, new, total)
+    c.check(c.attend(m, ws, 0, c.sinks), 0, c.sinks)
+    c.check(c.attend(m, ws, 391), 391)
