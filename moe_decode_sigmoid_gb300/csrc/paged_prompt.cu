@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   // Offsets that overlap could ask for more items than a call has tokens.
   const int n_items = min(sh.qpre[b.n_seqs], MAX_ITEMS);
+  const int start = b.max_q <= tile_toks ? SPLIT_START : PAIR_START;
   int4 info = make_int4(0, 0, 0, 0);
   cnt = 0;
   if (tid < n_items) {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int k0 = (a.window > 0 ? max(0, first - a.window + 1) : 0) >> 7;
     info = make_int4(lo, pair, k0, last >= 0 ? (last >> 7) + 1 - k0 : 0);
     sh.item[tid] = info;
-    cnt = PrCut::weight(info.w) * b.nkv;
+    cnt = PrCut::weight(info.w, start) * b.nkv;
   }
   pre = cnt;
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; k < 2; ++k) {
       const long long x = (long long)cuts.share * (blockIdx.x + k);
       if (pre <= x && x < pre + cnt) {  // this item holds the cut
-        sh.cut[k] = cuts.at((int)x, pre, info.w);
+        sh.cut[k] = cuts.at((int)x, pre, info.w, start);
         if (k == 0) sh.first = tid;
       }
     }
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int4 e = sh.item[it];
     const int4 sq = sh.seq[e.x];
     Item p;
-    const int weight = PrCut::weight(e.w);
+    const int weight = PrCut::weight(e.w, start);
     p.row0 = sh.pre[it];
     p.kvh = 0;
     while (cur >= p.row0 + weight) {
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ++p.kvh;
     }
     int from, to;
-    cuts.part(cur, end, p.row0, e.w, from, to);
+    cuts.part(cur, end, p.row0, e.w, from, to, start);
     p.next = min(end, p.row0 + weight);
     p.seq = e.x;
     p.kt0 = e.z + from;
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after();
       }
       int c0, c1;  // the CTAs that share the item
-      const bool whole = !cuts.shared(p.row0, p.all, c0, c1);
+      const bool whole = !cuts.shared(p.row0, p.all, c0, c1, start);
       // A finished row goes out by way of the query tile's place, which is free:
       // a thread writes chunks of its row there, and the warp takes its 32 rows
       // out two at a time, whole lines instead of 16 bytes of 32 rows.

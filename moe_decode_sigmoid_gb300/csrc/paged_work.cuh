@@ -29,21 +29,22 @@ struct Cut {
   int share, margin;
   __device__ __forceinline__ Cut(int total, int ctas)
       : share(max((total + ctas - 1) / ctas, START + 1)), margin(min(share >> 4, MARGIN)) {}
-  static __device__ __forceinline__ int weight(int n) { return n > 0 ? n + START : 0; }
+  static __device__ __forceinline__ int weight(int n, int start = START) { return n > 0 ? n + start : 0; }
   // Where a cut at place x falls, in a run of rows of n granules each from `first`.
-  __device__ __forceinline__ int at(int x, int first, int n) const {
-    const int w = weight(n), off = (x - first) % w, rest = w - off;
+  __device__ __forceinline__ int at(int x, int first, int n, int start = START) const {
+    const int w = weight(n, start), off = (x - first) % w, rest = w - off;
     if (n <= WHOLE) return off <= rest ? x - off : x + rest;
-    return off <= START + margin ? x - off : rest <= margin ? x + rest : x;
+    return off <= start + margin ? x - off : rest <= margin ? x + rest : x;
   }
   // The granules [from, to) of the row at row0 that the share cur .. end - 1 has.
-  __device__ __forceinline__ void part(int cur, int end, int row0, int n, int& from, int& to) const {
-    from = cur == row0 ? 0 : cur - row0 - START;
-    to = end >= row0 + weight(n) ? n : end - row0 - START;
+  __device__ __forceinline__ void part(int cur, int end, int row0, int n, int& from, int& to,
+                                       int start = START) const {
+    from = cur == row0 ? 0 : cur - row0 - start;
+    to = end >= row0 + weight(n, start) ? n : end - row0 - start;
   }
   // The CTAs c0 .. c1 that share the row at row0; false if one has it whole.
-  __device__ __forceinline__ bool shared(int row0, int n, int& c0, int& c1) const {
-    const int i0 = (row0 + START + margin) / share + 1, i1 = (row0 + weight(n) - margin - 1) / share;
+  __device__ __forceinline__ bool shared(int row0, int n, int& c0, int& c1, int start = START) const {
+    const int i0 = (row0 + start + margin) / share + 1, i1 = (row0 + weight(n, start) - margin - 1) / share;
     c0 = i0 - 1;
     c1 = i1;
     return n > WHOLE && i0 <= i1;
@@ -71,7 +72,12 @@ using DecCut = Cut<FP8 ? 64 : 40, 64, 32, FP8 ? 24 : 16>;
 // A slot of the prompt kernel: two tiles of 128 maxima, 128 sums and 128 x 128
 // outputs.
 constexpr int PR_TILE = 128 * (2 + HD), PR_SLOT = 2 * PR_TILE;
-using PrCut = Cut<3, 6, 3>;
+// A call of split items only (no sequence brings more than a tile) has twice the key
+// tiles in a step and pays more for an item beside them: 8 x 4 drafts 59 us at 3, 55
+// at 8; 64 x 4 over 1000 51, 45.  (By item, the last tiles of prompts too: windows
+// 45 -> 49 us.)
+constexpr int PAIR_START = 3, SPLIT_START = 8;
+using PrCut = Cut<PAIR_START, 6, 3>;
 static_assert(DEC_ROWS / 8 * DEC_SLOT <= PR_SLOT, "a workspace for either");
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
