@@ -185,6 +185,7 @@ def _ptr(t):
 
 
 _BF16, _F32, _I32T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_Tensor = torch.Tensor
 
 
 def _bad(where, name, what, t):
@@ -198,7 +199,7 @@ def _arg(where, name, t, dtype, shape, dev, optional=False, min_numel=None):
     """Device pointer of t after checking it against the layout the C call
     assumes: dtype, exact shape (or at least min_numel elements), contiguous,
     on device dev."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous() and t.device == dev and
+    if (type(t) is _Tensor and t.dtype is dtype and t.is_contiguous() and t.device == dev and
             t.shape == shape):
         return t.data_ptr()
     if t is None:
@@ -236,6 +237,9 @@ def _on_current_device(where, name, t):
 
 def _ws_arg(where, workspace, dev):
     """(pointer, bytes) of a workspace: a contiguous uint8 tensor on dev."""
+    if (type(workspace) is _Tensor and workspace.dtype is _U8 and workspace.dim() == 1 and
+            workspace.device == dev and workspace.is_contiguous()):
+        return workspace.data_ptr(), workspace.numel()
     if isinstance(workspace, torch.Tensor):
         if not (workspace.dtype == _U8 and workspace.dim() == 1 and workspace.device == dev and
                 workspace.is_contiguous()):
@@ -491,6 +495,7 @@ class PagedBatch:
                              (f, page_size, max_q_len))
         self.tensors = (q_start, kv_len, page_table)  # kept alive with the batch
         self.device, self.n_seqs, self.page_size, self.max_q_len = dev, n, page_size, max_q_len
+        self.index = dev.index
         self._fields = (n, max_q_len, page_size, max_pages)
         self._pointers = (_arg(f, "q_start", q_start, _I32T, (n + 1,), dev),
                           _arg(f, "kv_len", kv_len, _I32T, (n,), dev),
@@ -513,15 +518,15 @@ def _paged(where, name, rows, batch, k_cache, hd, nkv):
         raise FlintError(FLINT_ERR_INVALID_ARG, "%s: batch must be a PagedBatch, got %s" %
                          (where, type(batch).__name__))
     dev = batch.device
-    if not (isinstance(rows, torch.Tensor) and rows.device == dev and rows.dim() >= 2 and
-            1 <= rows.shape[0] <= PAGED_MAX_TOKENS):
+    shape = rows.shape if isinstance(rows, _Tensor) else ()
+    if not (len(shape) >= 2 and 1 <= shape[0] <= PAGED_MAX_TOKENS and rows.device == dev):
         _bad(where, name, "of 1 to %d token rows on %s" % (PAGED_MAX_TOKENS, dev), rows)
-    if dev.index != torch._C._cuda_getDevice():
+    if batch.index != torch._C._cuda_getDevice():
         _on_current_device(where, name, rows)
-    if not (isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 and k_cache.shape[0] >= 1):
+    cache = k_cache.shape if isinstance(k_cache, _Tensor) else ()
+    if not (len(cache) == 4 and cache[0] >= 1):
         _bad(where, "k_cache", "a [pages, %d, %d, %d] tensor" % (batch.page_size, nkv, hd), k_cache)
-    pages = k_cache.shape[0]
-    return rows.shape[0], dev, pages, batch._ref(pages)
+    return shape[0], dev, cache[0], batch._ref(cache[0])
 
 
 def _heads(dims):

@@ -106,12 +106,18 @@ flint_status append(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.q_norm = static_cast<const uint16_t*>(q_norm);
   a.k_norm = static_cast<const uint16_t*>(k_norm);
   a.rope = rope_theta > 0.0f;
-  // theta^(-2i/128) for i = 8 hi + lo, from 16 powers: a product of two is off by
-  // 2^-52 or so, and 64 calls of pow() cost more than the launch.
+  // theta^(-2i/128) for i = 8 hi + lo, from two powers and their products, a
+  // dozen roundings deep at most: off by 2^-49, and 64 calls of pow() cost more
+  // than the launch (16 of them half a microsecond).
   double hi[8] = {}, lo[8] = {};
-  for (int i = 0; a.rope && i < 8; ++i) {
-    hi[i] = std::pow((double)rope_theta, -16.0 * i / pg::HD);
-    lo[i] = std::pow((double)rope_theta, -2.0 * i / pg::HD);
+  if (a.rope) {
+    hi[0] = lo[0] = 1.0;
+    hi[1] = std::pow((double)rope_theta, -16.0 / pg::HD);
+    lo[1] = std::pow((double)rope_theta, -2.0 / pg::HD);
+    for (int i = 2; i < 8; ++i) {
+      hi[i] = hi[i >> 1] * hi[i - (i >> 1)];
+      lo[i] = lo[i >> 1] * lo[i - (i >> 1)];
+    }
   }
   for (int i = 0; i < pg::HD / 2; ++i) a.inv_freq[i] = hi[i >> 3] * lo[i & 7];
   a.eps = eps;
