@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       }
     }
     // Rows g and g + 8 of the fragments of row groups 2v and 2v + 1.
-    auto q_frag = [&](int v, int k, int half, int word) { return 2 * v + half < NT ? qa[2 * v + half][k][word] : 0u; };
+    auto q_frag = [&](int v, int k, int half, int word) {
+      return 2 * v + half < NT ? qa[2 * v + half][k][word] : 0u;
+    };
 
     float o[NT][8][4], m[NT], l[NT];
 #pragma unroll
@@ -641,11 +643,14 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         __syncthreads();
         weigh(jn.n);
         float* to = dec_slot(a.ws, jn.first, jn.begins(0), NT);
+        auto part_of = [&](int k) {
+          return reinterpret_cast<const float4*>(dec_slot(a.ws, jn.cta(k), jn.begins(k), NT) + C::ML);
+        };
         for (int i = tid; i < 256 * NT; i += THREADS) {
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll JOIN
           for (int k = 0; k < jn.n; ++k)
-            add(x, __ldcg(reinterpret_cast<const float4*>(dec_slot(a.ws, jn.cta(k), jn.begins(k), NT) + C::ML) + i), k, i);
+            add(x, __ldcg(part_of(k) + i), k, i);
           if (jn.top)
             finish(i, x);
           else

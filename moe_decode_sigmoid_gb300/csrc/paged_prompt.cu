@@ -429,48 +429,48 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int c = lane & 15;  // 16-byte chunk of the row
 #pragma unroll 1
         for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 w[8];
+          uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
-          const int tk = (rr >> gshift) + x * tile_toks;
-          w[i] = tk < p.tokens ? *reinterpret_cast<const uint4*>(
-                                     a.q + ((size_t)(p.q_row + tk) * nq + p.kvh * b.group + (rr & (b.group - 1))) * HD + 8 * c)
-                               : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
-          if constexpr (FP8) {
-            float q[8] = {bf_lo(w[i].x), bf_hi(w[i].x), bf_lo(w[i].y), bf_hi(w[i].y),
-                          bf_lo(w[i].z), bf_hi(w[i].z), bf_lo(w[i].w), bf_hi(w[i].w)};
-            float mx = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) mx = max3(mx, fabsf(q[j]), fabsf(q[j + 1]));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // The power of two that brings it to (224, 448] = (0.875, 1.75] 2^8
-            // (NaN for a row with an infinity, which E4M3 would turn into 448).
-            const uint32_t bits = __float_as_uint(mx);
-            const int e = min(max((int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 127);
-            const float up = __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : (uint32_t)(127 + 8 - e) << 23);
-            if (c == 0) sh.qs[x][rr] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float q0 = q[4 * j] * up, q1 = q[4 * j + 1] * up, q2 = q[4 * j + 2] * up, q3 = q[4 * j + 3] * up;
-              const uint32_t h0 = f32x2_to_e4m3x2(q0, q1), h1 = f32x2_to_e4m3x2(q2, q3);
-              const float2 g0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), g1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
-              hi[j] = h0 | h1 << 16;
-              lo[j] = f32x2_to_e4m3x2(q0 - g0.x, q1 - g0.y) | f32x2_to_e4m3x2(q2 - g1.x, q3 - g1.y) << 16;
-            }
-            const uint32_t at = dst + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + CODES), "r"(lo[0]), "r"(lo[1]) : "memory");
-          } else {
-            sts128(dst + row_chunk(rr, c), w[i].x, w[i].y, w[i].z, w[i].w);
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
+            const int tk = (rr >> gshift) + x * tile_toks;
+            const size_t head = (size_t)(p.q_row + tk) * nq + p.kvh * b.group + (rr & (b.group - 1));
+            w[i] = tk < p.tokens ? *reinterpret_cast<const uint4*>(a.q + head * HD + 8 * c)
+                                 : make_uint4(0u, 0u, 0u, 0u);
           }
-        }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 32 * (warp & 3) + 2 * (i0 + i) + (lane >> 4);
+            if constexpr (FP8) {
+              float q[8] = {bf_lo(w[i].x), bf_hi(w[i].x), bf_lo(w[i].y), bf_hi(w[i].y),
+                            bf_lo(w[i].z), bf_hi(w[i].z), bf_lo(w[i].w), bf_hi(w[i].w)};
+              float mx = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) mx = max3(mx, fabsf(q[j]), fabsf(q[j + 1]));
+#pragma unroll
+              for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              // The power of two that brings it to (224, 448] = (0.875, 1.75] 2^8
+              // (NaN for a row with an infinity, which E4M3 would turn into 448).
+              const uint32_t bits = __float_as_uint(mx);
+              const int e = min(max((int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 127);
+              const float up = __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : (uint32_t)(127 + 8 - e) << 23);
+              if (c == 0) sh.qs[x][rr] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+              uint32_t hi[2], lo[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float q0 = q[4 * j] * up, q1 = q[4 * j + 1] * up, q2 = q[4 * j + 2] * up, q3 = q[4 * j + 3] * up;
+                const uint32_t h0 = f32x2_to_e4m3x2(q0, q1), h1 = f32x2_to_e4m3x2(q2, q3);
+                const float2 g0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), g1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
+                hi[j] = h0 | h1 << 16;
+                lo[j] = f32x2_to_e4m3x2(q0 - g0.x, q1 - g0.y) | f32x2_to_e4m3x2(q2 - g1.x, q3 - g1.y) << 16;
+              }
+              const uint32_t at = dst + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + CODES), "r"(lo[0]), "r"(lo[1]) : "memory");
+            } else {
+              sts128(dst + row_chunk(rr, c), w[i].x, w[i].y, w[i].z, w[i].w);
+            }
+          }
         }
         tc::fence_smem_to_mma();
         mbar_arrive(smem_addr(&sh.q_full[x]));
