@@ -643,14 +643,13 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         __syncthreads();
         weigh(jn.n);
         float* to = dec_slot(a.ws, jn.first, jn.begins(0), NT);
-        auto part_of = [&](int k) {
-          return reinterpret_cast<const float4*>(dec_slot(a.ws, jn.cta(k), jn.begins(k), NT) + C::ML);
-        };
         for (int i = tid; i < 256 * NT; i += THREADS) {
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll JOIN
-          for (int k = 0; k < jn.n; ++k)
-            add(x, __ldcg(part_of(k) + i), k, i);
+          for (int k = 0; k < jn.n; ++k) {
+            const float* from = dec_slot(a.ws, jn.cta(k), jn.begins(k), NT) + C::ML;
+            add(x, __ldcg(reinterpret_cast<const float4*>(from) + i), k, i);
+          }
           if (jn.top)
             finish(i, x);
           else

@@ -243,10 +243,12 @@ __device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, uint32_t pa
 
 }  // namespace
 
-template <bool FP8>
+// DRAFTS: no sequence brings more than a tile, so that every item is split.
+template <bool FP8, bool DRAFTS>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_prompt_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<FP8>;
+  using Cuts = PrCut<DRAFTS>;
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -313,7 +315,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   // Offsets that overlap could ask for more items than a call has tokens.
   const int n_items = min(sh.qpre[b.n_seqs], MAX_ITEMS);
-  const int start = b.max_q <= tile_toks ? SPLIT_START : PAIR_START;
   int4 info = make_int4(0, 0, 0, 0);
   cnt = 0;
   if (tid < n_items) {
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int k0 = (a.window > 0 ? max(0, first - a.window + 1) : 0) >> 7;
     info = make_int4(lo, pair, k0, last >= 0 ? (last >> 7) + 1 - k0 : 0);
     sh.item[tid] = info;
-    cnt = PrCut::weight(info.w, start) * b.nkv;
+    cnt = Cuts::weight(info.w) * b.nkv;
   }
   pre = cnt;
 #pragma unroll
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (w == warp) pre += total;
     total += sh.scan[w];
   }
-  const PrCut cuts(total, gridDim.x);
+  const Cuts cuts(total, gridDim.x);
   if (tid < n_items) {
     sh.pre[tid + 1] = pre + cnt;
     if (tid == 0) sh.pre[0] = 0;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; k < 2; ++k) {
       const long long x = (long long)cuts.share * (blockIdx.x + k);
       if (pre <= x && x < pre + cnt) {  // this item holds the cut
-        sh.cut[k] = cuts.at((int)x, pre, info.w, start);
+        sh.cut[k] = cuts.at((int)x, pre, info.w);
         if (k == 0) sh.first = tid;
       }
     }
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int4 e = sh.item[it];
     const int4 sq = sh.seq[e.x];
     Item p;
-    const int weight = PrCut::weight(e.w, start);
+    const int weight = Cuts::weight(e.w);
     p.row0 = sh.pre[it];
     p.kvh = 0;
     while (cur >= p.row0 + weight) {
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ++p.kvh;
     }
     int from, to;
-    cuts.part(cur, end, p.row0, e.w, from, to, start);
+    cuts.part(cur, end, p.row0, e.w, from, to);
     p.next = min(end, p.row0 + weight);
     p.seq = e.x;
     p.kt0 = e.z + from;
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     p.tokens = min(sq.y - tok0, 2 * tile_toks);
     p.pos0 = sq.z + tok0;
     p.q_row = sq.x + tok0;
-    p.split = p.tokens <= tile_toks;
+    p.split = DRAFTS || p.tokens <= tile_toks;
     return p;
   };
 
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after();
       }
       int c0, c1;  // the CTAs that share the item
-      const bool whole = !cuts.shared(p.row0, p.all, c0, c1, start);
+      const bool whole = !cuts.shared(p.row0, p.all, c0, c1);
       // A finished row goes out by way of the query tile's place, which is free:
       // a thread writes chunks of its row there, and the warp takes its 32 rows
       // out two at a time, whole lines instead of 16 bytes of 32 rows.
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item p = part(cur, it);
       cur = p.next;
       const int tiles = __shfl_sync(0xffffffffu, p.n, 0);
-      const bool split = __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
+      const bool split = DRAFTS || __shfl_sync(0xffffffffu, (int)p.split, 0) != 0;
       // Of a split item A has the even key tiles and B the odd ones (a ring slot
       // is then one warp's throughout the item); both share A's queries, and a
       // key tile has one user, which counts for both.
@@ -1062,14 +1063,15 @@ bool encode_cache(CUtensorMap* map, const PagedAttnArgs& a, const void* base, bo
 }
 }  // namespace
 
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
-  static std::atomic<uint64_t> done[2];
-  const int smem = fp8 ? Cfg<true>::SMEM : Cfg<false>::SMEM;
-  const cudaError_t e = fp8 ? set_smem_limit_once(paged_prompt_kernel<true>, smem, done[1])
-                            : set_smem_limit_once(paged_prompt_kernel<false>, smem, done[0]);
+namespace {
+template <bool FP8, bool DRAFTS>
+cudaError_t launch(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done;
+  const int smem = Cfg<FP8>::SMEM;
+  const cudaError_t e = set_smem_limit_once(paged_prompt_kernel<FP8, DRAFTS>, smem, done);
   if (e != cudaSuccess) return e;
   Maps maps;
-  if (!encode_cache(&maps.k, a, a.k_cache, fp8) || !encode_cache(&maps.v, a, a.v_cache, fp8))
+  if (!encode_cache(&maps.k, a, a.k_cache, FP8) || !encode_cache(&maps.v, a, a.v_cache, FP8))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < MAX_CTAS ? sms : MAX_CTAS, 1, 1);
@@ -1081,8 +1083,14 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return fp8 ? cudaLaunchKernelEx(&cfg, paged_prompt_kernel<true>, a, maps)
-             : cudaLaunchKernelEx(&cfg, paged_prompt_kernel<false>, a, maps);
+  return cudaLaunchKernelEx(&cfg, paged_prompt_kernel<FP8, DRAFTS>, a, maps);
+}
+}  // namespace
+
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaStream_t stream) {
+  if (a.b.max_q <= TILE / a.b.group)
+    return fp8 ? launch<true, true>(a, sms, stream) : launch<false, true>(a, sms, stream);
+  return fp8 ? launch<true, false>(a, sms, stream) : launch<false, false>(a, sms, stream);
 }
 
 }  // namespace flint

@@ -21,30 +21,30 @@ static_assert(3 * MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
 // START of them: its queries, its first keys, its outputs.  The rows' weights are
 // laid end to end and cut into equal shares, one per CTA.  A cut near a row's end
 // moves to it (a join costs microseconds, MARGIN granules), and a row of at most
-// WHOLE is not cut at all.  START, measured: next tokens, 8 x 30K E4M3 61, 59, 58 us
+// WHOLE is not cut at all; a share is LOW at least (1 x 4 drafts over 1000: 16 us at 4,
+// 18 at 9).  START, measured: next tokens, 8 x 30K E4M3 61, 59, 58 us
 // at 24, 40, 64, but 128 ragged sequences of 2K 47.8, 48.4, 50.5; prompts, windows
 // of 513 (WHOLE 6) 45 us at 3, 49 at 6, and with WHOLE 4 50 us.
-template <int START, int WHOLE, int MARGIN, int LEAST = 0>
+template <int START, int WHOLE, int MARGIN, int LEAST = 0, int LOW = START + 1>
 struct Cut {
   int share, margin;
   __device__ __forceinline__ Cut(int total, int ctas)
-      : share(max((total + ctas - 1) / ctas, START + 1)), margin(min(share >> 4, MARGIN)) {}
-  static __device__ __forceinline__ int weight(int n, int start = START) { return n > 0 ? n + start : 0; }
+      : share(max((total + ctas - 1) / ctas, LOW)), margin(min(share >> 4, MARGIN)) {}
+  static __device__ __forceinline__ int weight(int n) { return n > 0 ? n + START : 0; }
   // Where a cut at place x falls, in a run of rows of n granules each from `first`.
-  __device__ __forceinline__ int at(int x, int first, int n, int start = START) const {
-    const int w = weight(n, start), off = (x - first) % w, rest = w - off;
+  __device__ __forceinline__ int at(int x, int first, int n) const {
+    const int w = weight(n), off = (x - first) % w, rest = w - off;
     if (n <= WHOLE) return off <= rest ? x - off : x + rest;
-    return off <= start + margin ? x - off : rest <= margin ? x + rest : x;
+    return off <= START + margin ? x - off : rest <= margin ? x + rest : x;
   }
   // The granules [from, to) of the row at row0 that the share cur .. end - 1 has.
-  __device__ __forceinline__ void part(int cur, int end, int row0, int n, int& from, int& to,
-                                       int start = START) const {
-    from = cur == row0 ? 0 : cur - row0 - start;
-    to = end >= row0 + weight(n, start) ? n : end - row0 - start;
+  __device__ __forceinline__ void part(int cur, int end, int row0, int n, int& from, int& to) const {
+    from = cur == row0 ? 0 : cur - row0 - START;
+    to = end >= row0 + weight(n) ? n : end - row0 - START;
   }
   // The CTAs c0 .. c1 that share the row at row0; false if one has it whole.
-  __device__ __forceinline__ bool shared(int row0, int n, int& c0, int& c1, int start = START) const {
-    const int i0 = (row0 + start + margin) / share + 1, i1 = (row0 + weight(n, start) - margin - 1) / share;
+  __device__ __forceinline__ bool shared(int row0, int n, int& c0, int& c1) const {
+    const int i0 = (row0 + START + margin) / share + 1, i1 = (row0 + weight(n) - margin - 1) / share;
     c0 = i0 - 1;
     c1 = i1;
     return n > WHOLE && i0 <= i1;
@@ -76,8 +76,8 @@ constexpr int PR_TILE = 128 * (2 + HD), PR_SLOT = 2 * PR_TILE;
 // tiles in a step and pays more for an item beside them: 8 x 4 drafts 59 us at 3, 55
 // at 8; 64 x 4 over 1000 51, 45.  (By item, the last tiles of prompts too: windows
 // 45 -> 49 us.)
-constexpr int PAIR_START = 3, SPLIT_START = 8;
-using PrCut = Cut<PAIR_START, 6, 3>;
+template <bool DRAFTS>
+using PrCut = Cut<DRAFTS ? 8 : 3, 6, 3, 0, 4>;
 static_assert(DEC_ROWS / 8 * DEC_SLOT <= PR_SLOT, "a workspace for either");
 
 __host__ __device__ constexpr size_t attn_ws_bytes() {
