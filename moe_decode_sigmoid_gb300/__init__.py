@@ -18,6 +18,7 @@ Build the library with `python -m moe_decode_sigmoid_gb300.build` (or
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -87,6 +88,8 @@ ATTN_DIMS = AttnDims(N_Q_HEADS, N_KV_HEADS, HEAD_DIM)
 # The paged KV cache (flint_qk_norm_rope_kv_paged_*, flint_attn_paged_*).
 KV_BLOCK = 16                  # token rows that share a scale in an E4M3 cache
 PAGED_MAX_SEQS, PAGED_MAX_TOKENS = 256, 8192
+PAGED_MAX_LENGTH = 1 << 23     # tokens a row of the page table has room for
+_INT32_MAX = (1 << 31) - 1
 
 
 class _PagedBatchStruct(ctypes.Structure):
@@ -481,18 +484,20 @@ class PagedBatch:
 
     def __init__(self, q_start, kv_len, page_table, page_size: int, max_q_len: int):
         f = "PagedBatch"
+        page_size, max_q_len = int(page_size), int(max_q_len)
+        # The C struct's fields have 32 bits, and ctypes cuts numbers beyond them.
+        if (page_size not in (16, 32, 64, 128, 256, 512, 1024) or
+                not 1 <= max_q_len <= _INT32_MAX):
+            raise FlintError(FLINT_ERR_INVALID_ARG, "%s: page_size %d, max_q_len %d" %
+                             (f, page_size, max_q_len))
         if not (isinstance(page_table, torch.Tensor) and page_table.is_cuda and
                 page_table.dim() == 2):
             _bad(f, "page_table", "a [sequences, pages] tensor on a CUDA device", page_table)
         n, max_pages = page_table.shape
         dev = page_table.device
-        if not (1 <= n <= PAGED_MAX_SEQS and max_pages >= 1):
-            _bad(f, "page_table", "of 1 to %d sequences and at least one page" % PAGED_MAX_SEQS,
-                 page_table)
-        page_size, max_q_len = int(page_size), int(max_q_len)
-        if page_size not in (16, 32, 64, 128, 256, 512, 1024) or max_q_len < 1:
-            raise FlintError(FLINT_ERR_INVALID_ARG, "%s: page_size %d, max_q_len %d" %
-                             (f, page_size, max_q_len))
+        if not (1 <= n <= PAGED_MAX_SEQS and 1 <= max_pages <= PAGED_MAX_LENGTH // page_size):
+            _bad(f, "page_table", "of 1 to %d sequences and of 1 to %d pages of %d tokens" %
+                 (PAGED_MAX_SEQS, PAGED_MAX_LENGTH // page_size, page_size), page_table)
         self.tensors = (q_start, kv_len, page_table)  # kept alive with the batch
         self.device, self.n_seqs, self.page_size, self.max_q_len = dev, n, page_size, max_q_len
         self.index = dev.index
@@ -592,8 +597,22 @@ def flint_attn_get_device_status(workspace: torch.Tensor, stream=None) -> int:
     return int(lib().flint_attn_get_device_status(wp, _stream(stream)))
 
 
+def _window(where, window):
+    """The window as an int of 32 bits, beyond which ctypes would cut it."""
+    try:
+        w = operator.index(window)
+    except TypeError:
+        w = -1
+    if not 0 <= w <= _INT32_MAX:
+        raise FlintError(FLINT_ERR_INVALID_ARG, "%s: window must be a whole number of 0 to %d, "
+                         "got %r" % (where, _INT32_MAX, window))
+    return w
+
+
 def _attend(f, q, k_cache, v_cache, scales, dtype, batch, out, workspace, sinks, window,
             softmax_scale, stream, dims):
+    if type(window) is not int or not 0 <= window <= _INT32_MAX:
+        window = _window(f, window)
     nq, nkv, hd, d = _heads(dims)
     T, dev, pages, b = _paged(f, "q", q, batch, k_cache, hd, nkv)
     cache, rows = (pages, batch.page_size, nkv, hd), (T, nq, hd)
