@@ -77,6 +77,19 @@ bool any_overlap(const Span* s, int n, int n_out) {
   return false;
 }
 
+// A theta below 1 has frequencies of more than a turn a token (the kernel's steps
+// of up to 8 tokens in fp32 would be off by 2^-21 of those): whole turns a token
+// are whole turns at any position, so each frequency is brought to [-pi, pi], from
+// powers of one rounding each and with 2 pi in two parts.
+void whole_turns_off(double theta, double* freq) {
+  constexpr double TWO_PI_HI = 6.283185307179586;  // 2 pi = HI + LO
+  constexpr double TWO_PI_LO = 2.4492935982947064e-16;
+  for (int i = 0; i < pg::HD / 2; ++i) {
+    const double f = std::pow(theta, -2.0 * i / pg::HD), k = std::rint(f / TWO_PI_HI);
+    freq[i] = std::fma(-k, TWO_PI_LO, std::fma(-k, TWO_PI_HI, f));
+  }
+}
+
 flint_status append(bool fp8, const flint_attn_dims* dims, const flint_paged_batch* batch,
                     int32_t n_tokens, const void* qkv, const void* q_norm, const void* k_norm,
                     float rope_theta, float eps, void* q_out, void* k_cache, void* v_cache,
@@ -120,6 +133,7 @@ flint_status append(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
     }
   }
   for (int i = 0; i < pg::HD / 2; ++i) a.inv_freq[i] = hi[i >> 3] * lo[i & 7];
+  if (a.rope && rope_theta < 1.0f) whole_turns_off(rope_theta, a.inv_freq);
   a.eps = eps;
   a.q_out = static_cast<uint16_t*>(q_out);
   a.k_cache = k_cache;

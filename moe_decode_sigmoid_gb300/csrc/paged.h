@@ -35,7 +35,7 @@ struct PagedAppendArgs {
   const uint16_t* q_norm;  // [HD] bf16
   const uint16_t* k_norm;  // [HD] bf16
   int rope;                // 0: no rotation
-  double inv_freq[pg::HD / 2];
+  double inv_freq[pg::HD / 2];  // theta^(-2i/HD), to whole turns in [-pi, pi]
   float eps;
   uint16_t* q_out;         // [n_tokens, nq, HD] bf16
   void* k_cache;           // [n_pages << page_shift, nkv, HD] bf16 or E4M3 codes
