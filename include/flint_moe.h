@@ -467,7 +467,7 @@ flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_page
                                    void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* The same over an E4M3 cache with its scales.  A weight meets the codes with 11
- * significant bits, and no finer than 2^-24 of the row's largest weight times
+ * significant bits, and no finer than 2^-31 of the row's largest weight times
  * scale; over prompts a query's elements count to 2^-18 of its largest. */
 flint_status flint_attn_paged_fp8(const flint_attn_dims* dims, const flint_paged_batch* batch,
                                   int32_t n_tokens, const void* q_bf16,

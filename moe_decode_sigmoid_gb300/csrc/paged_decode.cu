@@ -9,7 +9,9 @@
 // ks and vs a 16-key block, so ks multiplies the block's scores and vs enters
 // the exponent: p'_j = 2^(s_j + log2 vs - m) is the weight of the codes, and
 // l gets p'_j / vs.  A weight is thus held as f16 relative to the largest
-// contribution, whatever the scales of its block.
+// contribution, whatever the scales of its block; m is kept 7 below the largest
+// exponent, so that weights use f16's range up to 2^15 and its steps end at 2^-31
+// of the largest contribution: 2^23 keys of less than half of one are 2^-9 of it.
 //
 // Bound: the cache bytes.  16 (E4M3) or 8 (bf16) operations a byte at 8 query
 // heads a KV head are far below the tensor cores' ridge but above the CUDA
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
   using Cuts = DecCut<FP8>;
   constexpr int WARPS = C::WARPS, THREADS = C::THREADS, SLOTS = C::SLOTS;
   constexpr int ROW = C::ROW, SLOT = C::SLOT, ROWS = 8 * NT;
+  constexpr float LIFT = weight_lift<FP8>;
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_pre[MAX_SEQS + 1];            // weight (of all heads) before each sequence
   __shared__ int4 s_seq[MAX_SEQS];               // {position, row, first granule, granules}
@@ -375,9 +378,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       float scale = 1.0f, lv = 0.0f, iv = 1.0f;
       if constexpr (FP8) {
         scale = __shfl_sync(0xffffffffu, behind ? old.ks : now.ks, it & 31);
-        // A scale of zero would take a block's weights out of the sum: 2^-100.
-        const float vs = fmaxf(__shfl_sync(0xffffffffu, behind ? old.vs : now.vs, it & 31),
-                               7.8886090522101181e-31f);
+        const float vs = fmaxf(__shfl_sync(0xffffffffu, behind ? old.vs : now.vs, it & 31), LEAST_SCALE);
         lv = log2f(vs);
         iv = 1.0f / vs;
       }
@@ -442,14 +443,14 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
         mx[u] = fmaxf(fmaxf(p[u][0], p[u][1]), fmaxf(p[u][2], p[u][3]));
         mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
         mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-        grows |= mx[u] > m[u] + 8.0f;
+        grows |= mx[u] > m[u] + LIFT + 8.0f;
       }
-      // The maximum moves only when it grows by more than 2^8 (or from
-      // nothing): weights stay below 2^8, and the outputs are rarely scaled.
+      // The maximum moves only when it grows by more than 2^8 (or from nothing), so
+      // that the outputs are rarely scaled: weights stay below 2^(LIFT + 8).
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-          const float mn = fmaxf(m[u], mx[u]), r = ex2(m[u] - mn);
+          const float mn = fmaxf(m[u], mx[u] - LIFT), r = ex2(m[u] - mn);
           l[u] *= r;
           m[u] = mn;
           const float r0 = __shfl_sync(0xffffffffu, r, 8 * t), r1 = __shfl_sync(0xffffffffu, r, 8 * t + 4);

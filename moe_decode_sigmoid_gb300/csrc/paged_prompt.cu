@@ -12,10 +12,11 @@
 // [224, 448], is the sum of two E4M3 rows, hi + lo, exact down to 2^-18 of that
 // element (bf16 has 8 significant bits, each half 4), so S = hi K^T + lo K^T at
 // E4M3's double rate costs what one product of 16-bit operands does.  V's codes
-// are widened to f16 (exact) and P is f16, 2^-11 relative to the largest
-// contribution whatever the blocks' scales: P in E4M3 would lose the small
-// weights of a long context.  bf16: Q, K and V as they are, P rounded to bf16,
-// half a step 2^-8, as the output itself; l sums the weights before rounding.
+// are widened to f16 (exact) and P is f16, 11 bits down to 2^-21 of the largest
+// contribution and steps of 2^-31 of it below, whatever the blocks' scales: P in
+// E4M3 would lose the small weights of a long context.  bf16: Q, K and V as they are,
+// P rounded to bf16, half a step 2^-8, as the output itself; l sums the weights
+// before rounding.
 //
 // Bound: the tensor cores for prompts (4 * 128 operations a query-key pair
 // against 512 or 256 bytes a key), the cache's bytes for a few drafted tokens.
@@ -249,6 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     paged_prompt_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<FP8>;
   using Cuts = PrCut<DRAFTS>;
+  constexpr float LIFT = weight_lift<FP8>;
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -594,8 +596,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           mask(3, va);
           mx = max3(mx, highest(2, vc), highest(3, va));
           if constexpr (!BLOCKS) mx *= factor(0);
-          if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
-            const float mn = fmaxf(m, mx);
+          if (__any_sync(0xffffffffu, mx > m + LIFT + 8.0f)) {
+            const float mn = fmaxf(m, mx - LIFT);
             const float f = m > -INFINITY ? ex2(m - mn) : 0.0f;
             l *= f;
             m = mn;
@@ -920,8 +922,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int blk = lane0 + (lane & 7), info = t & (INFO - 1);
           const int at = __shfl_sync(0xffffffffu, row0, blk);
           const float k = FP8 ? __shfl_sync(0xffffffffu, ks0, blk) : 1.0f;
-          // A scale of zero would take a block's weights out of the sum: 2^-100.
-          const float z = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs0, blk), 7.8886090522101181e-31f) : 1.0f;
+          const float z = FP8 ? fmaxf(__shfl_sync(0xffffffffu, vs0, blk), LEAST_SCALE) : 1.0f;
           const int key = ((p.kt0 + j) << 7) + 16 * (lane & 7);
           // A block that nothing sees may have any scale.
           const bool live = at >= 0 && key <= see_hi && key + BLOCK - 1 >= see_lo;

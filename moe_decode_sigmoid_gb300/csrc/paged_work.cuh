@@ -129,6 +129,15 @@ __device__ __forceinline__ float* pr_slot(void* ws, int cta, bool begins, int ti
          (size_t)(2 * cta + (begins ? 1 : 0)) * PR_SLOT + (size_t)tile * PR_TILE;
 }
 
+// An E4M3 cache's weights meet V as f16, relative to 2^m: m stays this much below the
+// largest exponent (f16 reaches 2^16, and m lags by up to 8).  bf16 has fp32's range.
+template <bool FP8>
+constexpr float weight_lift = FP8 ? 7.0f : 0.0f;
+
+// What a value's scale counts as at least, 2^-80: one of zero would take its block's
+// weights out of the sum.  (2^15 times 2^80 times 2^23 keys is within fp32.)
+constexpr float LEAST_SCALE = 8.271806125530277e-25f;
+
 // What a row's unscaled outputs are multiplied by, from its maximum and sum:
 // the head's sink joins the denominator, and a row that saw nothing gets 0.
 __device__ __forceinline__ float row_factor(const PagedAttnArgs& a, int head, float m, float l) {
