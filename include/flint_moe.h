@@ -440,6 +440,13 @@ flint_status flint_attn_workspace_init(void* workspace, size_t ws_bytes, cudaStr
  * bounded by one second) ran out; that call's outputs are undefined. */
 flint_status flint_attn_get_device_status(const void* workspace, cudaStream_t stream);
 
+/* Fault-injection hook for tests, as flint_moe_debug_arm_stall: a one-shot wait in
+ * the next prompt call (more than 16 query rows a KV head) on this workspace that
+ * sees any key, on a barrier that nothing completes.  It runs out after a second,
+ * the call ends with FLINT_ERR_DEVICE_TIMEOUT as its device status, and the
+ * workspace has to be initialised again. */
+flint_status flint_attn_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* Grouped-query attention over a paged bf16 cache: for the new row t of a
  * sequence, at position p, and query head h of KV head g,
  *   out[t,h] = sum_j e_j V[j,g] / (sum_j e_j + exp(sinks[h])),

@@ -46,7 +46,8 @@ EXPORTS = (
     "flint_moe_decode_bf16_prenorm",
     "flint_qk_norm_rope_kv_paged_bf16", "flint_qk_norm_rope_kv_paged_fp8",
     "flint_attn_workspace_bytes", "flint_attn_workspace_init",
-    "flint_attn_get_device_status", "flint_attn_paged_bf16", "flint_attn_paged_fp8",
+    "flint_attn_get_device_status", "flint_attn_debug_arm_stall",
+    "flint_attn_paged_bf16", "flint_attn_paged_fp8",
 )
 NOALLOC_MAX_BATCH = 8
 # Batches up to which flint_moe_decode_bf16_prenorm is one launch (the
@@ -157,6 +158,8 @@ def lib() -> ctypes.CDLL:
     L.flint_attn_workspace_init.argtypes = [_P, _SZ, _P]
     L.flint_attn_get_device_status.restype = ctypes.c_int
     L.flint_attn_get_device_status.argtypes = [_P, _P]
+    L.flint_attn_debug_arm_stall.restype = ctypes.c_int
+    L.flint_attn_debug_arm_stall.argtypes = [_P, _SZ, _P]
     L.flint_attn_paged_bf16.restype = ctypes.c_int
     L.flint_attn_paged_bf16.argtypes = ([_P, _P, _I32] + [_P] * 4 + [ctypes.c_float, _I32] +
                                         [_P, _P, _SZ, _P])
@@ -595,6 +598,11 @@ def flint_attn_workspace_init(workspace: torch.Tensor, stream=None):
 def flint_attn_get_device_status(workspace: torch.Tensor, stream=None) -> int:
     wp, _ = _ws_only("flint_attn_get_device_status", workspace)
     return int(lib().flint_attn_get_device_status(wp, _stream(stream)))
+
+
+def flint_attn_debug_arm_stall(workspace: torch.Tensor, stream=None):
+    wp, wb = _ws_only("flint_attn_debug_arm_stall", workspace)
+    _check(lib().flint_attn_debug_arm_stall(wp, wb, _stream(stream)), "flint_attn_debug_arm_stall")
 
 
 def _window(where, window):

@@ -233,6 +233,12 @@ flint_status flint_attn_get_device_status(const void* workspace, cudaStream_t st
   return static_cast<flint_status>(code);
 }
 
+flint_status flint_attn_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!req(workspace) || ws_bytes < paged_attn_workspace_bytes()) return FLINT_ERR_WORKSPACE;
+  return cuda_status(cudaMemsetAsync(static_cast<char*>(workspace) + paged_attn_workspace_stall_at(),
+                                     1, sizeof(uint32_t), stream));
+}
+
 flint_status flint_attn_paged_bf16(const flint_attn_dims* dims, const flint_paged_batch* batch,
                                    int32_t n_tokens, const void* q_bf16, const void* k_cache_bf16,
                                    const void* v_cache_bf16, const float* sinks,

@@ -65,7 +65,8 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, bool fp8, int sms, cudaS
 size_t paged_attn_workspace_bytes();
 // Leading bytes of the workspace that flint_attn_workspace_init clears.
 size_t paged_attn_workspace_clear_bytes();
-// Where its error word (a device error code) lies.
+// Where its error word (a device error code) and its stall word lie.
 size_t paged_attn_workspace_error_at();
+size_t paged_attn_workspace_stall_at();
 
 }  // namespace flint

@@ -695,5 +695,6 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp8, int sms, cudaS
 size_t paged_attn_workspace_bytes() { return attn_ws_bytes(); }
 size_t paged_attn_workspace_clear_bytes() { return WS_HEAD; }
 size_t paged_attn_workspace_error_at() { return WS_ERROR; }
+size_t paged_attn_workspace_stall_at() { return WS_STALL; }
 
 }  // namespace flint

@@ -85,7 +85,7 @@ struct Shared {
   uint64_t k_in[4], k_out[4];        // K tiles: copied, used
   uint64_t v_in[2], v_taken[2];      // V tiles: copied; codes read
   uint64_t v_full[2], v_out[2];      // V operands: ready, used
-  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], b_free, drained;
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], b_free, drained, never;
   uint32_t tmem;
   int fail, last, cut[2], first;
   int scan[16];
@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     mbar_init(smem_addr(&sh.b_free), 4);
     mbar_init(smem_addr(&sh.drained), 2);
+    mbar_init(smem_addr(&sh.never), 1);
     sh.fail = 0;
     fence_mbar_init();
   }
@@ -959,11 +960,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       turns.item(p.n, shift);
     }
-    if (!ok) {  // nothing may land after the CTA has left
-      const uint64_t deadline = globaltimer_ns() + 1000000000ull;
-      for (int s = 0; s < C::KS; ++s)
-        if ((flying >> s) & 1u) mbar_wait(smem_addr(&in[s]), (flying_parity >> s) & 1u, deadline);
-    }
+    // Nothing may land after the CTA has left, whichever warp's wait ran out.
+    const uint64_t deadline = globaltimer_ns() + 1000000000ull;
+    for (int s = 0; s < C::KS; ++s)
+      if ((flying >> s) & 1u) mbar_wait(smem_addr(&in[s]), (flying_parity >> s) & 1u, deadline);
   } else if (warp == 12 || warp == 14) {
     // ===== the products of tile A, of tile B: a warp each, of which one thread issues ===
     // Issue blocks while the tensor core is busy, and the tensor core idles while
@@ -980,6 +980,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t q_phase = 0, p_phase = 0;
     Turns k_turns, v_turns;
     bool ok = true;
+    // The test hook, in the CTA that has the first item (its queries arrive later).
+    if (x == 0 && begin == 0 && end > 0 && __ldcg(ws_stall(a.ws)) != 0) {
+      if (lane == 0) *ws_stall(a.ws) = 0;
+      ok = warp_wait(sh, sh.never, 0);
+    }
     for (int cur = begin, it = sh.first; ok && cur < end;) {
       const Item p = part(cur, it);
       cur = p.next;

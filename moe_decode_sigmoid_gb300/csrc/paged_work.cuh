@@ -10,11 +10,11 @@ namespace pg {
 
 constexpr int MAX_CTAS = 160;  // CTAs of an attention launch (one per SM; GB300 has 152)
 
-// Workspace: three tickets per CTA and an error word, then two slots per CTA: one
-// for a row (or item) that began in an earlier CTA's share and one for one that
-// goes on in the next one's.
-constexpr size_t WS_HEAD = 4096, WS_ERROR = WS_HEAD - 4;
-static_assert(3 * MAX_CTAS * 4 <= WS_ERROR, "tickets fit");
+// Workspace: three tickets per CTA, the stall word (a test hook) and an error word, then
+// two slots per CTA: one for a row (or item) that began in an earlier CTA's share and
+// one for one that goes on in the next one's.
+constexpr size_t WS_HEAD = 4096, WS_ERROR = WS_HEAD - 4, WS_STALL = WS_HEAD - 8;
+static_assert(3 * MAX_CTAS * 4 <= WS_STALL, "tickets fit");
 
 // The cut.  A row (next tokens: a sequence and KV head; prompts: an item, a tile
 // pair and KV head) weighs its key granules (tiles) and what it costs besides,
@@ -117,6 +117,9 @@ struct Join {
     return last;
   }
 };
+__device__ __forceinline__ uint32_t* ws_stall(void* ws) {
+  return reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + WS_STALL);
+}
 __device__ __forceinline__ void ws_error(void* ws) {
   atomicCAS(reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + WS_ERROR), DEV_OK, DEV_TIMEOUT);
 }

@@ -45,3 +45,14 @@ def test_page_tables_beyond_the_longest_sequence(columns):
     with pytest.raises(m.FlintError) as e:
         m.PagedBatch(None, None, table.as_subclass(_Table), 16, 1)
     assert e.value.status == m.FLINT_ERR_INVALID_ARG and "page_table" in str(e.value)
+
+
+def test_arming_a_stall_wants_a_workspace():
+    from moe_decode_sigmoid_gb300 import build
+    build.build()
+    L, n = m.lib(), m.flint_attn_workspace_bytes()
+    assert L.flint_attn_debug_arm_stall(None, n, None) == m.FLINT_ERR_WORKSPACE
+    assert L.flint_attn_debug_arm_stall(0x100008, n, None) == m.FLINT_ERR_WORKSPACE
+    assert L.flint_attn_debug_arm_stall(0x100000, n - 1, None) == m.FLINT_ERR_WORKSPACE
+    with pytest.raises(m.FlintError):
+        m.flint_attn_debug_arm_stall(torch.zeros(n, dtype=torch.uint8))
