@@ -455,7 +455,9 @@ flint_status flint_attn_debug_arm_stall(void* workspace, size_t ws_bytes, cudaSt
  * 0: j <= p) whose page is held.  A row that sees no token gets zeros.
  *   q_bf16   [n_tokens, nq, D] (q_out of the append)
  *   k_cache_bf16, v_cache_bf16 [n_pages * page_size, nkv, D]
- *   sinks    [nq] fp32 or NULL (no term in the denominator)
+ *   sinks    [nq] fp32 or NULL (no term in the denominator); -infinity adds nothing,
+ *            infinity makes the head's outputs zero, NaN makes them NaN (but a row
+ *            that sees no token zeros)
  *   softmax_scale >= 0, finite; window >= 0
  *   out_bf16 [n_tokens, nq, D]
  *   workspace (16-byte aligned) as flint_attn_workspace_bytes says

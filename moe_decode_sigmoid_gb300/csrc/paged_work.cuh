@@ -141,14 +141,15 @@ constexpr float weight_lift = FP8 ? 7.0f : 0.0f;
 // weights out of the sum.  (2^15 times 2^80 times 2^23 keys is within fp32.)
 constexpr float LEAST_SCALE = 8.271806125530277e-25f;
 
-// What a row's unscaled outputs are multiplied by, from its maximum and sum:
-// the head's sink joins the denominator, and a row that saw nothing gets 0.
+// What a row's unscaled outputs are multiplied by, from its maximum and sum: the
+// head's sink joins the denominator (none for -infinity; 0 in the end for infinity,
+// NaN for NaN), and a row that saw nothing gets 0.
 __device__ __forceinline__ float row_factor(const PagedAttnArgs& a, int head, float m, float l) {
   const float sink = a.sinks ? a.sinks[head] * 1.4426950408889634f : -INFINITY;
   const float mm = fmaxf(m, sink);
   const float f = m > -INFINITY ? exp2f(m - mm) : 0.0f;
-  const float den = fmaf(l, f, sink > -INFINITY ? exp2f(sink - mm) : 0.0f);
-  return den == 0.0f ? 0.0f : f / den;  // NaN stays NaN
+  const float den = fmaf(l, f, sink == -INFINITY ? 0.0f : exp2f(sink - mm));
+  return f == 0.0f ? l * 0.0f : f / den;  // a NaN in l stays one
 }
 
 }  // namespace pg
