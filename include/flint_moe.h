@@ -426,8 +426,8 @@ flint_status flint_qk_norm_rope_kv_paged_fp8(const flint_attn_dims* dims,
                                              cudaStream_t stream);
 
 /* Bytes of workspace the attention calls need (0 for unsupported dims): room
- * for the partial results of a sequence that several CTAs share.  It depends
- * on the dims only; one workspace serves every call, one call at a time. */
+ * for the partial results of a sequence that several CTAs share, the same for all
+ * supported dims and batches; one workspace serves every call, one call at a time. */
 size_t flint_attn_workspace_bytes(const flint_attn_dims* dims);
 
 /* Clears a workspace's counters and error word (cudaMemsetAsync on `stream`).

@@ -14,14 +14,18 @@ using namespace flint;
 
 namespace {
 
-constexpr long long MAX_ROWS = 1ll << 30;    // token rows of a cache
-constexpr long long MAX_LENGTH = 1ll << 23;  // tokens of a sequence
+constexpr long long MAX_ROWS = 1ll << 30;  // token rows of a cache
+
+// What the kernels' tables and index widths are made for.
+static_assert(FLINT_PAGED_MAX_SEQS == pg::MAX_SEQS && FLINT_PAGED_MAX_TOKENS == pg::MAX_TOKENS &&
+                  FLINT_KV_BLOCK == pg::BLOCK,
+              "the public limits are the kernels'");
 
 flint_status dims_status(const flint_attn_dims* d) {
   if (d == nullptr) return FLINT_ERR_INVALID_ARG;
   if (d->head_dim != pg::HD) return FLINT_ERR_UNSUPPORTED;
   const int n = d->n_kv_heads;
-  if (n != 1 && n != 2 && n != 4 && n != 8) return FLINT_ERR_UNSUPPORTED;
+  if (n < 1 || n > pg::MAX_KV_HEADS || (n & (n - 1)) != 0) return FLINT_ERR_UNSUPPORTED;
   for (int g = 1; g <= pg::MAX_GROUP; g *= 2)
     if (d->n_q_heads == n * g) return FLINT_OK;
   return FLINT_ERR_UNSUPPORTED;
@@ -39,7 +43,7 @@ flint_status batch_view(const flint_attn_dims* dims, const flint_paged_batch* b,
     return FLINT_ERR_INVALID_ARG;
   int shift = 4;
   while (shift < 10 && (1 << shift) != b->page_size) ++shift;
-  if ((1 << shift) != b->page_size || ((long long)b->max_pages << shift) > MAX_LENGTH ||
+  if ((1 << shift) != b->page_size || ((long long)b->max_pages << shift) > pg::MAX_LENGTH ||
       ((long long)b->n_pages << shift) > MAX_ROWS)
     return FLINT_ERR_INVALID_ARG;
   if (!req4(b->q_start) || !req4(b->kv_len) || !req4(b->page_table)) return FLINT_ERR_INVALID_ARG;
@@ -180,7 +184,7 @@ flint_status attend(bool fp8, const flint_attn_dims* dims, const flint_paged_bat
   a.scale_log2 = std::fmin(softmax_scale * 1.4426950408889634f, FLT_MAX);
   // Positions lie within -MAX_TOKENS .. MAX_LENGTH: a wider window sees no more,
   // and position - window stays within 32 bits.
-  a.window = (int)std::min<long long>(window, 2 * MAX_LENGTH);
+  a.window = (int)std::min<long long>(window, 2 * pg::MAX_LENGTH);
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
   return cuda_status(a.b.max_q <= pg::DEC_ROWS / a.b.group ? launch_paged_decode(a, fp8, sms, stream)

@@ -1,5 +1,5 @@
 // paged.h — argument blocks and launch wrappers of the paged KV-cache kernels:
-// the append (paged_append.cu) and the attention (paged_attn*.cu).
+// the append (paged_append.cu) and the attention (paged_decode.cu, paged_prompt.cu).
 #pragma once
 
 #include <cstddef>
@@ -11,7 +11,8 @@ namespace pg {
 constexpr int HD = 128;            // head size
 constexpr int BLOCK = 16;          // token rows that share a scale
 constexpr int MAX_SEQS = 256;
-constexpr int MAX_TOKENS = 8192;
+constexpr int MAX_TOKENS = 8192;         // rows of a call
+constexpr long long MAX_LENGTH = 1ll << 23;  // tokens of a sequence
 constexpr int MAX_KV_HEADS = 8;
 constexpr int MAX_GROUP = 8;       // query heads per KV head
 constexpr int DEC_ROWS = 16;       // query rows (tokens x group) a KV head has at most in the next-token kernel

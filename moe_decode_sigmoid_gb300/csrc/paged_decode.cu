@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
   const int nq = b.nkv * b.group, gshift = 31 - __clz(b.group);  // group is a power of two
 
   // ---- the cuts ---------------------------------------------------------------
-  // Lengths are below 2^23 tokens, so 256 sequences of 8 heads weigh below 2^31.
+  static_assert(MAX_SEQS * MAX_KV_HEADS * (MAX_LENGTH / BLOCK + Cuts::weight(1)) < 1ll << 31, "32 bits");
   int cnt = 0, pre = 0, rows = 0;
   int4 info = make_int4(-1, -1, 0, 0);
   if (tid < MAX_SEQS) {

@@ -33,7 +33,8 @@
 //                   zero weight
 //   warps 12, 14:   issue the products of A, of B
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each; P takes its S's place.  O is
-// rescaled only when a row's maximum grows by more than 2^8.
+// rescaled only when a row's maximum grows by more than 2^8 (conditional rescaling
+// of an online softmax, a published method).
 //
 // Work: items (tile pair of a sequence, KV head) of so many key tiles, cut as the
 // next-token kernel's rows; cut items are joined through the workspace by the
@@ -68,6 +69,7 @@ constexpr int OPER = TILE * HD * 2;    // bytes of an operand tile (16-bit): 2 b
 constexpr int HALF = OPER / 2;
 constexpr int CODES = TILE * HD;       // bytes of a tile of codes
 constexpr int MAX_ITEMS = 512;         // tile pairs: tokens / (tokens a pair) + sequences
+static_assert(MAX_ITEMS >= MAX_TOKENS / (2 * TILE / MAX_GROUP) + MAX_SEQS, "room for every item");
 constexpr int INFO = 8;                // tiles whose block tables are kept
 
 template <bool FP8>

@@ -22,15 +22,16 @@ static_assert(3 * MAX_CTAS * 4 <= WS_STALL, "tickets fit");
 // laid end to end and cut into equal shares, one per CTA.  A cut near a row's end
 // moves to it (a join costs microseconds, MARGIN granules), and a row of at most
 // WHOLE is not cut at all; a share is LOW at least (1 x 4 drafts over 1000: 16 us at 4,
-// 18 at 9).  START, measured: next tokens, 8 x 30K E4M3 61, 59, 58 us
-// at 24, 40, 64, but 128 ragged sequences of 2K 47.8, 48.4, 50.5; prompts, windows
-// of 513 (WHOLE 6) 45 us at 3, 49 at 6, and with WHOLE 4 50 us.
+// 18 at 9).  START, measured at 32 / 4 heads (other layouts take the same): next
+// tokens, 8 x 30K E4M3 61, 59, 58 us at 24, 40, 64, but 128 ragged sequences of 2K
+// 47.8, 48.4, 50.5; prompts, windows of 513 (WHOLE 6) 45 us at 3, 49 at 6, and with
+// WHOLE 4 50 us.
 template <int START, int WHOLE, int MARGIN, int LEAST = 0, int LOW = START + 1>
 struct Cut {
   int share, margin;
   __device__ __forceinline__ Cut(int total, int ctas)
       : share(max((total + ctas - 1) / ctas, LOW)), margin(min(share >> 4, MARGIN)) {}
-  static __device__ __forceinline__ int weight(int n) { return n > 0 ? n + START : 0; }
+  static __host__ __device__ constexpr int weight(int n) { return n > 0 ? n + START : 0; }
   // Where a cut at place x falls, in a run of rows of n granules each from `first`.
   __device__ __forceinline__ int at(int x, int first, int n) const {
     const int w = weight(n), off = (x - first) % w, rest = w - off;
