@@ -422,16 +422,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // After a wait that ran out the items are only walked through: the other
     // tile's warps count on this one's arrivals at the joint barriers.
     bool ok = true;
-    // The arrivals on B's query barrier: of B's threads in a pair, of A's in a split
-    // item.  Each phase has to be complete, and seen by B's products, before the
-    // next one's arrivals: behind a split item its join orders them (B's last
-    // products come before B's part of it), behind a pair, which may have no join, A
-    // waits for B before a split item.  Items of one or two key tiles would let A run
-    // ahead of B by whole items otherwise: the rings hold it up from the third tile.
     for (int cur = begin, it = sh.first; cur < end;) {
       const Item p = part(cur, it);
       cur = p.next;
-      if (!DRAFTS && p.split) named_sync(1, 256);
       const int tok = tok_in_tile + (p.split ? 0 : x * tile_toks);
       const int pos = p.pos0 + min(tok, p.tokens - 1);
       const int head = p.kvh * b.group + head_in_group;
@@ -488,9 +481,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_smem_to_mma();
         mbar_arrive(smem_addr(&sh.q_full[x]));
         // B's products take them too, if B has key tiles: without any, nothing waits
-        // for B's product warp to have seen this phase.
-        if (p.split && p.n > 1) mbar_arrive(smem_addr(&sh.q_full[1]));
+        // for B's product warp to have seen this phase.  The phase before has to be
+        // complete and seen as well, and may be one of B's own arrivals: behind a
+        // split item its join orders them (B's last products come before B's part of
+        // it), behind a pair, which may have none, A waits for B here.  The rings hold
+        // A up only from an item's third key tile.  (At the item's start this barrier
+        // cost E4M3 registers: 2048 over 8192 233 us instead of 230.)
+        if (p.split && p.n > 1) {
+          if (!DRAFTS) named_sync(1, 256);
+          mbar_arrive(smem_addr(&sh.q_full[1]));
+        }
       }
+      if (!DRAFTS && p.split && x == 1 && p.n > 1) named_sync(1, 256);  // as above
       if (C::KS > 2 && p.split && x == 1) {  // B's queries' place is free for keys
         tc::fence_smem_to_mma();
         __syncwarp();
