@@ -37,7 +37,7 @@
 // the CTAs that arrive last join them in the order of the keys, so the bits do not
 // depend on timing.  The lengths are on the device: every CTA computes the cuts
 // itself, by a scan over the sequences.
-// Measured: 8 x 100K bf16 246-256 us, 6.4-6.7 TB/s; 32 x 100K E4M3 335-340 us, 6.5
+// Measured: 8 x 100K bf16 249-256 us, 6.4-6.6 TB/s; 32 x 100K E4M3 338-342 us, 6.4-6.5
 // (the copy rate: 6.7).  A single 100K E4M3 sequence: 31 us against 15 of bytes;
 // the rest is the launch, three dependent look-ups before the first key (~3 us),
 // and the joins (two tickets and reads through L2, ~4 us).

@@ -41,8 +41,8 @@
 // CTAs that arrive last.
 //
 // Measured: a chunk of 2048 tokens over 8192, 32 / 4 heads, 211 us in bf16, 1.14
-// PFLOP/s (of 1.92 measured for a plain product), 229 us in E4M3; four drafted
-// tokens for 8 sequences of 30K E4M3 55 us (25 of bytes).  A step of two tiles takes
+// PFLOP/s (of 1.92 measured for a plain product), 230 us in E4M3; four drafted
+// tokens for 8 sequences of 30K E4M3 54 us (25 of bytes).  A step of two tiles takes
 // 3200-3600 cycles where its products need 2056 and its softmax alone ~1750: the
 // chain scores -> softmax -> product of each tile, half hidden by the other tile, and
 // an item's start and end (~6 us: queries, first keys, first maximum, outputs).
