@@ -111,7 +111,7 @@ typedef struct {
 } flint_moe_dims;
 
 /* Largest batch (tokens per call) of every entry point but the paged KV-cache
- * calls, which have limits of their own. */
+ * calls and those of the linear side of a prompt, which have limits of their own. */
 #define FLINT_MOE_MAX_BATCH 256
 
 /* Human-readable name of a status code.  Never NULL. */
@@ -484,6 +484,137 @@ flint_status flint_attn_paged_fp8(const flint_attn_dims* dims, const flint_paged
                                   const float* k_scale, const float* v_scale, const float* sinks,
                                   float softmax_scale, int32_t window, void* out_bf16,
                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- the linear side of a prompt -------------------------------------------
+ *
+ * The matrix products around the paged attention (projections, dense MLPs,
+ * router scores), the same grouped by expert with ragged group sizes, and the
+ * mixture-of-experts layer of up to FLINT_PAGED_MAX_TOKENS tokens made of them:
+ * flint_moe_decode_bf16 takes 256.  The pages give the layer and its shapes;
+ * these calls' interfaces are this library's. */
+#define FLINT_LINEAR_MAX_ROWS 65536
+#define FLINT_LINEAR_MAX_IN 65536
+#define FLINT_LINEAR_MAX_OUT 1048576
+#define FLINT_LINEAR_MAX_GROUPS 1024
+
+/* Activations of a linear call: v, v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2,
+ * and gate / (1 + exp(-gate)) * up of a weight matrix that holds n_out gate rows,
+ * then n_out up rows (the layout of w13). */
+#define FLINT_ACT_NONE 0
+#define FLINT_ACT_SILU 1
+#define FLINT_ACT_GELU 2
+#define FLINT_ACT_SWIGLU 3
+
+/* n_in: a multiple of 8, 8 .. FLINT_LINEAR_MAX_IN; n_out: a multiple of 8 (of 16
+ * with FLINT_ACT_SWIGLU), 8 .. FLINT_LINEAR_MAX_OUT; out_f32: 0 for bf16 outputs, 1
+ * for fp32.  Anything else is FLINT_ERR_UNSUPPORTED. */
+typedef struct {
+  int32_t n_in, n_out, act, out_f32;
+} flint_linear_dims;
+
+/* Bytes of workspace: max_tokens = 0 serves flint_linear_bf16,
+ * flint_grouped_linear_bf16 and flint_moe_select (every size), max_tokens in
+ * [1, FLINT_PAGED_MAX_TOKENS] also flint_moe_prompt_bf16 of up to so many tokens
+ * (about 36 KB a token).  0 for any other max_tokens. */
+size_t flint_prompt_workspace_bytes(int32_t max_tokens);
+
+/* Clears a workspace's error word (cudaMemsetAsync on `stream`).  Once before the
+ * first call that uses it, and again after a call whose device status was not
+ * FLINT_OK.  One workspace serves any number of calls, one at a time. */
+flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Synchronises `stream`, then reads and returns the workspace's error word:
+ * FLINT_OK, or FLINT_ERR_DEVICE_TIMEOUT if a wait inside a kernel (each is
+ * bounded by one second) ran out; that call's outputs are undefined. */
+flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t stream);
+
+/* out = act(x w^T + bias) + residual for n_rows rows (1 .. FLINT_LINEAR_MAX_ROWS).
+ *   x_bf16   [n_rows, n_in]
+ *   w_bf16   [n_out, n_in], with FLINT_ACT_SWIGLU [2 n_out, n_in]
+ *   bias     fp32, one per row of w, or NULL
+ *   residual [n_rows, n_out] of out's type, or NULL; may be `out` itself
+ *   out      [n_rows, n_out] bf16 or fp32
+ *   workspace (16-byte aligned) as flint_prompt_workspace_bytes(0) says
+ * Sums are fp32, each output is rounded once.  The same call gives the same bits.
+ * An infinity or NaN reaches the outputs of its row of x, of its row of w.
+ * Errors (before any launch): FLINT_ERR_UNSUPPORTED for other dims;
+ * FLINT_ERR_INVALID_ARG for a NULL or misaligned pointer (16 bytes; 4 for bias),
+ * n_rows outside its range, or an output that overlaps anything but that one
+ * residual; FLINT_ERR_WORKSPACE for a NULL, misaligned or too small workspace. */
+flint_status flint_linear_bf16(const flint_linear_dims* dims, int32_t n_rows, const void* x_bf16,
+                               const void* w_bf16, const float* bias, const void* residual,
+                               void* out, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* The products of n_groups (1 .. FLINT_LINEAR_MAX_GROUPS) weight matrices with a
+ * ragged number of rows each: for row r of group g, group_start[g] <= r <
+ * group_start[g + 1],
+ *   out[r] = act(x[row_index[r]] w[g]^T + bias[g]).
+ *   group_start [n_groups + 1] int32 (device), ascending; a group may be empty
+ *   row_index   [n_rows] int32 (device): the row of x, or NULL for x[r] (then
+ *               n_x = n_rows)
+ *   x_bf16 [n_x, n_in], w_bf16 [n_groups, n_out or 2 n_out, n_in], bias
+ *   [n_groups, n_out or 2 n_out] fp32 or NULL, out [n_rows, n_out]
+ * n_rows and n_x: 1 .. FLINT_LINEAR_MAX_ROWS.  Rows of no group, and rows whose
+ * row_index is outside [0, n_x), are left as they were.  What the host cannot
+ * check is kept in bounds on the device: row numbers are clamped to n_rows, and a
+ * group that ends before it begins is empty (rows of two groups are undefined).
+ * The weights of an empty group are not read.  The rest as flint_linear_bf16. */
+flint_status flint_grouped_linear_bf16(const flint_linear_dims* dims, int32_t n_groups,
+                                       int32_t n_rows, const int32_t* group_start,
+                                       const int32_t* row_index, int32_t n_x, const void* x_bf16,
+                                       const void* w_bf16, const float* bias, void* out,
+                                       void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* The routing of n_tokens (1 .. FLINT_PAGED_MAX_TOKENS) tokens from their router
+ * scores, and the order of their (token, slot) pairs by expert, which is what
+ * flint_grouped_linear_bf16 takes (dims as the decode calls).
+ *   logits      [n_tokens, E] fp32
+ *   logit_bias  [E] fp32 or NULL; offsets as dims->offset_mode says
+ *   topk_idx    [n_tokens, k] int32 out, experts in rank order: (logit + offset
+ *               descending, expert ascending); NaN ranks above every number
+ *   topk_w      [n_tokens, k] fp32 out: the sigmoids over their sum; zeros where
+ *               that sum is zero (every kept expert masked by an offset of
+ *               -infinity or the type's lowest value)
+ *   group_start [E + 1] int32 out: the first pair of each expert, then
+ *               n_tokens * k
+ *   row_token   [n_tokens * k] int32 out: the token of each pair, ordered by
+ *               (expert, token)
+ *   pair_row    [n_tokens, k] int32 out: the place of each pair in that order
+ * Pointers need 4-byte alignment; no output may overlap another argument. */
+flint_status flint_moe_select(const flint_moe_dims* dims, int32_t n_tokens, const float* logits,
+                              const float* logit_bias, int32_t* topk_idx, float* topk_w,
+                              int32_t* group_start, int32_t* row_token, int32_t* pair_row,
+                              void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* out[t] = residual[t] + y_shared[t] + sum_j topk_w[t, j] * y[pair_row[t, j]]: the
+ * experts' rows back in the tokens' order.
+ *   residual_bf16, out_bf16 [n_tokens, H]; out may be residual itself
+ *   y_bf16        [n_tokens * k, H]; y_shared_bf16 [n_tokens, H] or NULL
+ *   pair_row, topk_w [n_tokens, k] as flint_moe_select writes them; a pair whose
+ *                 pair_row is outside [0, n_tokens * k) adds nothing
+ * fp32 sums in the order written (residual, shared, slots), rounded once.  Errors
+ * as flint_linear_bf16's; needs no workspace. */
+flint_status flint_moe_combine_bf16(const flint_moe_dims* dims, int32_t n_tokens,
+                                    const void* residual_bf16, const void* y_bf16,
+                                    const int32_t* pair_row, const float* topk_w,
+                                    const void* y_shared_bf16, void* out_bf16,
+                                    cudaStream_t stream);
+
+/* flint_moe_decode_bf16 for prompts: n_tokens in [1, FLINT_PAGED_MAX_TOKENS], the
+ * arguments and the layer as there.  Router scores, selection, gate/up products
+ * grouped by expert (the shared expert the last group), down products and the
+ * combine, chained on the stream.  h and the experts' outputs are rounded to bf16
+ * on the way (each half a step of 2^-8 of values that are summed), so results differ
+ * from flint_moe_decode_bf16's in their last bits; a token whose sixth and seventh
+ * score are within the scores' fp32 rounding may choose either.  workspace:
+ * flint_prompt_workspace_bytes(n_tokens). */
+flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
+                                   const void* x_bf16, const void* residual_bf16,
+                                   const void* w_router_bf16, const float* logit_bias,
+                                   const void* w13_bf16, const void* w2_bf16,
+                                   const void* ws13_bf16, const void* ws2_bf16, void* out_bf16,
+                                   int32_t* topk_idx_out, float* topk_w_out,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Fault-injection hook for tests: arms a one-shot device-side wait, in the
  * next routing launch on this workspace, on a workspace flag that nothing ever

@@ -48,6 +48,10 @@ EXPORTS = (
     "flint_attn_workspace_bytes", "flint_attn_workspace_init",
     "flint_attn_get_device_status", "flint_attn_debug_arm_stall",
     "flint_attn_paged_bf16", "flint_attn_paged_fp8",
+    "flint_prompt_workspace_bytes", "flint_prompt_workspace_init",
+    "flint_prompt_get_device_status", "flint_linear_bf16",
+    "flint_grouped_linear_bf16", "flint_moe_select", "flint_moe_combine_bf16",
+    "flint_moe_prompt_bf16",
 )
 NOALLOC_MAX_BATCH = 8
 # Batches up to which flint_moe_decode_bf16_prenorm is one launch (the
@@ -91,6 +95,16 @@ KV_BLOCK = 16                  # token rows that share a scale in an E4M3 cache
 PAGED_MAX_SEQS, PAGED_MAX_TOKENS = 256, 8192
 PAGED_MAX_LENGTH = 1 << 23     # tokens a row of the page table has room for
 _INT32_MAX = (1 << 31) - 1
+
+# The linear side of a prompt (flint_linear_bf16, flint_grouped_linear_bf16, flint_moe_select,
+# flint_moe_combine_bf16, flint_moe_prompt_bf16).
+FLINT_ACT_NONE, FLINT_ACT_SILU, FLINT_ACT_GELU, FLINT_ACT_SWIGLU = 0, 1, 2, 3
+LINEAR_MAX_ROWS, LINEAR_MAX_IN, LINEAR_MAX_OUT, LINEAR_MAX_GROUPS = 65536, 65536, 1 << 20, 1024
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_in", "n_out", "act", "out_f32")]
+
 
 
 class _PagedBatchStruct(ctypes.Structure):
@@ -166,6 +180,22 @@ def lib() -> ctypes.CDLL:
     L.flint_attn_paged_fp8.restype = ctypes.c_int
     L.flint_attn_paged_fp8.argtypes = ([_P, _P, _I32] + [_P] * 6 + [ctypes.c_float, _I32] +
                                        [_P, _P, _SZ, _P])
+    L.flint_prompt_workspace_bytes.restype = _SZ
+    L.flint_prompt_workspace_bytes.argtypes = [_I32]
+    L.flint_prompt_workspace_init.restype = ctypes.c_int
+    L.flint_prompt_workspace_init.argtypes = [_P, _SZ, _P]
+    L.flint_prompt_get_device_status.restype = ctypes.c_int
+    L.flint_prompt_get_device_status.argtypes = [_P, _P]
+    L.flint_linear_bf16.restype = ctypes.c_int
+    L.flint_linear_bf16.argtypes = [_P, _I32] + [_P] * 6 + [_SZ, _P]
+    L.flint_grouped_linear_bf16.restype = ctypes.c_int
+    L.flint_grouped_linear_bf16.argtypes = [_P, _I32, _I32, _P, _P, _I32] + [_P] * 5 + [_SZ, _P]
+    L.flint_moe_select.restype = ctypes.c_int
+    L.flint_moe_select.argtypes = [_P, _I32] + [_P] * 8 + [_SZ, _P]
+    L.flint_moe_combine_bf16.restype = ctypes.c_int
+    L.flint_moe_combine_bf16.argtypes = [_P, _I32] + [_P] * 7
+    L.flint_moe_prompt_bf16.restype = ctypes.c_int
+    L.flint_moe_prompt_bf16.argtypes = [_P, _I32] + [_P] * 12 + [_SZ, _P]
     _lib = L
     return L
 
@@ -660,6 +690,147 @@ def flint_attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, batch: PagedBatc
             workspace, sinks, window, softmax_scale, stream, dims)
 
 
+# ---------------------------------------------------------------- the linear side of a prompt
+
+def flint_prompt_workspace_bytes(max_tokens: int = 0) -> int:
+    n = operator.index(max_tokens)
+    return int(lib().flint_prompt_workspace_bytes(n)) if 0 <= n <= PAGED_MAX_TOKENS else 0
+
+
+def flint_prompt_workspace_init(workspace: torch.Tensor, stream=None):
+    wp, wb = _ws_only("flint_prompt_workspace_init", workspace)
+    _check(lib().flint_prompt_workspace_init(wp, wb, _stream(stream)), "flint_prompt_workspace_init")
+
+
+def flint_prompt_get_device_status(workspace: torch.Tensor, stream=None) -> int:
+    wp, _ = _ws_only("flint_prompt_get_device_status", workspace)
+    return int(lib().flint_prompt_get_device_status(wp, _stream(stream)))
+
+
+_LINEAR_REFS = {}  # the C struct of a call's dims, by its fields
+
+
+def _linear(f, x, w, out, w_dims, act):
+    """(C struct by reference, device, rows of x, n_in, rows of out, n_out, rows of a
+    weight matrix) of a linear call after checking x, w (of w_dims dimensions) and out."""
+    if not (isinstance(x, _Tensor) and x.is_cuda and x.dim() == 2 and
+            1 <= x.shape[0] <= LINEAR_MAX_ROWS and 8 <= x.shape[1] <= LINEAR_MAX_IN):
+        _bad(f, "x", "[1 to %d rows, 8 to %d] on a CUDA device" % (LINEAR_MAX_ROWS, LINEAR_MAX_IN), x)
+    dev = x.device
+    if dev.index != torch._C._cuda_getDevice():
+        _on_current_device(f, "x", x)
+    if not (isinstance(out, _Tensor) and out.dim() == 2 and 1 <= out.shape[0] <= LINEAR_MAX_ROWS and
+            8 <= out.shape[1] <= LINEAR_MAX_OUT and (out.dtype is _BF16 or out.dtype is _F32)):
+        _bad(f, "out", "a bf16 or float32 tensor [1 to %d rows, 8 to %d]" %
+             (LINEAR_MAX_ROWS, LINEAR_MAX_OUT), out)
+    if not (isinstance(w, _Tensor) and w.dim() == w_dims):
+        _bad(f, "w", "a tensor of %d dimensions" % w_dims, w)
+    key = (x.shape[1], out.shape[1], act, int(out.dtype is _F32))
+    ref = _LINEAR_REFS.get(key)
+    if ref is None:
+        if type(act) is not int or not FLINT_ACT_NONE <= act <= FLINT_ACT_SWIGLU:
+            raise FlintError(FLINT_ERR_UNSUPPORTED, "%s: act must be one of FLINT_ACT_*, got %r" %
+                             (f, act))
+        ref = _LINEAR_REFS.setdefault(key, ctypes.byref(LinearDims(*key)))
+    m = key[1] * 2 if act == FLINT_ACT_SWIGLU else key[1]
+    return ref, dev, x.shape[0], key[0], out.shape[0], key[1], m
+
+
+def flint_linear_bf16(x, w, out, workspace, bias=None, residual=None, act: int = FLINT_ACT_NONE,
+                      stream=None):
+    """out = act(x w^T + bias) + residual: x bf16 [rows, n_in], w bf16 [n_out, n_in]
+    (FLINT_ACT_SWIGLU: [2 n_out, n_in], gate rows first), bias fp32 of one value per row
+    of w, residual and out [rows, n_out] of one type, bf16 or fp32 (residual may be out
+    itself); workspace: new_prompt_workspace()."""
+    f = "flint_linear_bf16"
+    ref, dev, rows, k, r, n, m = _linear(f, x, w, out, 2, act)
+    wp, wb = _ws_arg(f, workspace, dev)
+    _check((_lib or lib()).flint_linear_bf16(
+        ref, rows, _arg(f, "x", x, _BF16, (rows, k), dev), _arg(f, "w", w, _BF16, (m, k), dev),
+        None if bias is None else _arg(f, "bias", bias, _F32, (m,), dev),
+        None if residual is None else _arg(f, "residual", residual, out.dtype, (rows, n), dev),
+        _arg(f, "out", out, out.dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+
+
+def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None, bias=None,
+                              act: int = FLINT_ACT_NONE, stream=None):
+    """out[r] = act(x[row_index[r]] w[g]^T + bias[g]) for the rows group_start[g] <= r <
+    group_start[g + 1] of every group g: w bf16 [groups, n_out, n_in] (FLINT_ACT_SWIGLU:
+    [groups, 2 n_out, n_in]), group_start int32 [groups + 1], row_index int32 of one
+    value per row of out (None: x[r]), bias fp32 [groups, rows of a matrix]."""
+    f = "flint_grouped_linear_bf16"
+    ref, dev, n_x, k, rows, n, m = _linear(f, x, w, out, 3, act)
+    groups = w.shape[0]
+    if not 1 <= groups <= LINEAR_MAX_GROUPS:
+        _bad(f, "w", "of 1 to %d groups" % LINEAR_MAX_GROUPS, w)
+    if row_index is None and n_x != rows:
+        _bad(f, "x", "of as many rows as out has (%d) without row_index" % rows, x)
+    wp, wb = _ws_arg(f, workspace, dev)
+    _check((_lib or lib()).flint_grouped_linear_bf16(
+        ref, groups, rows, _arg(f, "group_start", group_start, _I32T, (groups + 1,), dev),
+        None if row_index is None else _arg(f, "row_index", row_index, _I32T, (rows,), dev),
+        n_x, _arg(f, "x", x, _BF16, (n_x, k), dev), _arg(f, "w", w, _BF16, (groups, m, k), dev),
+        None if bias is None else _arg(f, "bias", bias, _F32, (groups, m), dev),
+        _arg(f, "out", out, out.dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+
+
+def _prompt_tokens(where, name, t, width):
+    """(tokens, device) of a [tokens, width] tensor of a call for prompts."""
+    n, dev = _batch(where, name, t, width)
+    if not 1 <= n <= PAGED_MAX_TOKENS:
+        _bad(where, name, "of 1 to %d tokens" % PAGED_MAX_TOKENS, t)
+    return n, dev
+
+
+def flint_moe_select(logits, logit_bias, topk_idx, topk_w, group_start, row_token, pair_row,
+                     workspace, stream=None, dims: Dims | None = None):
+    """The routing of router scores logits fp32 [T, 256] (topk_idx int32 and topk_w fp32
+    [T, 6]) and the order of the T * 6 pairs by expert: group_start int32 [257],
+    row_token int32 [T * 6], pair_row int32 [T, 6]."""
+    f, d = "flint_moe_select", _d(dims)
+    T, dev = _prompt_tokens(f, "logits", logits, d.n_experts)
+    K = d.top_k
+    args = (_arg(f, "logits", logits, _F32, (T, d.n_experts), dev),
+            _arg(f, "logit_bias", logit_bias, _F32, (d.n_experts,), dev, optional=True),
+            _arg(f, "topk_idx", topk_idx, _I32T, (T, K), dev),
+            _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
+            _arg(f, "group_start", group_start, _I32T, (d.n_experts + 1,), dev),
+            _arg(f, "row_token", row_token, _I32T, (T * K,), dev),
+            _arg(f, "pair_row", pair_row, _I32T, (T, K), dev))
+    wp, wb = _ws_arg(f, workspace, dev)
+    _check((_lib or lib()).flint_moe_select(_dims(dims), T, *args, wp, wb, _stream(stream)), f)
+
+
+def flint_moe_combine_bf16(residual, y, pair_row, topk_w, y_shared, out, stream=None,
+                           dims: Dims | None = None):
+    """out[t] = residual[t] + y_shared[t] + sum_j topk_w[t, j] y[pair_row[t, j]]: bf16
+    residual, out (may be residual itself) and y_shared (or None) [T, 2048], y
+    [T * 6, 2048]."""
+    f, d = "flint_moe_combine_bf16", _d(dims)
+    T, dev = _prompt_tokens(f, "residual", residual, d.hidden)
+    H, K = d.hidden, d.top_k
+    args = (_arg(f, "residual", residual, _BF16, (T, H), dev),
+            _arg(f, "y", y, _BF16, (T * K, H), dev),
+            _arg(f, "pair_row", pair_row, _I32T, (T, K), dev),
+            _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
+            _arg(f, "y_shared", y_shared, _BF16, (T, H), dev, optional=True),
+            _arg(f, "out", out, _BF16, (T, H), dev))
+    _check((_lib or lib()).flint_moe_combine_bf16(_dims(dims), T, *args, _stream(stream)), f)
+
+
+def flint_moe_prompt_bf16(x, residual, w_router, logit_bias, w13, w2, ws13, ws2, out, workspace,
+                          topk_idx_out=None, topk_w_out=None, stream=None,
+                          dims: Dims | None = None):
+    """flint_moe_decode_bf16 for prompts, 1 to 8192 tokens; workspace:
+    new_prompt_workspace(tokens)."""
+    f, d = "flint_moe_prompt_bf16", _d(dims)
+    T, dev = _prompt_tokens(f, "x", x, d.hidden)
+    args = _layer_args(f, d, T, dev, x, residual, w_router, logit_bias, w13, w2, ws13, ws2, out,
+                       topk_idx_out, topk_w_out)
+    wp, wb = _ws_arg(f, workspace, dev)
+    _check((_lib or lib()).flint_moe_prompt_bf16(_dims(dims), T, *args, wp, wb, _stream(stream)), f)
+
+
 # ---------------------------------------------------------------- conveniences
 
 def new_workspace(max_batch: int, device="cuda", wait_limit_ns: int = 0) -> torch.Tensor:
@@ -680,4 +851,15 @@ def new_attn_workspace(device="cuda", dims: AttnDims | None = None) -> torch.Ten
         raise FlintError(FLINT_ERR_UNSUPPORTED, "new_attn_workspace")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     flint_attn_workspace_init(ws)
+    return ws
+
+
+def new_prompt_workspace(max_tokens: int = 0, device="cuda") -> torch.Tensor:
+    """Allocates (through torch) and initialises a workspace of the linear calls, and of
+    flint_moe_prompt_bf16 for up to max_tokens tokens."""
+    n = flint_prompt_workspace_bytes(max_tokens)
+    if n == 0:
+        raise FlintError(FLINT_ERR_INVALID_ARG, "new_prompt_workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    flint_prompt_workspace_init(ws)
     return ws

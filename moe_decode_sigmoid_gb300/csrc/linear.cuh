@@ -1,0 +1,30 @@
+// linear.cuh — what the kernels of the linear side of a prompt share: a group's
+// rows with everything the host could not check kept in bounds, activations.
+#pragma once
+
+#include "common.cuh"
+#include "linear.h"
+
+namespace flint {
+namespace lin {
+
+// Rows [r0, r0 + n) of a group.
+struct Rows {
+  int r0, n;
+};
+__device__ __forceinline__ Rows group_rows(const LinearArgs& a, int g) {
+  if (a.start == nullptr) return {0, a.n_rows};
+  const int lo = min(max(__ldg(a.start + g), 0), a.n_rows);
+  return {lo, min(max(__ldg(a.start + g + 1), lo), a.n_rows) - lo};
+}
+
+// v / (1 + exp(-v)), and v (1 + erf(v / sqrt 2)) / 2 by the complement, which keeps
+// its relative accuracy where 1 + erf cancels.
+__device__ __forceinline__ float activate(float v, int act) {
+  if (act == ACT_SILU) return v / (1.0f + expf(-v));
+  if (act == ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  return v;
+}
+
+}  // namespace lin
+}  // namespace flint

@@ -1,0 +1,70 @@
+// linear.h — argument blocks and launch wrappers of the linear side of a prompt:
+// matrix products with an epilogue, plain or grouped (linear_rows.cu, linear_tiles.cu),
+// and the selection and combine around the experts' products (moe_prompt.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace flint {
+namespace lin {
+constexpr int MAX_ROWS = 65536;
+constexpr int MAX_IN = 65536;
+constexpr int MAX_OUT = 1 << 20;
+constexpr int MAX_GROUPS = 1024;
+constexpr int MAX_TOKENS = 8192;   // of a selection and of the layer
+constexpr int CHUNK = 64;          // tokens a CTA of the selection takes
+constexpr int MAX_CHUNKS = MAX_TOKENS / CHUNK;
+
+// Workspace: error and stall word, the selection's counts, then the layer's arrays.
+constexpr size_t WS_ERROR = 0, WS_STALL = 8, WS_COUNTS = 256;
+constexpr size_t WS_HEAD = WS_COUNTS + sizeof(int) * 256 * (size_t)MAX_CHUNKS;
+}  // namespace lin
+
+enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_SWIGLU = 3 };
+
+// One call: a plain product is one group of all rows (start null).
+struct LinearArgs {
+  const uint16_t* x;       // [n_x, n_in] bf16
+  const uint16_t* w;       // [n_groups, rows of a matrix, n_in] bf16
+  const uint16_t* w_last;  // the last group's matrix lies here, or null
+  const float* bias;       // [n_groups, rows of a matrix] or null
+  const void* residual;    // [n_rows, n_out] of out's type or null
+  void* out;               // [n_rows, n_out]
+  const int32_t* start;    // [n_groups + 1] or null
+  const int32_t* index;    // [n_rows] row of x, or null
+  int n_groups, n_rows, n_x, n_in, n_out, act, out_f32;
+  void* ws;
+};
+// A few rows a group, and any number.
+cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
+
+struct SelectArgs {
+  const float* logits;     // [n, E]
+  const float* bias;       // [E] or null
+  int select_only, n;
+  int* idx;                // [n, TOPK]
+  float* w;                // [n, TOPK]
+  int* start;              // [E + 1], [E + 2] with the shared expert's group
+  int* row_token;          // [n TOPK], [n (TOPK + 1)] with it
+  int* pair_row;           // [n, TOPK]
+  int* idx_out;            // optional copies
+  float* w_out;
+  int shared_group;        // a last group of all tokens
+  int* counts;             // [chunks, E] scratch
+};
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream);
+
+struct CombineArgs {
+  const uint16_t* residual;  // [n, H]
+  const uint16_t* y;         // [n TOPK, H]
+  const uint16_t* y_shared;  // [n, H] or null
+  const int* pair_row;       // [n, TOPK]
+  const float* w;            // [n, TOPK]
+  uint16_t* out;
+  int n;
+};
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
+
+}  // namespace flint

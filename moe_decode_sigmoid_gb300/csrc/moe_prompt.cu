@@ -1,0 +1,233 @@
+// moe_prompt.cu — around the experts' grouped products: the selection of every
+// token's experts with the order of all (token, slot) pairs by expert, and the
+// weighted sum that brings the experts' rows back to the tokens.
+#include "common.cuh"
+#include "linear.h"
+#include "select.cuh"
+
+namespace flint {
+namespace {
+
+using namespace lin;
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+static_assert(E == THREADS, "a thread has an expert");
+constexpr int WORDS = CHUNK / 32;
+
+// The top k of one token's scores by one warp, as topk_warp ranks them, for scores of
+// any bits: zeros are equal whatever their sign, NaN ranks above every number, and the
+// weights are zeros where all the kept sigmoids are.
+__device__ __forceinline__ void topk_any(const float* row, const float* bias, bool select_only,
+                                         int& idx_out, float& w_out) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k[8], e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float score = __ldg(row + lane + 32 * j);
+    // + 0 makes -0 the other zero
+    const float key = (bias != nullptr ? score + __ldg(bias + lane + 32 * j) : score) + 0.0f;
+    k[j] = key == key ? f2key(key) : ~0u;
+    e[j] = (uint32_t)(lane + 32 * j);
+  }
+  int sel_e[TOPK];
+  float sel_v[TOPK];
+  topk_rank(k, e, sel_e, sel_v);
+  float mine = 0.0f;
+  idx_out = 0;
+#pragma unroll
+  for (int r = 0; r < TOPK; ++r)
+    if (r == lane) {
+      mine = sel_v[r];
+      idx_out = sel_e[r];
+    }
+  if (select_only && lane < TOPK) mine = __ldg(row + idx_out);
+  const float s = 1.0f / (1.0f + expf(-mine));
+  float sum = 0.0f;
+#pragma unroll
+  for (int r = 0; r < TOPK; ++r) sum += __shfl_sync(0xffffffffu, s, r);
+  w_out = sum == 0.0f ? 0.0f : s / sum;
+}
+
+// Ranks of a chunk's pairs: an expert's tokens are the bits of a mask (an expert
+// is at most once among a token's), so a pair's rank among its expert's is the bits
+// below its token's, whatever order the warps ran in.
+struct Chunk {
+  uint32_t mask[E][WORDS];
+  int base[E];      // first row of the expert's pairs of this chunk
+  int warp_tot[8];
+};
+
+__device__ __forceinline__ void copy_choice(const SelectArgs& a, int p, int e, float w) {
+  a.idx[p] = e;
+  a.w[p] = w;
+  if (a.idx_out != nullptr) a.idx_out[p] = e;
+  if (a.w_out != nullptr) a.w_out[p] = w;
+}
+
+// The top k of the chunk's tokens, a warp each, and the experts' masks.
+__device__ __forceinline__ void choose(const SelectArgs& a, Chunk& sh, int t0, int n) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < E * WORDS; i += THREADS) (&sh.mask[0][0])[i] = 0;
+  __syncthreads();
+  for (int t = warp; t < n; t += WARPS) {
+    int e;
+    float w;
+    topk_any(a.logits + (size_t)(t0 + t) * E, a.bias, a.select_only != 0, e, w);
+    if (lane < TOPK) {
+      atomicOr(&sh.mask[e][t >> 5], 1u << (t & 31));
+      copy_choice(a, (t0 + t) * TOPK + lane, e, w);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int mask_count(const uint32_t (&m)[WORDS]) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) n += __popc(m[i]);
+  return n;
+}
+
+// Rows of the chunk's pairs, once sh.base is known.
+__device__ __forceinline__ void place(const SelectArgs& a, Chunk& sh, int t0, int n) {
+  for (int p = threadIdx.x; p < n * TOPK; p += THREADS) {
+    const int t = p / TOPK, e = a.idx[t0 * TOPK + p];
+    int row = sh.base[e];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      if (32 * i <= t) row += __popc(sh.mask[e][i] & (t - 32 * i >= 32 ? ~0u : (1u << (t - 32 * i)) - 1u));
+    a.row_token[row] = t0 + t;
+    a.pair_row[t0 * TOPK + p] = row;
+  }
+  if (a.shared_group)
+    for (int t = threadIdx.x; t < n; t += THREADS) a.row_token[a.n * TOPK + t0 + t] = t0 + t;
+}
+
+__device__ __forceinline__ void write_start(const SelectArgs& a, int excl) {
+  a.start[threadIdx.x] = excl;
+  if (threadIdx.x == 0) {
+    a.start[E] = a.n * TOPK;
+    if (a.shared_group) a.start[E + 1] = a.n * (TOPK + 1);
+  }
+}
+
+// All tokens in one CTA.
+__global__ void __launch_bounds__(THREADS) select_small_kernel(const SelectArgs a) {
+  __shared__ Chunk sh;
+  pdl_wait();
+  pdl_trigger();
+  choose(a, sh, 0, a.n);
+  int total;
+  const int cnt = mask_count(sh.mask[threadIdx.x]);
+  const int excl = scan256(cnt, sh.warp_tot, &total, [] { __syncthreads(); });
+  sh.base[threadIdx.x] = excl;
+  write_start(a, excl);
+  __syncthreads();
+  place(a, sh, 0, a.n);
+}
+
+__global__ void __launch_bounds__(THREADS) select_choose_kernel(const SelectArgs a) {
+  __shared__ Chunk sh;
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, a.n - t0);
+  choose(a, sh, t0, n);
+  a.counts[blockIdx.x * E + threadIdx.x] = mask_count(sh.mask[threadIdx.x]);
+}
+
+__global__ void __launch_bounds__(THREADS) select_place_kernel(const SelectArgs a) {
+  __shared__ Chunk sh;
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, a.n - t0);
+  for (int i = threadIdx.x; i < E * WORDS; i += THREADS) (&sh.mask[0][0])[i] = 0;
+  int before = 0, all = 0;
+#pragma unroll 16
+  for (int i = 0; i < (int)gridDim.x; ++i) {
+    const int v = __ldcg(a.counts + i * E + threadIdx.x);
+    all += v;
+    if (i < (int)blockIdx.x) before += v;
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < n * TOPK; p += THREADS) {
+    const int t = p / TOPK;
+    atomicOr(&sh.mask[a.idx[t0 * TOPK + p]][t >> 5], 1u << (t & 31));
+  }
+  int total;
+  const int excl = scan256(all, sh.warp_tot, &total, [] { __syncthreads(); });
+  sh.base[threadIdx.x] = excl + before;
+  if (blockIdx.x == 0) write_start(a, excl);
+  __syncthreads();
+  place(a, sh, t0, n);
+}
+
+// A token a CTA, 8 values of the row a thread.
+__global__ void __launch_bounds__(THREADS) combine_kernel(const CombineArgs a) {
+  static_assert(H == 8 * THREADS, "8 values a thread");
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x;
+  const size_t at = (size_t)t * H + 8 * threadIdx.x;
+  int row[TOPK];
+  float w[TOPK];
+#pragma unroll
+  for (int j = 0; j < TOPK; ++j) {
+    row[j] = __ldg(a.pair_row + t * TOPK + j);
+    w[j] = __ldg(a.w + t * TOPK + j);
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 v[TOPK], s = zero;
+  const uint4 r = __ldcs(reinterpret_cast<const uint4*>(a.residual + at));
+  if (a.y_shared != nullptr) s = __ldcs(reinterpret_cast<const uint4*>(a.y_shared + at));
+#pragma unroll
+  for (int j = 0; j < TOPK; ++j) {
+    v[j] = zero;
+    if ((unsigned)row[j] < (unsigned)(a.n * TOPK))
+      v[j] = __ldcs(reinterpret_cast<const uint4*>(a.y + (size_t)row[j] * H + 8 * threadIdx.x));
+    else
+      w[j] = 0.0f;
+  }
+  const uint32_t rw[4] = {r.x, r.y, r.z, r.w}, sw[4] = {s.x, s.y, s.z, s.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo = bf_lo(rw[i]) + bf_lo(sw[i]), hi = bf_hi(rw[i]) + bf_hi(sw[i]);
+#pragma unroll
+    for (int j = 0; j < TOPK; ++j) {
+      const uint32_t y = i == 0 ? v[j].x : i == 1 ? v[j].y : i == 2 ? v[j].z : v[j].w;
+      lo = fmaf(w[j], bf_lo(y), lo);
+      hi = fmaf(w[j], bf_hi(y), hi);
+    }
+    o[i] = pack_bf2(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(a.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <class Args>
+cudaError_t launch(void (*kernel)(const Args), int grid, const Args& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
+  const int chunks = (a.n + CHUNK - 1) / CHUNK;
+  if (chunks == 1) return launch(select_small_kernel, 1, a, stream);
+  const cudaError_t e = launch(select_choose_kernel, chunks, a, stream);
+  return e != cudaSuccess ? e : launch(select_place_kernel, chunks, a, stream);
+}
+
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
+  return launch(combine_kernel, a.n, a, stream);
+}
+
+}  // namespace flint

@@ -30,37 +30,18 @@ __device__ __forceinline__ void topk_cas(uint32_t (&k)[E / 32], uint32_t (&e)[E 
   e[j] = swap ? ei : e[j];
 }
 
-// Top-k of one token's E router scores by one warp.  The ranking key of
-// expert e is its score plus its logit offset (bias, may be null); lane l
-// holds experts l + 32 j and first sorts its 8 (key, expert) pairs -- key
-// descending, expert ascending -- with a 19-comparator sorting network
-// (Batcher's odd-even merge sort).  Each round then takes the largest lane
-// head; among equal keys the lowest expert index wins (a lane's head is its
-// lowest index for that key, and across lanes the minimum index is taken).
-// Each kept expert's weight is the sigmoid of its key -- or, with
-// select_only, of its score without the offset -- divided by the sum over the
-// kept experts.  Lanes 0..k-1 return slot `lane`'s expert and weight.
-template <bool GLOBAL_SRC>
-__device__ __forceinline__ void topk_warp(const float* logits_row, const float* bias,
-                                          bool select_only, int& idx_out, float& w_out) {
+// The k best of a warp's E (key, expert) pairs, lane l's being those of experts
+// l + 32 j in k[j], e[j] (which it consumes): sel_e, sel_v in rank order, in every lane.
+__device__ __forceinline__ void topk_rank(uint32_t (&k)[E / 32], uint32_t (&e)[E / 32],
+                                          int (&sel_e)[TOPK], float (&sel_v)[TOPK]) {
   static_assert(E / 32 == 8, "the sorting network is written for 8 values per lane");
   const int lane = threadIdx.x & 31;
-  uint32_t k[8], e[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float score =
-        GLOBAL_SRC ? __ldcg(logits_row + lane + 32 * j) : logits_row[lane + 32 * j];
-    k[j] = f2key(bias ? score + __ldg(bias + lane + 32 * j) : score);
-    e[j] = (uint32_t)(lane + 32 * j);
-  }
   topk_cas(k, e, 0, 1); topk_cas(k, e, 2, 3); topk_cas(k, e, 4, 5); topk_cas(k, e, 6, 7);
   topk_cas(k, e, 0, 2); topk_cas(k, e, 1, 3); topk_cas(k, e, 4, 6); topk_cas(k, e, 5, 7);
   topk_cas(k, e, 1, 2); topk_cas(k, e, 5, 6);
   topk_cas(k, e, 0, 4); topk_cas(k, e, 1, 5); topk_cas(k, e, 2, 6); topk_cas(k, e, 3, 7);
   topk_cas(k, e, 2, 4); topk_cas(k, e, 3, 5);
   topk_cas(k, e, 1, 2); topk_cas(k, e, 3, 4); topk_cas(k, e, 5, 6);
-  int sel_e[TOPK];
-  float sel_v[TOPK];
 #pragma unroll
   for (int r = 0; r < TOPK; ++r) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, k[0]);
@@ -82,6 +63,33 @@ __device__ __forceinline__ void topk_warp(const float* logits_row, const float* 
     sel_e[r] = (int)win;
     sel_v[r] = key2f(top);
   }
+}
+
+// Top-k of one token's E router scores by one warp.  The ranking key of
+// expert e is its score plus its logit offset (bias, may be null); lane l
+// holds experts l + 32 j and first sorts its 8 (key, expert) pairs -- key
+// descending, expert ascending -- with a 19-comparator sorting network
+// (Batcher's odd-even merge sort).  Each round then takes the largest lane
+// head; among equal keys the lowest expert index wins (a lane's head is its
+// lowest index for that key, and across lanes the minimum index is taken).
+// Each kept expert's weight is the sigmoid of its key -- or, with
+// select_only, of its score without the offset -- divided by the sum over the
+// kept experts.  Lanes 0..k-1 return slot `lane`'s expert and weight.
+template <bool GLOBAL_SRC>
+__device__ __forceinline__ void topk_warp(const float* logits_row, const float* bias,
+                                          bool select_only, int& idx_out, float& w_out) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k[8], e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float score =
+        GLOBAL_SRC ? __ldcg(logits_row + lane + 32 * j) : logits_row[lane + 32 * j];
+    k[j] = f2key(bias ? score + __ldg(bias + lane + 32 * j) : score);
+    e[j] = (uint32_t)(lane + 32 * j);
+  }
+  int sel_e[TOPK];
+  float sel_v[TOPK];
+  topk_rank(k, e, sel_e, sel_v);
   // Lane r < k computes sigmoid r; every lane then sums the k values in rank
   // order (the same order and rounding in every lane).
   float sv = 0.f, mine = 0.f;
