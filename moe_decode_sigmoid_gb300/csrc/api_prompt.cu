@@ -13,7 +13,7 @@ using namespace flint;
 namespace {
 
 static_assert(FLINT_LINEAR_MAX_ROWS == lin::MAX_ROWS && FLINT_LINEAR_MAX_IN == lin::MAX_IN &&
-                  FLINT_LINEAR_MAX_OUT == lin::MAX_OUT && FLINT_LINEAR_MAX_GROUPS == lin::MAX_GROUPS &&
+                  FLINT_LINEAR_MAX_OUT == lin::MAX_OUT && FLINT_LINEAR_MAX_GROUPS == lin::GROUP_LIMIT &&
                   FLINT_PAGED_MAX_TOKENS == lin::MAX_TOKENS,
               "the public limits are the kernels'");
 static_assert(FLINT_ACT_NONE == ACT_NONE && FLINT_ACT_SILU == ACT_SILU && FLINT_ACT_GELU == ACT_GELU &&
@@ -74,7 +74,10 @@ bool any_overlap(const Span (&s)[N], int n_out) {
 }
 
 flint_status launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  return cuda_status(launch_linear_rows(a, stream));
+  if (a.start == nullptr && a.n_rows <= 32) return cuda_status(launch_linear_rows(a, stream));
+  const int sms = num_sms();
+  if (sms < 2) return FLINT_ERR_CUDA;
+  return cuda_status(launch_linear_tiles(a, sms, stream));
 }
 
 bool ws_ok(const void* ws, size_t bytes, int tokens) { return req(ws) && bytes >= workspace_bytes(tokens); }

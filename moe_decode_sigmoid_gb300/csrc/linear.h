@@ -12,7 +12,7 @@ namespace lin {
 constexpr int MAX_ROWS = 65536;
 constexpr int MAX_IN = 65536;
 constexpr int MAX_OUT = 1 << 20;
-constexpr int MAX_GROUPS = 1024;
+constexpr int GROUP_LIMIT = 1024;
 constexpr int MAX_TOKENS = 8192;   // of a selection and of the layer
 constexpr int CHUNK = 64;          // tokens a CTA of the selection takes
 constexpr int MAX_CHUNKS = MAX_TOKENS / CHUNK;
@@ -39,6 +39,7 @@ struct LinearArgs {
 };
 // A few rows a group, and any number.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream);
 
 struct SelectArgs {
   const float* logits;     // [n, E]

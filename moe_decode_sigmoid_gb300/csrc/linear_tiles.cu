@@ -1,0 +1,729 @@
+// linear_tiles.cu — matrix products of many rows, plain or grouped, on the tensor
+// cores' tcgen05 path.
+//
+// D^T = W X^T: the weights' rows are the M side of the product (128 a CTA, TMEM
+// lanes) and the rows of x the N side, 32 to 256 of them (TMEM columns), so that a
+// group of few rows costs few columns and its weights are read once.  With CG = 2 a
+// cluster of two CTAs works on one tile of 256 weight rows (cta_group::2): each loads
+// its 128 weight rows and half the rows of x.  SwiGLU: a CTA's 128 weight rows are
+// blocks of 16 gate and the 16 up rows of the same outputs (one 5-dimensional tensor
+// copy), so that a warp of the epilogue has both in its 32 lanes.
+//
+// One CTA per SM, persistent:
+//   warp 0      copies W, 64 k a stage (TMA, 128-byte swizzle)
+//   warp 1      issues the products (of the pair: the first CTA's)
+//   warps 2, 3, 12, 13  copy X: boxes of rows, or four rows an instruction where an
+//               index says which
+//   warps 4-11  epilogue: bias, activation and residual on fragments of 16 outputs x
+//               8 rows, transposed to rows through shared memory 8 x 8 at a time
+// TMEM holds two accumulators: a tile's epilogue runs beside the next one's products.
+//
+// Groups: the tiles' costs (their rows, and COST0 for what a tile costs besides) are
+// laid end to end and cut into equal shares, a tile belonging to the share where it
+// begins.  Plain products, tiles of one cost, are dealt out in turn.
+#include "linear.cuh"
+#include "tcgen05.cuh"
+#include "tmap.h"
+
+namespace flint {
+namespace {
+
+using namespace lin;
+
+constexpr int THREADS = 448, WARPS = THREADS / 32;
+constexpr int EPI0 = 4, EPI_WARPS = 8;     // warps of the epilogue, two a quarter of TMEM's lanes
+constexpr int X_WARPS = 4;                // warps 2, 3, 12, 13 copy X of groups
+constexpr int KS = 64;                    // k of a stage: a 128-byte row
+constexpr int A_BYTES = 128 * KS * 2;
+constexpr int MAX_STAGES = 12;
+constexpr int STAGE_AREA = 192 * 1024;
+constexpr int EPI_BYTES = 32 * 48;        // a warp's 16 rows of 32 outputs or 32 of 16, padded
+constexpr int SMEM = STAGE_AREA + EPI_WARPS * EPI_BYTES + 1024;
+constexpr int NT_MAX = 256;
+constexpr int COST0 = 64;                 // of a tile, in rows
+constexpr int STRIP = 8;                  // tiles of weights that share their rows of x in L2
+
+struct Shared {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained, never;
+  uint32_t tmem;
+  int fail;
+  long long warp_tot[WARPS];
+  long long pre[GROUP_LIMIT + 2];          // cost of all tiles before a group's
+};
+static_assert(SMEM + sizeof(Shared) <= 227 * 1024, "fits");
+
+// Tensor maps: the weights (all groups but a last one of its own, and that one), x.
+struct Maps {
+  CUtensorMap w, w_last, x;
+};
+
+struct Plan {
+  int nt;          // most rows of a tile, a multiple of 32
+  int stages, stage_bytes;
+  int n_m;         // tiles of weight rows of a group
+  int k_steps;
+  int box_rows;    // rows of a box of x; 0: four rows an instruction by index
+  int n_main;      // groups whose weights are in the first map
+  int x_warps;     // warps that copy X: X_WARPS for groups, 1
+};
+
+struct Tile {
+  int g, m, r0, n, rows;  // group, tile of weight rows, first row, rows rounded up, rows
+};
+
+template <int CG>
+struct Ops {
+  static __device__ __forceinline__ void alloc(uint32_t word) {
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(word) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tc::alloc512(word);
+    }
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t t) {
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+    else
+      tc::dealloc512(t);
+  }
+  static __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+    if constexpr (CG == 2)
+      asm volatile(
+          "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
+          "  mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
+          "  tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
+          "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "r"(tc::DESC_HI)
+          : "memory");
+    else
+      tc::mma_ss<false>(d, a_lo, b_lo, idesc, add);
+  }
+  // One arrival on `bar` of every CTA of the tile once all earlier products are complete.
+  static __device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (CG == 2)
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+          "h"((uint16_t)3)
+          : "memory");
+    else
+      tc::commit(bar);
+  }
+  // The address of the first CTA's barrier, for the copies and arrivals of both.
+  static __device__ __forceinline__ uint32_t leader(uint32_t bar) {
+    if constexpr (CG == 2) {
+      uint32_t r;
+      asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+      return r;
+    }
+    return bar;
+  }
+  // Relaxed: neither arrival publishes a write of the thread's, and with the default
+  // release each cost ~1000 cycles behind the copies (stores) the thread had under way:
+  // 33 x 4096 -> 2048 54 us with it, 24 without, 8192 x 2048 -> 2 x 4096 381, 178.
+  static __device__ __forceinline__ void expect(uint32_t leader_bar, uint32_t bytes) {
+    if constexpr (CG == 2)
+      asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar), "r"(bytes)
+                   : "memory");
+    else
+      asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(leader_bar), "r"(bytes)
+                   : "memory");
+  }
+  static __device__ __forceinline__ void arrive(uint32_t leader_bar) {
+    if constexpr (CG == 2)
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+    else
+      asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+  }
+  static __device__ __forceinline__ void sync_all() {
+    if constexpr (CG == 2) {
+      asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  }
+#define FLINT_GROUP_COPY(DIM, MODE, COORDS, ...)                                                                       \
+  if constexpr (CG == 2)                                                                                               \
+    asm volatile("cp.async.bulk.tensor." DIM ".shared::cluster.global." MODE                                           \
+                 ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, " COORDS "], [%2];" ::"r"(dst), "l"(map),      \
+                 "r"(bar), __VA_ARGS__                                                                                 \
+                 : "memory");                                                                                          \
+  else                                                                                                                 \
+    asm volatile("cp.async.bulk.tensor." DIM ".shared::cluster.global." MODE                                           \
+                 ".mbarrier::complete_tx::bytes [%0], [%1, " COORDS "], [%2];" ::"r"(dst), "l"(map), "r"(bar),         \
+                 __VA_ARGS__                                                                                           \
+                 : "memory")
+  static __device__ __forceinline__ void copy2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    FLINT_GROUP_COPY("2d", "tile", "{%3, %4}", "r"(x), "r"(y));
+  }
+  static __device__ __forceinline__ void copy3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    FLINT_GROUP_COPY("3d", "tile", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
+  }
+  static __device__ __forceinline__ void copy5(uint32_t dst, const CUtensorMap* map, int x, int block, int g, uint32_t bar) {
+    FLINT_GROUP_COPY("5d", "tile", "{%3, %6, %6, %4, %5}", "r"(x), "r"(block), "r"(g), "r"(0));
+  }
+  static __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
+    FLINT_GROUP_COPY("2d", "tile::gather4", "{%3, %4, %5, %6, %7}", "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]));
+  }
+#undef FLINT_GROUP_COPY
+};
+
+// 32 (16) columns of 16 TMEM lanes: register 4 j + i of lane 4 r + c is row r + 8 (i / 2),
+// column 8 j + 2 c + i % 2.
+__device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// Four 8 x 8 blocks of 16-bit elements, transposed on the way; lane l has the address
+// of row l % 8 of block l / 8.
+__device__ __forceinline__ void st_blocks(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ld_blocks(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Waits for a phase, a second at most, by a whole warp, which goes on converged; a
+// wait that runs out (in any warp) ends every other one of the CTA too.
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, uint32_t parity) {
+  const uint32_t b = smem_addr(&bar);
+  bool ok = mbar_try_wait(b, parity);
+  if (!ok) {
+    const uint64_t deadline = globaltimer_ns() + 1000000000ull;
+    while (!(ok = mbar_try_wait(b, parity))) {
+      if (*reinterpret_cast<volatile int*>(&sh.fail) != 0) break;
+      if (globaltimer_ns() > deadline) {
+        *reinterpret_cast<volatile int*>(&sh.fail) = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The tiles of one CTA (pair), in order.
+struct Walk {
+  const LinearArgs& a;
+  const Plan& p;
+  const Shared& sh;
+  int unit, units;              // this pair, pairs
+  // plain: the tile's number; groups: where the share goes on and ends
+  int t, tiles, tiles_n;
+  long long at, end;
+  int g, i, count, cost, size;  // group, tile in it, tiles, a tile's cost, a tile's rows
+  Rows rows;
+
+  __device__ __forceinline__ Walk(const LinearArgs& a_, const Plan& p_, const Shared& sh_, int unit_, int units_)
+      : a(a_), p(p_), sh(sh_), unit(unit_), units(units_) {
+    if (a.start == nullptr) {
+      tiles_n = (a.n_rows + p.nt - 1) / p.nt;
+      tiles = tiles_n * p.n_m;
+      t = unit;
+    } else {
+      const long long total = sh.pre[a.n_groups];
+      at = total * unit / units;
+      end = total * (unit + 1) / units;
+      if (at < end) {
+        enter();
+        // the first tile that begins here
+        i = (int)((at - sh.pre[g] + cost - 1) / cost);
+        settle();
+      }
+    }
+  }
+  // The group that the place `at` (before the end of all) falls in.
+  __device__ __forceinline__ void enter() {
+    int lo = 0, hi = a.n_groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sh.pre[mid + 1] > at) hi = mid;
+      else lo = mid + 1;
+    }
+    g = lo;
+    i = 0;
+    rows = group_rows(a, g);
+    const int nt_g = max((rows.n + p.nt - 1) / p.nt, 1);
+    size = tile_rows(rows.n, p.nt);
+    count = nt_g * p.n_m;
+    cost = size + COST0;
+  }
+  __device__ __forceinline__ void settle() {
+    at = sh.pre[g] + (long long)i * cost;
+    if (i >= count && at < end) enter();
+  }
+  // Rows of a group's tiles: of so many as nt asks for, alike but for the last.
+  static __device__ __forceinline__ int tile_rows(int n, int nt) {
+    const int k = max((n + nt - 1) / nt, 1);
+    return ((n + k - 1) / k + 31) & ~31;
+  }
+  __device__ __forceinline__ bool more() const { return a.start == nullptr ? t < tiles : at < end; }
+  __device__ __forceinline__ Tile get() const {
+    Tile o;
+    if (a.start == nullptr) {
+      const int strip = t / (STRIP * tiles_n), in = t - strip * STRIP * tiles_n;
+      const int width = min(STRIP, p.n_m - strip * STRIP);
+      const int n = in / width;
+      o.g = 0;
+      o.m = strip * STRIP + in - n * width;
+      o.r0 = n * p.nt;
+      o.n = p.nt;
+      o.rows = min(p.nt, a.n_rows - o.r0);
+    } else {
+      const int n = i / p.n_m;
+      o.g = g;
+      o.m = i - n * p.n_m;
+      o.r0 = rows.r0 + n * size;
+      // the last tile of a group may have fewer rows, or (rounding) none
+      o.rows = max(min(size, rows.n - n * size), 0);
+      o.n = max((o.rows + 31) & ~31, 32);
+    }
+    return o;
+  }
+  __device__ __forceinline__ void next() {
+    if (a.start == nullptr) {
+      t += units;
+    } else {
+      ++i;
+      settle();
+    }
+  }
+};
+
+// silu of an output that is rounded to bf16: exponential and quotient of the fast
+// kind, within 2^-18 of the value (|v| < 32; below, both are zero to 2^-40).
+__device__ __forceinline__ float silu_bf16(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
+template <int CG, bool SWIGLU>
+__global__ void __launch_bounds__(THREADS, 1)
+    linear_tiles_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Plan p,
+                        const __grid_constant__ Maps maps) {
+  using O = Ops<CG>;
+  constexpr int FE = SWIGLU ? 64 : 128;   // outputs of a CTA's tile
+  constexpr int WF = FE / 4;              // of a warp
+  constexpr int ROW = WF * 2 + 16;        // bytes of a row of the transposition
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const uint32_t smem = (smem_addr(s_raw) + 1023u) & ~1023u;
+
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), (1 + p.x_warps) * CG);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.acc_full[i]), 1);
+      mbar_init(smem_addr(&sh.acc_empty[i]), EPI_WARPS * CG);
+    }
+    mbar_init(smem_addr(&sh.drained), 1);
+    mbar_init(smem_addr(&sh.never), 1);
+    sh.fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) O::alloc(smem_addr(&sh.tmem));
+  pdl_wait();
+  pdl_trigger();
+
+  if (a.start != nullptr) {
+    // Costs before each group: a thread sums a few neighbouring groups, then a scan.
+    const int per = (a.n_groups + THREADS - 1) / THREADS, g0 = min(tid * per, a.n_groups), g1 = min(g0 + per, a.n_groups);
+    long long sum = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int n = group_rows(a, g).n;
+      sh.pre[g] = sum;
+      if (n > 0) sum += (long long)((n + p.nt - 1) / p.nt) * p.n_m * (Walk::tile_rows(n, p.nt) + COST0);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.warp_tot[warp] = incl;
+    __syncthreads();
+    long long base = incl - sum, all = 0;
+    for (int i = 0; i < WARPS; ++i) {
+      if (i < warp) base += sh.warp_tot[i];
+      all += sh.warp_tot[i];
+    }
+    for (int g = g0; g < g1; ++g) sh.pre[g] += base;
+    if (tid == 0) sh.pre[a.n_groups] = all;
+  }
+  tc::fence_before();
+  __syncthreads();
+  O::sync_all();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+
+  // Which of the warps that copy X this is.
+  const int xw = warp == 2 ? 0 : warp == 3 ? 1 : warp >= EPI0 + EPI_WARPS ? warp - EPI0 - EPI_WARPS + 2 : X_WARPS;
+  if (warp == 0 || xw < p.x_warps) {
+    // ===== copies: W (warp 0), X (the others) ======================================
+    int s = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next()) {
+      const Tile t = walk.get();
+      const bool main = t.g < p.n_main;
+      const CUtensorMap* wm = main ? &maps.w : &maps.w_last;
+      const int wg = main ? t.g : 0;
+      const int f = (t.m * CG + rank) * FE;
+      const int rows_b = t.n / CG, row0 = t.r0 + rank * rows_b;
+      const uint32_t bytes = (p.box_rows > 0 ? p.box_rows : 4) * KS * 2;   // of a copy of X
+      int y[4] = {}, copies = 0, box = 0;
+      if (warp != 0) {
+        const int all = rows_b * KS * 2 / bytes;
+        copies = (all - xw + p.x_warps - 1) / p.x_warps;
+        box = lane * p.x_warps + xw;
+        if (p.box_rows > 0) {
+          y[0] = row0 + box * p.box_rows;
+        } else if (lane < copies) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // A row of no index is not stored: any row will do.
+            const int r = row0 + 4 * box + j;
+            if (r < a.n_rows) y[j] = __ldg(a.index + r);
+            if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
+          }
+        }
+      }
+      for (int k = 0; k < p.k_steps; ++k) {
+        if (!(ok = warp_wait(sh, sh.empty[s], phase))) break;
+        const uint32_t bar = O::leader(smem_addr(&sh.full[s])), dst = smem + s * p.stage_bytes;
+        if (warp == 0) {
+          if (tc::one_thread()) {
+            O::expect(bar, A_BYTES);
+            if constexpr (SWIGLU) O::copy5(dst, wm, k * KS, f / 16, wg, bar);
+            else O::copy3(dst, wm, k * KS, f, wg, bar);
+          }
+        } else {
+          if (lane == 0) O::expect(bar, copies * bytes);
+          __syncwarp();
+          if (lane < copies) {
+            if (p.box_rows > 0) O::copy2(dst + A_BYTES + box * bytes, &maps.x, k * KS, y[0], bar);
+            else O::gather4(dst + A_BYTES + box * bytes, &maps.x, k * KS, y, bar);
+          }
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // A wait ran out: what was asked for lands long before this.
+    if (*reinterpret_cast<volatile int*>(&sh.fail) != 0)
+      for (const uint64_t until = globaltimer_ns() + 50000000ull; globaltimer_ns() < until;) {}
+  } else if (warp == 1 && rank == 0) {
+    // ===== products ================================================================
+    const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
+    int s = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    if (unit == 0 && __ldcg(reinterpret_cast<const int*>(static_cast<const char*>(a.ws) + WS_STALL)) != 0) {
+      if (lane == 0) *reinterpret_cast<int*>(static_cast<char*>(a.ws) + WS_STALL) = 0;   // the test hook
+      ok = warp_wait(sh, sh.never, 0);
+    }
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
+      const int n = __shfl_sync(0xffffffffu, walk.get().n, 0);
+      const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
+      const int b = it & 1;
+      const uint32_t d = d0 + b * NT_MAX;
+      if (!(ok = warp_wait(sh, sh.acc_empty[b], ((it >> 1) & 1) ^ 1))) break;
+      tc::fence_after();
+      for (int k = 0; k < p.k_steps; ++k) {
+        if (!(ok = warp_wait(sh, sh.full[s], phase))) break;
+        tc::fence_after();
+        const uint32_t at = smem + s * p.stage_bytes;
+        const uint32_t a_lo = tc::desc_lo(at, 16), b_lo = tc::desc_lo(at + A_BYTES, 16);
+        if (tc::one_thread()) {
+#pragma unroll
+          for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + 2 * j, idesc, k > 0 || j > 0);
+          O::commit(smem_addr(&sh.empty[s]));
+          if (k == p.k_steps - 1) O::commit(smem_addr(&sh.acc_full[b]));
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // Every product is complete before the TMEM is given back (and has arrived in both CTAs
+    // before they leave).
+    if (tc::one_thread()) O::commit(smem_addr(&sh.drained));
+    __syncwarp();
+    mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
+  } else if (warp >= EPI0 && warp < EPI0 + EPI_WARPS) {
+    // ===== epilogue ================================================================
+    const int w = warp & 3, half = (warp - EPI0) >> 2, r = lane >> 2, c = lane & 3;
+    const uint32_t stage = smem + STAGE_AREA + (warp - EPI0) * EPI_BYTES;
+    const uint32_t t0 = tmem + ((uint32_t)(32 * w) << 16);
+    const int m = a.n_out * (SWIGLU ? 2 : 1);
+    // Where this lane's rows of the 8 x 8 blocks lie.
+    const uint32_t block = SWIGLU ? stage + ((lane >> 4) * 8 + (lane & 7)) * ROW + ((lane >> 3) & 1) * 16
+                                  : stage + (lane & 7) * ROW + (lane >> 3) * 16;
+    constexpr int PARTS = WF / 8;           // 16-byte parts of a row
+    constexpr int CH = SWIGLU ? 32 : 16;    // rows of x at a time: 16 outputs a lane
+    bool ok = true;
+    int it = 0;
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
+      const Tile t = walk.get();
+      const int f0 = (t.m * CG + rank) * FE + WF * w;
+      const int b = it & 1;
+      float bias[4] = {};
+      if (a.bias != nullptr) {
+        const float* src = a.bias + (size_t)t.g * m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int f = SWIGLU ? f0 + r + 8 * (i & 1) : f0 + r + 8 * i;
+          if (f < a.n_out) bias[i] = __ldg(src + f + (SWIGLU && i >= 2 ? a.n_out : 0));
+        }
+      }
+      if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
+      tc::fence_after();
+      const int chunks = t.n / CH;
+      if (half >= chunks && lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
+      // Two warps have the same lanes; each takes every other CH rows.
+      for (int ch = half; ch < chunks; ch += 2) {
+        const int row0 = t.r0 + CH * ch, left = t.rows - CH * ch;
+        // Residual rows, as they lie, while the accumulators are read.
+        uint4 res[2];
+        if (!a.out_f32 && a.residual != nullptr)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+            res[i] = make_uint4(0, 0, 0, 0);
+            if (tok < left && f < a.n_out)
+              res[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
+                                                       (size_t)(row0 + tok) * a.n_out + f);
+          }
+        uint32_t lo[CH / 2], hi[CH / 2];
+        ld_frag(t0 + b * NT_MAX + CH * ch, lo);
+        ld_frag(t0 + b * NT_MAX + CH * ch + (16u << 16), hi);
+        tc::wait_ld();
+        tc::arrived(lo);
+        tc::arrived(hi);
+        if (ch + 2 >= chunks) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
+        }
+        // 16 outputs: of the first 16 lanes' rows (SwiGLU), of those 8 and of the others' 8.
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const float x = __uint_as_float(lo[i]) + bias[(i >> 1) & 1], y = __uint_as_float(hi[i]) + bias[2 + ((i >> 1) & 1)];
+          if constexpr (SWIGLU) {
+            v[i] = (a.out_f32 ? activate(x, ACT_SILU) : silu_bf16(x)) * y;
+          } else {
+            v[i] = x;
+            v[8 + i] = y;
+          }
+        }
+        if constexpr (!SWIGLU) {
+          if (a.act == ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = a.out_f32 ? activate(v[i], ACT_SILU) : silu_bf16(v[i]);
+          } else if (a.act == ACT_GELU) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT_GELU);
+          }
+        }
+        if (a.out_f32) {
+          // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int in = SWIGLU ? i : i & 7;
+            const int tok = 8 * (in >> 2) + 2 * c + (i & 1), f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
+            if (tok < left && f < a.n_out) {
+              const int row = row0 + tok;
+              if (a.index != nullptr && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
+              const size_t at = (size_t)row * a.n_out + f;
+              float o = v[i];
+              if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
+              static_cast<float*>(a.out)[at] = o;
+            }
+          }
+          continue;
+        }
+        // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
+        // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
+        auto reg = [](int j, int q) { return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1); };
+        if (a.residual != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int u = lane + 32 * i;
+            st_shared16(stage + (u / PARTS) * ROW + (u % PARTS) * 16, res[i]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t x[4];
+            ld_blocks(block + (SWIGLU ? 16 : 8) * j * ROW, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[reg(j, q)] += bf_lo(x[q]);
+              v[reg(j, q) + 1] += bf_hi(x[q]);
+            }
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
+          st_blocks(block + (SWIGLU ? 16 : 8) * j * ROW, x[0], x[1], x[2], x[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+          const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
+          if (tok < left && f < a.n_out) {
+            const int row = row0 + tok;
+            if (a.index == nullptr || (unsigned)__ldg(a.index + row) < (unsigned)a.n_x)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)row * a.n_out + f) = o;
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  O::sync_all();
+  // The second CTA's share of the last arrival, which nothing else waits for.
+  if (CG == 2 && rank == 1 && warp == 1) mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
+  __syncthreads();
+  if (tid == 0 && sh.fail != 0) atomicCAS(reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + WS_ERROR), DEV_OK, DEV_TIMEOUT);
+  if (warp == 3) {
+    tc::fence_after();
+    O::dealloc(tmem);
+  }
+}
+
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const EncodeTiledFn enc = encode_tiled();
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int groups) {
+  const cuuint64_t k = a.n_in, n = a.n_out, row = k * 2;
+  if (a.act == ACT_SWIGLU) {
+    const cuuint64_t dims[5] = {k, 16, 2, n / 16, (cuuint64_t)groups};
+    const cuuint64_t strides[4] = {row, n * row, 16 * row, 2 * n * row};
+    const cuuint32_t box[5] = {KS, 16, 2, 4, 1};
+    return encode(map, base, 5, dims, strides, box);
+  }
+  const cuuint64_t dims[3] = {k, n, (cuuint64_t)groups};
+  const cuuint64_t strides[2] = {row, n * row};
+  const cuuint32_t box[3] = {KS, 128, 1};
+  return encode(map, base, 3, dims, strides, box);
+}
+
+template <int CG, bool SWIGLU>
+cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU>, SMEM, done);
+  if (e != cudaSuccess) return e;
+  constexpr int FE = (SWIGLU ? 64 : 128) * CG;
+  Plan p;
+  p.nt = nt;
+  p.stage_bytes = A_BYTES + nt / CG * KS * 2;
+  p.stages = STAGE_AREA / p.stage_bytes < MAX_STAGES ? STAGE_AREA / p.stage_bytes : MAX_STAGES;
+  p.n_m = (a.n_out + FE - 1) / FE;
+  p.k_steps = (a.n_in + KS - 1) / KS;
+  p.box_rows = a.start == nullptr ? nt / CG : a.index == nullptr ? 32 / CG : 0;
+  p.n_main = a.w_last != nullptr ? a.n_groups - 1 : a.n_groups;
+  p.x_warps = a.start == nullptr ? 1 : X_WARPS;
+  Maps maps;
+  if (!encode_w(&maps.w, a, a.w, p.n_main)) return cudaErrorInvalidValue;
+  maps.w_last = maps.w;
+  if (a.w_last != nullptr && !encode_w(&maps.w_last, a, a.w_last, 1)) return cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_x};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.n_in * 2};
+  const cuuint32_t box[2] = {KS, (cuuint32_t)(p.box_rows > 0 ? p.box_rows : 1)};
+  if (!encode(&maps.x, a.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
+
+  int units = sms / CG;
+  if (a.start == nullptr) {
+    const long long tiles = (long long)((a.n_rows + nt - 1) / nt) * p.n_m;
+    if (tiles < units) units = (int)tiles;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * CG, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU>, a, p, maps);
+}
+
+// The rows of a plain product's tiles: those whose rounds of tiles take least, each
+// its rows and COST0 for what it costs besides.
+long long best_rows(int n_rows, int n_m, int units, int* nt) {
+  long long best = -1;
+  for (int k = 1; k <= NT_MAX / 32; ++k) {
+    const int n = 32 * k;
+    const long long tiles = (long long)((n_rows + n - 1) / n) * n_m, cost = (tiles + units - 1) / units * (n + COST0);
+    if (best < 0 || cost <= best) {
+      best = cost;
+      *nt = n;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
+  const bool sw = a.act == ACT_SWIGLU;
+  if (a.start != nullptr)
+    return sw ? launch<2, true>(a, NT_MAX, sms, stream) : launch<2, false>(a, NT_MAX, sms, stream);
+  const int fe = sw ? 64 : 128;
+  int nt1 = 0, nt2 = 0;
+  const long long c1 = best_rows(a.n_rows, (a.n_out + fe - 1) / fe, sms, &nt1);
+  const long long c2 = best_rows(a.n_rows, (a.n_out + 2 * fe - 1) / (2 * fe), sms / 2, &nt2);
+  if (c2 <= c1) return sw ? launch<2, true>(a, nt2, sms, stream) : launch<2, false>(a, nt2, sms, stream);
+  return sw ? launch<1, true>(a, nt1, sms, stream) : launch<1, false>(a, nt1, sms, stream);
+}
+
+}  // namespace flint
