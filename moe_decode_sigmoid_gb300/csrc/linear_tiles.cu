@@ -10,10 +10,10 @@
 // copy), so that a warp of the epilogue has both in its 32 lanes.
 //
 // One CTA per SM, persistent:
-//   warp 0      copies W, 64 k a stage (TMA, 128-byte swizzle)
-//   warp 1      issues the products (of the pair: the first CTA's)
-//   warps 2, 3, 12, 13  copy X: boxes of rows, or four rows an instruction where an
-//               index says which
+//   warp 0      issues the products (of the pair: the first CTA's)
+//   warps 1-3, 12, 13  copy W and X, 64 k a stage, a stage each in turn (TMA, 128-byte
+//               swizzle); X as boxes of rows, or four rows an instruction where an index
+//               says which
 //   warps 4-11  epilogue: bias, activation and residual on fragments of 16 outputs x
 //               8 rows, transposed to rows through shared memory 8 x 8 at a time
 // TMEM holds two accumulators: a tile's epilogue runs beside the next one's products.
@@ -32,15 +32,17 @@ using namespace lin;
 
 constexpr int THREADS = 448, WARPS = THREADS / 32;
 constexpr int EPI0 = 4, EPI_WARPS = 8;     // warps of the epilogue, two a quarter of TMEM's lanes
-constexpr int X_WARPS = 4;                // warps 2, 3, 12, 13 copy X of groups
+constexpr int COPY_WARPS = 5;             // warps 1, 2, 3, 12, 13, a stage each in turn
 constexpr int KS = 64;                    // k of a stage: a 128-byte row
 constexpr int A_BYTES = 128 * KS * 2;
 constexpr int MAX_STAGES = 12;
 constexpr int STAGE_AREA = 192 * 1024;
-constexpr int EPI_BYTES = 32 * 48;        // a warp's 16 rows of 32 outputs or 32 of 16, padded
+constexpr int EPI_BYTES = 32 * 80;        // a warp's 32 rows of 32 outputs, padded
 constexpr int SMEM = STAGE_AREA + EPI_WARPS * EPI_BYTES + 1024;
 constexpr int NT_MAX = 256;
-constexpr int COST0 = 64;                 // of a tile, in rows
+// What a tile costs besides its rows, in rows; and what its weights' bytes from HBM do,
+// which a group's first tile of rows fetches.
+constexpr int COST_TILE = 512, COST_WEIGHTS = 0;
 constexpr int STRIP = 8;                  // tiles of weights that share their rows of x in L2
 
 struct Shared {
@@ -64,7 +66,7 @@ struct Plan {
   int k_steps;
   int box_rows;    // rows of a box of x; 0: four rows an instruction by index
   int n_main;      // groups whose weights are in the first map
-  int x_warps;     // warps that copy X: X_WARPS for groups, 1
+  int checked;     // rows whose index is out of range are not stored
 };
 
 struct Tile {
@@ -145,30 +147,34 @@ struct Ops {
 #define FLINT_GROUP_COPY(DIM, MODE, COORDS, ...)                                                                       \
   if constexpr (CG == 2)                                                                                               \
     asm volatile("cp.async.bulk.tensor." DIM ".shared::cluster.global." MODE                                           \
-                 ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, " COORDS "], [%2];" ::"r"(dst), "l"(map),      \
-                 "r"(bar), __VA_ARGS__                                                                                 \
+                 ".mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint [%0], [%1, " COORDS "], [%2], %3;" ::      \
+                     "r"(dst), "l"(map), "r"(bar), "l"(policy), __VA_ARGS__                                            \
                  : "memory");                                                                                          \
   else                                                                                                                 \
     asm volatile("cp.async.bulk.tensor." DIM ".shared::cluster.global." MODE                                           \
-                 ".mbarrier::complete_tx::bytes [%0], [%1, " COORDS "], [%2];" ::"r"(dst), "l"(map), "r"(bar),         \
-                 __VA_ARGS__                                                                                           \
+                 ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, " COORDS "], [%2], %3;" ::"r"(dst),          \
+                 "l"(map), "r"(bar), "l"(policy), __VA_ARGS__                                                          \
                  : "memory")
-  static __device__ __forceinline__ void copy2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    FLINT_GROUP_COPY("2d", "tile", "{%3, %4}", "r"(x), "r"(y));
+  static __device__ __forceinline__ void copy2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                               uint64_t policy) {
+    FLINT_GROUP_COPY("2d", "tile", "{%4, %5}", "r"(x), "r"(y));
   }
-  static __device__ __forceinline__ void copy3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    FLINT_GROUP_COPY("3d", "tile", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
+  static __device__ __forceinline__ void copy3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                               uint64_t policy) {
+    FLINT_GROUP_COPY("3d", "tile", "{%4, %5, %6}", "r"(x), "r"(y), "r"(z));
   }
-  static __device__ __forceinline__ void copy5(uint32_t dst, const CUtensorMap* map, int x, int block, int g, uint32_t bar) {
-    FLINT_GROUP_COPY("5d", "tile", "{%3, %6, %6, %4, %5}", "r"(x), "r"(block), "r"(g), "r"(0));
+  static __device__ __forceinline__ void copy5(uint32_t dst, const CUtensorMap* map, int x, int block, int g,
+                                               uint32_t bar, uint64_t policy) {
+    FLINT_GROUP_COPY("5d", "tile", "{%4, %7, %7, %5, %6}", "r"(x), "r"(block), "r"(g), "r"(0));
   }
-  static __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
-    FLINT_GROUP_COPY("2d", "tile::gather4", "{%3, %4, %5, %6, %7}", "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]));
+  static __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4],
+                                                 uint32_t bar, uint64_t policy) {
+    FLINT_GROUP_COPY("2d", "tile::gather4", "{%4, %5, %6, %7, %8}", "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]));
   }
 #undef FLINT_GROUP_COPY
 };
 
-// 32 (16) columns of 16 TMEM lanes: register 4 j + i of lane 4 r + c is row r + 8 (i / 2),
+// 32 columns of 16 TMEM lanes: register 4 j + i of lane 4 r + c is row r + 8 (i / 2),
 // column 8 j + 2 c + i % 2.
 __device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -178,11 +184,6 @@ __device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-__device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
 }
 // Four 8 x 8 blocks of 16-bit elements, transposed on the way; lane l has the address
 // of row l % 8 of block l / 8.
@@ -233,7 +234,8 @@ struct Walk {
   // plain: the tile's number; groups: where the share goes on and ends
   int t, tiles, tiles_n;
   long long at, end;
-  int g, i, count, cost, size;  // group, tile in it, tiles, a tile's cost, a tile's rows
+  int g, m, n, count, cost, size;  // group, tile in it (weights, rows), tiles of rows, a tile's cost, rows
+  long long block;
   Rows rows;
 
   __device__ __forceinline__ Walk(const LinearArgs& a_, const Plan& p_, const Shared& sh_, int unit_, int units_)
@@ -249,7 +251,9 @@ struct Walk {
       if (at < end) {
         enter();
         // the first tile that begins here
-        i = (int)((at - sh.pre[g] + cost - 1) / cost);
+        const int off = (int)((at - sh.pre[g]) % block);
+        m = (int)((at - sh.pre[g]) / block);
+        n = off == 0 ? 0 : max((off - COST_WEIGHTS + cost - 1) / cost, 1);
         settle();
       }
     }
@@ -263,16 +267,25 @@ struct Walk {
       else lo = mid + 1;
     }
     g = lo;
-    i = 0;
+    m = n = 0;
     rows = group_rows(a, g);
-    const int nt_g = max((rows.n + p.nt - 1) / p.nt, 1);
+    count = max((rows.n + p.nt - 1) / p.nt, 1);
     size = tile_rows(rows.n, p.nt);
-    count = nt_g * p.n_m;
-    cost = size + COST0;
+    cost = size + COST_TILE;
+    block = block_cost(count, size);
   }
+  // A group's tiles of rows in turn on the same weights, which L2 then has.
   __device__ __forceinline__ void settle() {
-    at = sh.pre[g] + (long long)i * cost;
-    if (i >= count && at < end) enter();
+    if (n >= count) {
+      n = 0;
+      ++m;
+    }
+    at = sh.pre[g] + (long long)m * block + (n > 0 ? COST_WEIGHTS + n * cost : 0);
+    if (m >= p.n_m && at < end) enter();
+  }
+  // Of all a group's tiles of rows on one tile of weights.
+  static __device__ __forceinline__ long long block_cost(int count, int size) {
+    return (long long)count * (size + COST_TILE) + COST_WEIGHTS;
   }
   // Rows of a group's tiles: of so many as nt asks for, alike but for the last.
   static __device__ __forceinline__ int tile_rows(int n, int nt) {
@@ -292,9 +305,8 @@ struct Walk {
       o.n = p.nt;
       o.rows = min(p.nt, a.n_rows - o.r0);
     } else {
-      const int n = i / p.n_m;
       o.g = g;
-      o.m = i - n * p.n_m;
+      o.m = m;
       o.r0 = rows.r0 + n * size;
       // the last tile of a group may have fewer rows, or (rounding) none
       o.rows = max(min(size, rows.n - n * size), 0);
@@ -306,7 +318,7 @@ struct Walk {
     if (a.start == nullptr) {
       t += units;
     } else {
-      ++i;
+      ++n;
       settle();
     }
   }
@@ -316,7 +328,7 @@ struct Walk {
 // kind, within 2^-18 of the value (|v| < 32; below, both are zero to 2^-40).
 __device__ __forceinline__ float silu_bf16(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
-template <int CG, bool SWIGLU>
+template <int CG, bool SWIGLU, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tiles_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Plan p,
                         const __grid_constant__ Maps maps) {
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), (1 + p.x_warps) * CG);
+      mbar_init(smem_addr(&sh.full[i]), CG);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int g = g0; g < g1; ++g) {
       const int n = group_rows(a, g).n;
       sh.pre[g] = sum;
-      if (n > 0) sum += (long long)((n + p.nt - 1) / p.nt) * p.n_m * (Walk::tile_rows(n, p.nt) + COST0);
+      if (n > 0) sum += Walk::block_cost((n + p.nt - 1) / p.nt, Walk::tile_rows(n, p.nt)) * p.n_m;
     }
     long long incl = sum;
 #pragma unroll
@@ -379,14 +391,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
-  // Which of the warps that copy X this is.
-  const int xw = warp == 2 ? 0 : warp == 3 ? 1 : warp >= EPI0 + EPI_WARPS ? warp - EPI0 - EPI_WARPS + 2 : X_WARPS;
-  if (warp == 0 || xw < p.x_warps) {
-    // ===== copies: W (warp 0), X (the others) ======================================
-    int s = 0;
+  const int copier = warp >= EPI0 + EPI_WARPS ? warp - EPI0 - EPI_WARPS + 3 : warp - 1;
+  if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS)) {
+    // ===== copies: every COPY_WARPS-th stage =======================================
+    int s = copier, turn = copier, step = 0;   // stage, first and present step of all tiles
     uint32_t phase = 1;
     bool ok = true;
-    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next()) {
+    // x, which every tile of weights reads, stays in L2; weights that no other tile reads
+    // leave it (49152 rows of gate/up 294 -> 277 us for this, 229 -> 224 for that).
+    uint64_t keep, normal;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+    while (s >= p.stages) {
+      s -= p.stages;
+      phase ^= 1;
+    }
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), step += p.k_steps) {
+      if (turn >= step + p.k_steps) continue;
       const Tile t = walk.get();
       const bool main = t.g < p.n_main;
       const CUtensorMap* wm = main ? &maps.w : &maps.w_last;
@@ -394,51 +415,42 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int f = (t.m * CG + rank) * FE;
       const int rows_b = t.n / CG, row0 = t.r0 + rank * rows_b;
       const uint32_t bytes = (p.box_rows > 0 ? p.box_rows : 4) * KS * 2;   // of a copy of X
-      int y[4] = {}, copies = 0, box = 0;
-      if (warp != 0) {
-        const int all = rows_b * KS * 2 / bytes;
-        copies = (all - xw + p.x_warps - 1) / p.x_warps;
-        box = lane * p.x_warps + xw;
-        if (p.box_rows > 0) {
-          y[0] = row0 + box * p.box_rows;
-        } else if (lane < copies) {
+      const int copies = rows_b * KS * 2 / bytes;
+      const uint64_t policy = a.start != nullptr && walk.rows.n <= p.nt ? l2_evict_first() : normal;
+      int y[4] = {};
+      if (p.box_rows > 0) {
+        y[0] = row0 + lane * p.box_rows;
+      } else if (lane < copies) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // A row of no index is not stored: any row will do.
-            const int r = row0 + 4 * box + j;
-            if (r < a.n_rows) y[j] = __ldg(a.index + r);
-            if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
-          }
+        for (int j = 0; j < 4; ++j) {
+          // A row of no index is not stored: any row will do.
+          const int r = row0 + 4 * lane + j;
+          if (r < a.n_rows) y[j] = __ldg(a.index + r);
+          if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
         }
       }
-      for (int k = 0; k < p.k_steps; ++k) {
+      for (; turn < step + p.k_steps; turn += COPY_WARPS) {
         if (!(ok = warp_wait(sh, sh.empty[s], phase))) break;
         const uint32_t bar = O::leader(smem_addr(&sh.full[s])), dst = smem + s * p.stage_bytes;
-        if (warp == 0) {
-          if (tc::one_thread()) {
-            O::expect(bar, A_BYTES);
-            if constexpr (SWIGLU) O::copy5(dst, wm, k * KS, f / 16, wg, bar);
-            else O::copy3(dst, wm, k * KS, f, wg, bar);
-          }
-        } else {
-          if (lane == 0) O::expect(bar, copies * bytes);
-          __syncwarp();
-          if (lane < copies) {
-            if (p.box_rows > 0) O::copy2(dst + A_BYTES + box * bytes, &maps.x, k * KS, y[0], bar);
-            else O::gather4(dst + A_BYTES + box * bytes, &maps.x, k * KS, y, bar);
-          }
+        const int k = (turn - step) * KS;
+        if (tc::one_thread()) {
+          O::expect(bar, A_BYTES + rows_b * KS * 2);
+          if constexpr (SWIGLU) O::copy5(dst, wm, k, f / 16, wg, bar, policy);
+          else O::copy3(dst, wm, k, f, wg, bar, policy);
         }
         __syncwarp();
-        if (++s == p.stages) {
-          s = 0;
-          phase ^= 1;
+        if (lane < copies) {
+          if (p.box_rows > 0) O::copy2(dst + A_BYTES + lane * bytes, &maps.x, k, y[0], bar, keep);
+          else O::gather4(dst + A_BYTES + lane * bytes, &maps.x, k, y, bar, keep);
         }
+        __syncwarp();
+        for (s += COPY_WARPS; s >= p.stages; s -= p.stages) phase ^= 1;
       }
     }
     // A wait ran out: what was asked for lands long before this.
     if (*reinterpret_cast<volatile int*>(&sh.fail) != 0)
       for (const uint64_t until = globaltimer_ns() + 50000000ull; globaltimer_ns() < until;) {}
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 0 && rank == 0) {
     // ===== products ================================================================
     const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
     int s = 0, it = 0;
@@ -455,19 +467,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t d = d0 + b * NT_MAX;
       if (!(ok = warp_wait(sh, sh.acc_empty[b], ((it >> 1) & 1) ^ 1))) break;
       tc::fence_after();
-      for (int k = 0; k < p.k_steps; ++k) {
+      // Two stages at a time: their waits and their products' issue run one behind the
+      // other, ~150 and ~200 cycles, and a stage of 192 rows executes in 384.
+      for (int k = 0; k < p.k_steps; k += 2) {
+        const bool two = k + 1 < p.k_steps;
+        int s1 = s + 1;
+        uint32_t phase1 = phase;
+        if (s1 == p.stages) {
+          s1 = 0;
+          phase1 ^= 1;
+        }
         if (!(ok = warp_wait(sh, sh.full[s], phase))) break;
+        if (two && !(ok = warp_wait(sh, sh.full[s1], phase1))) break;
         tc::fence_after();
-        const uint32_t at = smem + s * p.stage_bytes;
+        const uint32_t at = smem + s * p.stage_bytes, at1 = smem + s1 * p.stage_bytes;
         const uint32_t a_lo = tc::desc_lo(at, 16), b_lo = tc::desc_lo(at + A_BYTES, 16);
+        const uint32_t a1_lo = tc::desc_lo(at1, 16), b1_lo = tc::desc_lo(at1 + A_BYTES, 16);
         if (tc::one_thread()) {
 #pragma unroll
           for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + 2 * j, idesc, k > 0 || j > 0);
           O::commit(smem_addr(&sh.empty[s]));
-          if (k == p.k_steps - 1) O::commit(smem_addr(&sh.acc_full[b]));
+          if (two) {
+#pragma unroll
+            for (int j = 0; j < KS / 16; ++j) O::mma(d, a1_lo + 2 * j, b1_lo + 2 * j, idesc, 1);
+            O::commit(smem_addr(&sh.empty[s1]));
+          }
+          if (k + 2 >= p.k_steps) O::commit(smem_addr(&sh.acc_full[b]));
         }
         __syncwarp();
-        if (++s == p.stages) {
+        s = s1;
+        phase = phase1;
+        if (two && ++s == p.stages) {
           s = 0;
           phase ^= 1;
         }
@@ -487,8 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Where this lane's rows of the 8 x 8 blocks lie.
     const uint32_t block = SWIGLU ? stage + ((lane >> 4) * 8 + (lane & 7)) * ROW + ((lane >> 3) & 1) * 16
                                   : stage + (lane & 7) * ROW + (lane >> 3) * 16;
-    constexpr int PARTS = WF / 8;           // 16-byte parts of a row
-    constexpr int CH = SWIGLU ? 32 : 16;    // rows of x at a time: 16 outputs a lane
+    constexpr int PARTS = WF / 8;           // 16-byte parts of a row: a lane has as many of 32 rows
+    constexpr int HALVES = SWIGLU ? 1 : 2;  // 16 outputs a lane at a time: of 32 rows (SwiGLU), of 16
     bool ok = true;
     int it = 0;
     for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
@@ -506,25 +536,36 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
       tc::fence_after();
-      const int chunks = t.n / CH;
+      const int chunks = t.n / 32;
       if (half >= chunks && lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
-      // Two warps have the same lanes; each takes every other CH rows.
+      // Two warps have the same lanes; each takes every other 32 rows.
       for (int ch = half; ch < chunks; ch += 2) {
-        const int row0 = t.r0 + CH * ch, left = t.rows - CH * ch;
-        // Residual rows, as they lie, while the accumulators are read.
-        uint4 res[2];
-        if (!a.out_f32 && a.residual != nullptr)
+        const int row0 = t.r0 + 32 * ch, left = t.rows - 32 * ch;
+        uint32_t lo[16], hi[16];
+        ld_frag(t0 + b * NT_MAX + 32 * ch, lo);
+        ld_frag(t0 + b * NT_MAX + 32 * ch + (16u << 16), hi);
+        // This lane's parts of the rows, whether they are stored, and the residual there.
+        bool store[PARTS];
+        if constexpr (!F32) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < PARTS; ++i) {
             const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
-            res[i] = make_uint4(0, 0, 0, 0);
-            if (tok < left && f < a.n_out)
-              res[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
-                                                       (size_t)(row0 + tok) * a.n_out + f);
+            store[i] = tok < left && f < a.n_out;
+            if (p.checked && store[i]) store[i] = (unsigned)__ldg(a.index + row0 + tok) < (unsigned)a.n_x;
           }
-        uint32_t lo[CH / 2], hi[CH / 2];
-        ld_frag(t0 + b * NT_MAX + CH * ch, lo);
-        ld_frag(t0 + b * NT_MAX + CH * ch + (16u << 16), hi);
+          if (a.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+              const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (store[i])
+                v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
+                                                    (size_t)(row0 + tok) * a.n_out + f);
+              st_shared16(stage + tok * ROW + (u % PARTS) * 16, v);
+            }
+            __syncwarp();
+          }
+        }
         tc::wait_ld();
         tc::arrived(lo);
         tc::arrived(hi);
@@ -533,85 +574,82 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
         }
-        // 16 outputs: of the first 16 lanes' rows (SwiGLU), of those 8 and of the others' 8.
-        float v[16];
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-          const float x = __uint_as_float(lo[i]) + bias[(i >> 1) & 1], y = __uint_as_float(hi[i]) + bias[2 + ((i >> 1) & 1)];
-          if constexpr (SWIGLU) {
-            v[i] = (a.out_f32 ? activate(x, ACT_SILU) : silu_bf16(x)) * y;
+        for (int h = 0; h < HALVES; ++h) {
+          // Outputs r, r + 8 (of 16 of the first lanes' rows; not SwiGLU: v[8 ..] those of
+          // the others') of rows 8 j + 2 c, + 1.
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16 / HALVES; ++i) {
+            const float x = __uint_as_float(lo[8 * h + i]) + bias[(i >> 1) & 1];
+            const float y = __uint_as_float(hi[8 * h + i]) + bias[2 + ((i >> 1) & 1)];
+            if constexpr (SWIGLU) {
+              v[i] = (F32 ? activate(x, ACT_SILU) : silu_bf16(x)) * y;
+            } else {
+              v[i] = x;
+              v[8 + i] = y;
+            }
+          }
+          if constexpr (!SWIGLU) {
+            if (a.act == ACT_SILU) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = F32 ? activate(v[i], ACT_SILU) : silu_bf16(v[i]);
+            } else if (a.act == ACT_GELU) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT_GELU);
+            }
+          }
+          if constexpr (F32) {
+            // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int in = SWIGLU ? i : i & 7;
+              const int tok = 16 * h + 8 * (in >> 2) + 2 * c + (i & 1);
+              const int f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
+              if (tok < left && f < a.n_out) {
+                const int row = row0 + tok;
+                if (p.checked && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
+                const size_t at = (size_t)row * a.n_out + f;
+                float o = v[i];
+                if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
+                static_cast<float*>(a.out)[at] = o;
+              }
+            }
           } else {
-            v[i] = x;
-            v[8 + i] = y;
-          }
-        }
-        if constexpr (!SWIGLU) {
-          if (a.act == ACT_SILU) {
+            // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
+            // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
+            auto reg = [](int j, int q) {
+              return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1);
+            };
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = a.out_f32 ? activate(v[i], ACT_SILU) : silu_bf16(v[i]);
-          } else if (a.act == ACT_GELU) {
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t at = block + (SWIGLU ? 16 * j : 16 * h + 8 * j) * ROW;
+              uint32_t x[4];
+              if (a.residual != nullptr) {
+                ld_blocks(at, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT_GELU);
-          }
-        }
-        if (a.out_f32) {
-          // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
+                for (int q = 0; q < 4; ++q) {
+                  v[reg(j, q)] += bf_lo(x[q]);
+                  v[reg(j, q) + 1] += bf_hi(x[q]);
+                }
+              }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int in = SWIGLU ? i : i & 7;
-            const int tok = 8 * (in >> 2) + 2 * c + (i & 1), f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
-            if (tok < left && f < a.n_out) {
-              const int row = row0 + tok;
-              if (a.index != nullptr && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
-              const size_t at = (size_t)row * a.n_out + f;
-              float o = v[i];
-              if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
-              static_cast<float*>(a.out)[at] = o;
+              for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
+              st_blocks(at, x[0], x[1], x[2], x[3]);
             }
           }
-          continue;
         }
-        // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
-        // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
-        auto reg = [](int j, int q) { return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1); };
-        if (a.residual != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int u = lane + 32 * i;
-            st_shared16(stage + (u / PARTS) * ROW + (u % PARTS) * 16, res[i]);
-          }
+        if constexpr (!F32) {
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t x[4];
-            ld_blocks(block + (SWIGLU ? 16 : 8) * j * ROW, x);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[reg(j, q)] += bf_lo(x[q]);
-              v[reg(j, q) + 1] += bf_hi(x[q]);
-            }
+          for (int i = 0; i < PARTS; ++i) {
+            const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+            const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
+            if (store[i])
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(row0 + tok) * a.n_out + f) = o;
           }
           __syncwarp();
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t x[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
-          st_blocks(block + (SWIGLU ? 16 : 8) * j * ROW, x[0], x[1], x[2], x[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
-          const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
-          if (tok < left && f < a.n_out) {
-            const int row = row0 + tok;
-            if (a.index == nullptr || (unsigned)__ldg(a.index + row) < (unsigned)a.n_x)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)row * a.n_out + f) = o;
-          }
-        }
-        __syncwarp();
       }
     }
   }
@@ -619,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::fence_before();
   O::sync_all();
   // The second CTA's share of the last arrival, which nothing else waits for.
-  if (CG == 2 && rank == 1 && warp == 1) mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
+  if (CG == 2 && rank == 1 && warp == 0) mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
   __syncthreads();
   if (tid == 0 && sh.fail != 0) atomicCAS(reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + WS_ERROR), DEV_OK, DEV_TIMEOUT);
   if (warp == 3) {
@@ -652,10 +690,10 @@ bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int group
   return encode(map, base, 3, dims, strides, box);
 }
 
-template <int CG, bool SWIGLU>
+template <int CG, bool SWIGLU, bool F32>
 cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done;
-  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU>, SMEM, done);
+  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU, F32>, SMEM, done);
   if (e != cudaSuccess) return e;
   constexpr int FE = (SWIGLU ? 64 : 128) * CG;
   Plan p;
@@ -666,7 +704,8 @@ cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   p.k_steps = (a.n_in + KS - 1) / KS;
   p.box_rows = a.start == nullptr ? nt / CG : a.index == nullptr ? 32 / CG : 0;
   p.n_main = a.w_last != nullptr ? a.n_groups - 1 : a.n_groups;
-  p.x_warps = a.start == nullptr ? 1 : X_WARPS;
+  // (the layer's own indices are in range)
+  p.checked = a.index != nullptr && a.w_last == nullptr;
   Maps maps;
   if (!encode_w(&maps.w, a, a.w, p.n_main)) return cudaErrorInvalidValue;
   maps.w_last = maps.w;
@@ -694,16 +733,23 @@ cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU>, a, p, maps);
+  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU, F32>, a, p, maps);
+}
+
+template <int CG>
+cudaError_t launch_as(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
+  if (a.act == ACT_SWIGLU)
+    return a.out_f32 ? launch<CG, true, true>(a, nt, sms, stream) : launch<CG, true, false>(a, nt, sms, stream);
+  return a.out_f32 ? launch<CG, false, true>(a, nt, sms, stream) : launch<CG, false, false>(a, nt, sms, stream);
 }
 
 // The rows of a plain product's tiles: those whose rounds of tiles take least, each
-// its rows and COST0 for what it costs besides.
+// its rows and COST_TILE for what it costs besides.
 long long best_rows(int n_rows, int n_m, int units, int* nt) {
   long long best = -1;
   for (int k = 1; k <= NT_MAX / 32; ++k) {
     const int n = 32 * k;
-    const long long tiles = (long long)((n_rows + n - 1) / n) * n_m, cost = (tiles + units - 1) / units * (n + COST0);
+    const long long tiles = (long long)((n_rows + n - 1) / n) * n_m, cost = (tiles + units - 1) / units * (n + 64);
     if (best < 0 || cost <= best) {
       best = cost;
       *nt = n;
@@ -716,14 +762,12 @@ long long best_rows(int n_rows, int n_m, int units, int* nt) {
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
   const bool sw = a.act == ACT_SWIGLU;
-  if (a.start != nullptr)
-    return sw ? launch<2, true>(a, NT_MAX, sms, stream) : launch<2, false>(a, NT_MAX, sms, stream);
+  if (a.start != nullptr) return launch_as<2>(a, NT_MAX, sms, stream);
   const int fe = sw ? 64 : 128;
   int nt1 = 0, nt2 = 0;
   const long long c1 = best_rows(a.n_rows, (a.n_out + fe - 1) / fe, sms, &nt1);
   const long long c2 = best_rows(a.n_rows, (a.n_out + 2 * fe - 1) / (2 * fe), sms / 2, &nt2);
-  if (c2 <= c1) return sw ? launch<2, true>(a, nt2, sms, stream) : launch<2, false>(a, nt2, sms, stream);
-  return sw ? launch<1, true>(a, nt1, sms, stream) : launch<1, false>(a, nt1, sms, stream);
+  return c2 <= c1 ? launch_as<2>(a, nt2, sms, stream) : launch_as<1>(a, nt1, sms, stream);
 }
 
 }  // namespace flint
