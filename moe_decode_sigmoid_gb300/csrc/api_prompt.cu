@@ -74,7 +74,7 @@ bool any_overlap(const Span (&s)[N], int n_out) {
 }
 
 flint_status launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  if (a.start == nullptr && a.n_rows <= 32) return cuda_status(launch_linear_rows(a, stream));
+  if (a.start == nullptr && a.n_rows <= lin::FEW_ROWS) return cuda_status(launch_linear_rows(a, stream));
   const int sms = num_sms();
   if (sms < 2) return FLINT_ERR_CUDA;
   return cuda_status(launch_linear_tiles(a, sms, stream));
@@ -212,7 +212,7 @@ flint_status flint_moe_select(const flint_moe_dims* dims, int32_t n_tokens, cons
   a.start = group_start;
   a.row_token = row_token;
   a.pair_row = pair_row;
-  a.counts = reinterpret_cast<int*>(static_cast<char*>(workspace) + lin::WS_COUNTS);
+  a.counts = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + lin::WS_COUNTS);
   return cuda_status(launch_select(a, stream));
 }
 
@@ -301,7 +301,7 @@ flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
   s.idx_out = topk_idx_out;
   s.w_out = topk_w_out;
   s.shared_group = 1;
-  s.counts = reinterpret_cast<int*>(ws + lin::WS_COUNTS);
+  s.counts = reinterpret_cast<uint8_t*>(ws + lin::WS_COUNTS);
   if ((st = cuda_status(launch_select(s, stream))) != FLINT_OK) return st;
 
   LinearArgs g = {};

@@ -13,13 +13,14 @@ constexpr int MAX_ROWS = 65536;
 constexpr int MAX_IN = 65536;
 constexpr int MAX_OUT = 1 << 20;
 constexpr int GROUP_LIMIT = 1024;
+constexpr int FEW_ROWS = 16;       // of a plain product that linear_rows.cu takes
 constexpr int MAX_TOKENS = 8192;   // of a selection and of the layer
 constexpr int CHUNK = 64;          // tokens a CTA of the selection takes
 constexpr int MAX_CHUNKS = MAX_TOKENS / CHUNK;
 
 // Workspace: error and stall word, the selection's counts, then the layer's arrays.
 constexpr size_t WS_ERROR = 0, WS_STALL = 8, WS_COUNTS = 256;
-constexpr size_t WS_HEAD = WS_COUNTS + sizeof(int) * 256 * (size_t)MAX_CHUNKS;
+constexpr size_t WS_HEAD = WS_COUNTS + 256 * (size_t)MAX_CHUNKS;
 }  // namespace lin
 
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_SWIGLU = 3 };
@@ -37,7 +38,7 @@ struct LinearArgs {
   int n_groups, n_rows, n_x, n_in, n_out, act, out_f32;
   void* ws;
 };
-// A few rows a group, and any number.
+// A plain product of up to FEW_ROWS rows, and anything.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream);
 
@@ -53,7 +54,7 @@ struct SelectArgs {
   int* idx_out;            // optional copies
   float* w_out;
   int shared_group;        // a last group of all tokens
-  int* counts;             // [chunks, E] scratch
+  uint8_t* counts;         // [chunks, E] scratch
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream);
 

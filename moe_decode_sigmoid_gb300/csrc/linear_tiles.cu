@@ -40,6 +40,7 @@ constexpr int STAGE_AREA = 192 * 1024;
 constexpr int EPI_BYTES = 32 * 80;        // a warp's 32 rows of 32 outputs, padded
 constexpr int SMEM = STAGE_AREA + EPI_WARPS * EPI_BYTES + 1024;
 constexpr int NT_MAX = 256;
+constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
 // What a tile costs besides its rows, in rows; and what its weights' bytes from HBM do,
 // which a group's first tile of rows fetches.
 constexpr int COST_TILE = 512, COST_WEIGHTS = 0;
@@ -52,6 +53,7 @@ struct Shared {
   long long warp_tot[WARPS];
   long long pre[GROUP_LIMIT + 2];          // cost of all tiles before a group's
 };
+static_assert(NT_MAX / 32 * 4 * PART_BYTES <= STAGE_AREA, "a tile's sums fit the ring's place");
 static_assert(SMEM + sizeof(Shared) <= 227 * 1024, "fits");
 
 // Tensor maps: the weights (all groups but a last one of its own, and that one), x.
@@ -66,12 +68,18 @@ struct Plan {
   int k_steps;
   int box_rows;    // rows of a box of x; 0: four rows an instruction by index
   int n_main;      // groups whose weights are in the first map
+  int splits;      // CTAs that share a tile's k
   int checked;     // rows whose index is out of range are not stored
 };
 
 struct Tile {
   int g, m, r0, n, rows;  // group, tile of weight rows, first row, rows rounded up, rows
 };
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 
 template <int CG>
 struct Ops {
@@ -137,12 +145,8 @@ struct Ops {
       asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(leader_bar) : "memory");
   }
   static __device__ __forceinline__ void sync_all() {
-    if constexpr (CG == 2) {
-      asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    } else {
-      __syncthreads();
-    }
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
   }
 #define FLINT_GROUP_COPY(DIM, MODE, COORDS, ...)                                                                       \
   if constexpr (CG == 2)                                                                                               \
@@ -328,18 +332,154 @@ struct Walk {
 // kind, within 2^-18 of the value (|v| < 32; below, both are zero to 2^-40).
 __device__ __forceinline__ float silu_bf16(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
-template <int CG, bool SWIGLU, bool F32>
+// Where a lane's row of the epilogue's four 8 x 8 blocks lies.
+template <bool SWIGLU>
+__device__ __forceinline__ uint32_t block_row(uint32_t stage, int lane) {
+  return SWIGLU ? stage + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16
+                : stage + (lane & 7) * 80 + (lane >> 3) * 16;
+}
+
+// Bias of a lane's rows of the fragments.
+template <bool SWIGLU>
+__device__ __forceinline__ void load_bias(const LinearArgs& a, int g, int f0, float (&bias)[4]) {
+  const int r = (threadIdx.x & 31) >> 2;
+  const float* src = a.bias + (size_t)g * a.n_out * (SWIGLU ? 2 : 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int f = SWIGLU ? f0 + r + 8 * (i & 1) : f0 + r + 8 * i;
+    bias[i] = a.bias != nullptr && f < a.n_out ? __ldg(src + f + (SWIGLU && i >= 2 ? a.n_out : 0)) : 0.0f;
+  }
+}
+
+// The epilogue of 32 rows (from row0, `left` of them there) and a warp's weight rows, whose
+// sums are in lo, hi once land() has returned: bias, activation, residual, rounding, and
+// the outputs f0 .. in whole 16-byte parts of rows (fp32: sectors).
+template <bool SWIGLU, bool F32, class Land>
+__device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint32_t stage, uint32_t block, int f0, int row0,
+                                       int left, const float (&bias)[4], uint32_t (&lo)[16], uint32_t (&hi)[16], Land land) {
+  constexpr int WF = SWIGLU ? 16 : 32;    // outputs of a warp
+  constexpr int ROW = WF * 2 + 16;        // bytes of a row of the transposition
+  constexpr int PARTS = WF / 8;           // 16-byte parts of a row: a lane has as many of 32 rows
+  constexpr int HALVES = SWIGLU ? 1 : 2;  // 16 outputs a lane at a time: of 32 rows (SwiGLU), of 16
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  // This lane's parts of the rows, whether they are stored, and the residual there.
+  bool store[PARTS];
+  if constexpr (!F32) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+      store[i] = tok < left && f < a.n_out;
+      if (p.checked && store[i]) store[i] = (unsigned)__ldg(a.index + row0 + tok) < (unsigned)a.n_x;
+    }
+    if (a.residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (store[i])
+          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
+                                              (size_t)(row0 + tok) * a.n_out + f);
+        st_shared16(stage + tok * ROW + (u % PARTS) * 16, v);
+      }
+      __syncwarp();
+    }
+  }
+  land();
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) {
+    // Outputs r, r + 8 (of 16 of the first lanes' rows; not SwiGLU: v[8 ..] those of
+    // the others') of rows 8 j + 2 c, + 1.
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16 / HALVES; ++i) {
+      const float x = __uint_as_float(lo[8 * h + i]) + bias[(i >> 1) & 1];
+      const float y = __uint_as_float(hi[8 * h + i]) + bias[2 + ((i >> 1) & 1)];
+      if constexpr (SWIGLU) {
+        v[i] = (F32 ? activate(x, ACT_SILU) : silu_bf16(x)) * y;
+      } else {
+        v[i] = x;
+        v[8 + i] = y;
+      }
+    }
+    if constexpr (!SWIGLU) {
+      if (a.act == ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = F32 ? activate(v[i], ACT_SILU) : silu_bf16(v[i]);
+      } else if (a.act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT_GELU);
+      }
+    }
+    if constexpr (F32) {
+      // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int in = SWIGLU ? i : i & 7;
+        const int tok = 16 * h + 8 * (in >> 2) + 2 * c + (i & 1);
+        const int f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
+        if (tok < left && f < a.n_out) {
+          const int row = row0 + tok;
+          if (p.checked && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
+          const size_t at = (size_t)row * a.n_out + f;
+          float o = v[i];
+          if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
+          static_cast<float*>(a.out)[at] = o;
+        }
+      }
+    } else {
+      // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
+      // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
+      auto reg = [](int j, int q) {
+        return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1);
+      };
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = block + (SWIGLU ? 16 * j : 16 * h + 8 * j) * ROW;
+        uint32_t x[4];
+        if (a.residual != nullptr) {
+          ld_blocks(at, x);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[reg(j, q)] += bf_lo(x[q]);
+            v[reg(j, q) + 1] += bf_hi(x[q]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
+        st_blocks(at, x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+  if constexpr (!F32) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+      const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
+      if (store[i])
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(row0 + tok) * a.n_out + f) = o;
+    }
+    __syncwarp();
+  }
+}
+
+// SPLIT: one tile a cluster of `splits` CTAs, each of which has a part of k.
+template <int CG, bool SWIGLU, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tiles_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Plan p,
                         const __grid_constant__ Maps maps) {
   using O = Ops<CG>;
   constexpr int FE = SWIGLU ? 64 : 128;   // outputs of a CTA's tile
   constexpr int WF = FE / 4;              // of a warp
-  constexpr int ROW = WF * 2 + 16;        // bytes of a row of the transposition
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int rank = CG == 2 ? blockIdx.x & 1 : 0;
+  const int splits = SPLIT ? p.splits : 1, part = SPLIT ? blockIdx.x % splits : 0;   // of k
+  const int unit = blockIdx.x / (CG * splits), units = gridDim.x / (CG * splits);
+  // Steps of k of a tile, the first of which is k0.
+  const int k0 = SPLIT ? p.k_steps * part / splits : 0;
+  const int k_steps = SPLIT ? p.k_steps * (part + 1) / splits - k0 : p.k_steps;
   const uint32_t smem = (smem_addr(s_raw) + 1023u) & ~1023u;
 
   if (tid == 0) {
@@ -392,8 +532,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
   const int copier = warp >= EPI0 + EPI_WARPS ? warp - EPI0 - EPI_WARPS + 3 : warp - 1;
-  if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS)) {
-    // ===== copies: every COPY_WARPS-th stage =======================================
+  // No more of them than stages: a warp waits for a slot's last use but one to be over,
+  // and parities tell it from the one before only if the warp's own last stage is within
+  // a round of the ring.
+  const int copiers = min(COPY_WARPS, p.stages);
+  if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS) && copier < copiers) {
+    // ===== copies: every copiers-th stage ==========================================
     int s = copier, turn = copier, step = 0;   // stage, first and present step of all tiles
     uint32_t phase = 1;
     bool ok = true;
@@ -402,12 +546,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t keep, normal;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
-    while (s >= p.stages) {
-      s -= p.stages;
-      phase ^= 1;
-    }
-    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), step += p.k_steps) {
-      if (turn >= step + p.k_steps) continue;
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), step += k_steps) {
+      if (turn >= step + k_steps) continue;
       const Tile t = walk.get();
       const bool main = t.g < p.n_main;
       const CUtensorMap* wm = main ? &maps.w : &maps.w_last;
@@ -429,10 +569,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
         }
       }
-      for (; turn < step + p.k_steps; turn += COPY_WARPS) {
+      for (; turn < step + k_steps; turn += copiers) {
         if (!(ok = warp_wait(sh, sh.empty[s], phase))) break;
         const uint32_t bar = O::leader(smem_addr(&sh.full[s])), dst = smem + s * p.stage_bytes;
-        const int k = (turn - step) * KS;
+        const int k = (k0 + turn - step) * KS;
         if (tc::one_thread()) {
           O::expect(bar, A_BYTES + rows_b * KS * 2);
           if constexpr (SWIGLU) O::copy5(dst, wm, k, f / 16, wg, bar, policy);
@@ -444,7 +584,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           else O::gather4(dst + A_BYTES + lane * bytes, &maps.x, k, y, bar, keep);
         }
         __syncwarp();
-        for (s += COPY_WARPS; s >= p.stages; s -= p.stages) phase ^= 1;
+        if ((s += copiers) >= p.stages) {
+          s -= p.stages;
+          phase ^= 1;
+        }
       }
     }
     // A wait ran out: what was asked for lands long before this.
@@ -469,8 +612,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::fence_after();
       // Two stages at a time: their waits and their products' issue run one behind the
       // other, ~150 and ~200 cycles, and a stage of 192 rows executes in 384.
-      for (int k = 0; k < p.k_steps; k += 2) {
-        const bool two = k + 1 < p.k_steps;
+      for (int k = 0; k < k_steps; k += 2) {
+        const bool two = k + 1 < k_steps;
         int s1 = s + 1;
         uint32_t phase1 = phase;
         if (s1 == p.stages) {
@@ -492,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < KS / 16; ++j) O::mma(d, a1_lo + 2 * j, b1_lo + 2 * j, idesc, 1);
             O::commit(smem_addr(&sh.empty[s1]));
           }
-          if (k + 2 >= p.k_steps) O::commit(smem_addr(&sh.acc_full[b]));
+          if (k + 2 >= k_steps) O::commit(smem_addr(&sh.acc_full[b]));
         }
         __syncwarp();
         s = s1;
@@ -510,148 +653,97 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_wait(smem_addr(&sh.drained), 0, globaltimer_ns() + 1000000000ull);
   } else if (warp >= EPI0 && warp < EPI0 + EPI_WARPS) {
     // ===== epilogue ================================================================
-    const int w = warp & 3, half = (warp - EPI0) >> 2, r = lane >> 2, c = lane & 3;
+    const int w = warp & 3, half = (warp - EPI0) >> 2;
     const uint32_t stage = smem + STAGE_AREA + (warp - EPI0) * EPI_BYTES;
     const uint32_t t0 = tmem + ((uint32_t)(32 * w) << 16);
-    const int m = a.n_out * (SWIGLU ? 2 : 1);
-    // Where this lane's rows of the 8 x 8 blocks lie.
-    const uint32_t block = SWIGLU ? stage + ((lane >> 4) * 8 + (lane & 7)) * ROW + ((lane >> 3) & 1) * 16
-                                  : stage + (lane & 7) * ROW + (lane >> 3) * 16;
-    constexpr int PARTS = WF / 8;           // 16-byte parts of a row: a lane has as many of 32 rows
-    constexpr int HALVES = SWIGLU ? 1 : 2;  // 16 outputs a lane at a time: of 32 rows (SwiGLU), of 16
+    const uint32_t block = block_row<SWIGLU>(stage, lane);
     bool ok = true;
     int it = 0;
     for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
       const Tile t = walk.get();
       const int f0 = (t.m * CG + rank) * FE + WF * w;
       const int b = it & 1;
-      float bias[4] = {};
-      if (a.bias != nullptr) {
-        const float* src = a.bias + (size_t)t.g * m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int f = SWIGLU ? f0 + r + 8 * (i & 1) : f0 + r + 8 * i;
-          if (f < a.n_out) bias[i] = __ldg(src + f + (SWIGLU && i >= 2 ? a.n_out : 0));
-        }
-      }
+      float bias[4];
+      if constexpr (!SPLIT) load_bias<SWIGLU>(a, t.g, f0, bias);
       if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
       tc::fence_after();
       const int chunks = t.n / 32;
       if (half >= chunks && lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
       // Two warps have the same lanes; each takes every other 32 rows.
       for (int ch = half; ch < chunks; ch += 2) {
-        const int row0 = t.r0 + 32 * ch, left = t.rows - 32 * ch;
         uint32_t lo[16], hi[16];
         ld_frag(t0 + b * NT_MAX + 32 * ch, lo);
         ld_frag(t0 + b * NT_MAX + 32 * ch + (16u << 16), hi);
-        // This lane's parts of the rows, whether they are stored, and the residual there.
-        bool store[PARTS];
-        if constexpr (!F32) {
+        if constexpr (SPLIT) {
+          // This CTA's part of the sums, in the products' place (they are through with it).
+          tc::wait_ld();
+          tc::arrived(lo);
+          tc::arrived(hi);
+          const uint32_t at = smem + (4 * ch + w) * PART_BYTES + lane * 16;
 #pragma unroll
-          for (int i = 0; i < PARTS; ++i) {
-            const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
-            store[i] = tok < left && f < a.n_out;
-            if (p.checked && store[i]) store[i] = (unsigned)__ldg(a.index + row0 + tok) < (unsigned)a.n_x;
+          for (int i = 0; i < 4; ++i) {
+            st_shared16(at + i * 512, make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
+            st_shared16(at + 2048 + i * 512, make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]));
           }
-          if (a.residual != nullptr) {
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-              const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (store[i])
-                v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
-                                                    (size_t)(row0 + tok) * a.n_out + f);
-              st_shared16(stage + tok * ROW + (u % PARTS) * 16, v);
+        } else {
+          finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [&] {
+            tc::wait_ld();
+            tc::arrived(lo);
+            tc::arrived(hi);
+            if (ch + 2 >= chunks) {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
             }
-            __syncwarp();
-          }
-        }
-        tc::wait_ld();
-        tc::arrived(lo);
-        tc::arrived(hi);
-        if (ch + 2 >= chunks) {
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
-        }
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          // Outputs r, r + 8 (of 16 of the first lanes' rows; not SwiGLU: v[8 ..] those of
-          // the others') of rows 8 j + 2 c, + 1.
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16 / HALVES; ++i) {
-            const float x = __uint_as_float(lo[8 * h + i]) + bias[(i >> 1) & 1];
-            const float y = __uint_as_float(hi[8 * h + i]) + bias[2 + ((i >> 1) & 1)];
-            if constexpr (SWIGLU) {
-              v[i] = (F32 ? activate(x, ACT_SILU) : silu_bf16(x)) * y;
-            } else {
-              v[i] = x;
-              v[8 + i] = y;
-            }
-          }
-          if constexpr (!SWIGLU) {
-            if (a.act == ACT_SILU) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = F32 ? activate(v[i], ACT_SILU) : silu_bf16(v[i]);
-            } else if (a.act == ACT_GELU) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT_GELU);
-            }
-          }
-          if constexpr (F32) {
-            // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int in = SWIGLU ? i : i & 7;
-              const int tok = 16 * h + 8 * (in >> 2) + 2 * c + (i & 1);
-              const int f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
-              if (tok < left && f < a.n_out) {
-                const int row = row0 + tok;
-                if (p.checked && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
-                const size_t at = (size_t)row * a.n_out + f;
-                float o = v[i];
-                if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
-                static_cast<float*>(a.out)[at] = o;
-              }
-            }
-          } else {
-            // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
-            // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
-            auto reg = [](int j, int q) {
-              return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1);
-            };
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t at = block + (SWIGLU ? 16 * j : 16 * h + 8 * j) * ROW;
-              uint32_t x[4];
-              if (a.residual != nullptr) {
-                ld_blocks(at, x);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  v[reg(j, q)] += bf_lo(x[q]);
-                  v[reg(j, q) + 1] += bf_hi(x[q]);
-                }
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
-              st_blocks(at, x[0], x[1], x[2], x[3]);
-            }
-          }
-        }
-        if constexpr (!F32) {
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i) {
-            const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
-            const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
-            if (store[i])
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(row0 + tok) * a.n_out + f) = o;
-          }
-          __syncwarp();
+          });
         }
       }
     }
+  }
+  if constexpr (SPLIT) {
+    // ===== the parts of all CTAs of the cluster, joined in their order: 32 rows x 32
+    // weight rows a warp, dealt out over the CTAs ====================================
+    __syncwarp();
+    cluster_sync();
+    const int e = warp - EPI0;
+    Walk walk(a, p, sh, unit, units);
+    if (e >= 0 && e < EPI_WARPS && walk.more() && *reinterpret_cast<volatile int*>(&sh.fail) == 0) {
+      const Tile t = walk.get();
+      const uint32_t stage = smem + STAGE_AREA + e * EPI_BYTES;
+      const uint32_t block = block_row<SWIGLU>(stage, lane);
+      for (int u = part + splits * e; u < t.n / 8; u += splits * EPI_WARPS) {
+        const int w = u & 3, ch = u >> 2, f0 = t.m * FE + WF * w;
+        if (32 * ch >= t.rows) continue;
+        float bias[4];
+        load_bias<SWIGLU>(a, t.g, f0, bias);
+        float sum[32] = {};
+        for (int q = 0; q < splits; ++q) {
+          uint32_t at;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem + u * PART_BYTES + lane * 16), "r"(q));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y, z, o;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x), "=f"(y), "=f"(z), "=f"(o)
+                         : "r"(at + i * 512)
+                         : "memory");
+            sum[4 * i] += x;
+            sum[4 * i + 1] += y;
+            sum[4 * i + 2] += z;
+            sum[4 * i + 3] += o;
+          }
+        }
+        uint32_t lo[16], hi[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          lo[i] = __float_as_uint(sum[i]);
+          hi[i] = __float_as_uint(sum[16 + i]);
+        }
+        finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [] {});
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // nobody leaves while his part is read
   }
   __syncwarp();
   tc::fence_before();
@@ -690,10 +782,10 @@ bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int group
   return encode(map, base, 3, dims, strides, box);
 }
 
-template <int CG, bool SWIGLU, bool F32>
-cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
+template <int CG, bool SWIGLU, bool F32, bool SPLIT>
+cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done;
-  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU, F32>, SMEM, done);
+  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU, F32, SPLIT>, SMEM, done);
   if (e != cudaSuccess) return e;
   constexpr int FE = (SWIGLU ? 64 : 128) * CG;
   Plan p;
@@ -702,6 +794,7 @@ cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   p.stages = STAGE_AREA / p.stage_bytes < MAX_STAGES ? STAGE_AREA / p.stage_bytes : MAX_STAGES;
   p.n_m = (a.n_out + FE - 1) / FE;
   p.k_steps = (a.n_in + KS - 1) / KS;
+  p.splits = splits;
   p.box_rows = a.start == nullptr ? nt / CG : a.index == nullptr ? 32 / CG : 0;
   p.n_main = a.w_last != nullptr ? a.n_groups - 1 : a.n_groups;
   // (the layer's own indices are in range)
@@ -715,13 +808,13 @@ cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   const cuuint32_t box[2] = {KS, (cuuint32_t)(p.box_rows > 0 ? p.box_rows : 1)};
   if (!encode(&maps.x, a.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
 
-  int units = sms / CG;
+  int units = sms / (CG * splits);
   if (a.start == nullptr) {
     const long long tiles = (long long)((a.n_rows + nt - 1) / nt) * p.n_m;
     if (tiles < units) units = (int)tiles;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units * CG, 1, 1);
+  cfg.gridDim = dim3(units * CG * splits, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = stream;
@@ -729,31 +822,45 @@ cudaError_t launch(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = CG * splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU, F32>, a, p, maps);
+  cfg.numAttrs = CG * splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU, F32, SPLIT>, a, p, maps);
 }
 
-template <int CG>
-cudaError_t launch_as(const LinearArgs& a, int nt, int sms, cudaStream_t stream) {
+template <int CG, bool SPLIT>
+cudaError_t launch_as(const LinearArgs& a, int nt, int splits, int sms, cudaStream_t stream) {
   if (a.act == ACT_SWIGLU)
-    return a.out_f32 ? launch<CG, true, true>(a, nt, sms, stream) : launch<CG, true, false>(a, nt, sms, stream);
-  return a.out_f32 ? launch<CG, false, true>(a, nt, sms, stream) : launch<CG, false, false>(a, nt, sms, stream);
+    return a.out_f32 ? launch<CG, true, true, SPLIT>(a, nt, splits, sms, stream)
+                     : launch<CG, true, false, SPLIT>(a, nt, splits, sms, stream);
+  return a.out_f32 ? launch<CG, false, true, SPLIT>(a, nt, splits, sms, stream)
+                   : launch<CG, false, false, SPLIT>(a, nt, splits, sms, stream);
 }
 
-// The rows of a plain product's tiles: those whose rounds of tiles take least, each
-// its rows and COST_TILE for what it costs besides.
-long long best_rows(int n_rows, int n_m, int units, int* nt) {
-  long long best = -1;
-  for (int k = 1; k <= NT_MAX / 32; ++k) {
-    const int n = 32 * k;
-    const long long tiles = (long long)((n_rows + n - 1) / n) * n_m, cost = (tiles + units - 1) / units * (n + 64);
-    if (best < 0 || cost <= best) {
-      best = cost;
-      *nt = n;
-    }
+// How a plain product is cut: CTAs a tile, rows of a tile, parts of k.  Cycles, as
+// measured: a stage of n rows takes 2 n (the products), and 350 at least (its barriers and
+// copies); a tile's epilogue 12 n, hidden but for the last tile's; joining parts 3000.
+struct Choice {
+  int cg, nt, splits;
+  long long cost;
+};
+Choice choose(const LinearArgs& a, int sms) {
+  const int fe = a.act == ACT_SWIGLU ? 64 : 128, k_steps = (a.n_in + KS - 1) / KS;
+  Choice best = {0, 0, 0, 0};
+  const auto consider = [&](int cg, int n, int splits) {
+    const long long tiles = (long long)((a.n_rows + n - 1) / n) * ((a.n_out + fe * cg - 1) / (fe * cg));
+    // Clusters of 4 and 8 CTAs leave a few SMs of a GPC without one.
+    const long long units = splits == 8 ? sms * 2 / 19 : splits == 4 ? sms * 4 / 17 : sms / (cg * splits);
+    const long long rounds = units > 0 ? (tiles + units - 1) / units : 1ll << 30;
+    if (splits > 1 && (rounds > 1 || k_steps < 2 * splits)) return;
+    const int step = 2 * n > 350 ? 2 * n : 350;
+    const long long cost = rounds * ((k_steps + splits - 1) / splits) * step + 12 * n / splits + (splits > 1 ? 3000 : 0);
+    if (best.cg == 0 || cost < best.cost) best = {cg, n, splits, cost};
+  };
+  for (int n = NT_MAX; n >= 32; n -= 32) {
+    consider(2, n, 1);
+    for (int s = 1; s <= 8; s *= 2) consider(1, n, s);
   }
   return best;
 }
@@ -761,13 +868,10 @@ long long best_rows(int n_rows, int n_m, int units, int* nt) {
 }  // namespace
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
-  const bool sw = a.act == ACT_SWIGLU;
-  if (a.start != nullptr) return launch_as<2>(a, NT_MAX, sms, stream);
-  const int fe = sw ? 64 : 128;
-  int nt1 = 0, nt2 = 0;
-  const long long c1 = best_rows(a.n_rows, (a.n_out + fe - 1) / fe, sms, &nt1);
-  const long long c2 = best_rows(a.n_rows, (a.n_out + 2 * fe - 1) / (2 * fe), sms / 2, &nt2);
-  return c2 <= c1 ? launch_as<2>(a, nt2, sms, stream) : launch_as<1>(a, nt1, sms, stream);
+  if (a.start != nullptr) return launch_as<2, false>(a, NT_MAX, 1, sms, stream);
+  const Choice c = choose(a, sms);
+  if (c.splits > 1) return launch_as<1, true>(a, c.nt, c.splits, sms, stream);
+  return c.cg == 2 ? launch_as<2, false>(a, c.nt, 1, sms, stream) : launch_as<1, false>(a, c.nt, 1, sms, stream);
 }
 
 }  // namespace flint

@@ -10,9 +10,10 @@ namespace {
 
 using namespace lin;
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
-static_assert(E == THREADS, "a thread has an expert");
+constexpr int COMBINE = 256;                 // threads of the combine
+constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int WORDS = CHUNK / 32;
+static_assert(CHUNK <= 255, "a chunk's count of an expert fits a byte");
 
 // The top k of one token's scores by one warp, as topk_warp ranks them, for scores of
 // any bits: zeros are equal whatever their sign, NaN ranks above every number, and the
@@ -54,6 +55,7 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
 struct Chunk {
   uint32_t mask[E][WORDS];
   int base[E];      // first row of the expert's pairs of this chunk
+  int all[E], before[E];
   int warp_tot[8];
 };
 
@@ -103,12 +105,20 @@ __device__ __forceinline__ void place(const SelectArgs& a, Chunk& sh, int t0, in
     for (int t = threadIdx.x; t < n; t += THREADS) a.row_token[a.n * TOPK + t0 + t] = t0 + t;
 }
 
-__device__ __forceinline__ void write_start(const SelectArgs& a, int excl) {
-  a.start[threadIdx.x] = excl;
-  if (threadIdx.x == 0) {
+// The experts' first rows from sh.all, their pairs of all chunks, and sh.before, those of
+// the chunks before this one; by all threads.
+__device__ __forceinline__ void starts(const SelectArgs& a, Chunk& sh, bool write) {
+  if (threadIdx.x < E) {
+    int total;
+    const int excl = scan256(sh.all[threadIdx.x], sh.warp_tot, &total, [] { named_sync(1, E); });
+    sh.base[threadIdx.x] = excl + sh.before[threadIdx.x];
+    if (write) a.start[threadIdx.x] = excl;
+  }
+  if (write && threadIdx.x == E) {
     a.start[E] = a.n * TOPK;
     if (a.shared_group) a.start[E + 1] = a.n * (TOPK + 1);
   }
+  __syncthreads();
 }
 
 // All tokens in one CTA.
@@ -117,53 +127,67 @@ __global__ void __launch_bounds__(THREADS) select_small_kernel(const SelectArgs 
   pdl_wait();
   pdl_trigger();
   choose(a, sh, 0, a.n);
-  int total;
-  const int cnt = mask_count(sh.mask[threadIdx.x]);
-  const int excl = scan256(cnt, sh.warp_tot, &total, [] { __syncthreads(); });
-  sh.base[threadIdx.x] = excl;
-  write_start(a, excl);
+  if (threadIdx.x < E) {
+    sh.all[threadIdx.x] = mask_count(sh.mask[threadIdx.x]);
+    sh.before[threadIdx.x] = 0;
+  }
   __syncthreads();
+  starts(a, sh, true);
   place(a, sh, 0, a.n);
 }
 
+// Many tokens, a chunk a CTA: the choice and the chunks' counts, a byte each, ...
 __global__ void __launch_bounds__(THREADS) select_choose_kernel(const SelectArgs a) {
   __shared__ Chunk sh;
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, a.n - t0);
   choose(a, sh, t0, n);
-  a.counts[blockIdx.x * E + threadIdx.x] = mask_count(sh.mask[threadIdx.x]);
+  if (threadIdx.x < E) a.counts[blockIdx.x * E + threadIdx.x] = (uint8_t)mask_count(sh.mask[threadIdx.x]);
 }
 
+// ... and the rows.  Sixteen groups of 64 threads sum every sixteenth chunk's counts, four
+// experts a thread.
 __global__ void __launch_bounds__(THREADS) select_place_kernel(const SelectArgs a) {
   __shared__ Chunk sh;
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, a.n - t0);
   for (int i = threadIdx.x; i < E * WORDS; i += THREADS) (&sh.mask[0][0])[i] = 0;
-  int before = 0, all = 0;
-#pragma unroll 16
-  for (int i = 0; i < (int)gridDim.x; ++i) {
-    const int v = __ldcg(a.counts + i * E + threadIdx.x);
-    all += v;
-    if (i < (int)blockIdx.x) before += v;
-  }
+  if (threadIdx.x < E) sh.all[threadIdx.x] = sh.before[threadIdx.x] = 0;
   __syncthreads();
+  const int e0 = 4 * (threadIdx.x & 63), first = threadIdx.x >> 6;
+  int all[4] = {}, before[4] = {};
+#pragma unroll
+  for (int k = 0; k < MAX_CHUNKS / 16; ++k) {
+    const int i = first + 16 * k;
+    if (i < (int)gridDim.x) {
+      const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(a.counts + i * E + e0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = (v >> (8 * j)) & 255;
+        all[j] += c;
+        if (i < (int)blockIdx.x) before[j] += c;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {   // whole numbers: the order does not matter
+    atomicAdd(&sh.all[e0 + j], all[j]);
+    atomicAdd(&sh.before[e0 + j], before[j]);
+  }
   for (int p = threadIdx.x; p < n * TOPK; p += THREADS) {
     const int t = p / TOPK;
     atomicOr(&sh.mask[a.idx[t0 * TOPK + p]][t >> 5], 1u << (t & 31));
   }
-  int total;
-  const int excl = scan256(all, sh.warp_tot, &total, [] { __syncthreads(); });
-  sh.base[threadIdx.x] = excl + before;
-  if (blockIdx.x == 0) write_start(a, excl);
   __syncthreads();
+  starts(a, sh, blockIdx.x == 0);
   place(a, sh, t0, n);
 }
 
 // A token a CTA, 8 values of the row a thread.
-__global__ void __launch_bounds__(THREADS) combine_kernel(const CombineArgs a) {
-  static_assert(H == 8 * THREADS, "8 values a thread");
+__global__ void __launch_bounds__(COMBINE) combine_kernel(const CombineArgs a) {
+  static_assert(H == 8 * COMBINE, "8 values a thread");
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x;
@@ -204,10 +228,10 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const CombineArgs a) {
 }
 
 template <class Args>
-cudaError_t launch(void (*kernel)(const Args), int grid, const Args& a, cudaStream_t stream) {
+cudaError_t launch(void (*kernel)(const Args), int grid, int threads, const Args& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -221,13 +245,13 @@ cudaError_t launch(void (*kernel)(const Args), int grid, const Args& a, cudaStre
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
   const int chunks = (a.n + CHUNK - 1) / CHUNK;
-  if (chunks == 1) return launch(select_small_kernel, 1, a, stream);
-  const cudaError_t e = launch(select_choose_kernel, chunks, a, stream);
-  return e != cudaSuccess ? e : launch(select_place_kernel, chunks, a, stream);
+  if (chunks == 1) return launch(select_small_kernel, 1, THREADS, a, stream);
+  const cudaError_t e = launch(select_choose_kernel, chunks, THREADS, a, stream);
+  return e != cudaSuccess ? e : launch(select_place_kernel, chunks, THREADS, a, stream);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
-  return launch(combine_kernel, a.n, a, stream);
+  return launch(combine_kernel, a.n, COMBINE, a, stream);
 }
 
 }  // namespace flint
