@@ -6,8 +6,7 @@
 // inside a step is free as long as both operands take the same: lane 4 r + c reads
 // the 16 bytes of k = 8c .. 8c + 7 of weight rows r and r + 8 and of x row r, which
 // are the fragments of two m16n8k16 products as they come, with no staging.  The
-// eight warps of a CTA share the 16 weight rows and take every eighth step; their
-// sums meet in shared memory in a fixed order.  SwiGLU: the 16 weight rows are 8 gate
+// warps of a CTA share the 16 weight rows and take steps in turn; their sums meet in shared memory in a fixed order.  SwiGLU: the 16 weight rows are 8 gate
 // and the 8 up rows of the same outputs.
 //
 // Bound: the weights' bytes for one row, launch and first-load latency at a few MB.
@@ -18,7 +17,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int DEEP = 8;   // steps of weights in flight a warp
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p, bool there) {
   uint4 v = make_uint4(0, 0, 0, 0);
@@ -29,10 +28,9 @@ __device__ __forceinline__ uint4 ld16(const uint16_t* p, bool there) {
 // All rows of x, NB blocks of 8.
 static_assert(FEW_ROWS == 16, "one or two blocks of rows");
 
-template <int NB, bool SWIGLU>
-__global__ void __launch_bounds__(THREADS) linear_rows_kernel(const LinearArgs a) {
+template <int NB, bool SWIGLU, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const LinearArgs a) {
   constexpr int FE = SWIGLU ? 8 : 16, NT = 8 * NB;
-  constexpr int DEEP = 8;   // steps of weights in flight: all of 2048 inputs
   __shared__ float part[WARPS][NT][17];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   const int f0 = blockIdx.x * FE;
@@ -72,7 +70,7 @@ __global__ void __launch_bounds__(THREADS) linear_rows_kernel(const LinearArgs a
     for (int i = 0; i < 4; ++i) part[warp][8 * b + 2 * c + (i & 1)][r + 8 * (i >> 1)] = acc[b][i];
   __syncthreads();
 #pragma unroll
-  for (int o = tid; o < FE * NT; o += THREADS) {
+  for (int o = tid; o < FE * NT; o += 32 * WARPS) {
     const int t = o / FE, f = o % FE;
     if (t < a.n_rows && f0 + f < a.n_out) {
       float v = 0.0f, up = 0.0f;
@@ -101,26 +99,29 @@ __global__ void __launch_bounds__(THREADS) linear_rows_kernel(const LinearArgs a
   }
 }
 
-template <int NB>
+template <int NB, int WARPS>
 cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
   const int fe = a.act == ACT_SWIGLU ? 8 : 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.n_out + fe - 1) / fe, 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(32 * WARPS, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.act == ACT_SWIGLU ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<NB, true>, a)
-                             : cudaLaunchKernelEx(&cfg, linear_rows_kernel<NB, false>, a);
+  return a.act == ACT_SWIGLU ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<NB, true, WARPS>, a)
+                             : cudaLaunchKernelEx(&cfg, linear_rows_kernel<NB, false, WARPS>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream) {
-  return a.n_rows <= 8 ? launch<1>(a, stream) : launch<2>(a, stream);
+  // Sixteen warps where eight do not have all the weights in flight at once.
+  const bool deep = a.n_in > 32 * 8 * DEEP;
+  if (a.n_rows <= 8) return deep ? launch<1, 16>(a, stream) : launch<1, 8>(a, stream);
+  return deep ? launch<2, 16>(a, stream) : launch<2, 8>(a, stream);
 }
 
 }  // namespace flint

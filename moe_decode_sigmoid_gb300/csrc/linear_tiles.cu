@@ -40,6 +40,7 @@ constexpr int STAGE_AREA = 192 * 1024;
 constexpr int EPI_BYTES = 32 * 80;        // a warp's 32 rows of 32 outputs, padded
 constexpr int SMEM = STAGE_AREA + EPI_WARPS * EPI_BYTES + 1024;
 constexpr int NT_MAX = 256;
+constexpr int MAX_SPLITS = 8;             // parts of k: a portable cluster
 constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
 // What a tile costs besides its rows, in rows; and what its weights' bytes from HBM do,
 // which a group's first tile of rows fetches.
@@ -53,7 +54,6 @@ struct Shared {
   long long warp_tot[WARPS];
   long long pre[GROUP_LIMIT + 2];          // cost of all tiles before a group's
 };
-static_assert(NT_MAX / 32 * 4 * PART_BYTES <= STAGE_AREA, "a tile's sums fit the ring's place");
 static_assert(SMEM + sizeof(Shared) <= 227 * 1024, "fits");
 
 // Tensor maps: the weights (all groups but a last one of its own, and that one), x.
@@ -69,6 +69,7 @@ struct Plan {
   int box_rows;    // rows of a box of x; 0: four rows an instruction by index
   int n_main;      // groups whose weights are in the first map
   int splits;      // CTAs that share a tile's k
+  int part_bytes;  // room for their sums, behind the ring
   int checked;     // rows whose index is out of range are not stored
 };
 
@@ -209,6 +210,13 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Waits for a phase, a second at most, by a whole warp, which goes on converged; a
@@ -411,21 +419,35 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint3
       }
     }
     if constexpr (F32) {
-      // 8 neighbouring outputs of a row by 8 lanes: whole 32-byte sectors.
+      // Rows of these outputs (as many bytes as FROW holds) through shared memory.
+      constexpr int FROW = WF * 4 + 16, FROWS = SWIGLU ? 32 : 16;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int in = SWIGLU ? i : i & 7;
-        const int tok = 16 * h + 8 * (in >> 2) + 2 * c + (i & 1);
-        const int f = f0 + r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
+        const int tok = 8 * (in >> 2) + 2 * c + (i & 1), f = r + 8 * ((i >> 1) & 1) + (SWIGLU || i < 8 ? 0 : 16);
+        st_shared4(stage + tok * FROW + f * 4, v[i]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        constexpr int FPARTS = WF / 4;
+        const int u = lane + 32 * i, tok = 16 * h + u / FPARTS, f = f0 + 4 * (u % FPARTS);
+        static_assert(FROWS * FPARTS == 128, "4 parts a lane");
         if (tok < left && f < a.n_out) {
           const int row = row0 + tok;
-          if (p.checked && (unsigned)__ldg(a.index + row) >= (unsigned)a.n_x) continue;
-          const size_t at = (size_t)row * a.n_out + f;
-          float o = v[i];
-          if (a.residual != nullptr) o += static_cast<const float*>(a.residual)[at];
-          static_cast<float*>(a.out)[at] = o;
+          if (!p.checked || (unsigned)__ldg(a.index + row) < (unsigned)a.n_x) {
+            const size_t at = (size_t)row * a.n_out + f;
+            uint4 o = ld_shared16(stage + (u / FPARTS) * FROW + (u % FPARTS) * 16);
+            if (a.residual != nullptr) {
+              const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
+              o = make_uint4(__float_as_uint(__uint_as_float(o.x) + x.x), __float_as_uint(__uint_as_float(o.y) + x.y),
+                             __float_as_uint(__uint_as_float(o.z) + x.z), __float_as_uint(__uint_as_float(o.w) + x.w));
+            }
+            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at) = o;
+          }
         }
       }
+      __syncwarp();
     } else {
       // Block q of the four that move at a time: outputs 8 q .. of rows 8 j .. (SwiGLU:
       // outputs 8 (q % 2) .. of rows 8 (2 j + q / 2) ..); the register of its first row.
@@ -481,6 +503,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int k0 = SPLIT ? p.k_steps * part / splits : 0;
   const int k_steps = SPLIT ? p.k_steps * (part + 1) / splits - k0 : p.k_steps;
   const uint32_t smem = (smem_addr(s_raw) + 1023u) & ~1023u;
+  const uint32_t parts = smem + STAGE_AREA - p.part_bytes;   // SPLIT: other CTAs write here
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -675,15 +698,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         ld_frag(t0 + b * NT_MAX + 32 * ch, lo);
         ld_frag(t0 + b * NT_MAX + 32 * ch + (16u << 16), hi);
         if constexpr (SPLIT) {
-          // This CTA's part of the sums, in the products' place (they are through with it).
+          // This CTA's part of the sums, to the CTA that finishes these 32 x 32.
           tc::wait_ld();
           tc::arrived(lo);
           tc::arrived(hi);
-          const uint32_t at = smem + (4 * ch + w) * PART_BYTES + lane * 16;
+          const int u = 4 * ch + w;
+          uint32_t at;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(parts + (u / splits * splits + part) * PART_BYTES + lane * 16), "r"(u % splits));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            st_shared16(at + i * 512, make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
-            st_shared16(at + 2048 + i * 512, make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]));
+            st_cluster16(at + i * 512, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            st_cluster16(at + 2048 + i * 512, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
           }
         } else {
           finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [&] {
@@ -702,7 +727,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if constexpr (SPLIT) {
     // ===== the parts of all CTAs of the cluster, joined in their order: 32 rows x 32
-    // weight rows a warp, dealt out over the CTAs ====================================
+    // weight rows a warp, dealt out over the CTAs.  (Each wrote them to where they are
+    // read, which took 3 us less at 8 parts than to read them from one another.) ======
     __syncwarp();
     cluster_sync();
     const int e = warp - EPI0;
@@ -718,19 +744,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         load_bias<SWIGLU>(a, t.g, f0, bias);
         float sum[32] = {};
         for (int q = 0; q < splits; ++q) {
-          uint32_t at;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem + u * PART_BYTES + lane * 16), "r"(q));
+          const uint32_t at = parts + (u / splits * splits + q) * PART_BYTES + lane * 16;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float x, y, z, o;
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x), "=f"(y), "=f"(z), "=f"(o)
-                         : "r"(at + i * 512)
-                         : "memory");
-            sum[4 * i] += x;
-            sum[4 * i + 1] += y;
-            sum[4 * i + 2] += z;
-            sum[4 * i + 3] += o;
+            const uint4 x = ld_shared16(at + i * 512);
+            sum[4 * i] += __uint_as_float(x.x);
+            sum[4 * i + 1] += __uint_as_float(x.y);
+            sum[4 * i + 2] += __uint_as_float(x.z);
+            sum[4 * i + 3] += __uint_as_float(x.w);
           }
         }
         uint32_t lo[16], hi[16];
@@ -742,8 +763,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [] {});
       }
     }
-    __syncwarp();
-    cluster_sync();   // nobody leaves while his part is read
   }
   __syncwarp();
   tc::fence_before();
@@ -791,7 +810,9 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
   Plan p;
   p.nt = nt;
   p.stage_bytes = A_BYTES + nt / CG * KS * 2;
-  p.stages = STAGE_AREA / p.stage_bytes < MAX_STAGES ? STAGE_AREA / p.stage_bytes : MAX_STAGES;
+  p.part_bytes = splits > 1 ? (nt / 8 + splits - 1) / splits * splits * PART_BYTES : 0;
+  p.stages = (STAGE_AREA - p.part_bytes) / p.stage_bytes;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   p.n_m = (a.n_out + FE - 1) / FE;
   p.k_steps = (a.n_in + KS - 1) / KS;
   p.splits = splits;
@@ -838,6 +859,36 @@ cudaError_t launch_as(const LinearArgs& a, int nt, int splits, int sms, cudaStre
                    : launch<CG, false, false, SPLIT>(a, nt, splits, sms, stream);
 }
 
+// Clusters of so many CTAs that the device runs at once: GPCs have no whole number of
+// them (of GB300's 152 SMs 8-CTA clusters take 120, 6-CTA ones 138).
+int clusters(int splits, int sms) {
+  static std::atomic<int> known[64][MAX_SPLITS + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][splits].load(std::memory_order_relaxed);
+  if (n == 0) {
+    static std::atomic<uint64_t> done;
+    const auto kernel = linear_tiles_kernel<1, false, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits * (sms / splits), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (set_smem_limit_once(kernel, SMEM, done) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
+    }
+    known[dev][splits].store(n > 0 ? n : -1, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // How a plain product is cut: CTAs a tile, rows of a tile, parts of k.  Cycles, as
 // measured: a stage of n rows takes 2 n (the products), and 350 at least (its barriers and
 // copies); a tile's epilogue 12 n, hidden but for the last tile's; joining parts 3000.
@@ -850,17 +901,19 @@ Choice choose(const LinearArgs& a, int sms) {
   Choice best = {0, 0, 0, 0};
   const auto consider = [&](int cg, int n, int splits) {
     const long long tiles = (long long)((a.n_rows + n - 1) / n) * ((a.n_out + fe * cg - 1) / (fe * cg));
-    // Clusters of 4 and 8 CTAs leave a few SMs of a GPC without one.
-    const long long units = splits == 8 ? sms * 2 / 19 : splits == 4 ? sms * 4 / 17 : sms / (cg * splits);
-    const long long rounds = units > 0 ? (tiles + units - 1) / units : 1ll << 30;
-    if (splits > 1 && (rounds > 1 || k_steps < 2 * splits)) return;
+    const long long units = splits > 1 ? clusters(splits, sms) : sms / cg;
+    if (units < 1 || (splits > 1 && (tiles > units || k_steps < 4 * splits))) return;
     const int step = 2 * n > 350 ? 2 * n : 350;
-    const long long cost = rounds * ((k_steps + splits - 1) / splits) * step + 12 * n / splits + (splits > 1 ? 3000 : 0);
+    const long long cost = (tiles + units - 1) / units * ((k_steps + splits - 1) / splits) * step +
+                           12 * n / splits + (splits > 1 ? 3000 : 0);
     if (best.cg == 0 || cost < best.cost) best = {cg, n, splits, cost};
   };
   for (int n = NT_MAX; n >= 32; n -= 32) {
     consider(2, n, 1);
-    for (int s = 1; s <= 8; s *= 2) consider(1, n, s);
+    consider(1, n, 1);
+    // Three stages at least beside the parts.
+    if (n <= 128)
+      for (int s = 2; s <= MAX_SPLITS; ++s) consider(1, n, s);
   }
   return best;
 }
