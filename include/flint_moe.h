@@ -528,6 +528,13 @@ flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaS
  * bounded by one second) ran out; that call's outputs are undefined. */
 flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t stream);
 
+/* Fault-injection hook for tests, as flint_moe_debug_arm_stall: a one-shot wait in
+ * the next call on this workspace that runs the tiled kernel (any grouped product;
+ * a plain one of more than 16 rows), on a barrier that nothing completes.  It runs
+ * out after a second, the call ends with FLINT_ERR_DEVICE_TIMEOUT as its device
+ * status, and the workspace has to be initialised again. */
+flint_status flint_prompt_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* out = act(x w^T + bias) + residual for n_rows rows (1 .. FLINT_LINEAR_MAX_ROWS).
  *   x_bf16   [n_rows, n_in]
  *   w_bf16   [n_out, n_in], with FLINT_ACT_SWIGLU [2 n_out, n_in]

@@ -49,7 +49,7 @@ EXPORTS = (
     "flint_attn_get_device_status", "flint_attn_debug_arm_stall",
     "flint_attn_paged_bf16", "flint_attn_paged_fp8",
     "flint_prompt_workspace_bytes", "flint_prompt_workspace_init",
-    "flint_prompt_get_device_status", "flint_linear_bf16",
+    "flint_prompt_get_device_status", "flint_prompt_debug_arm_stall", "flint_linear_bf16",
     "flint_grouped_linear_bf16", "flint_moe_select", "flint_moe_combine_bf16",
     "flint_moe_prompt_bf16",
 )
@@ -186,6 +186,8 @@ def lib() -> ctypes.CDLL:
     L.flint_prompt_workspace_init.argtypes = [_P, _SZ, _P]
     L.flint_prompt_get_device_status.restype = ctypes.c_int
     L.flint_prompt_get_device_status.argtypes = [_P, _P]
+    L.flint_prompt_debug_arm_stall.restype = ctypes.c_int
+    L.flint_prompt_debug_arm_stall.argtypes = [_P, _SZ, _P]
     L.flint_linear_bf16.restype = ctypes.c_int
     L.flint_linear_bf16.argtypes = [_P, _I32] + [_P] * 6 + [_SZ, _P]
     L.flint_grouped_linear_bf16.restype = ctypes.c_int
@@ -705,6 +707,12 @@ def flint_prompt_workspace_init(workspace: torch.Tensor, stream=None):
 def flint_prompt_get_device_status(workspace: torch.Tensor, stream=None) -> int:
     wp, _ = _ws_only("flint_prompt_get_device_status", workspace)
     return int(lib().flint_prompt_get_device_status(wp, _stream(stream)))
+
+
+def flint_prompt_debug_arm_stall(workspace: torch.Tensor, stream=None):
+    wp, wb = _ws_only("flint_prompt_debug_arm_stall", workspace)
+    _check(lib().flint_prompt_debug_arm_stall(wp, wb, _stream(stream)),
+           "flint_prompt_debug_arm_stall")
 
 
 _LINEAR_REFS = {}  # the C struct of a call's dims, by its fields

@@ -107,6 +107,11 @@ flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t 
   return static_cast<flint_status>(code);
 }
 
+flint_status flint_prompt_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!ws_ok(workspace, ws_bytes, 0)) return FLINT_ERR_WORKSPACE;
+  return cuda_status(cudaMemsetAsync(static_cast<char*>(workspace) + lin::WS_STALL, 1, sizeof(uint32_t), stream));
+}
+
 flint_status flint_linear_bf16(const flint_linear_dims* dims, int32_t n_rows, const void* x_bf16,
                                const void* w_bf16, const float* bias, const void* residual,
                                void* out, void* workspace, size_t ws_bytes, cudaStream_t stream) {

@@ -73,6 +73,8 @@ def test_workspace_bytes(L):
     assert L.flint_prompt_workspace_init(A, head - 1, None) == WORKSPACE
     assert L.flint_prompt_workspace_init(A + 8, head, None) == WORKSPACE
     assert L.flint_prompt_get_device_status(None, None) == WORKSPACE
+    assert L.flint_prompt_debug_arm_stall(None, head, None) == WORKSPACE
+    assert L.flint_prompt_debug_arm_stall(A, head - 1, None) == WORKSPACE
 
 
 BAD_DIMS = [(0, 32, 0, 0), (60, 32, 0, 0), (m.LINEAR_MAX_IN + 8, 32, 0, 0), (64, 0, 0, 0),
