@@ -39,7 +39,9 @@ constexpr int MAX_STAGES = 12;
 constexpr int STAGE_AREA = 192 * 1024;
 constexpr int EPI_BYTES = 32 * 80;        // a warp's 32 rows of 32 outputs, padded
 constexpr int SMEM = STAGE_AREA + EPI_WARPS * EPI_BYTES + 1024;
-constexpr int NT_MAX = 256;
+constexpr int NT_MAX = 256, NT_MAX_F32 = 128;
+static_assert(NT_MAX_F32 == 4 * 32, "two chunks of rows a warp of the epilogue");
+constexpr int SEGMENT = 8;                // fp32 outputs: stages that are summed in TMEM
 constexpr int MAX_SPLITS = 8;             // parts of k: a portable cluster
 constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
 // What a tile costs besides its rows, in rows; and what its weights' bytes from HBM do,
@@ -626,17 +628,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) *reinterpret_cast<int*>(static_cast<char*>(a.ws) + WS_STALL) = 0;   // the test hook
       ok = warp_wait(sh, sh.never, 0);
     }
-    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next()) {
       const int n = __shfl_sync(0xffffffffu, walk.get().n, 0);
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
-      const int b = it & 1;
-      const uint32_t d = d0 + b * NT_MAX;
-      if (!(ok = warp_wait(sh, sh.acc_empty[b], ((it >> 1) & 1) ^ 1))) break;
-      tc::fence_after();
+      int b = 0;
+      uint32_t d = 0;
       // Two stages at a time: their waits and their products' issue run one behind the
       // other, ~150 and ~200 cycles, and a stage of 192 rows executes in 384.
       for (int k = 0; k < k_steps; k += 2) {
         const bool two = k + 1 < k_steps;
+        const bool first = F32 ? k % SEGMENT == 0 : k == 0;
+        const bool last = k + 2 >= k_steps || (F32 && (k + 2) % SEGMENT == 0);
+        if (first) {
+          b = it & 1;
+          d = d0 + b * NT_MAX;
+          if (!(ok = warp_wait(sh, sh.acc_empty[b], ((it >> 1) & 1) ^ 1))) break;
+          tc::fence_after();
+          ++it;
+        }
         int s1 = s + 1;
         uint32_t phase1 = phase;
         if (s1 == p.stages) {
@@ -651,14 +660,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t a1_lo = tc::desc_lo(at1, 16), b1_lo = tc::desc_lo(at1 + A_BYTES, 16);
         if (tc::one_thread()) {
 #pragma unroll
-          for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + 2 * j, idesc, k > 0 || j > 0);
+          for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + 2 * j, idesc, !first || j > 0);
           O::commit(smem_addr(&sh.empty[s]));
           if (two) {
 #pragma unroll
             for (int j = 0; j < KS / 16; ++j) O::mma(d, a1_lo + 2 * j, b1_lo + 2 * j, idesc, 1);
             O::commit(smem_addr(&sh.empty[s1]));
           }
-          if (k + 2 >= k_steps) O::commit(smem_addr(&sh.acc_full[b]));
+          if (last) O::commit(smem_addr(&sh.acc_full[b]));
         }
         __syncwarp();
         s = s1;
@@ -682,36 +691,74 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t block = block_row<SWIGLU>(stage, lane);
     bool ok = true;
     int it = 0;
-    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next(), ++it) {
+    for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next()) {
       const Tile t = walk.get();
       const int f0 = (t.m * CG + rank) * FE + WF * w;
-      const int b = it & 1;
       float bias[4];
       if constexpr (!SPLIT) load_bias<SWIGLU>(a, t.g, f0, bias);
-      if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
-      tc::fence_after();
       const int chunks = t.n / 32;
-      if (half >= chunks && lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
-      // Two warps have the same lanes; each takes every other 32 rows.
-      for (int ch = half; ch < chunks; ch += 2) {
-        uint32_t lo[16], hi[16];
-        ld_frag(t0 + b * NT_MAX + 32 * ch, lo);
-        ld_frag(t0 + b * NT_MAX + 32 * ch + (16u << 16), hi);
-        if constexpr (SPLIT) {
-          // This CTA's part of the sums, to the CTA that finishes these 32 x 32.
-          tc::wait_ld();
-          tc::arrived(lo);
-          tc::arrived(hi);
-          const int u = 4 * ch + w;
-          uint32_t at;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(parts + (u / splits * splits + part) * PART_BYTES + lane * 16), "r"(u % splits));
+      // This CTA's part of the sums of 32 rows, to the CTA that finishes these 32 x 32.
+      const auto push = [&](int ch, const uint32_t (&lo)[16], const uint32_t (&hi)[16]) {
+        const int u = 4 * ch + w;
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(at)
+            : "r"(parts + (u / splits * splits + part) * PART_BYTES + lane * 16), "r"(u % splits));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st_cluster16(at + i * 512, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-            st_cluster16(at + 2048 + i * 512, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          st_cluster16(at + i * 512, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          st_cluster16(at + 2048 + i * 512, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        }
+      };
+      if constexpr (F32) {
+        // fp32 outputs: the tensor core cuts what it adds to its sums, a bias of up to half
+        // a unit a step (rel. error 1e-6 at k = 2048, growing with k); so TMEM sums no more
+        // than SEGMENT stages, and registers, which round, the segments.
+        uint32_t lo[2][16] = {}, hi[2][16] = {};
+        for (int k = 0; k < k_steps; k += SEGMENT, ++it) {
+          const int b = it & 1;
+          if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
+          tc::fence_after();
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (half + 2 * i < chunks) {
+              uint32_t x[16], y[16];
+              ld_frag(t0 + b * NT_MAX + 32 * (half + 2 * i), x);
+              ld_frag(t0 + b * NT_MAX + 32 * (half + 2 * i) + (16u << 16), y);
+              tc::wait_ld();
+              tc::arrived(x);
+              tc::arrived(y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                lo[i][j] = __float_as_uint(__uint_as_float(lo[i][j]) + __uint_as_float(x[j]));
+                hi[i][j] = __float_as_uint(__uint_as_float(hi[i][j]) + __uint_as_float(y[j]));
+              }
+            }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ch = half + 2 * i;
+          if (ch < chunks) {
+            if constexpr (SPLIT) push(ch, lo[i], hi[i]);
+            else finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo[i], hi[i], [] {});
           }
-        } else {
-          finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [&] {
+        }
+      } else {
+        const int b = it & 1;
+        if (!(ok = warp_wait(sh, sh.acc_full[b], (it >> 1) & 1))) break;
+        ++it;
+        tc::fence_after();
+        if (half >= chunks && lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
+        // Two warps have the same lanes; each takes every other 32 rows.
+        for (int ch = half; ch < chunks; ch += 2) {
+          uint32_t lo[16], hi[16];
+          ld_frag(t0 + b * NT_MAX + 32 * ch, lo);
+          ld_frag(t0 + b * NT_MAX + 32 * ch + (16u << 16), hi);
+          const auto land = [&] {
             tc::wait_ld();
             tc::arrived(lo);
             tc::arrived(hi);
@@ -720,7 +767,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               __syncwarp();
               if (lane == 0) O::arrive(O::leader(smem_addr(&sh.acc_empty[b])));
             }
-          });
+          };
+          if constexpr (SPLIT) {
+            land();
+            push(ch, lo, hi);
+          } else {
+            finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, land);
+          }
         }
       }
     }
@@ -908,7 +961,7 @@ Choice choose(const LinearArgs& a, int sms) {
                            12 * n / splits + (splits > 1 ? 3000 : 0);
     if (best.cg == 0 || cost < best.cost) best = {cg, n, splits, cost};
   };
-  for (int n = NT_MAX; n >= 32; n -= 32) {
+  for (int n = a.out_f32 ? NT_MAX_F32 : NT_MAX; n >= 32; n -= 32) {
     consider(2, n, 1);
     consider(1, n, 1);
     // Three stages at least beside the parts.
@@ -921,7 +974,7 @@ Choice choose(const LinearArgs& a, int sms) {
 }  // namespace
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
-  if (a.start != nullptr) return launch_as<2, false>(a, NT_MAX, 1, sms, stream);
+  if (a.start != nullptr) return launch_as<2, false>(a, a.out_f32 ? NT_MAX_F32 : NT_MAX, 1, sms, stream);
   const Choice c = choose(a, sms);
   if (c.splits > 1) return launch_as<1, true>(a, c.nt, c.splits, sms, stream);
   return c.cg == 2 ? launch_as<2, false>(a, c.nt, 1, sms, stream) : launch_as<1, false>(a, c.nt, 1, sms, stream);
