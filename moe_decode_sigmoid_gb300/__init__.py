@@ -715,33 +715,48 @@ def flint_prompt_debug_arm_stall(workspace: torch.Tensor, stream=None):
            "flint_prompt_debug_arm_stall")
 
 
-_LINEAR_REFS = {}  # the C struct of a call's dims, by its fields
+# (C struct by reference, rows of a weight matrix) of a linear call, by its n_in, n_out, act and
+# whether out is fp32.
+_LINEAR_DIMS = {}
 
 
-def _linear(f, x, w, out, w_dims, act):
-    """(C struct by reference, device, rows of x, n_in, rows of out, n_out, rows of a
-    weight matrix) of a linear call after checking x, w (of w_dims dimensions) and out."""
+def _linear_dims(f, x, out, act):
+    """The entry of _LINEAR_DIMS that x and out need, made; raises if they or act cannot be."""
     if not (isinstance(x, _Tensor) and x.is_cuda and x.dim() == 2 and
-            1 <= x.shape[0] <= LINEAR_MAX_ROWS and 8 <= x.shape[1] <= LINEAR_MAX_IN):
-        _bad(f, "x", "[1 to %d rows, 8 to %d] on a CUDA device" % (LINEAR_MAX_ROWS, LINEAR_MAX_IN), x)
+            8 <= x.shape[1] <= LINEAR_MAX_IN):
+        _bad(f, "x", "[rows, 8 to %d] on a CUDA device" % LINEAR_MAX_IN, x)
+    if not (isinstance(out, _Tensor) and out.dim() == 2 and 8 <= out.shape[1] <= LINEAR_MAX_OUT and
+            (out.dtype is _BF16 or out.dtype is _F32)):
+        _bad(f, "out", "a bf16 or float32 tensor [rows, 8 to %d]" % LINEAR_MAX_OUT, out)
+    if type(act) is not int or not FLINT_ACT_NONE <= act <= FLINT_ACT_SWIGLU:
+        raise FlintError(FLINT_ERR_UNSUPPORTED, "%s: act must be one of FLINT_ACT_*, got %r" %
+                         (f, act))
+    k, n, f32 = x.shape[1], out.shape[1], out.dtype is _F32
+    return _LINEAR_DIMS.setdefault(
+        (k, n, act, f32), (ctypes.byref(LinearDims(k, n, act, int(f32))),
+                           2 * n if act == FLINT_ACT_SWIGLU else n))
+
+
+def _linear(f, x, out, act):
+    """(C struct by reference, device, rows of x, n_in, rows of out, n_out, out's type, rows of a
+    weight matrix) of a linear call; the calls check what is left of x and out."""
+    dtype = getattr(out, "dtype", None)
+    try:
+        n_x, k = x.shape
+        rows, n = out.shape
+        ref, m = _LINEAR_DIMS[k, n, act, dtype is _F32]
+    except (AttributeError, ValueError, TypeError, KeyError):
+        ref, m = _linear_dims(f, x, out, act)
+        (n_x, k), (rows, n) = x.shape, out.shape
+    if dtype is not _F32:
+        dtype = _BF16
+    for name, t, r in (("x", x, n_x), ("out", out, rows)):
+        if not 1 <= r <= LINEAR_MAX_ROWS:
+            _bad(f, name, "of 1 to %d rows" % LINEAR_MAX_ROWS, t)
     dev = x.device
     if dev.index != torch._C._cuda_getDevice():
         _on_current_device(f, "x", x)
-    if not (isinstance(out, _Tensor) and out.dim() == 2 and 1 <= out.shape[0] <= LINEAR_MAX_ROWS and
-            8 <= out.shape[1] <= LINEAR_MAX_OUT and (out.dtype is _BF16 or out.dtype is _F32)):
-        _bad(f, "out", "a bf16 or float32 tensor [1 to %d rows, 8 to %d]" %
-             (LINEAR_MAX_ROWS, LINEAR_MAX_OUT), out)
-    if not (isinstance(w, _Tensor) and w.dim() == w_dims):
-        _bad(f, "w", "a tensor of %d dimensions" % w_dims, w)
-    key = (x.shape[1], out.shape[1], act, int(out.dtype is _F32))
-    ref = _LINEAR_REFS.get(key)
-    if ref is None:
-        if type(act) is not int or not FLINT_ACT_NONE <= act <= FLINT_ACT_SWIGLU:
-            raise FlintError(FLINT_ERR_UNSUPPORTED, "%s: act must be one of FLINT_ACT_*, got %r" %
-                             (f, act))
-        ref = _LINEAR_REFS.setdefault(key, ctypes.byref(LinearDims(*key)))
-    m = key[1] * 2 if act == FLINT_ACT_SWIGLU else key[1]
-    return ref, dev, x.shape[0], key[0], out.shape[0], key[1], m
+    return ref, dev, n_x, k, rows, n, dtype, m
 
 
 def flint_linear_bf16(x, w, out, workspace, bias=None, residual=None, act: int = FLINT_ACT_NONE,
@@ -751,13 +766,13 @@ def flint_linear_bf16(x, w, out, workspace, bias=None, residual=None, act: int =
     of w, residual and out [rows, n_out] of one type, bf16 or fp32 (residual may be out
     itself); workspace: new_prompt_workspace()."""
     f = "flint_linear_bf16"
-    ref, dev, rows, k, r, n, m = _linear(f, x, w, out, 2, act)
+    ref, dev, rows, k, _, n, dtype, m = _linear(f, x, out, act)
     wp, wb = _ws_arg(f, workspace, dev)
     _check((_lib or lib()).flint_linear_bf16(
         ref, rows, _arg(f, "x", x, _BF16, (rows, k), dev), _arg(f, "w", w, _BF16, (m, k), dev),
         None if bias is None else _arg(f, "bias", bias, _F32, (m,), dev),
-        None if residual is None else _arg(f, "residual", residual, out.dtype, (rows, n), dev),
-        _arg(f, "out", out, out.dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+        None if residual is None else _arg(f, "residual", residual, dtype, (rows, n), dev),
+        _arg(f, "out", out, dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
 
 
 def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None, bias=None,
@@ -767,10 +782,10 @@ def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None,
     [groups, 2 n_out, n_in]), group_start int32 [groups + 1], row_index int32 of one
     value per row of out (None: x[r]), bias fp32 [groups, rows of a matrix]."""
     f = "flint_grouped_linear_bf16"
-    ref, dev, n_x, k, rows, n, m = _linear(f, x, w, out, 3, act)
+    ref, dev, n_x, k, rows, n, dtype, m = _linear(f, x, out, act)
+    if not (isinstance(w, _Tensor) and w.dim() == 3 and 1 <= w.shape[0] <= LINEAR_MAX_GROUPS):
+        _bad(f, "w", "[1 to %d groups, rows, n_in]" % LINEAR_MAX_GROUPS, w)
     groups = w.shape[0]
-    if not 1 <= groups <= LINEAR_MAX_GROUPS:
-        _bad(f, "w", "of 1 to %d groups" % LINEAR_MAX_GROUPS, w)
     if row_index is None and n_x != rows:
         _bad(f, "x", "of as many rows as out has (%d) without row_index" % rows, x)
     wp, wb = _ws_arg(f, workspace, dev)
@@ -779,15 +794,31 @@ def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None,
         None if row_index is None else _arg(f, "row_index", row_index, _I32T, (rows,), dev),
         n_x, _arg(f, "x", x, _BF16, (n_x, k), dev), _arg(f, "w", w, _BF16, (groups, m, k), dev),
         None if bias is None else _arg(f, "bias", bias, _F32, (groups, m), dev),
-        _arg(f, "out", out, out.dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+        _arg(f, "out", out, dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
 
 
-def _prompt_tokens(where, name, t, width):
-    """(tokens, device) of a [tokens, width] tensor of a call for prompts."""
-    n, dev = _batch(where, name, t, width)
-    if not 1 <= n <= PAGED_MAX_TOKENS:
+def _prompt_tokens(where, name, t):
+    """(tokens, device) of a [tokens, width] tensor of a call for prompts; the calls check
+    what is left of it."""
+    shape = t.shape if isinstance(t, _Tensor) else ()
+    if not (len(shape) == 2 and 1 <= shape[0] <= PAGED_MAX_TOKENS):
         _bad(where, name, "of 1 to %d tokens" % PAGED_MAX_TOKENS, t)
-    return n, dev
+    dev = t.device
+    if dev.type != "cuda":
+        _bad(where, name, "on a CUDA device", t)
+    if dev.index != torch._C._cuda_getDevice():
+        _on_current_device(where, name, t)
+    return shape[0], dev
+
+
+_FULL_DIMS_REF, _SELECT_DIMS_REF = ctypes.byref(FULL_DIMS), ctypes.byref(SELECT_DIMS)
+
+
+def _moe_dims(dims):
+    """(dims, C struct by reference) of a call for prompts."""
+    if dims is None or dims is FULL_DIMS:
+        return FULL_DIMS, _FULL_DIMS_REF
+    return dims, _SELECT_DIMS_REF if dims is SELECT_DIMS else ctypes.byref(dims)
 
 
 def flint_moe_select(logits, logit_bias, topk_idx, topk_w, group_start, row_token, pair_row,
@@ -795,18 +826,18 @@ def flint_moe_select(logits, logit_bias, topk_idx, topk_w, group_start, row_toke
     """The routing of router scores logits fp32 [T, 256] (topk_idx int32 and topk_w fp32
     [T, 6]) and the order of the T * 6 pairs by expert: group_start int32 [257],
     row_token int32 [T * 6], pair_row int32 [T, 6]."""
-    f, d = "flint_moe_select", _d(dims)
-    T, dev = _prompt_tokens(f, "logits", logits, d.n_experts)
-    K = d.top_k
-    args = (_arg(f, "logits", logits, _F32, (T, d.n_experts), dev),
-            _arg(f, "logit_bias", logit_bias, _F32, (d.n_experts,), dev, optional=True),
+    f, (d, ref) = "flint_moe_select", _moe_dims(dims)
+    T, dev = _prompt_tokens(f, "logits", logits)
+    E, K = d.n_experts, d.top_k
+    args = (_arg(f, "logits", logits, _F32, (T, E), dev),
+            None if logit_bias is None else _arg(f, "logit_bias", logit_bias, _F32, (E,), dev),
             _arg(f, "topk_idx", topk_idx, _I32T, (T, K), dev),
             _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
-            _arg(f, "group_start", group_start, _I32T, (d.n_experts + 1,), dev),
+            _arg(f, "group_start", group_start, _I32T, (E + 1,), dev),
             _arg(f, "row_token", row_token, _I32T, (T * K,), dev),
             _arg(f, "pair_row", pair_row, _I32T, (T, K), dev))
     wp, wb = _ws_arg(f, workspace, dev)
-    _check((_lib or lib()).flint_moe_select(_dims(dims), T, *args, wp, wb, _stream(stream)), f)
+    _check((_lib or lib()).flint_moe_select(ref, T, *args, wp, wb, _stream(stream)), f)
 
 
 def flint_moe_combine_bf16(residual, y, pair_row, topk_w, y_shared, out, stream=None,
@@ -814,16 +845,16 @@ def flint_moe_combine_bf16(residual, y, pair_row, topk_w, y_shared, out, stream=
     """out[t] = residual[t] + y_shared[t] + sum_j topk_w[t, j] y[pair_row[t, j]]: bf16
     residual, out (may be residual itself) and y_shared (or None) [T, 2048], y
     [T * 6, 2048]."""
-    f, d = "flint_moe_combine_bf16", _d(dims)
-    T, dev = _prompt_tokens(f, "residual", residual, d.hidden)
+    f, (d, ref) = "flint_moe_combine_bf16", _moe_dims(dims)
+    T, dev = _prompt_tokens(f, "residual", residual)
     H, K = d.hidden, d.top_k
     args = (_arg(f, "residual", residual, _BF16, (T, H), dev),
             _arg(f, "y", y, _BF16, (T * K, H), dev),
             _arg(f, "pair_row", pair_row, _I32T, (T, K), dev),
             _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
-            _arg(f, "y_shared", y_shared, _BF16, (T, H), dev, optional=True),
+            None if y_shared is None else _arg(f, "y_shared", y_shared, _BF16, (T, H), dev),
             _arg(f, "out", out, _BF16, (T, H), dev))
-    _check((_lib or lib()).flint_moe_combine_bf16(_dims(dims), T, *args, _stream(stream)), f)
+    _check((_lib or lib()).flint_moe_combine_bf16(ref, T, *args, _stream(stream)), f)
 
 
 def flint_moe_prompt_bf16(x, residual, w_router, logit_bias, w13, w2, ws13, ws2, out, workspace,
@@ -831,12 +862,12 @@ def flint_moe_prompt_bf16(x, residual, w_router, logit_bias, w13, w2, ws13, ws2,
                           dims: Dims | None = None):
     """flint_moe_decode_bf16 for prompts, 1 to 8192 tokens; workspace:
     new_prompt_workspace(tokens)."""
-    f, d = "flint_moe_prompt_bf16", _d(dims)
-    T, dev = _prompt_tokens(f, "x", x, d.hidden)
+    f, (d, ref) = "flint_moe_prompt_bf16", _moe_dims(dims)
+    T, dev = _prompt_tokens(f, "x", x)
     args = _layer_args(f, d, T, dev, x, residual, w_router, logit_bias, w13, w2, ws13, ws2, out,
                        topk_idx_out, topk_w_out)
     wp, wb = _ws_arg(f, workspace, dev)
-    _check((_lib or lib()).flint_moe_prompt_bf16(_dims(dims), T, *args, wp, wb, _stream(stream)), f)
+    _check((_lib or lib()).flint_moe_prompt_bf16(ref, T, *args, wp, wb, _stream(stream)), f)
 
 
 # ---------------------------------------------------------------- conveniences

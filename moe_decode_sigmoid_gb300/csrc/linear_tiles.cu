@@ -971,11 +971,38 @@ Choice choose(const LinearArgs& a, int sms) {
   return best;
 }
 
+// The same for groups, as if they had equal numbers of rows (what they have is on the
+// device): smaller tiles where there are too few for all SMs.
+Choice choose_grouped(const LinearArgs& a, int sms) {
+  const int fe = a.act == ACT_SWIGLU ? 64 : 128, each = (a.n_rows + a.n_groups - 1) / a.n_groups;
+  Choice best = {0, 0, 0, 0};
+  for (int n = a.out_f32 ? NT_MAX_F32 : NT_MAX; n >= 32; n /= 2)
+    for (int cg = 2; cg >= 1; --cg) {
+      const long long k = (each + n - 1) / n, units = sms / cg;
+      const long long tiles = k * (a.n_rows < a.n_groups ? a.n_rows : a.n_groups) * ((a.n_out + fe * cg - 1) / (fe * cg));
+      const long long rows = each / k, step = 2 * rows > 350 ? 2 * rows : 350;
+      // (a pair reads x once for 256 weight rows, ~10 % where the weights' bytes bound both)
+      const long long cost = (tiles + units - 1) / units * step * (cg == 1 ? 11 : 10);
+      if (best.cg == 0 || cost < best.cost) best = {cg, n, 1, cost};
+    }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
-  if (a.start != nullptr) return launch_as<2, false>(a, a.out_f32 ? NT_MAX_F32 : NT_MAX, 1, sms, stream);
-  const Choice c = choose(a, sms);
+  // (Weighing the cuts takes a microsecond: a thread remembers its last calls' sizes.)
+  struct Known {
+    int rows, groups, in, out, act, f32, sms;
+    Choice c;
+  };
+  static thread_local Known known[16] = {};
+  const int groups = a.start != nullptr ? a.n_groups : 0;
+  Known& k = known[(a.n_rows + 3 * a.n_in / 8 + 5 * a.n_out / 8 + groups) & 15];
+  if (k.rows != a.n_rows || k.groups != groups || k.in != a.n_in || k.out != a.n_out || k.act != a.act ||
+      k.f32 != a.out_f32 || k.sms != sms)
+    k = {a.n_rows, groups, a.n_in, a.n_out, a.act, a.out_f32, sms, groups > 0 ? choose_grouped(a, sms) : choose(a, sms)};
+  const Choice c = k.c;
   if (c.splits > 1) return launch_as<1, true>(a, c.nt, c.splits, sms, stream);
   return c.cg == 2 ? launch_as<2, false>(a, c.nt, 1, sms, stream) : launch_as<1, false>(a, c.nt, 1, sms, stream);
 }
