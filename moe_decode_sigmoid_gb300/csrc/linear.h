@@ -29,7 +29,7 @@ enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_SWIGLU = 3 };
 struct LinearArgs {
   const uint16_t* x;       // [n_x, n_in] bf16
   const uint16_t* w;       // [n_groups, rows of a matrix, n_in] bf16
-  const uint16_t* w_last;  // the last group's matrix lies here, or null
+  const uint16_t* w_last;  // the last group's matrix lies here (its rows: x's in order), or null
   const float* bias;       // [n_groups, rows of a matrix] or null
   const void* residual;    // [n_rows, n_out] of out's type or null
   void* out;               // [n_rows, n_out]

@@ -11,8 +11,8 @@
 //
 // One CTA per SM, persistent:
 //   warp 0      issues the products (of the pair: the first CTA's)
-//   warps 1-3, 12, 13  copy W and X, 64 k a stage, a stage each in turn (TMA, 128-byte
-//               swizzle); X as boxes of rows, or four rows an instruction where an index
+//   warps 1-3, 12-14  copy W and X, 64 k a stage, a stage each (or two) in turn (TMA,
+//               128-byte swizzle); X as boxes of rows, or four rows an instruction where an index
 //               says which
 //   warps 4-11  epilogue: bias, activation and residual on fragments of 16 outputs x
 //               8 rows, transposed to rows through shared memory 8 x 8 at a time
@@ -30,9 +30,9 @@ namespace {
 
 using namespace lin;
 
-constexpr int THREADS = 448, WARPS = THREADS / 32;
+constexpr int THREADS = 480, WARPS = THREADS / 32;
 constexpr int EPI0 = 4, EPI_WARPS = 8;     // warps of the epilogue, two a quarter of TMEM's lanes
-constexpr int COPY_WARPS = 5;             // warps 1, 2, 3, 12, 13, a stage each in turn
+constexpr int COPY_WARPS = 6;             // warps 1, 2, 3, 12, 13, 14: alone or in twos, a stage each in turn
 constexpr int KS = 64;                    // k of a stage: a 128-byte row
 constexpr int A_BYTES = 128 * KS * 2;
 constexpr int MAX_STAGES = 12;
@@ -44,9 +44,9 @@ static_assert(NT_MAX_F32 == 4 * 32, "two chunks of rows a warp of the epilogue")
 constexpr int SEGMENT = 8;                // fp32 outputs: stages that are summed in TMEM
 constexpr int MAX_SPLITS = 8;             // parts of k: a portable cluster
 constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
-// What a tile costs besides its rows, in rows; and what its weights' bytes from HBM do,
-// which a group's first tile of rows fetches.
-constexpr int COST_TILE = 512, COST_WEIGHTS = 0;
+// What a tile of a group costs besides its rows, in rows: its weights' copies, whether
+// they come from HBM or, as those of a group's further tiles of rows, from L2.
+constexpr int COST_TILE = 512;
 constexpr int STRIP = 8;                  // tiles of weights that share their rows of x in L2
 
 struct Shared {
@@ -58,9 +58,10 @@ struct Shared {
 };
 static_assert(SMEM + sizeof(Shared) <= 227 * 1024, "fits");
 
-// Tensor maps: the weights (all groups but a last one of its own, and that one), x.
+// Tensor maps: the weights (all groups but a last one of its own, and that one), x, and
+// x for that last group, whose rows are x's in order.
 struct Maps {
-  CUtensorMap w, w_last, x;
+  CUtensorMap w, w_last, x, x_last;
 };
 
 struct Plan {
@@ -72,6 +73,7 @@ struct Plan {
   int n_main;      // groups whose weights are in the first map
   int splits;      // CTAs that share a tile's k
   int part_bytes;  // room for their sums, behind the ring
+  int team;        // copying warps a stage: 2 where rows are gathered
   int checked;     // rows whose index is out of range are not stored
 };
 
@@ -249,7 +251,6 @@ struct Walk {
   int t, tiles, tiles_n;
   long long at, end;
   int g, m, n, count, cost, size;  // group, tile in it (weights, rows), tiles of rows, a tile's cost, rows
-  long long block;
   Rows rows;
 
   __device__ __forceinline__ Walk(const LinearArgs& a_, const Plan& p_, const Shared& sh_, int unit_, int units_)
@@ -265,9 +266,9 @@ struct Walk {
       if (at < end) {
         enter();
         // the first tile that begins here
-        const int off = (int)((at - sh.pre[g]) % block);
-        m = (int)((at - sh.pre[g]) / block);
-        n = off == 0 ? 0 : max((off - COST_WEIGHTS + cost - 1) / cost, 1);
+        const int i = (int)((at - sh.pre[g] + cost - 1) / cost);
+        m = i / count;
+        n = i - m * count;
         settle();
       }
     }
@@ -286,7 +287,6 @@ struct Walk {
     count = max((rows.n + p.nt - 1) / p.nt, 1);
     size = tile_rows(rows.n, p.nt);
     cost = size + COST_TILE;
-    block = block_cost(count, size);
   }
   // A group's tiles of rows in turn on the same weights, which L2 then has.
   __device__ __forceinline__ void settle() {
@@ -294,12 +294,8 @@ struct Walk {
       n = 0;
       ++m;
     }
-    at = sh.pre[g] + (long long)m * block + (n > 0 ? COST_WEIGHTS + n * cost : 0);
+    at = sh.pre[g] + (long long)(m * count + n) * cost;
     if (m >= p.n_m && at < end) enter();
-  }
-  // Of all a group's tiles of rows on one tile of weights.
-  static __device__ __forceinline__ long long block_cost(int count, int size) {
-    return (long long)count * (size + COST_TILE) + COST_WEIGHTS;
   }
   // Rows of a group's tiles: of so many as nt asks for, alike but for the last.
   static __device__ __forceinline__ int tile_rows(int n, int nt) {
@@ -509,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), CG);
+      mbar_init(smem_addr(&sh.full[i]), CG * p.team);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -532,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int g = g0; g < g1; ++g) {
       const int n = group_rows(a, g).n;
       sh.pre[g] = sum;
-      if (n > 0) sum += Walk::block_cost((n + p.nt - 1) / p.nt, Walk::tile_rows(n, p.nt)) * p.n_m;
+      if (n > 0) sum += (long long)((n + p.nt - 1) / p.nt) * p.n_m * (Walk::tile_rows(n, p.nt) + COST_TILE);
     }
     long long incl = sum;
 #pragma unroll
@@ -557,13 +553,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
   const int copier = warp >= EPI0 + EPI_WARPS ? warp - EPI0 - EPI_WARPS + 3 : warp - 1;
-  // No more of them than stages: a warp waits for a slot's last use but one to be over,
+  // No more teams than stages: a warp waits for a slot's last use but one to be over,
   // and parities tell it from the one before only if the warp's own last stage is within
   // a round of the ring.
-  const int copiers = min(COPY_WARPS, p.stages);
-  if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS) && copier < copiers) {
-    // ===== copies: every copiers-th stage ==========================================
-    int s = copier, turn = copier, step = 0;   // stage, first and present step of all tiles
+  const int teams = min(COPY_WARPS / p.team, p.stages), team = copier / p.team, mate = copier - team * p.team;
+  if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS) && team < teams) {
+    // ===== copies: a team every teams-th stage =====================================
+    int s = team, turn = team, step = 0;   // stage, step and the tile's first step, of all tiles
     uint32_t phase = 1;
     bool ok = true;
     // x, which every tile of weights reads, stays in L2; weights that no other tile reads
@@ -579,37 +575,44 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int wg = main ? t.g : 0;
       const int f = (t.m * CG + rank) * FE;
       const int rows_b = t.n / CG, row0 = t.r0 + rank * rows_b;
-      const uint32_t bytes = (p.box_rows > 0 ? p.box_rows : 4) * KS * 2;   // of a copy of X
-      const int copies = rows_b * KS * 2 / bytes;
+      // The last group of its own has the rows of x in order: boxes, also where the others
+      // gather (four rows an instruction take ~22 cycles, 704 a stage of 256 rows).
+      const int box_rows = main ? p.box_rows : 32 / CG;
+      const CUtensorMap* xm = main ? &maps.x : &maps.x_last;
+      const uint32_t bytes = (box_rows > 0 ? box_rows : 4) * KS * 2;   // of a copy of X
+      const int all = rows_b * KS * 2 / bytes, copies = (all - mate + p.team - 1) / p.team;
+      const int box = lane * p.team + mate;   // of this lane
       const uint64_t policy = a.start != nullptr && walk.rows.n <= p.nt ? l2_evict_first() : normal;
       int y[4] = {};
-      if (p.box_rows > 0) {
-        y[0] = row0 + lane * p.box_rows;
+      if (box_rows > 0) {
+        y[0] = row0 + box * box_rows - (main || a.index == nullptr ? 0 : walk.rows.r0);
       } else if (lane < copies) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // A row of no index is not stored: any row will do.
-          const int r = row0 + 4 * lane + j;
+          const int r = row0 + 4 * box + j;
           if (r < a.n_rows) y[j] = __ldg(a.index + r);
           if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
         }
       }
-      for (; turn < step + k_steps; turn += copiers) {
+      for (; turn < step + k_steps; turn += teams) {
         if (!(ok = warp_wait(sh, sh.empty[s], phase))) break;
         const uint32_t bar = O::leader(smem_addr(&sh.full[s])), dst = smem + s * p.stage_bytes;
         const int k = (k0 + turn - step) * KS;
         if (tc::one_thread()) {
-          O::expect(bar, A_BYTES + rows_b * KS * 2);
-          if constexpr (SWIGLU) O::copy5(dst, wm, k, f / 16, wg, bar, policy);
-          else O::copy3(dst, wm, k, f, wg, bar, policy);
+          O::expect(bar, (mate == 0 ? A_BYTES : 0) + copies * bytes);
+          if (mate == 0) {
+            if constexpr (SWIGLU) O::copy5(dst, wm, k, f / 16, wg, bar, policy);
+            else O::copy3(dst, wm, k, f, wg, bar, policy);
+          }
         }
         __syncwarp();
         if (lane < copies) {
-          if (p.box_rows > 0) O::copy2(dst + A_BYTES + lane * bytes, &maps.x, k, y[0], bar, keep);
-          else O::gather4(dst + A_BYTES + lane * bytes, &maps.x, k, y, bar, keep);
+          if (box_rows > 0) O::copy2(dst + A_BYTES + box * bytes, xm, k, y[0], bar, keep);
+          else O::gather4(dst + A_BYTES + box * bytes, xm, k, y, bar, keep);
         }
         __syncwarp();
-        if ((s += copiers) >= p.stages) {
+        if ((s += teams) >= p.stages) {
           s -= p.stages;
           phase ^= 1;
         }
@@ -854,6 +857,13 @@ bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int group
   return encode(map, base, 3, dims, strides, box);
 }
 
+bool encode_x(CUtensorMap* map, const LinearArgs& a, int rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_x};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.n_in * 2};
+  const cuuint32_t box[2] = {KS, (cuuint32_t)rows};
+  return encode(map, a.x, 2, dims, strides, box);
+}
+
 template <int CG, bool SWIGLU, bool F32, bool SPLIT>
 cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done;
@@ -870,6 +880,7 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
   p.k_steps = (a.n_in + KS - 1) / KS;
   p.splits = splits;
   p.box_rows = a.start == nullptr ? nt / CG : a.index == nullptr ? 32 / CG : 0;
+  p.team = p.box_rows > 0 ? 1 : 2;
   p.n_main = a.w_last != nullptr ? a.n_groups - 1 : a.n_groups;
   // (the layer's own indices are in range)
   p.checked = a.index != nullptr && a.w_last == nullptr;
@@ -877,10 +888,9 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
   if (!encode_w(&maps.w, a, a.w, p.n_main)) return cudaErrorInvalidValue;
   maps.w_last = maps.w;
   if (a.w_last != nullptr && !encode_w(&maps.w_last, a, a.w_last, 1)) return cudaErrorInvalidValue;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_x};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.n_in * 2};
-  const cuuint32_t box[2] = {KS, (cuuint32_t)(p.box_rows > 0 ? p.box_rows : 1)};
-  if (!encode(&maps.x, a.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  if (!encode_x(&maps.x, a, p.box_rows > 0 ? p.box_rows : 1)) return cudaErrorInvalidValue;
+  maps.x_last = maps.x;
+  if (a.w_last != nullptr && a.index != nullptr && !encode_x(&maps.x_last, a, 32 / CG)) return cudaErrorInvalidValue;
 
   int units = sms / (CG * splits);
   if (a.start == nullptr) {
