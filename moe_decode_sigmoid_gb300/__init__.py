@@ -715,6 +715,8 @@ def flint_prompt_debug_arm_stall(workspace: torch.Tensor, stream=None):
            "flint_prompt_debug_arm_stall")
 
 
+_current_gpu, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 # (C struct by reference, rows of a weight matrix) of a linear call, by its n_in, n_out, act and
 # whether out is fp32.
 _LINEAR_DIMS = {}
@@ -766,13 +768,33 @@ def flint_linear_bf16(x, w, out, workspace, bias=None, residual=None, act: int =
     of w, residual and out [rows, n_out] of one type, bf16 or fp32 (residual may be out
     itself); workspace: new_prompt_workspace()."""
     f = "flint_linear_bf16"
-    ref, dev, rows, k, _, n, dtype, m = _linear(f, x, out, act)
-    wp, wb = _ws_arg(f, workspace, dev)
+    try:  # everything in order, in one look: half the look-ups of the checks that can say what is not
+        rows, k = x.shape
+        r, n = out.shape
+        f32 = out.dtype is _F32
+        ref, m = _LINEAR_DIMS[k, n, act, f32]
+        gpu = _current_gpu()
+        good = (r == rows <= LINEAR_MAX_ROWS and x.dtype is _BF16 and w.dtype is _BF16 and
+                (f32 or out.dtype is _BF16) and w.shape == (m, k) and x.is_contiguous() and
+                w.is_contiguous() and out.is_contiguous() and
+                x.get_device() == w.get_device() == out.get_device() == workspace.get_device() == gpu and
+                workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous())
+    except (AttributeError, ValueError, TypeError, LookupError, RuntimeError):
+        good = False
+    if good and rows > 0:
+        dtype, dev = out.dtype, None if bias is None and residual is None else x.device
+        args = (x.data_ptr(), w.data_ptr())
+        last = (out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    else:
+        ref, dev, rows, k, _, n, dtype, m = _linear(f, x, out, act)
+        args = (_arg(f, "x", x, _BF16, (rows, k), dev), _arg(f, "w", w, _BF16, (m, k), dev))
+        last = (_arg(f, "out", out, dtype, (rows, n), dev), *_ws_arg(f, workspace, dev))
+        gpu = dev.index
     _check((_lib or lib()).flint_linear_bf16(
-        ref, rows, _arg(f, "x", x, _BF16, (rows, k), dev), _arg(f, "w", w, _BF16, (m, k), dev),
+        ref, rows, *args,
         None if bias is None else _arg(f, "bias", bias, _F32, (m,), dev),
         None if residual is None else _arg(f, "residual", residual, dtype, (rows, n), dev),
-        _arg(f, "out", out, dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+        *last, _raw_stream(gpu) if stream is None else _stream(stream)), f)
 
 
 def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None, bias=None,
@@ -782,19 +804,44 @@ def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None,
     [groups, 2 n_out, n_in]), group_start int32 [groups + 1], row_index int32 of one
     value per row of out (None: x[r]), bias fp32 [groups, rows of a matrix]."""
     f = "flint_grouped_linear_bf16"
-    ref, dev, n_x, k, rows, n, dtype, m = _linear(f, x, out, act)
-    if not (isinstance(w, _Tensor) and w.dim() == 3 and 1 <= w.shape[0] <= LINEAR_MAX_GROUPS):
-        _bad(f, "w", "[1 to %d groups, rows, n_in]" % LINEAR_MAX_GROUPS, w)
-    groups = w.shape[0]
+    try:  # as flint_linear_bf16
+        n_x, k = x.shape
+        rows, n = out.shape
+        f32 = out.dtype is _F32
+        ref, m = _LINEAR_DIMS[k, n, act, f32]
+        groups = w.shape[0]
+        gpu = _current_gpu()
+        good = (0 < n_x <= LINEAR_MAX_ROWS and 0 < rows <= LINEAR_MAX_ROWS and
+                0 < groups <= LINEAR_MAX_GROUPS and x.dtype is _BF16 and w.dtype is _BF16 and
+                (f32 or out.dtype is _BF16) and group_start.dtype is _I32T and
+                w.shape == (groups, m, k) and group_start.shape == (groups + 1,) and
+                x.is_contiguous() and w.is_contiguous() and out.is_contiguous() and
+                group_start.is_contiguous() and
+                x.get_device() == w.get_device() == out.get_device() == group_start.get_device() ==
+                workspace.get_device() == gpu and
+                workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous())
+    except (AttributeError, ValueError, TypeError, LookupError, RuntimeError):
+        good = False
+    if good:
+        dev = None if bias is None and row_index is None else x.device
+        start, xw = group_start.data_ptr(), (x.data_ptr(), w.data_ptr())
+        last = (out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    else:
+        ref, dev, n_x, k, rows, n, dtype, m = _linear(f, x, out, act)
+        if not (isinstance(w, _Tensor) and w.dim() == 3 and 1 <= w.shape[0] <= LINEAR_MAX_GROUPS):
+            _bad(f, "w", "[1 to %d groups, rows, n_in]" % LINEAR_MAX_GROUPS, w)
+        groups = w.shape[0]
+        start = _arg(f, "group_start", group_start, _I32T, (groups + 1,), dev)
+        xw = (_arg(f, "x", x, _BF16, (n_x, k), dev), _arg(f, "w", w, _BF16, (groups, m, k), dev))
+        last = (_arg(f, "out", out, dtype, (rows, n), dev), *_ws_arg(f, workspace, dev))
+        gpu = dev.index
     if row_index is None and n_x != rows:
         _bad(f, "x", "of as many rows as out has (%d) without row_index" % rows, x)
-    wp, wb = _ws_arg(f, workspace, dev)
     _check((_lib or lib()).flint_grouped_linear_bf16(
-        ref, groups, rows, _arg(f, "group_start", group_start, _I32T, (groups + 1,), dev),
-        None if row_index is None else _arg(f, "row_index", row_index, _I32T, (rows,), dev),
-        n_x, _arg(f, "x", x, _BF16, (n_x, k), dev), _arg(f, "w", w, _BF16, (groups, m, k), dev),
+        ref, groups, rows, start,
+        None if row_index is None else _arg(f, "row_index", row_index, _I32T, (rows,), dev), n_x, *xw,
         None if bias is None else _arg(f, "bias", bias, _F32, (groups, m), dev),
-        _arg(f, "out", out, dtype, (rows, n), dev), wp, wb, _stream(stream)), f)
+        *last, _raw_stream(gpu) if stream is None else _stream(stream)), f)
 
 
 def _prompt_tokens(where, name, t):
@@ -827,17 +874,41 @@ def flint_moe_select(logits, logit_bias, topk_idx, topk_w, group_start, row_toke
     [T, 6]) and the order of the T * 6 pairs by expert: group_start int32 [257],
     row_token int32 [T * 6], pair_row int32 [T, 6]."""
     f, (d, ref) = "flint_moe_select", _moe_dims(dims)
-    T, dev = _prompt_tokens(f, "logits", logits)
     E, K = d.n_experts, d.top_k
-    args = (_arg(f, "logits", logits, _F32, (T, E), dev),
-            None if logit_bias is None else _arg(f, "logit_bias", logit_bias, _F32, (E,), dev),
-            _arg(f, "topk_idx", topk_idx, _I32T, (T, K), dev),
-            _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
-            _arg(f, "group_start", group_start, _I32T, (E + 1,), dev),
-            _arg(f, "row_token", row_token, _I32T, (T * K,), dev),
-            _arg(f, "pair_row", pair_row, _I32T, (T, K), dev))
-    wp, wb = _ws_arg(f, workspace, dev)
-    _check((_lib or lib()).flint_moe_select(ref, T, *args, wp, wb, _stream(stream)), f)
+    try:  # as flint_linear_bf16
+        T, e = logits.shape
+        gpu, pairs = _current_gpu(), (T, K)
+        good = (0 < T <= PAGED_MAX_TOKENS and e == E and logits.dtype is _F32 and
+                topk_w.dtype is _F32 and topk_idx.dtype is _I32T and group_start.dtype is _I32T and
+                row_token.dtype is _I32T and pair_row.dtype is _I32T and topk_idx.shape == pairs and
+                topk_w.shape == pairs and pair_row.shape == pairs and row_token.shape == (T * K,) and
+                group_start.shape == (E + 1,) and logits.is_contiguous() and
+                topk_idx.is_contiguous() and topk_w.is_contiguous() and pair_row.is_contiguous() and
+                row_token.is_contiguous() and group_start.is_contiguous() and
+                logits.get_device() == topk_idx.get_device() == topk_w.get_device() ==
+                group_start.get_device() == row_token.get_device() == pair_row.get_device() ==
+                workspace.get_device() == gpu and
+                workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous())
+    except (AttributeError, ValueError, TypeError, RuntimeError):
+        good = False
+    if good:
+        bias = logit_bias
+        args = (logits.data_ptr(),
+                None if bias is None else _arg(f, "logit_bias", bias, _F32, (E,), logits.device),
+                topk_idx.data_ptr(), topk_w.data_ptr(), group_start.data_ptr(),
+                row_token.data_ptr(), pair_row.data_ptr(), workspace.data_ptr(), workspace.numel())
+    else:
+        T, dev = _prompt_tokens(f, "logits", logits)
+        args = (_arg(f, "logits", logits, _F32, (T, E), dev),
+                _arg(f, "logit_bias", logit_bias, _F32, (E,), dev, optional=True),
+                _arg(f, "topk_idx", topk_idx, _I32T, (T, K), dev),
+                _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
+                _arg(f, "group_start", group_start, _I32T, (E + 1,), dev),
+                _arg(f, "row_token", row_token, _I32T, (T * K,), dev),
+                _arg(f, "pair_row", pair_row, _I32T, (T, K), dev), *_ws_arg(f, workspace, dev))
+        gpu = dev.index
+    _check((_lib or lib()).flint_moe_select(
+        ref, T, *args, _raw_stream(gpu) if stream is None else _stream(stream)), f)
 
 
 def flint_moe_combine_bf16(residual, y, pair_row, topk_w, y_shared, out, stream=None,
@@ -846,15 +917,35 @@ def flint_moe_combine_bf16(residual, y, pair_row, topk_w, y_shared, out, stream=
     residual, out (may be residual itself) and y_shared (or None) [T, 2048], y
     [T * 6, 2048]."""
     f, (d, ref) = "flint_moe_combine_bf16", _moe_dims(dims)
-    T, dev = _prompt_tokens(f, "residual", residual)
     H, K = d.hidden, d.top_k
-    args = (_arg(f, "residual", residual, _BF16, (T, H), dev),
-            _arg(f, "y", y, _BF16, (T * K, H), dev),
-            _arg(f, "pair_row", pair_row, _I32T, (T, K), dev),
-            _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
-            None if y_shared is None else _arg(f, "y_shared", y_shared, _BF16, (T, H), dev),
-            _arg(f, "out", out, _BF16, (T, H), dev))
-    _check((_lib or lib()).flint_moe_combine_bf16(ref, T, *args, _stream(stream)), f)
+    try:  # as flint_linear_bf16
+        T, h = residual.shape
+        gpu, pairs, rows = _current_gpu(), (T, K), (T, H)
+        good = (0 < T <= PAGED_MAX_TOKENS and h == H and residual.dtype is _BF16 and
+                y.dtype is _BF16 and out.dtype is _BF16 and pair_row.dtype is _I32T and
+                topk_w.dtype is _F32 and y.shape == (T * K, H) and out.shape == rows and
+                pair_row.shape == pairs and topk_w.shape == pairs and residual.is_contiguous() and
+                y.is_contiguous() and out.is_contiguous() and pair_row.is_contiguous() and
+                topk_w.is_contiguous() and
+                residual.get_device() == y.get_device() == out.get_device() ==
+                pair_row.get_device() == topk_w.get_device() == gpu)
+    except (AttributeError, ValueError, TypeError, RuntimeError):
+        good = False
+    if good:
+        args = (residual.data_ptr(), y.data_ptr(), pair_row.data_ptr(), topk_w.data_ptr(),
+                None if y_shared is None else
+                _arg(f, "y_shared", y_shared, _BF16, rows, residual.device), out.data_ptr())
+    else:
+        T, dev = _prompt_tokens(f, "residual", residual)
+        args = (_arg(f, "residual", residual, _BF16, (T, H), dev),
+                _arg(f, "y", y, _BF16, (T * K, H), dev),
+                _arg(f, "pair_row", pair_row, _I32T, (T, K), dev),
+                _arg(f, "topk_w", topk_w, _F32, (T, K), dev),
+                _arg(f, "y_shared", y_shared, _BF16, (T, H), dev, optional=True),
+                _arg(f, "out", out, _BF16, (T, H), dev))
+        gpu = dev.index
+    _check((_lib or lib()).flint_moe_combine_bf16(
+        ref, T, *args, _raw_stream(gpu) if stream is None else _stream(stream)), f)
 
 
 def flint_moe_prompt_bf16(x, residual, w_router, logit_bias, w13, w2, ws13, ws2, out, workspace,
