@@ -515,12 +515,14 @@ typedef struct {
 /* Bytes of workspace: max_tokens = 0 serves flint_linear_bf16,
  * flint_grouped_linear_bf16 and flint_moe_select (every size), max_tokens in
  * [1, FLINT_PAGED_MAX_TOKENS] also flint_moe_prompt_bf16 of up to so many tokens
- * (about 36 KB a token).  0 for any other max_tokens. */
+ * (1.6 to 10.7 MB up to 128, then about 38 KB a token).  0 for any other
+ * max_tokens. */
 size_t flint_prompt_workspace_bytes(int32_t max_tokens);
 
-/* Clears a workspace's error word (cudaMemsetAsync on `stream`).  Once before the
- * first call that uses it, and again after a call whose device status was not
- * FLINT_OK.  One workspace serves any number of calls, one at a time. */
+/* Prepares a workspace (cudaMemsetAsync on `stream`; ws_bytes says whether it serves the
+ * layer, and for how many tokens).  Once before the first call that uses it, and again
+ * after a call whose device status was not FLINT_OK.  One workspace serves any number
+ * of calls, one at a time. */
 flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Synchronises `stream`, then reads and returns the workspace's error word:
@@ -529,8 +531,8 @@ flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaS
 flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t stream);
 
 /* Fault-injection hook for tests, as flint_moe_debug_arm_stall: a one-shot wait in
- * the next call on this workspace that runs the tiled kernel (any grouped product;
- * a plain one of more than 16 rows), on a barrier that nothing completes.  It runs
+ * the next call on this workspace that runs the tiled kernel (any grouped product, a
+ * plain one of more than 16 rows, the layer above 128 tokens), on a barrier that nothing completes.  It runs
  * out after a second, the call ends with FLINT_ERR_DEVICE_TIMEOUT as its device
  * status, and the workspace has to be initialised again. */
 flint_status flint_prompt_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream);
@@ -608,13 +610,14 @@ flint_status flint_moe_combine_bf16(const flint_moe_dims* dims, int32_t n_tokens
                                     cudaStream_t stream);
 
 /* flint_moe_decode_bf16 for prompts: n_tokens in [1, FLINT_PAGED_MAX_TOKENS], the
- * arguments and the layer as there.  Router scores, selection, gate/up products
+ * arguments and the layer as there.  Up to 128 tokens it is that call, bit for bit.
+ * Above, where it was measured faster: router scores, selection, gate/up products
  * grouped by expert (the shared expert the last group), down products and the
- * combine, chained on the stream.  h and the experts' outputs are rounded to bf16
- * on the way (each half a step of 2^-8 of values that are summed), so results differ
- * from flint_moe_decode_bf16's in their last bits; a token whose sixth and seventh
- * score are within the scores' fp32 rounding may choose either.  workspace:
- * flint_prompt_workspace_bytes(n_tokens). */
+ * combine, chained on the stream.  h and the experts' outputs are then rounded to
+ * bf16 on the way (each at most half a step, 2^-8, of values that are summed), so
+ * results differ from flint_moe_decode_bf16's in their last bits, and a token whose
+ * sixth and seventh score are within the scores' fp32 rounding may choose either.
+ * workspace: flint_prompt_workspace_bytes(n_tokens). */
 flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
                                    const void* x_bf16, const void* residual_bf16,
                                    const void* w_router_bf16, const float* logit_bias,

@@ -3,6 +3,8 @@
 // the experts' products, and the layer made of them.  Host-side argument checks,
 // argument blocks and launches; nothing here allocates, and only
 // flint_prompt_get_device_status synchronises.
+#include <cstring>
+
 #include "common.cuh"
 #include "flint_moe.h"
 #include "host_checks.h"
@@ -20,11 +22,24 @@ static_assert(FLINT_ACT_NONE == ACT_NONE && FLINT_ACT_SILU == ACT_SILU && FLINT_
                   FLINT_ACT_SWIGLU == ACT_SWIGLU,
               "the public activations are the kernels'");
 
-// The layer's arrays behind the workspace's head, for n tokens.
+// Up to so many tokens the layer is flint_moe_decode_bf16, in a workspace of its own behind
+// the head.  Measured with the weights in HBM, decode against products by expert, us: 1
+// token 17 / 32, 16 90 / 104, 64 198 / 214, 96 224 / 236, 128 250 / 257, 192 279 / 262; with
+// skewed routing 64 152 / 162, 96 185 / 189, 128 202 / 198, 192 248 / 212.
+constexpr int DECODE_TOKENS = 128;
+static_assert(DECODE_TOKENS <= MAX_B, "a batch of the decode call");
+constexpr size_t DECODE_WS = align256(lin::WS_HEAD);
+size_t decode_ws_bytes(size_t n) { return WsLayout::total((int)(n < DECODE_TOKENS ? n : DECODE_TOKENS)); }
+
+// The layer's arrays behind that, for n tokens.
 struct Layer {
   size_t logits, idx, w, start, row_token, pair_row, h, y, end;
   explicit Layer(size_t n) {
-    logits = align256(lin::WS_HEAD);
+    logits = align256(DECODE_WS + decode_ws_bytes(n));
+    if (n <= DECODE_TOKENS) {
+      end = logits;
+      return;
+    }
     idx = align256(logits + n * E * 4);
     w = align256(idx + n * TOPK * 4);
     start = align256(w + n * TOPK * 4);
@@ -92,18 +107,27 @@ size_t flint_prompt_workspace_bytes(int32_t max_tokens) {
 
 flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!ws_ok(workspace, ws_bytes, 0)) return FLINT_ERR_WORKSPACE;
-  return cuda_status(cudaMemsetAsync(workspace, 0, lin::WS_COUNTS, stream));
+  char* ws = static_cast<char*>(workspace);
+  const flint_status st = cuda_status(cudaMemsetAsync(ws, 0, lin::WS_COUNTS, stream));
+  if (st != FLINT_OK || ws_bytes < workspace_bytes(1)) return st;
+  // Of a layer: the decode call's workspace too, and a mark that it is there.
+  const size_t rest = ws_bytes - DECODE_WS, most = WsLayout::total(DECODE_TOKENS);
+  const flint_status ds = flint_moe_workspace_init(ws + DECODE_WS, rest < most ? rest : most, 0, stream);
+  return ds != FLINT_OK ? ds : cuda_status(cudaMemsetAsync(ws + lin::WS_LAYER, 1, 1, stream));
 }
 
 flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t stream) {
   if (!req(workspace)) return FLINT_ERR_WORKSPACE;
-  uint32_t code = 0;
-  if (cudaMemcpyAsync(&code, static_cast<const char*>(workspace) + lin::WS_ERROR, sizeof(code),
-                      cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+  char head[lin::WS_COUNTS] = {};
+  if (cudaMemcpyAsync(head, workspace, sizeof(head), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess) {
     (void)cudaGetLastError();
     return FLINT_ERR_CUDA;
   }
+  uint32_t code;
+  std::memcpy(&code, head + lin::WS_ERROR, sizeof(code));
+  if (code == FLINT_OK && head[lin::WS_LAYER] != 0)
+    return flint_moe_get_device_status(static_cast<const char*>(workspace) + DECODE_WS, stream);
   return static_cast<flint_status>(code);
 }
 
@@ -280,6 +304,10 @@ flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
   if (any_overlap(spans, 4)) return FLINT_ERR_INVALID_ARG;
 
   char* ws = static_cast<char*>(workspace);
+  if (n_tokens <= DECODE_TOKENS)
+    return flint_moe_decode_bf16(dims, n_tokens, x_bf16, residual_bf16, w_router_bf16, logit_bias, w13_bf16, w2_bf16,
+                                 ws13_bf16, ws2_bf16, out_bf16, topk_idx_out, topk_w_out, ws + DECODE_WS,
+                                 decode_ws_bytes(n_tokens), stream);
   const Layer at(n_tokens);
   LinearArgs r = {};
   r.x = static_cast<const uint16_t*>(x_bf16);

@@ -18,8 +18,9 @@ constexpr int MAX_TOKENS = 8192;   // of a selection and of the layer
 constexpr int CHUNK = 64;          // tokens a CTA of the selection takes
 constexpr int MAX_CHUNKS = MAX_TOKENS / CHUNK;
 
-// Workspace: error and stall word, the selection's counts, then the layer's arrays.
-constexpr size_t WS_ERROR = 0, WS_STALL = 8, WS_COUNTS = 256;
+// Workspace: error and stall word, a mark that it serves the layer, the selection's counts,
+// then the layer's arrays.
+constexpr size_t WS_ERROR = 0, WS_STALL = 8, WS_LAYER = 16, WS_COUNTS = 256;
 constexpr size_t WS_HEAD = WS_COUNTS + 256 * (size_t)MAX_CHUNKS;
 }  // namespace lin
 

@@ -197,7 +197,7 @@ def _check_layer(out, ref):
     return sure
 
 
-@pytest.mark.parametrize("n", [1, 2, 9, 40, 257, 700, 1500])
+@pytest.mark.parametrize("n", [1, 2, 9, 40, 128, 129, 150, 257, 700, 1500])
 @pytest.mark.parametrize("mode", ["none", "logit", "select"])
 def test_layer(layer, n, mode):
     x, res = fs.tokens(2000 + n, n, device="cuda")
@@ -251,9 +251,28 @@ def test_layer_is_its_parts(layer):
     _check_layer(outs[0], ref)
 
 
+@pytest.mark.parametrize("n", [3, 64, 128])
+def test_layer_is_the_decode_call_for_few_tokens(layer, n):
+    """Bit for bit, in a workspace of its own and in one that larger calls use in between."""
+    x, res = fs.tokens(6, n, device="cuda")
+    args = (layer["wr"], None, layer["w13"], layer["w2"], layer["ws13"], layer["ws2"])
+    want = torch.empty_like(res)
+    m.flint_moe_decode_bf16(x, res, *args, want, m.new_workspace(n))
+    more, more_res = fs.tokens(7, 300, device="cuda")
+    big = m.new_prompt_workspace(300)
+    for ws in (m.new_prompt_workspace(n), big, big):
+        out = torch.empty_like(res)
+        m.flint_moe_prompt_bf16(x, res, *args, out, ws)
+        assert m.flint_prompt_get_device_status(ws) == m.FLINT_OK
+        assert torch.equal(out, want)
+        if ws is big:
+            m.flint_moe_prompt_bf16(more, more_res, *args, torch.empty_like(more), big)
+            assert m.flint_prompt_get_device_status(big) == m.FLINT_OK
+
+
 def test_layer_against_the_decode_call(layer):
     """The decode call, whose intermediates are exact to 2^-16, is within the same bounds."""
-    n = 64
+    n = 200
     x, res = fs.tokens(6, n, device="cuda")
     out, dec = torch.empty_like(res), torch.empty_like(res)
     m.flint_moe_decode_bf16(x, res, layer["wr"], None, layer["w13"], layer["w2"], layer["ws13"],
@@ -265,8 +284,8 @@ def test_layer_against_the_decode_call(layer):
     _check_layer(dec, ref)
 
 
-def test_layer_in_a_graph(layer):
-    n = 300
+@pytest.mark.parametrize("n", [5, 40, 300])
+def test_layer_in_a_graph(layer, n):
     x, res = fs.tokens(7, n, device="cuda")
     ws, out = m.new_prompt_workspace(n), torch.empty_like(res)
     args = (layer["wr"], None, layer["w13"], layer["w2"], layer["ws13"], layer["ws2"])
@@ -285,17 +304,17 @@ def test_layer_in_a_graph(layer):
 def test_a_decoder_layer(layer):
     """Projection, append, attention, output projection into the residual stream, and the
     experts: two prompts through one layer, against 64 bits step by step."""
-    lens, page = [37, 75], 16
+    lens, page = [137, 75], 16
     n = sum(lens)
     g = p.gen(11)
     x, res = fs.tokens(10, n, device="cuda")
     w_qkv, w_o = p.bf(g, 40 * 128, H, scale=H ** -0.5), p.bf(g, H, 32 * 128, scale=4096 ** -0.5)
     gain = torch.ones(128, dtype=torch.bfloat16, device="cuda")
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
-    table = i32(*([0, 1, 2, -1, -1] + [3, 4, 5, 6, 7])).view(2, 5)
+    table = i32(*(list(range(9)) + [9, 10, 11, 12, 13, -1, -1, -1, -1])).view(2, 9)
     batch = m.PagedBatch(i32(0, lens[0], n), i32(*lens), table, page, max(lens))
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
-    qkv, q, o, k, v = bf(n, 5120), bf(n, 32, 128), bf(n, 32, 128), bf(8, page, 4, 128), bf(8, page, 4, 128)
+    qkv, q, o, k, v = bf(n, 5120), bf(n, 32, 128), bf(n, 32, 128), bf(14, page, 4, 128), bf(14, page, 4, 128)
     stream, normed, out = res.clone(), bf(n, H), bf(n, H)
     ws, aws = m.new_prompt_workspace(n), m.new_attn_workspace()
     m.flint_linear_bf16(x, w_qkv, qkv, ws)
@@ -311,7 +330,7 @@ def test_a_decoder_layer(layer):
     keys, vals = k.view(-1, 4, 128).double(), v.view(-1, 4, 128).double()
     at = 0
     for s, ln in enumerate(lens):
-        first = [0, 3][s] * page
+        first = [0, 9][s] * page
         kk, vv = (t[first:first + ln].repeat_interleave(8, 1) for t in (keys, vals))
         score = torch.einsum("thd,jhd->htj", q[at:at + ln].double(), kk) * 128 ** -0.5
         mask = torch.ones(ln, ln, device="cuda").triu(1).bool()

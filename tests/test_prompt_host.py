@@ -64,7 +64,7 @@ def test_workspace_bytes(L):
     last = head
     for n in (1, 2, 77, 8191, 8192):
         b = m.flint_prompt_workspace_bytes(n)
-        assert b > last and b <= 40000 * n + (1 << 20)
+        assert b > last and b <= 37500 * n + (8 << 20)
         last = b
     for n in (-1, 8193, 1 << 31, 1 << 40):
         assert m.flint_prompt_workspace_bytes(n) == 0
