@@ -18,9 +18,19 @@
 //               8 rows, transposed to rows through shared memory 8 x 8 at a time
 // TMEM holds two accumulators: a tile's epilogue runs beside the next one's products.
 //
-// Groups: the tiles' costs (their rows, and COST0 for what a tile costs besides) are
+// Groups: the tiles' costs (their rows, and COST_TILE for what a tile costs besides) are
 // laid end to end and cut into equal shares, a tile belonging to the share where it
-// begins.  Plain products, tiles of one cost, are dealt out in turn.
+// begins.  Plain products, tiles of one cost, are dealt out in turn; few tiles have k cut
+// over a cluster of CTAs (SPLIT), whose sums are joined in their order.
+//
+// Bound: the tensor pipe for many rows of few matrices (8192 x 2048 -> SwiGLU 4096: 142 us,
+// 1.94 PFLOP/s, in short runs; 162 at the power limit), HBM for groups (4200 rows, 512 ->
+// 2048, 256 groups 90 us, 6.2 TB/s; 49152 rows, 2048 -> SwiGLU 512 217 us, 5.3 TB/s: a tile
+// of 256 weight rows takes ~13 us whatever its rows, 15.2 tiles a pair), latencies for few
+// tiles (33 x 4096 -> 2048 9.9 us).
+// Tried, and not faster: L2 prefetches of the next tile's weights (285 -> 436 us for the
+// gathered gate/up: 78 MB ahead of use, L2 lost its x), the next rows' accumulators loaded
+// ahead in the epilogue, a last share weighed by where its weights come from.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
@@ -81,9 +91,11 @@ struct Tile {
   int g, m, r0, n, rows;  // group, tile of weight rows, first row, rows rounded up, rows
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 template <int CG>
@@ -335,7 +347,8 @@ struct Walk {
 };
 
 // silu of an output that is rounded to bf16: exponential and quotient of the fast
-// kind, within 2^-18 of the value (|v| < 32; below, both are zero to 2^-40).
+// kind, off by ~|v| + 4 units of fp32's last place (2^-17 of the value at v = -87; below
+// that the value, under 1e-36, becomes zero), against a rounding of 2^-8.
 __device__ __forceinline__ float silu_bf16(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
 // Where a lane's row of the epilogue's four 8 x 8 blocks lies.
@@ -549,6 +562,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::fence_before();
   __syncthreads();
   O::sync_all();
+  // (Nobody writes to a CTA of the cluster that has not begun.)
+  if constexpr (SPLIT) cluster_arrive();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
@@ -692,6 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t stage = smem + STAGE_AREA + (warp - EPI0) * EPI_BYTES;
     const uint32_t t0 = tmem + ((uint32_t)(32 * w) << 16);
     const uint32_t block = block_row<SWIGLU>(stage, lane);
+    if constexpr (SPLIT) cluster_wait();
     bool ok = true;
     int it = 0;
     for (Walk walk(a, p, sh, unit, units); ok && walk.more(); walk.next()) {
@@ -785,9 +801,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ===== the parts of all CTAs of the cluster, joined in their order: 32 rows x 32
     // weight rows a warp, dealt out over the CTAs.  (Each wrote them to where they are
     // read, which took 3 us less at 8 parts than to read them from one another.) ======
-    __syncwarp();
-    cluster_sync();
     const int e = warp - EPI0;
+    __syncwarp();
+    if (e < 0 || e >= EPI_WARPS) cluster_wait();
+    cluster_sync();
     Walk walk(a, p, sh, unit, units);
     if (e >= 0 && e < EPI_WARPS && walk.more() && *reinterpret_cast<volatile int*>(&sh.fail) == 0) {
       const Tile t = walk.get();
