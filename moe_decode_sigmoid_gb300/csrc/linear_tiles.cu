@@ -74,17 +74,30 @@ struct Maps {
   CUtensorMap w, w_last, x, x_last;
 };
 
+// Divisions by a number the host knows, of values below 2^24 by divisors below 2^16: a
+// kernel's start is a chain of them, ~200 cycles each (33 x 4096 -> 2048 10.0 -> 9.5 us).
+struct Divisor {
+  uint64_t magic;  // 2^40 / d, rounded up
+  int d;
+  explicit Divisor(int d_ = 1) : magic(((1ull << 40) + d_ - 1) / d_), d(d_) {}
+  __device__ __forceinline__ int div(int x) const { return (int)(((uint64_t)(uint32_t)x * magic) >> 40); }
+};
+
 struct Plan {
-  int nt;          // most rows of a tile, a multiple of 32
+  int nt;          // most rows of a tile, a multiple of 32 (groups: a power of two)
+  int nt_shift;    // its logarithm, for groups
   int stages, stage_bytes;
   int n_m;         // tiles of weight rows of a group
   int k_steps;
   int box_rows;    // rows of a box of x; 0: four rows an instruction by index
+  int box_shift;   // logarithm of a copy's rows, for groups
   int n_main;      // groups whose weights are in the first map
   int splits;      // CTAs that share a tile's k
   int part_bytes;  // room for their sums, behind the ring
-  int team;        // copying warps a stage: 2 where rows are gathered
+  int team_shift;  // copying warps a stage: 2^1 where rows are gathered, 2^0
   int checked;     // rows whose index is out of range are not stored
+  int tiles;       // plain: tiles; rows' tiles of a strip of STRIP of weights, a last strip's
+  Divisor strip, last;
 };
 
 struct Tile {
@@ -260,7 +273,7 @@ struct Walk {
   const Shared& sh;
   int unit, units;              // this pair, pairs
   // plain: the tile's number; groups: where the share goes on and ends
-  int t, tiles, tiles_n;
+  int t;
   long long at, end;
   int g, m, n, count, cost, size;  // group, tile in it (weights, rows), tiles of rows, a tile's cost, rows
   Rows rows;
@@ -268,8 +281,6 @@ struct Walk {
   __device__ __forceinline__ Walk(const LinearArgs& a_, const Plan& p_, const Shared& sh_, int unit_, int units_)
       : a(a_), p(p_), sh(sh_), unit(unit_), units(units_) {
     if (a.start == nullptr) {
-      tiles_n = (a.n_rows + p.nt - 1) / p.nt;
-      tiles = tiles_n * p.n_m;
       t = unit;
     } else {
       const long long total = sh.pre[a.n_groups];
@@ -296,8 +307,8 @@ struct Walk {
     g = lo;
     m = n = 0;
     rows = group_rows(a, g);
-    count = max((rows.n + p.nt - 1) / p.nt, 1);
-    size = tile_rows(rows.n, p.nt);
+    count = max((rows.n + p.nt - 1) >> p.nt_shift, 1);
+    size = tile_rows(rows.n, count);
     cost = size + COST_TILE;
   }
   // A group's tiles of rows in turn on the same weights, which L2 then has.
@@ -309,20 +320,19 @@ struct Walk {
     at = sh.pre[g] + (long long)(m * count + n) * cost;
     if (m >= p.n_m && at < end) enter();
   }
-  // Rows of a group's tiles: of so many as nt asks for, alike but for the last.
-  static __device__ __forceinline__ int tile_rows(int n, int nt) {
-    const int k = max((n + nt - 1) / nt, 1);
-    return ((n + k - 1) / k + 31) & ~31;
+  // Rows of a group's tiles: of `count` tiles, alike but for the last.
+  static __device__ __forceinline__ int tile_rows(int n, int count) {
+    return ((count == 1 ? n : (n + count - 1) / count) + 31) & ~31;
   }
-  __device__ __forceinline__ bool more() const { return a.start == nullptr ? t < tiles : at < end; }
+  __device__ __forceinline__ bool more() const { return a.start == nullptr ? t < p.tiles : at < end; }
   __device__ __forceinline__ Tile get() const {
     Tile o;
     if (a.start == nullptr) {
-      const int strip = t / (STRIP * tiles_n), in = t - strip * STRIP * tiles_n;
-      const int width = min(STRIP, p.n_m - strip * STRIP);
-      const int n = in / width;
+      const int strip = p.strip.div(t), in = t - strip * p.strip.d;
+      const bool whole = (strip + 1) * STRIP <= p.n_m;
+      const int n = whole ? in / STRIP : p.last.div(in);
       o.g = 0;
-      o.m = strip * STRIP + in - n * width;
+      o.m = strip * STRIP + in - n * (whole ? STRIP : p.last.d);
       o.r0 = n * p.nt;
       o.n = p.nt;
       o.rows = min(p.nt, a.n_rows - o.r0);
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), CG * p.team);
+      mbar_init(smem_addr(&sh.full[i]), CG << p.team_shift);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -541,7 +551,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int g = g0; g < g1; ++g) {
       const int n = group_rows(a, g).n;
       sh.pre[g] = sum;
-      if (n > 0) sum += (long long)((n + p.nt - 1) / p.nt) * p.n_m * (Walk::tile_rows(n, p.nt) + COST_TILE);
+      const int count = (n + p.nt - 1) >> p.nt_shift;
+      if (n > 0) sum += (long long)count * p.n_m * (Walk::tile_rows(n, count) + COST_TILE);
     }
     long long incl = sum;
 #pragma unroll
@@ -571,7 +582,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // No more teams than stages: a warp waits for a slot's last use but one to be over,
   // and parities tell it from the one before only if the warp's own last stage is within
   // a round of the ring.
-  const int teams = min(COPY_WARPS / p.team, p.stages), team = copier / p.team, mate = copier - team * p.team;
+  const int teams = min(COPY_WARPS >> p.team_shift, p.stages), team = copier >> p.team_shift;
+  const int mate = copier - (team << p.team_shift);
   if (warp > 0 && (warp < EPI0 || warp >= EPI0 + EPI_WARPS) && team < teams) {
     // ===== copies: a team every teams-th stage =====================================
     int s = team, turn = team, step = 0;   // stage, step and the tile's first step, of all tiles
@@ -592,11 +604,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int rows_b = t.n / CG, row0 = t.r0 + rank * rows_b;
       // The last group of its own has the rows of x in order: boxes, also where the others
       // gather (four rows an instruction take ~22 cycles, 704 a stage of 256 rows).
+      static_assert(32 / CG == 1 << (6 - CG), "32 rows, or 16 each");
       const int box_rows = main ? p.box_rows : 32 / CG;
       const CUtensorMap* xm = main ? &maps.x : &maps.x_last;
       const uint32_t bytes = (box_rows > 0 ? box_rows : 4) * KS * 2;   // of a copy of X
-      const int all = rows_b * KS * 2 / bytes, copies = (all - mate + p.team - 1) / p.team;
-      const int box = lane * p.team + mate;   // of this lane
+      const int all = a.start == nullptr ? 1 : rows_b >> (main ? p.box_shift : 6 - CG);
+      const int copies = (all - mate + (1 << p.team_shift) - 1) >> p.team_shift;
+      const int box = (lane << p.team_shift) + mate;   // of this lane
       const uint64_t policy = a.start != nullptr && walk.rows.n <= p.nt ? l2_evict_first() : normal;
       int y[4] = {};
       if (box_rows > 0) {
@@ -651,8 +665,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
       int b = 0;
       uint32_t d = 0;
-      // Two stages at a time: their waits and their products' issue run one behind the
-      // other, ~150 and ~200 cycles, and a stage of 192 rows executes in 384.
+      // Two stages at a time: a wait (~150 cycles) and a stage's issue (~200) run one behind
+      // the other, and a stage of 192 rows executes in 384.
       for (int k = 0; k < k_steps; k += 2) {
         const bool two = k + 1 < k_steps;
         const bool first = F32 ? k % SEGMENT == 0 : k == 0;
@@ -816,6 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float bias[4];
         load_bias<SWIGLU>(a, t.g, f0, bias);
         float sum[32] = {};
+#pragma unroll 2
         for (int q = 0; q < splits; ++q) {
           const uint32_t at = parts + (u / splits * splits + q) * PART_BYTES + lane * 16;
 #pragma unroll
@@ -896,8 +911,15 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
   p.n_m = (a.n_out + FE - 1) / FE;
   p.k_steps = (a.n_in + KS - 1) / KS;
   p.splits = splits;
+  p.nt_shift = 0;
+  while ((1 << p.nt_shift) < nt) ++p.nt_shift;
   p.box_rows = a.start == nullptr ? nt / CG : a.index == nullptr ? 32 / CG : 0;
-  p.team = p.box_rows > 0 ? 1 : 2;
+  p.box_shift = p.box_rows > 0 ? 6 - CG : 2;
+  p.team_shift = p.box_rows > 0 ? 0 : 1;
+  const int tiles_n = (a.n_rows + nt - 1) / nt;
+  p.tiles = tiles_n * p.n_m;
+  p.strip = Divisor(STRIP * tiles_n);
+  p.last = Divisor(p.n_m % STRIP != 0 ? p.n_m % STRIP : STRIP);
   p.n_main = a.w_last != nullptr ? a.n_groups - 1 : a.n_groups;
   // (the layer's own indices are in range)
   p.checked = a.index != nullptr && a.w_last == nullptr;
@@ -911,8 +933,7 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
 
   int units = sms / (CG * splits);
   if (a.start == nullptr) {
-    const long long tiles = (long long)((a.n_rows + nt - 1) / nt) * p.n_m;
-    if (tiles < units) units = (int)tiles;
+    if (p.tiles < units) units = p.tiles;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * CG * splits, 1, 1);
@@ -984,7 +1005,7 @@ Choice choose(const LinearArgs& a, int sms) {
   const auto consider = [&](int cg, int n, int splits) {
     const long long tiles = (long long)((a.n_rows + n - 1) / n) * ((a.n_out + fe * cg - 1) / (fe * cg));
     const long long units = splits > 1 ? clusters(splits, sms) : sms / cg;
-    if (units < 1 || (splits > 1 && (tiles > units || k_steps < 4 * splits))) return;
+    if (units < 1 || tiles >= 1 << 24 || (splits > 1 && (tiles > units || k_steps < 4 * splits))) return;
     const int rows = 2 * n + (cg == 2 ? 96 : 224), step = rows > 400 ? rows : 400;
     const long long cost = (tiles + units - 1) / units * ((k_steps + splits - 1) / splits) * step +
                            8 * n / splits + (splits > 1 ? 3000 : cg == 2 ? 700 : 0);

@@ -18,8 +18,13 @@ static_assert(CHUNK <= 255, "a chunk's count of an expert fits a byte");
 // The top k of one token's scores by one warp, as topk_warp ranks them, for scores of
 // any bits: zeros are equal whatever their sign, NaN ranks above every number, and the
 // weights are zeros where all the kept sigmoids are.
+//
+// The k-th largest of the lanes' maxima (each of 8 scores) is at most the k-th largest
+// score, and few scores reach it: those go to a lane each, in the experts' order, and are
+// ranked there, ties to the lower lane.  Half the instructions of sorting every lane's
+// scores, which more than 32 that reach it still take (8192 tokens, 12.0 -> 10.5 us).
 __device__ __forceinline__ void topk_any(const float* row, const float* bias, bool select_only,
-                                         int& idx_out, float& w_out) {
+                                         uint2* slots, int& idx_out, float& w_out) {
   const int lane = threadIdx.x & 31;
   uint32_t k[8], e[8];
 #pragma unroll
@@ -30,9 +35,41 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
     k[j] = key == key ? f2key(key) : ~0u;
     e[j] = (uint32_t)(lane + 32 * j);
   }
+  uint32_t top = k[0], least = 0;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) top = max(top, k[j]);
+#pragma unroll
+  for (int r = 0; r < TOPK; ++r) {
+    least = __reduce_max_sync(0xffffffffu, top);
+    const uint32_t m = __ballot_sync(0xffffffffu, top == least);
+    if (lane == __ffs(m) - 1) top = 0;   // below every key
+  }
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t m = __ballot_sync(0xffffffffu, k[j] >= least);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (k[j] >= least && at < 32) slots[at] = make_uint2(k[j], e[j]);
+    n += __popc(m);
+  }
+  __syncwarp();
   int sel_e[TOPK];
   float sel_v[TOPK];
-  topk_rank(k, e, sel_e, sel_v);
+  if (n <= 32) {
+    uint2 mine = make_uint2(0, 0);
+    if (lane < n) mine = slots[lane];
+#pragma unroll
+    for (int r = 0; r < TOPK; ++r) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, mine.x);
+      const int win = __ffs(__ballot_sync(0xffffffffu, mine.x == best)) - 1;
+      sel_e[r] = (int)__shfl_sync(0xffffffffu, mine.y, win);
+      sel_v[r] = key2f(best);
+      if (lane == win) mine.x = 0;
+    }
+  } else {
+    topk_rank(k, e, sel_e, sel_v);
+  }
+  __syncwarp();   // the slots are the next token's
   float mine = 0.0f;
   idx_out = 0;
 #pragma unroll
@@ -57,6 +94,8 @@ struct Chunk {
   int base[E];      // first row of the expert's pairs of this chunk
   int all[E], before[E];
   int warp_tot[8];
+  uint2 slots[WARPS][32];
+  int expert[CHUNK * TOPK];
 };
 
 __device__ __forceinline__ void copy_choice(const SelectArgs& a, int p, int e, float w) {
@@ -74,8 +113,9 @@ __device__ __forceinline__ void choose(const SelectArgs& a, Chunk& sh, int t0, i
   for (int t = warp; t < n; t += WARPS) {
     int e;
     float w;
-    topk_any(a.logits + (size_t)(t0 + t) * E, a.bias, a.select_only != 0, e, w);
+    topk_any(a.logits + (size_t)(t0 + t) * E, a.bias, a.select_only != 0, sh.slots[warp], e, w);
     if (lane < TOPK) {
+      sh.expert[t * TOPK + lane] = e;
       atomicOr(&sh.mask[e][t >> 5], 1u << (t & 31));
       copy_choice(a, (t0 + t) * TOPK + lane, e, w);
     }
@@ -93,7 +133,7 @@ __device__ __forceinline__ int mask_count(const uint32_t (&m)[WORDS]) {
 // Rows of the chunk's pairs, once sh.base is known.
 __device__ __forceinline__ void place(const SelectArgs& a, Chunk& sh, int t0, int n) {
   for (int p = threadIdx.x; p < n * TOPK; p += THREADS) {
-    const int t = p / TOPK, e = a.idx[t0 * TOPK + p];
+    const int t = p / TOPK, e = sh.expert[p];
     int row = sh.base[e];
 #pragma unroll
     for (int i = 0; i < WORDS; ++i)
@@ -150,19 +190,20 @@ __global__ void __launch_bounds__(THREADS) select_choose_kernel(const SelectArgs
 // experts a thread.
 __global__ void __launch_bounds__(THREADS) select_place_kernel(const SelectArgs a) {
   __shared__ Chunk sh;
+  __shared__ int4 all_of[16][E / 4], before_of[16][E / 4];
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, a.n - t0);
+  static_assert(CHUNK * TOPK <= THREADS, "a pair a thread");
+  const int e = (int)threadIdx.x < n * TOPK ? a.idx[t0 * TOPK + threadIdx.x] : 0;
   for (int i = threadIdx.x; i < E * WORDS; i += THREADS) (&sh.mask[0][0])[i] = 0;
-  if (threadIdx.x < E) sh.all[threadIdx.x] = sh.before[threadIdx.x] = 0;
-  __syncthreads();
-  const int e0 = 4 * (threadIdx.x & 63), first = threadIdx.x >> 6;
+  const int quad = threadIdx.x & 63, first = threadIdx.x >> 6;
   int all[4] = {}, before[4] = {};
 #pragma unroll
   for (int k = 0; k < MAX_CHUNKS / 16; ++k) {
     const int i = first + 16 * k;
     if (i < (int)gridDim.x) {
-      const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(a.counts + i * E + e0));
+      const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(a.counts + i * E + 4 * quad));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = (v >> (8 * j)) & 255;
@@ -171,14 +212,20 @@ __global__ void __launch_bounds__(THREADS) select_place_kernel(const SelectArgs 
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {   // whole numbers: the order does not matter
-    atomicAdd(&sh.all[e0 + j], all[j]);
-    atomicAdd(&sh.before[e0 + j], before[j]);
+  all_of[first][quad] = make_int4(all[0], all[1], all[2], all[3]);
+  before_of[first][quad] = make_int4(before[0], before[1], before[2], before[3]);
+  __syncthreads();
+  if ((int)threadIdx.x < n * TOPK) {
+    const int t = threadIdx.x / TOPK;
+    sh.expert[threadIdx.x] = e;
+    atomicOr(&sh.mask[e][t >> 5], 1u << (t & 31));
   }
-  for (int p = threadIdx.x; p < n * TOPK; p += THREADS) {
-    const int t = p / TOPK;
-    atomicOr(&sh.mask[a.idx[t0 * TOPK + p]][t >> 5], 1u << (t & 31));
+  if (threadIdx.x < 2 * E) {
+    const int* of = reinterpret_cast<const int*>(threadIdx.x < E ? all_of : before_of);
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += of[i * E + (threadIdx.x & (E - 1))];
+    (threadIdx.x < E ? sh.all : sh.before)[threadIdx.x & (E - 1)] = sum;
   }
   __syncthreads();
   starts(a, sh, blockIdx.x == 0);
