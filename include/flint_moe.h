@@ -531,8 +531,8 @@ flint_status flint_prompt_workspace_init(void* workspace, size_t ws_bytes, cudaS
 flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t stream);
 
 /* Fault-injection hook for tests, as flint_moe_debug_arm_stall: a one-shot wait in
- * the next call on this workspace that runs the tiled kernel (any grouped product, a
- * plain one of more than 16 rows, the layer above 128 tokens), on a barrier that nothing completes.  It runs
+ * the next call on this workspace that runs the tiled kernel (a plain product of more
+ * than 16 rows, a grouped one of more than 8, the layer above 128 tokens), on a barrier that nothing completes.  It runs
  * out after a second, the call ends with FLINT_ERR_DEVICE_TIMEOUT as its device
  * status, and the workspace has to be initialised again. */
 flint_status flint_prompt_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream);

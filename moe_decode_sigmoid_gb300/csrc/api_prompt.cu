@@ -89,7 +89,8 @@ bool any_overlap(const Span (&s)[N], int n_out) {
 }
 
 flint_status launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  if (a.start == nullptr && a.n_rows <= lin::FEW_ROWS) return cuda_status(launch_linear_rows(a, stream));
+  if (a.n_rows <= (a.start != nullptr ? lin::FEW_GROUPED : lin::FEW_ROWS))
+    return cuda_status(launch_linear_rows(a, stream));
   const int sms = num_sms();
   if (sms < 2) return FLINT_ERR_CUDA;
   return cuda_status(launch_linear_tiles(a, sms, stream));

@@ -14,6 +14,7 @@ constexpr int MAX_IN = 65536;
 constexpr int MAX_OUT = 1 << 20;
 constexpr int GROUP_LIMIT = 1024;
 constexpr int FEW_ROWS = 16;       // of a plain product that linear_rows.cu takes
+constexpr int FEW_GROUPED = 8;     // of a grouped one, in all
 constexpr int MAX_TOKENS = 8192;   // of a selection and of the layer
 constexpr int CHUNK = 64;          // tokens a CTA of the selection takes
 constexpr int MAX_CHUNKS = MAX_TOKENS / CHUNK;
@@ -39,7 +40,7 @@ struct LinearArgs {
   int n_groups, n_rows, n_x, n_in, n_out, act, out_f32;
   void* ws;
 };
-// A plain product of up to FEW_ROWS rows, and anything.
+// A product of few rows (FEW_ROWS, FEW_GROUPED; no last group of its own), and anything.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream);
 

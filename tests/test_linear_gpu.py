@@ -229,6 +229,21 @@ def test_starts_out_of_range_are_clamped(ws):
     _check_groups(ws, None, 64, 48, p.NONE, start=[30, 20, 25, 25], rows=40)   # the first ends early
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_few_rows_in_groups(ws, act):
+    """Up to nine rows in all (both sides of a kernel's limit): any number of groups, gathered,
+    bad indices, rows of no group, hostile starts, long rows."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for sizes in ([1], [8], [9], [3, 0, 5], [0, 0, 1, 0, 7], [1] * 8, [0] * 700 + [4] + [0] * 323):
+            _check_groups(ws, sizes, 72, 48, act, bias=True, dtype=dtype)
+            _check_groups(ws, sizes, 72, 48, act, n_x=3, dtype=dtype)
+    _check_groups(ws, [2, 0, 6], 4104, 144, act, bias=True)
+    idx = torch.tensor([0, -1, 5, 2, 2 ** 31 - 1, 4, 4], dtype=torch.int32, device="cuda")
+    _check_groups(ws, None, 64, 48, act, start=[1, 3, 3, 6], rows=7, n_x=5, index=idx)
+    for start in ([-5, 3, 8, 2 ** 31 - 1], [2 ** 31 - 1, 5, 6, 9], [-2 ** 31, -7, 0, 0], [6, 2, 4, 4], [0, 0, 0, 0]):
+        _check_groups(ws, None, 64, 48, act, start=start, rows=7)
+
+
 def test_empty_groups_weights_do_not_matter(ws):
     g = p.gen(3)
     x, w = p.bf(g, 12, 64), p.bf(g, 3, 32, 64, scale=0.125)
