@@ -110,8 +110,9 @@ typedef struct {
   int32_t offset_mode;  /* FLINT_OFFSET_LOGIT or FLINT_OFFSET_SELECT */
 } flint_moe_dims;
 
-/* Largest batch (tokens per call) of every entry point but the paged KV-cache
- * calls and those of the linear side of a prompt, which have limits of their own. */
+/* Largest batch (tokens per call) of every entry point but flint_moe_rmsnorm_bf16, the
+ * paged KV-cache calls and those of the linear side of a prompt, which have limits of
+ * their own. */
 #define FLINT_MOE_MAX_BATCH 256
 
 /* Human-readable name of a status code.  Never NULL. */
@@ -257,7 +258,8 @@ flint_status flint_moe_decode_nvfp4_w4a16(
     void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Pre-norm between stacked layers: out[t] = bf16( in[t] / sqrt(mean(in[t]^2) + eps) )
- * (unit gain).  in_bf16 and out_bf16 are [batch, H] and must not overlap.
+ * (unit gain).  in_bf16 and out_bf16 are [batch, H] and must not overlap; batch 1 ..
+ * FLINT_PAGED_MAX_TOKENS (a prompt's rows too).
  * Pre-norm decoder: [vLLM Day-0 Support for Recursive's Flint, "Flint Model
  * Architecture"]. */
 flint_status flint_moe_rmsnorm_bf16(const flint_moe_dims* dims, int32_t batch,

@@ -391,7 +391,7 @@ flint_status flint_moe_rmsnorm_bf16(const flint_moe_dims* dims, int32_t batch, c
                                     void* out_bf16, float eps, cudaStream_t stream) {
   if (dims == nullptr) return FLINT_ERR_INVALID_ARG;
   if (dims->hidden != H) return FLINT_ERR_UNSUPPORTED;
-  if (batch < 1 || batch > MAX_B || !req(in_bf16) || !req(out_bf16) || !(eps >= 0.0f))
+  if (batch < 1 || batch > FLINT_PAGED_MAX_TOKENS || !req(in_bf16) || !req(out_bf16) || !(eps >= 0.0f))
     return FLINT_ERR_INVALID_ARG;
   const size_t act = (size_t)batch * H * 2;
   if (overlap(in_bf16, act, out_bf16, act)) return FLINT_ERR_INVALID_ARG;

@@ -301,6 +301,25 @@ def test_layer_in_a_graph(layer, n):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("n", [257, 1000, 8192])
+def test_rmsnorm_of_a_prompt(n):
+    """The norm in front of the experts for more rows than a decode step has: the bits of
+    calls of 256 rows each, which are within two roundings of 64 bits."""
+    x, _ = fs.tokens(12, n, device="cuda")
+    x = (x.float() * torch.linspace(0.01, 30, n, device="cuda")[:, None]).bfloat16()
+    out, parts = torch.empty_like(x), torch.empty_like(x)
+    m.flint_moe_rmsnorm_bf16(x, out)
+    for i in range(0, n, 256):
+        m.flint_moe_rmsnorm_bf16(x[i:i + 256], parts[i:i + 256])
+    assert torch.equal(out, parts)
+    d = x.double()
+    want = d / (d.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    p.check(out, (want, HALF * want.abs() + 2.0 ** -18 * want.abs() + 1e-38))
+    with pytest.raises(m.FlintError):
+        m.flint_moe_rmsnorm_bf16(torch.zeros(8193, H, dtype=torch.bfloat16, device="cuda"),
+                                 torch.zeros(8193, H, dtype=torch.bfloat16, device="cuda"))
+
+
 def test_a_decoder_layer(layer):
     """Projection, append, attention, output projection into the residual stream, and the
     experts: two prompts through one layer, against 64 bits step by step."""

@@ -166,6 +166,12 @@ def test_layer_refusals(L):
     assert _layer(L, res=A + 7 * STEP + 16) == BAD
 
 
+def test_rmsnorm_rows(L):
+    d = ctypes.byref(m.FULL_DIMS)
+    for n in (0, -1, m.PAGED_MAX_TOKENS + 1):
+        assert L.flint_moe_rmsnorm_bf16(d, n, A, A + STEP, 1e-6, None) == BAD
+
+
 def test_binding_refuses_before_the_library():
     """Tensors that are not what the header lays out: the binding names the argument."""
     x, w, out = torch.zeros(4, 64), torch.zeros(32, 64), torch.zeros(4, 32)
