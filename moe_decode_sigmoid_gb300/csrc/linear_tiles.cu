@@ -104,6 +104,9 @@ struct Tile {
   int g, m, r0, n, rows;  // group, tile of weight rows, first row, rows rounded up, rows
 };
 
+// `begin`: at a kernel's start, where nothing but barriers' initialisation is published,
+// which has a fence of its own.
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -572,9 +575,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc::fence_before();
   __syncthreads();
-  O::sync_all();
+  if constexpr (CG == 2) {
+    cluster_begin();
+    cluster_wait();
+  }
   // (Nobody writes to a CTA of the cluster that has not begun.)
-  if constexpr (SPLIT) cluster_arrive();
+  if constexpr (SPLIT) cluster_begin();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
