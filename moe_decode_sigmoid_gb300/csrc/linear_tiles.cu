@@ -30,7 +30,10 @@
 // tiles (33 x 4096 -> 2048 9.9 us).
 // Tried, and not faster: L2 prefetches of the next tile's weights (285 -> 436 us for the
 // gathered gate/up: 78 MB ahead of use, L2 lost its x), the next rows' accumulators loaded
-// ahead in the epilogue, a last share weighed by where its weights come from.
+// ahead in the epilogue, a last share weighed by where its weights come from; tiles of groups
+// dealt to the pairs from a counter instead of shares (49152 rows 211 -> 205 us, but 4200 rows
+// 87 -> 92, and 2000 tokens' layer 297 -> 305: a pair's own tiles, one after another, read HBM
+// faster).
 #include "linear.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
@@ -55,8 +58,10 @@ constexpr int SEGMENT = 8;                // fp32 outputs: stages that are summe
 constexpr int MAX_SPLITS = 8;             // parts of k: a portable cluster
 constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
 // What a tile of a group costs besides its rows, in rows: its weights' copies, whether
-// they come from HBM or, as those of a group's further tiles of rows, from L2.
-constexpr int COST_TILE = 512;
+// they come from HBM or, as those of a group's further tiles of rows, from L2.  Measured for
+// k = 2048: 9.7 us and 11 ns a row.  (512, 896, 1504, 2496 rows, 49152 rows of the gate/up:
+// 211, 207, 208, 210 us; at k = 512 they do not differ.)
+constexpr int COST_TILE = 896;
 constexpr int STRIP = 8;                  // tiles of weights that share their rows of x in L2
 
 struct Shared {
