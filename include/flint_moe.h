@@ -534,9 +534,10 @@ flint_status flint_prompt_get_device_status(const void* workspace, cudaStream_t 
 
 /* Fault-injection hook for tests, as flint_moe_debug_arm_stall: a one-shot wait in
  * the next call on this workspace that runs the tiled kernel (a plain product of more
- * than 16 rows, a grouped one of more than 8, the layer above 128 tokens), on a barrier that nothing completes.  It runs
- * out after a second, the call ends with FLINT_ERR_DEVICE_TIMEOUT as its device
- * status, and the workspace has to be initialised again. */
+ * than 16 rows, a grouped one of more than 8, the layer above 128 tokens), on a barrier
+ * that nothing completes.  It runs out after a second, the call ends with
+ * FLINT_ERR_DEVICE_TIMEOUT as its device status, and the workspace has to be
+ * initialised again. */
 flint_status flint_prompt_debug_arm_stall(void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* out = act(x w^T + bias) + residual for n_rows rows (1 .. FLINT_LINEAR_MAX_ROWS).

@@ -1,13 +1,14 @@
 // linear_rows.cu — matrix products of a few rows (plain up to FEW_ROWS, grouped up to
-// FEW_GROUPED in all): every weight is read once, straight from global memory into the operands of the warp-level tensor-core
-// product.
+// FEW_GROUPED in all): every weight is read once, straight from global memory into the
+// operands of the warp-level tensor-core product.
 //
 // D (16 weight rows x 8 NB rows of x) += W X^T in steps of 32 k.  The order of k
 // inside a step is free as long as both operands take the same: lane 4 r + c reads
 // the 16 bytes of k = 8c .. 8c + 7 of weight rows r and r + 8 and of x row r, which
 // are the fragments of two m16n8k16 products as they come, with no staging.  The
-// warps of a CTA share the 16 weight rows and take steps in turn; their sums meet in shared memory in a fixed order.  SwiGLU: the 16 weight rows are 8 gate
-// and the 8 up rows of the same outputs.
+// warps of a CTA share the 16 weight rows and take steps in turn; their sums meet in shared
+// memory in a fixed order.  SwiGLU: the 16 weight rows are 8 gate and the 8 up rows of the
+// same outputs.
 //
 // Groups: a CTA for every row and 16 weight rows, which works if the row is the first of a
 // group, for all of the group's.

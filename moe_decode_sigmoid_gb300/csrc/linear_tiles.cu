@@ -26,8 +26,8 @@
 // Bound: the tensor pipe for many rows of few matrices (8192 x 2048 -> SwiGLU 4096: 142 us,
 // 1.94 PFLOP/s, in short runs; 162 at the power limit), HBM for groups (4200 rows, 512 ->
 // 2048, 256 groups 90 us, 6.2 TB/s; 49152 rows, 2048 -> SwiGLU 512 217 us, 5.3 TB/s: a tile
-// of 256 weight rows takes ~13 us whatever its rows, 15.2 tiles a pair), latencies for few
-// tiles (33 x 4096 -> 2048 9.9 us).
+// of 256 weight rows takes 9.7 us and 11 ns a row, 15.2 tiles a pair), latencies for few
+// tiles (33 x 4096 -> 2048 9.0 us).
 // Tried, and not faster: L2 prefetches of the next tile's weights (285 -> 436 us for the
 // gathered gate/up: 78 MB ahead of use, L2 lost its x), the next rows' accumulators loaded
 // ahead in the epilogue, a last share weighed by where its weights come from; tiles of groups
