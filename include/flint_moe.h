@@ -517,8 +517,8 @@ typedef struct {
 /* Bytes of workspace: max_tokens = 0 serves flint_linear_bf16,
  * flint_grouped_linear_bf16 and flint_moe_select (every size), max_tokens in
  * [1, FLINT_PAGED_MAX_TOKENS] also flint_moe_prompt_bf16 of up to so many tokens
- * (1.6 to 10.7 MB up to 128, then about 38 KB a token).  0 for any other
- * max_tokens. */
+ * (1.6 to 10.7 MB up to 128, then about 45 KB a token up to 4096 and 31 KB a token
+ * above, the 193 MB of 4096 tokens at least).  0 for any other max_tokens. */
 size_t flint_prompt_workspace_bytes(int32_t max_tokens);
 
 /* Prepares a workspace (cudaMemsetAsync on `stream`; ws_bytes says whether it serves the
@@ -616,10 +616,11 @@ flint_status flint_moe_combine_bf16(const flint_moe_dims* dims, int32_t n_tokens
  * arguments and the layer as there.  Up to 128 tokens it is that call, bit for bit.
  * Above, where it was measured faster: router scores, selection, gate/up products
  * grouped by expert (the shared expert the last group), down products and the
- * combine, chained on the stream.  h and the experts' outputs are then rounded to
- * bf16 on the way (each at most half a step, 2^-8, of values that are summed), so
- * results differ from flint_moe_decode_bf16's in their last bits, and a token whose
- * sixth and seventh score are within the scores' fp32 rounding may choose either.
+ * combine, chained on the stream.  On the way h is a bf16 pair hi + lo, as in the
+ * decode call, and an expert's output an f16 with a power-of-two scale for every 32
+ * (off by 2^-12 of itself at most, whatever its range), so results differ from
+ * flint_moe_decode_bf16's in their last bits, and a token whose sixth and seventh
+ * score are within the scores' fp32 rounding may choose either.
  * workspace: flint_prompt_workspace_bytes(n_tokens). */
 flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
                                    const void* x_bf16, const void* residual_bf16,

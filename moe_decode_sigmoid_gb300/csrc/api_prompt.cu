@@ -31,10 +31,15 @@ static_assert(DECODE_TOKENS <= MAX_B, "a batch of the decode call");
 constexpr size_t DECODE_WS = align256(lin::WS_HEAD);
 size_t decode_ws_bytes(size_t n) { return WsLayout::total((int)(n < DECODE_TOKENS ? n : DECODE_TOKENS)); }
 
-// The layer's arrays behind that, for n tokens.
+// The layer's arrays behind that, for n tokens: h in pairs of bf16, y in scaled f16 (both rounded
+// to bf16, outputs were off by 9e-2 of max(|out - residual|, a tenth of its rms), against 2e-2 of
+// the decode call).  y has all columns at once, or above WHOLE_TOKENS, where memory counts more
+// than two more launches and h read again (10 to 14 us), half of them in turn.
+constexpr size_t COLUMNS = H / 2, WHOLE_TOKENS = 4096;
+static_assert(COLUMNS % 256 == 0, "whole tiles of weight rows");
 struct Layer {
-  size_t logits, idx, w, start, row_token, pair_row, h, y, end;
-  explicit Layer(size_t n) {
+  size_t logits, idx, w, start, row_token, pair_row, scale, h, y, cols, end;
+  explicit Layer(size_t n) : cols(n <= WHOLE_TOKENS ? H : COLUMNS) {
     logits = align256(DECODE_WS + decode_ws_bytes(n));
     if (n <= DECODE_TOKENS) {
       end = logits;
@@ -45,14 +50,17 @@ struct Layer {
     start = align256(w + n * TOPK * 4);
     row_token = align256(start + (E + 2) * 4);
     pair_row = align256(row_token + n * SLOTS * 4);
-    h = align256(pair_row + n * TOPK * 4);
-    y = align256(h + n * SLOTS * I * 2);
-    end = align256(y + n * SLOTS * H * 2);
+    scale = align256(pair_row + n * TOPK * 4);
+    h = align256(scale + n * SLOTS * (cols / lin::SCALED));
+    y = align256(h + n * SLOTS * I * 4);
+    end = align256(y + n * SLOTS * cols * 2);
   }
 };
 
 size_t workspace_bytes(int tokens) {
-  return tokens == 0 ? align256(lin::WS_HEAD) : Layer(tokens).end;
+  if (tokens == 0) return align256(lin::WS_HEAD);
+  const size_t own = Layer(tokens).end, whole = Layer(tokens < (int)WHOLE_TOKENS ? tokens : WHOLE_TOKENS).end;
+  return own > whole ? own : whole;   // (of every call of fewer tokens too)
 }
 
 flint_status linear_status(const flint_linear_dims* d) {
@@ -272,6 +280,7 @@ flint_status flint_moe_combine_bf16(const flint_moe_dims* dims, int32_t n_tokens
   a.w = topk_w;
   a.out = static_cast<uint16_t*>(out_bf16);
   a.n = n_tokens;
+  a.cols = H;
   return cuda_status(launch_combine(a, stream));
 }
 
@@ -351,30 +360,42 @@ flint_status flint_moe_prompt_bf16(const flint_moe_dims* dims, int32_t n_tokens,
   g.n_in = H;
   g.n_out = I;
   g.act = ACT_SWIGLU;
+  g.pair_out = 1;
   g.ws = workspace;
   if ((st = launch_linear(g, stream)) != FLINT_OK) return st;
 
-  LinearArgs d = g;
-  d.x = reinterpret_cast<const uint16_t*>(ws + at.h);
-  d.w = static_cast<const uint16_t*>(w2_bf16);
-  d.w_last = static_cast<const uint16_t*>(ws2_bf16);
-  d.out = ws + at.y;
-  d.index = nullptr;
-  d.n_x = d.n_rows;
-  d.n_in = I;
-  d.n_out = H;
-  d.act = ACT_NONE;
-  if ((st = launch_linear(d, stream)) != FLINT_OK) return st;
+  for (size_t c0 = 0; c0 < H; c0 += at.cols) {
+    const int cols = (int)(H - c0 < at.cols ? H - c0 : at.cols);
+    LinearArgs d = g;
+    d.x = reinterpret_cast<const uint16_t*>(ws + at.h);
+    d.w = static_cast<const uint16_t*>(w2_bf16) + c0 * I;
+    d.w_last = static_cast<const uint16_t*>(ws2_bf16) + c0 * I;
+    d.out = ws + at.y;
+    d.index = nullptr;
+    d.n_x = d.n_rows;
+    d.n_in = I;
+    d.n_out = cols;
+    d.w_rows = H;
+    d.scale = reinterpret_cast<uint8_t*>(ws + at.scale);
+    d.act = ACT_NONE;
+    d.pair_out = 0;
+    d.pair_in = 1;
+    if ((st = launch_linear(d, stream)) != FLINT_OK) return st;
 
-  CombineArgs c = {};
-  c.residual = static_cast<const uint16_t*>(residual_bf16);
-  c.y = reinterpret_cast<const uint16_t*>(ws + at.y);
-  c.y_shared = c.y + (size_t)n_tokens * TOPK * H;
-  c.pair_row = s.pair_row;
-  c.w = s.w;
-  c.out = static_cast<uint16_t*>(out_bf16);
-  c.n = n_tokens;
-  return cuda_status(launch_combine(c, stream));
+    CombineArgs c = {};
+    c.residual = static_cast<const uint16_t*>(residual_bf16) + c0;
+    c.y = ws + at.y;
+    c.y_shared = reinterpret_cast<const uint16_t*>(ws + at.y) + (size_t)n_tokens * TOPK * cols;
+    c.scale = d.scale;
+    c.scale_shared = d.scale + (size_t)n_tokens * TOPK * (cols / lin::SCALED);
+    c.pair_row = s.pair_row;
+    c.w = s.w;
+    c.out = static_cast<uint16_t*>(out_bf16) + c0;
+    c.n = n_tokens;
+    c.cols = cols;
+    if ((st = cuda_status(launch_combine(c, stream))) != FLINT_OK) return st;
+  }
+  return FLINT_OK;
 }
 
 }  // extern "C"

@@ -9,6 +9,10 @@
 
 namespace flint {
 namespace lin {
+// Scaled f16: SCALED values of a row have one scale, a power of two by its biased exponent,
+// that puts the largest finite one into [2^14, 2^15).  Each is off by 2^-12 of itself at most
+// (2^-39 of the largest, if that is more), whatever their range; 2^-9 for the same bytes in bf16.
+constexpr int SCALED = 32;
 constexpr int MAX_ROWS = 65536;
 constexpr int MAX_IN = 65536;
 constexpr int MAX_OUT = 1 << 20;
@@ -39,6 +43,13 @@ struct LinearArgs {
   const int32_t* index;    // [n_rows] row of x, or null
   int n_groups, n_rows, n_x, n_in, n_out, act, out_f32;
   void* ws;
+  // Of the layer's tiled products.  A pair is two bf16 rows, hi = bf16(v) and lo =
+  // bf16(v - hi), one behind the other: ~16 significant bits and fp32's range.
+  int pair_out;            // out is [n_rows, 2 n_out], pairs (SwiGLU, grouped)
+  int pair_in;             // x is [n_x, 2 n_in], pairs; out scaled f16 (no activation, grouped,
+                           // n_in a multiple of 64, n_out of 32, no index)
+  uint8_t* scale;          // [n_rows, n_out / SCALED] of scaled f16
+  int w_rows;              // rows of a matrix in memory, of which n_out are used, or 0: as many
 };
 // A product of few rows (FEW_ROWS, FEW_GROUPED; no last group of its own), and anything.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
@@ -60,14 +71,18 @@ struct SelectArgs {
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream);
 
+// Columns of H at once: residual and out point at the first one, y and y_shared are
+// [rows, cols], bf16 or, with scales, scaled f16.
 struct CombineArgs {
   const uint16_t* residual;  // [n, H]
-  const uint16_t* y;         // [n TOPK, H]
-  const uint16_t* y_shared;  // [n, H] or null
+  const void* y;             // [n TOPK, cols]
+  const void* y_shared;      // [n, cols] or null
   const int* pair_row;       // [n, TOPK]
   const float* w;            // [n, TOPK]
   uint16_t* out;
-  int n;
+  const uint8_t* scale;        // [n TOPK, cols / SCALED], or null
+  const uint8_t* scale_shared; // [n, cols / SCALED]
+  int n, cols;
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 

@@ -34,6 +34,8 @@
 // dealt to the pairs from a counter instead of shares (49152 rows 211 -> 205 us, but 4200 rows
 // 87 -> 92, and 2000 tokens' layer 297 -> 305: a pair's own tiles, one after another, read HBM
 // faster).
+#include <cuda_fp16.h>
+
 #include "linear.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
@@ -64,6 +66,9 @@ constexpr int PART_BYTES = 4096;          // 32 rows x 32 weight rows of sums
 constexpr int COST_TILE = 896;
 constexpr int STRIP = 8;                  // tiles of weights that share their rows of x in L2
 
+// What a kernel's outputs are, and x: bf16 of bf16, fp32, pairs, and scaled f16 of pairs.
+enum Form { BF16, FP32, PAIR_OUT, PAIR_IN };
+
 struct Shared {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained, never;
   uint32_t tmem;
@@ -92,6 +97,7 @@ struct Plan {
   int nt;          // most rows of a tile, a multiple of 32 (groups: a power of two)
   int nt_shift;    // its logarithm, for groups
   int stages, stage_bytes;
+  int x_bytes;     // of a stage's rows of x (a pair's lo: as many behind them)
   int n_m;         // tiles of weight rows of a group
   int k_steps;
   int box_rows;    // rows of a box of x; 0: four rows an instruction by index
@@ -391,9 +397,10 @@ __device__ __forceinline__ void load_bias(const LinearArgs& a, int g, int f0, fl
 // The epilogue of 32 rows (from row0, `left` of them there) and a warp's weight rows, whose
 // sums are in lo, hi once land() has returned: bias, activation, residual, rounding, and
 // the outputs f0 .. in whole 16-byte parts of rows (fp32: sectors).
-template <bool SWIGLU, bool F32, class Land>
+template <bool SWIGLU, Form FORM, class Land>
 __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint32_t stage, uint32_t block, int f0, int row0,
                                        int left, const float (&bias)[4], uint32_t (&lo)[16], uint32_t (&hi)[16], Land land) {
+  constexpr bool F32 = FORM == FP32;
   constexpr int WF = SWIGLU ? 16 : 32;    // outputs of a warp
   constexpr int ROW = WF * 2 + 16;        // bytes of a row of the transposition
   constexpr int PARTS = WF / 8;           // 16-byte parts of a row: a lane has as many of 32 rows
@@ -483,25 +490,82 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint3
       auto reg = [](int j, int q) {
         return SWIGLU ? 4 * (2 * j + (q >> 1)) + 2 * (q & 1) : 4 * j + 2 * (q & 1) + 8 * (q >> 1);
       };
+      if constexpr (FORM == PAIR_OUT) {
+        static_assert(SWIGLU, "v holds the warp's outputs");
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t at = block + (SWIGLU ? 16 * j : 16 * h + 8 * j) * ROW;
-        uint32_t x[4];
-        if (a.residual != nullptr) {
-          ld_blocks(at, x);
+        for (int lo_part = 0; lo_part < 2; ++lo_part) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[reg(j, q)] += bf_lo(x[q]);
-            v[reg(j, q) + 1] += bf_hi(x[q]);
+          for (int j = 0; j < 2; ++j) {
+            uint32_t x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float &u0 = v[reg(j, q)], &u1 = v[reg(j, q) + 1];
+              x[q] = pack_bf2(u0, u1);
+              u0 -= bf_lo(x[q]);
+              u1 -= bf_hi(x[q]);
+            }
+            st_blocks(block + 16 * j * ROW, x[0], x[1], x[2], x[3]);
           }
-        }
+          __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
-        st_blocks(at, x[0], x[1], x[2], x[3]);
+          for (int i = 0; i < PARTS; ++i) {
+            const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
+            const uint4 o = ld_shared16(stage + tok * ROW + (u % PARTS) * 16);
+            if (store[i])
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                        ((size_t)(row0 + tok) * 2 + lo_part) * a.n_out + f) = o;
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = block + (SWIGLU ? 16 * j : 16 * h + 8 * j) * ROW;
+          uint32_t x[4];
+          if (a.residual != nullptr) {
+            ld_blocks(at, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[reg(j, q)] += bf_lo(x[q]);
+              v[reg(j, q) + 1] += bf_hi(x[q]);
+            }
+          }
+          if constexpr (FORM == PAIR_IN) {
+            // The largest of the 32 outputs of rows 2 c and 2 c + 1 of these: four a lane,
+            // eight lanes.
+            static_assert(WF == SCALED, "a warp's outputs have one scale");
+            float big[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float size = fabsf(v[reg(j, i >> 1) + (i & 1)]);
+              if (size < __int_as_float(0x7f800000)) big[i & 1] = fmaxf(big[i & 1], size);
+            }
+            float inv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+              const int e = max((int)(__float_as_uint(big[i]) >> 23) - 14, 1);
+              inv[i] = __uint_as_float((uint32_t)(254 - e) << 23);
+              const int tok = 16 * h + 8 * j + 2 * c + i;
+              if (r == 0 && tok < left && f0 < a.n_out)
+                a.scale[(size_t)(row0 + tok) * (a.n_out / SCALED) + f0 / SCALED] = (uint8_t)e;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __half2 two = __floats2half2_rn(v[reg(j, q)] * inv[0], v[reg(j, q) + 1] * inv[1]);
+              x[q] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = pack_bf2(v[reg(j, q)], v[reg(j, q) + 1]);
+          }
+          st_blocks(at, x[0], x[1], x[2], x[3]);
+        }
       }
     }
   }
-  if constexpr (!F32) {
+  if constexpr (FORM == BF16 || FORM == PAIR_IN) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
@@ -515,11 +579,13 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint3
 }
 
 // SPLIT: one tile a cluster of `splits` CTAs, each of which has a part of k.
-template <int CG, bool SWIGLU, bool F32, bool SPLIT>
+template <int CG, bool SWIGLU, Form FORM, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tiles_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ Plan p,
                         const __grid_constant__ Maps maps) {
   using O = Ops<CG>;
+  constexpr bool F32 = FORM == FP32;
+  constexpr int X_PARTS = FORM == PAIR_IN ? 2 : 1;
   constexpr int FE = SWIGLU ? 64 : 128;   // outputs of a CTA's tile
   constexpr int WF = FE / 4;              // of a warp
   extern __shared__ uint8_t s_raw[];
@@ -640,7 +706,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t bar = O::leader(smem_addr(&sh.full[s])), dst = smem + s * p.stage_bytes;
         const int k = (k0 + turn - step) * KS;
         if (tc::one_thread()) {
-          O::expect(bar, (mate == 0 ? A_BYTES : 0) + copies * bytes);
+          O::expect(bar, (mate == 0 ? A_BYTES : 0) + X_PARTS * copies * bytes);
           if (mate == 0) {
             if constexpr (SWIGLU) O::copy5(dst, wm, k, f / 16, wg, bar, policy);
             else O::copy3(dst, wm, k, f, wg, bar, policy);
@@ -650,6 +716,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane < copies) {
           if (box_rows > 0) O::copy2(dst + A_BYTES + box * bytes, xm, k, y[0], bar, keep);
           else O::gather4(dst + A_BYTES + box * bytes, xm, k, y, bar, keep);
+          if constexpr (FORM == PAIR_IN)
+            O::copy2(dst + A_BYTES + p.x_bytes + box * bytes, xm, a.n_in + k, y[0], bar, keep);
         }
         __syncwarp();
         if ((s += teams) >= p.stages) {
@@ -664,6 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 0 && rank == 0) {
     // ===== products ================================================================
     const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t x16 = p.x_bytes >> 4;   // of a matrix descriptor's address
     int s = 0, it = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -704,10 +773,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tc::one_thread()) {
 #pragma unroll
           for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + 2 * j, idesc, !first || j > 0);
+          if constexpr (FORM == PAIR_IN)
+#pragma unroll
+            for (int j = 0; j < KS / 16; ++j) O::mma(d, a_lo + 2 * j, b_lo + x16 + 2 * j, idesc, 1);
           O::commit(smem_addr(&sh.empty[s]));
           if (two) {
 #pragma unroll
             for (int j = 0; j < KS / 16; ++j) O::mma(d, a1_lo + 2 * j, b1_lo + 2 * j, idesc, 1);
+            if constexpr (FORM == PAIR_IN)
+#pragma unroll
+              for (int j = 0; j < KS / 16; ++j) O::mma(d, a1_lo + 2 * j, b1_lo + x16 + 2 * j, idesc, 1);
             O::commit(smem_addr(&sh.empty[s1]));
           }
           if (last) O::commit(smem_addr(&sh.acc_full[b]));
@@ -788,7 +863,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int ch = half + 2 * i;
           if (ch < chunks) {
             if constexpr (SPLIT) push(ch, lo[i], hi[i]);
-            else finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo[i], hi[i], [] {});
+            else finish<SWIGLU, FORM>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo[i], hi[i], [] {});
           }
         }
       } else {
@@ -816,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             land();
             push(ch, lo, hi);
           } else {
-            finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, land);
+            finish<SWIGLU, FORM>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, land);
           }
         }
       }
@@ -859,7 +934,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           lo[i] = __float_as_uint(sum[i]);
           hi[i] = __float_as_uint(sum[16 + i]);
         }
-        finish<SWIGLU, F32>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [] {});
+        finish<SWIGLU, FORM>(a, p, stage, block, f0, t.r0 + 32 * ch, t.rows - 32 * ch, bias, lo, hi, [] {});
       }
     }
   }
@@ -887,7 +962,7 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 }
 
 bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int groups) {
-  const cuuint64_t k = a.n_in, n = a.n_out, row = k * 2;
+  const cuuint64_t k = a.n_in, n = a.n_out, row = k * 2, all = a.w_rows > 0 ? a.w_rows : n;
   if (a.act == ACT_SWIGLU) {
     const cuuint64_t dims[5] = {k, 16, 2, n / 16, (cuuint64_t)groups};
     const cuuint64_t strides[4] = {row, n * row, 16 * row, 2 * n * row};
@@ -895,27 +970,29 @@ bool encode_w(CUtensorMap* map, const LinearArgs& a, const void* base, int group
     return encode(map, base, 5, dims, strides, box);
   }
   const cuuint64_t dims[3] = {k, n, (cuuint64_t)groups};
-  const cuuint64_t strides[2] = {row, n * row};
+  const cuuint64_t strides[2] = {row, all * row};
   const cuuint32_t box[3] = {KS, 128, 1};
   return encode(map, base, 3, dims, strides, box);
 }
 
 bool encode_x(CUtensorMap* map, const LinearArgs& a, int rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_x};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.n_in * 2};
+  const cuuint64_t k = (cuuint64_t)a.n_in * (a.pair_in ? 2 : 1);
+  const cuuint64_t dims[2] = {k, (cuuint64_t)a.n_x};
+  const cuuint64_t strides[1] = {k * 2};
   const cuuint32_t box[2] = {KS, (cuuint32_t)rows};
   return encode(map, a.x, 2, dims, strides, box);
 }
 
-template <int CG, bool SWIGLU, bool F32, bool SPLIT>
+template <int CG, bool SWIGLU, Form FORM, bool SPLIT>
 cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done;
-  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU, F32, SPLIT>, SMEM, done);
+  const cudaError_t e = set_smem_limit_once(linear_tiles_kernel<CG, SWIGLU, FORM, SPLIT>, SMEM, done);
   if (e != cudaSuccess) return e;
   constexpr int FE = (SWIGLU ? 64 : 128) * CG;
   Plan p;
   p.nt = nt;
-  p.stage_bytes = A_BYTES + nt / CG * KS * 2;
+  p.x_bytes = nt / CG * KS * 2;
+  p.stage_bytes = A_BYTES + p.x_bytes * (FORM == PAIR_IN ? 2 : 1);
   p.part_bytes = splits > 1 ? (nt / 8 + splits - 1) / splits * splits * PART_BYTES : 0;
   p.stages = (STAGE_AREA - p.part_bytes) / p.stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
@@ -959,16 +1036,20 @@ cudaError_t launch(const LinearArgs& a, int nt, int splits, int sms, cudaStream_
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG * splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU, F32, SPLIT>, a, p, maps);
+  return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<CG, SWIGLU, FORM, SPLIT>, a, p, maps);
 }
 
 template <int CG, bool SPLIT>
 cudaError_t launch_as(const LinearArgs& a, int nt, int splits, int sms, cudaStream_t stream) {
+  if constexpr (!SPLIT) {
+    if (a.pair_out) return launch<CG, true, PAIR_OUT, SPLIT>(a, nt, splits, sms, stream);
+    if (a.pair_in) return launch<CG, false, PAIR_IN, SPLIT>(a, nt, splits, sms, stream);
+  }
   if (a.act == ACT_SWIGLU)
-    return a.out_f32 ? launch<CG, true, true, SPLIT>(a, nt, splits, sms, stream)
-                     : launch<CG, true, false, SPLIT>(a, nt, splits, sms, stream);
-  return a.out_f32 ? launch<CG, false, true, SPLIT>(a, nt, splits, sms, stream)
-                   : launch<CG, false, false, SPLIT>(a, nt, splits, sms, stream);
+    return a.out_f32 ? launch<CG, true, FP32, SPLIT>(a, nt, splits, sms, stream)
+                     : launch<CG, true, BF16, SPLIT>(a, nt, splits, sms, stream);
+  return a.out_f32 ? launch<CG, false, FP32, SPLIT>(a, nt, splits, sms, stream)
+                   : launch<CG, false, BF16, SPLIT>(a, nt, splits, sms, stream);
 }
 
 // Clusters of so many CTAs that the device runs at once: GPCs have no whole number of
@@ -980,7 +1061,7 @@ int clusters(int splits, int sms) {
   int n = known[dev][splits].load(std::memory_order_relaxed);
   if (n == 0) {
     static std::atomic<uint64_t> done;
-    const auto kernel = linear_tiles_kernel<1, false, false, true>;
+    const auto kernel = linear_tiles_kernel<1, false, BF16, true>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits * (sms / splits), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
@@ -1043,9 +1124,11 @@ Choice choose_grouped(const LinearArgs& a, int sms) {
   Choice best = {0, 0, 0, 0};
   for (int n = most; n >= 32; n /= 2)
     for (int cg = 2; cg >= 1; --cg) {
+      // (two stages of pairs are all that one CTA has room for)
+      if (a.pair_in && cg == 1 && n == NT_MAX) continue;
       const long long k = (each + n - 1) / n, units = sms / cg;
       const long long tiles = k * used * ((a.n_out + fe * cg - 1) / (fe * cg));
-      const int rows = (int)((each + k - 1) / k), full = 2 * rows + (cg == 2 ? 96 : 224), least = cg == 2 ? 400 : 440;
+      const int rows = (int)((each + k - 1) / k), full = (a.pair_in ? 4 : 2) * rows + (cg == 2 ? 96 : 224), least = cg == 2 ? 400 : 440;
       const long long cost = (tiles + units - 1) / units * k_steps * (full > least ? full : least) +
                              8 * ((rows + 31) & ~31) + (cg == 2 ? 700 : 0);
       if (best.cg == 0 || cost < best.cost) best = {cg, n, 1, cost};
@@ -1058,15 +1141,15 @@ Choice choose_grouped(const LinearArgs& a, int sms) {
 cudaError_t launch_linear_tiles(const LinearArgs& a, int sms, cudaStream_t stream) {
   // (Weighing the cuts takes a microsecond: a thread remembers its last calls' sizes.)
   struct Known {
-    int rows, groups, in, out, act, f32, sms;
+    int rows, groups, in, out, act, form, sms;
     Choice c;
   };
   static thread_local Known known[16] = {};
-  const int groups = a.start != nullptr ? a.n_groups : 0;
+  const int groups = a.start != nullptr ? a.n_groups : 0, form = a.out_f32 + 2 * a.pair_out + 4 * a.pair_in;
   Known& k = known[(a.n_rows + 3 * a.n_in / 8 + 5 * a.n_out / 8 + groups) & 15];
   if (k.rows != a.n_rows || k.groups != groups || k.in != a.n_in || k.out != a.n_out || k.act != a.act ||
-      k.f32 != a.out_f32 || k.sms != sms)
-    k = {a.n_rows, groups, a.n_in, a.n_out, a.act, a.out_f32, sms, groups > 0 ? choose_grouped(a, sms) : choose(a, sms)};
+      k.form != form || k.sms != sms)
+    k = {a.n_rows, groups, a.n_in, a.n_out, a.act, form, sms, groups > 0 ? choose_grouped(a, sms) : choose(a, sms)};
   const Choice c = k.c;
   if (c.splits > 1) return launch_as<1, true>(a, c.nt, c.splits, sms, stream);
   return c.cg == 2 ? launch_as<2, false>(a, c.nt, 1, sms, stream) : launch_as<1, false>(a, c.nt, 1, sms, stream);

@@ -1,10 +1,13 @@
 // moe_prompt.cu — around the experts' grouped products: the selection of every
 // token's experts with the order of all (token, slot) pairs by expert, and the
-// weighted sum that brings the experts' rows back to the tokens.
+// weighted sum that brings the experts' rows back to the tokens (bf16 rows, or the layer's
+// scaled f16 of some of the columns).
 //
 // Bound: the selection by latencies and the ranking's issue (8192 tokens 10.6 us: 4.7 of
 // ranking, 3.5 of counts and places, two launches; 17 tokens 3.3 us), the combine by HBM (8191
 // tokens 48.9 us, 6.2 TB/s).
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "linear.h"
 #include "select.cuh"
@@ -237,7 +240,17 @@ __global__ void __launch_bounds__(THREADS) select_place_kernel(const SelectArgs 
   place(a, sh, t0, n);
 }
 
-// A token a CTA, 8 values of the row a thread.
+// Two 16-bit values of an expert's row, without their scale.
+template <bool SCALED_F16>
+__device__ __forceinline__ float2 two_of(uint32_t w) {
+  if constexpr (SCALED_F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(bf_lo(w), bf_hi(w));
+}
+__device__ __forceinline__ float scale_of(const uint8_t* at) { return __uint_as_float((uint32_t)*at << 23); }
+
+// A token a CTA, 8 values of the row a thread.  A scale, a power of two, goes into its row's
+// weight.
+template <bool SCALED_F16>
 __global__ void __launch_bounds__(COMBINE) combine_kernel(const CombineArgs a) {
   static_assert(H == 8 * COMBINE, "8 values a thread");
   pdl_wait();
@@ -252,27 +265,38 @@ __global__ void __launch_bounds__(COMBINE) combine_kernel(const CombineArgs a) {
     w[j] = __ldg(a.w + t * TOPK + j);
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const auto row_part = [&](const void* y, int i) {
+    return __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(y) + (size_t)i * a.cols + 8 * threadIdx.x));
+  };
+  const int block = 8 * threadIdx.x / SCALED;
   uint4 v[TOPK], s = zero;
+  float ws = 1.0f;
   const uint4 r = __ldcs(reinterpret_cast<const uint4*>(a.residual + at));
-  if (a.y_shared != nullptr) s = __ldcs(reinterpret_cast<const uint4*>(a.y_shared + at));
+  if (a.y_shared != nullptr) {
+    s = row_part(a.y_shared, t);
+    if constexpr (SCALED_F16) ws = scale_of(a.scale_shared + (size_t)t * (a.cols / SCALED) + block);
+  }
 #pragma unroll
   for (int j = 0; j < TOPK; ++j) {
     v[j] = zero;
-    if ((unsigned)row[j] < (unsigned)(a.n * TOPK))
-      v[j] = __ldcs(reinterpret_cast<const uint4*>(a.y + (size_t)row[j] * H + 8 * threadIdx.x));
-    else
+    if ((unsigned)row[j] < (unsigned)(a.n * TOPK)) {
+      v[j] = row_part(a.y, row[j]);
+      if constexpr (SCALED_F16) w[j] *= scale_of(a.scale + (size_t)row[j] * (a.cols / SCALED) + block);
+    } else {
       w[j] = 0.0f;
+    }
   }
   const uint32_t rw[4] = {r.x, r.y, r.z, r.w}, sw[4] = {s.x, s.y, s.z, s.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo = bf_lo(rw[i]) + bf_lo(sw[i]), hi = bf_hi(rw[i]) + bf_hi(sw[i]);
+    const float2 shared = two_of<SCALED_F16>(sw[i]);
+    float lo = fmaf(ws, shared.x, bf_lo(rw[i])), hi = fmaf(ws, shared.y, bf_hi(rw[i]));
 #pragma unroll
     for (int j = 0; j < TOPK; ++j) {
-      const uint32_t y = i == 0 ? v[j].x : i == 1 ? v[j].y : i == 2 ? v[j].z : v[j].w;
-      lo = fmaf(w[j], bf_lo(y), lo);
-      hi = fmaf(w[j], bf_hi(y), hi);
+      const float2 y = two_of<SCALED_F16>(i == 0 ? v[j].x : i == 1 ? v[j].y : i == 2 ? v[j].z : v[j].w);
+      lo = fmaf(w[j], y.x, lo);
+      hi = fmaf(w[j], y.y, hi);
     }
     o[i] = pack_bf2(lo, hi);
   }
@@ -303,7 +327,8 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
-  return launch(combine_kernel, a.n, COMBINE, a, stream);
+  return a.scale != nullptr ? launch(combine_kernel<true>, a.n, a.cols / 8, a, stream)
+                            : launch(combine_kernel<false>, a.n, a.cols / 8, a, stream);
 }
 
 }  // namespace flint
