@@ -145,8 +145,13 @@ flint_status flint_moe_get_device_status(const void* workspace, cudaStream_t str
  *   logit_bias    [E] fp32 or NULL; per-expert logit offsets, applied as
  *                 dims->offset_mode says (by default added to the logit
  *                 before ranking and before the sigmoid)
- *   topk_idx      [batch, k]   int32 out, expert ids in rank order
- *   topk_w        [batch, k]   fp32 out, renormalised weights
+ *   topk_idx      [batch, k]   int32 out, expert ids in rank order: (logit + offset
+ *                 descending, expert ascending); both zeros are equal, NaN ranks
+ *                 above every number
+ *   topk_w        [batch, k]   fp32 out, renormalised weights: the sigmoids over
+ *                 their sum; zeros where the sum is zero in fp32 (every kept score
+ *                 below -88.8, as those of experts that an offset masks)
+ * Every call that routes does so by this rule.
  * Also leaves the token-to-expert buckets in the workspace for the stage
  * calls below (flint_moe_gateup_bf16 / flint_moe_down_bf16).
  * Router matrix and logits follow "sigmoid top-6" routing:
@@ -582,11 +587,8 @@ flint_status flint_grouped_linear_bf16(const flint_linear_dims* dims, int32_t n_
  * flint_grouped_linear_bf16 takes (dims as the decode calls).
  *   logits      [n_tokens, E] fp32
  *   logit_bias  [E] fp32 or NULL; offsets as dims->offset_mode says
- *   topk_idx    [n_tokens, k] int32 out, experts in rank order: (logit + offset
- *               descending, expert ascending); NaN ranks above every number
- *   topk_w      [n_tokens, k] fp32 out: the sigmoids over their sum; zeros where
- *               that sum is zero (every kept expert masked by an offset of
- *               -infinity or the type's lowest value)
+ *   topk_idx    [n_tokens, k] int32 out, topk_w [n_tokens, k] fp32 out: as
+ *               flint_moe_route ranks and weighs
  *   group_start [E + 1] int32 out: the first pair of each expert, then
  *               n_tokens * k
  *   row_token   [n_tokens * k] int32 out: the token of each pair, ordered by

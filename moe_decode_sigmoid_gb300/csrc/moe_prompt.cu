@@ -22,9 +22,7 @@ constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int WORDS = CHUNK / 32;
 static_assert(CHUNK <= 255, "a chunk's count of an expert fits a byte");
 
-// The top k of one token's scores by one warp, as topk_warp ranks them, for scores of
-// any bits: zeros are equal whatever their sign, NaN ranks above every number, and the
-// weights are zeros where all the kept sigmoids are.
+// The top k of one token's scores by one warp, as topk_warp ranks and weighs them.
 //
 // The k-th largest of the lanes' maxima (each of 8 scores) is at most the k-th largest
 // score, and few scores reach it: those go to a lane each, in the experts' order, and are
@@ -38,9 +36,7 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float score = __ldg(row + lane + 32 * j);
-    // + 0 makes -0 the other zero
-    const float key = (bias != nullptr ? score + __ldg(bias + lane + 32 * j) : score) + 0.0f;
-    k[j] = key == key ? f2key(key) : ~0u;
+    k[j] = rank_key(bias != nullptr ? score + __ldg(bias + lane + 32 * j) : score);
     e[j] = (uint32_t)(lane + 32 * j);
   }
   uint32_t top = k[0], least = 0;
@@ -91,7 +87,7 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
   float sum = 0.0f;
 #pragma unroll
   for (int r = 0; r < TOPK; ++r) sum += __shfl_sync(0xffffffffu, s, r);
-  w_out = sum == 0.0f ? 0.0f : s / sum;
+  w_out = topk_weight(s, sum);
 }
 
 // Ranks of a chunk's pairs: an expert's tokens are the bits of a mask (an expert

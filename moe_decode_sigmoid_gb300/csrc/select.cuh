@@ -20,6 +20,16 @@ __device__ __forceinline__ float key2f(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+// The ranking key of any score: both zeros are equal (+ 0 makes -0 the other one), NaN of
+// either sign ranks above every number.
+__device__ __forceinline__ uint32_t rank_key(float score) {
+  const float f = score + 0.0f;
+  return f == f ? f2key(f) : ~0u;
+}
+// A kept expert's weight: its sigmoid over the kept ones' sum, or zero where they all are (every
+// kept expert masked).
+__device__ __forceinline__ float topk_weight(float sigmoid, float sum) { return sum == 0.0f ? 0.0f : sigmoid / sum; }
+
 // Compare-exchange of a sorting network: (key descending, expert ascending).
 __device__ __forceinline__ void topk_cas(uint32_t (&k)[E / 32], uint32_t (&e)[E / 32], int i, int j) {
   const bool swap = k[j] > k[i] || (k[j] == k[i] && e[j] < e[i]);
@@ -84,7 +94,7 @@ __device__ __forceinline__ void topk_warp(const float* logits_row, const float* 
   for (int j = 0; j < 8; ++j) {
     const float score =
         GLOBAL_SRC ? __ldcg(logits_row + lane + 32 * j) : logits_row[lane + 32 * j];
-    k[j] = f2key(bias ? score + __ldg(bias + lane + 32 * j) : score);
+    k[j] = rank_key(bias ? score + __ldg(bias + lane + 32 * j) : score);
     e[j] = (uint32_t)(lane + 32 * j);
   }
   int sel_e[TOPK];
@@ -106,7 +116,7 @@ __device__ __forceinline__ void topk_warp(const float* logits_row, const float* 
   float ssum = 0.f;
 #pragma unroll
   for (int r = 0; r < TOPK; ++r) ssum += __shfl_sync(0xffffffffu, sv, r);
-  w_out = lane < TOPK ? sv / ssum : 0.f;
+  w_out = lane < TOPK ? topk_weight(sv, ssum) : 0.f;
 }
 
 // Optional plain description of the buckets (flint_moe_bucket).
