@@ -1,5 +1,9 @@
 // linear.cuh — what the kernels of the linear side of a prompt share: a group's
 // rows with everything the host could not check kept in bounds, activations.
+//
+// Every input of these calls, weights and bias too, can be what the library's kernel before
+// wrote, which may still run when this one begins.  So all are read by ordinary loads behind
+// pdl_wait(), none through the read-only path, which is for what nobody writes while a kernel runs.
 #pragma once
 
 #include "common.cuh"
@@ -14,8 +18,8 @@ struct Rows {
 };
 __device__ __forceinline__ Rows group_rows(const LinearArgs& a, int g) {
   if (a.start == nullptr) return {0, a.n_rows};
-  const int lo = min(max(__ldg(a.start + g), 0), a.n_rows);
-  return {lo, min(max(__ldg(a.start + g + 1), lo), a.n_rows) - lo};
+  const int lo = min(max(a.start[g], 0), a.n_rows);
+  return {lo, min(max(a.start[g + 1], lo), a.n_rows) - lo};
 }
 
 // v / (1 + exp(-v)), and v (1 + erf(v / sqrt 2)) / 2 by the complement, which keeps

@@ -30,7 +30,7 @@ constexpr int DEEP = 8;   // steps of weights in flight a warp
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p, bool there) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  if (there) v = __ldg(reinterpret_cast<const uint4*>(p));
+  if (there) v = *reinterpret_cast<const uint4*>(p);
   return v;
 }
 
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const LinearArg
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     int row = 8 * b + r < rows.n ? rows.r0 + 8 * b + r : -1;
-    if (GROUPED && row >= 0 && a.index != nullptr) row = __ldg(a.index + row);
+    if (GROUPED && row >= 0 && a.index != nullptr) row = a.index[row];
     xr[b] = (unsigned)row < (unsigned)a.n_x ? a.x + (size_t)row * a.n_in : nullptr;
   }
   float acc[NB][4] = {};
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const LinearArg
     const int t = o / FE, f = o % FE;
     const int row = rows.r0 + t;
     bool store = t < rows.n && f0 + f < a.n_out;
-    if (GROUPED && store && a.index != nullptr) store = (unsigned)__ldg(a.index + row) < (unsigned)a.n_x;
+    if (GROUPED && store && a.index != nullptr) store = (unsigned)a.index[row] < (unsigned)a.n_x;
     if (store) {
       float v = 0.0f, up = 0.0f;
 #pragma unroll
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const LinearArg
         if constexpr (SWIGLU) up += part[i][t][f + 8];
       }
       if (a.bias != nullptr) {
-        v += __ldg(a.bias + (size_t)g * m + f0 + f);
-        if constexpr (SWIGLU) up += __ldg(a.bias + (size_t)g * m + a.n_out + f0 + f);
+        v += a.bias[(size_t)g * m + f0 + f];
+        if constexpr (SWIGLU) up += a.bias[(size_t)g * m + a.n_out + f0 + f];
       }
       if constexpr (SWIGLU)
         v = activate(v, ACT_SILU) * up;

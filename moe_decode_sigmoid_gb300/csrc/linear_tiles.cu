@@ -390,7 +390,7 @@ __device__ __forceinline__ void load_bias(const LinearArgs& a, int g, int f0, fl
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int f = SWIGLU ? f0 + r + 8 * (i & 1) : f0 + r + 8 * i;
-    bias[i] = a.bias != nullptr && f < a.n_out ? __ldg(src + f + (SWIGLU && i >= 2 ? a.n_out : 0)) : 0.0f;
+    bias[i] = a.bias != nullptr && f < a.n_out ? src[f + (SWIGLU && i >= 2 ? a.n_out : 0)] : 0.0f;
   }
 }
 
@@ -413,7 +413,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint3
     for (int i = 0; i < PARTS; ++i) {
       const int u = lane + 32 * i, tok = u / PARTS, f = f0 + 8 * (u % PARTS);
       store[i] = tok < left && f < a.n_out;
-      if (p.checked && store[i]) store[i] = (unsigned)__ldg(a.index + row0 + tok) < (unsigned)a.n_x;
+      if (p.checked && store[i]) store[i] = (unsigned)a.index[row0 + tok] < (unsigned)a.n_x;
     }
     if (a.residual != nullptr) {
 #pragma unroll
@@ -471,7 +471,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const Plan& p, uint3
         static_assert(FROWS * FPARTS == 128, "4 parts a lane");
         if (tok < left && f < a.n_out) {
           const int row = row0 + tok;
-          if (!p.checked || (unsigned)__ldg(a.index + row) < (unsigned)a.n_x) {
+          if (!p.checked || (unsigned)a.index[row] < (unsigned)a.n_x) {
             const size_t at = (size_t)row * a.n_out + f;
             uint4 o = ld_shared16(stage + (u / FPARTS) * FROW + (u % FPARTS) * 16);
             if (a.residual != nullptr) {
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 4; ++j) {
           // A row of no index is not stored: any row will do.
           const int r = row0 + 4 * box + j;
-          if (r < a.n_rows) y[j] = __ldg(a.index + r);
+          if (r < a.n_rows) y[j] = a.index[r];
           if ((unsigned)y[j] >= (unsigned)a.n_x) y[j] = 0;
         }
       }

@@ -35,8 +35,8 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
   uint32_t k[8], e[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float score = __ldg(row + lane + 32 * j);
-    k[j] = rank_key(bias != nullptr ? score + __ldg(bias + lane + 32 * j) : score);
+    const float score = row[lane + 32 * j];
+    k[j] = rank_key(bias != nullptr ? score + bias[lane + 32 * j] : score);
     e[j] = (uint32_t)(lane + 32 * j);
   }
   uint32_t top = k[0], least = 0;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void topk_any(const float* row, const float* bias, bo
       mine = sel_v[r];
       idx_out = sel_e[r];
     }
-  if (select_only && lane < TOPK) mine = __ldg(row + idx_out);
+  if (select_only && lane < TOPK) mine = row[idx_out];
   const float s = 1.0f / (1.0f + expf(-mine));
   float sum = 0.0f;
 #pragma unroll
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(COMBINE) combine_kernel(const CombineArgs a) {
   float w[TOPK];
 #pragma unroll
   for (int j = 0; j < TOPK; ++j) {
-    row[j] = __ldg(a.pair_row + t * TOPK + j);
-    w[j] = __ldg(a.w + t * TOPK + j);
+    row[j] = a.pair_row[t * TOPK + j];
+    w[j] = a.w[t * TOPK + j];
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const auto row_part = [&](const void* y, int i) {
