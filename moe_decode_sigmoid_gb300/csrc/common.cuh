@@ -168,6 +168,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // Programmatic dependent launch: wait for the preceding grid's completion and
 // memory flush / allow the next grid to start launching.
+// What the preceding grid writes is written while this one runs: it is read by ordinary loads
+// behind the wait, never through the read-only path (__ldg), which is for what was complete
+// before this grid began (a grid before the preceding one is: that one waited for it before it
+// let this one start).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -870,7 +870,7 @@ __device__ __forceinline__ void moe_small_body(ExpertArgs a, RouterArgs r) {
     uint4 v[fz::MAXB];
 #pragma unroll
     for (int t = 0; t < fz::MAXB; ++t)
-      v[t] = t < B ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * H) + tid)
+      v[t] = t < B ? reinterpret_cast<const uint4*>(a.x + (size_t)t * H)[tid]
                    : make_uint4(0u, 0u, 0u, 0u);
     if constexpr (PRENORM) {
       __shared__ float s_norm[fz::MAXB][fz::CW];

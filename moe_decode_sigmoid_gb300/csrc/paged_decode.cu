@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(Cfg<FP8, NT>::THREADS, 1)
       now.row = cache_row(b, sg.seq, (sg.g0 + i) << 4);
       if (FP8 && now.row >= 0) {
         const size_t at = (size_t)(now.row >> 4) * b.nkv + sg.kvh;
-        now.ks = __ldg(a.k_scale + at);
-        now.vs = __ldg(a.v_scale + at);
+        now.ks = a.k_scale[at];
+        now.vs = a.v_scale[at];
       }
     }
   };

@@ -897,8 +897,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto scales = [&]() {
         if (FP8 && !v && row1 >= 0) {
           const size_t at = (size_t)(row1 >> 4) * b.nkv + p.kvh;
-          ks1 = __ldg(a.k_scale + at);
-          vs1 = __ldg(a.v_scale + at);
+          ks1 = a.k_scale[at];
+          vs1 = a.v_scale[at];
         }
       };
       scales();

@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(256) router_kernel(RouterArgs a) {
   for (int t = 0; t < 8; ++t) {
     if (t < nt) {
       const uint4* xrow = reinterpret_cast<const uint4*>(a.x + (size_t)(t0 + t) * H);
-      xv[t][0] = __ldg(xrow + c0);
-      xv[t][1] = __ldg(xrow + c1);
+      xv[t][0] = xrow[c0];
+      xv[t][1] = xrow[c1];
     } else {
       xv[t][0] = xv[t][1] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(256) router_mma_kernel(RouterArgs a) {
 #pragma unroll
   for (int b = 0; b < 8; ++b) {  // all loads of the slice in flight at once
     const int c = warp * 32 + b * 4 + q;  // 16-byte chunk: columns 256w + 32b + 8q
-    xl[b] = lo_in ? __ldg(xlo + c) : zero;
-    xh[b] = hi_in ? __ldg(xhi + c) : zero;
+    xl[b] = lo_in ? xlo[c] : zero;
+    xh[b] = hi_in ? xhi[c] : zero;
   }
   float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
