@@ -746,6 +746,8 @@ def _linear(f, x, out, act):
     try:
         n_x, k = x.shape
         rows, n = out.shape
+        if type(act) is not int:   # 1.0 and True would find the entry of 1
+            raise KeyError(act)
         ref, m = _LINEAR_DIMS[k, n, act, dtype is _F32]
     except (AttributeError, ValueError, TypeError, KeyError):
         ref, m = _linear_dims(f, x, out, act)
@@ -774,8 +776,8 @@ def flint_linear_bf16(x, w, out, workspace, bias=None, residual=None, act: int =
         f32 = out.dtype is _F32
         ref, m = _LINEAR_DIMS[k, n, act, f32]
         gpu = _current_gpu()
-        good = (r == rows <= LINEAR_MAX_ROWS and x.dtype is _BF16 and w.dtype is _BF16 and
-                (f32 or out.dtype is _BF16) and w.shape == (m, k) and x.is_contiguous() and
+        good = (type(act) is int and r == rows <= LINEAR_MAX_ROWS and x.dtype is _BF16 and
+                w.dtype is _BF16 and (f32 or out.dtype is _BF16) and w.shape == (m, k) and x.is_contiguous() and
                 w.is_contiguous() and out.is_contiguous() and
                 x.get_device() == w.get_device() == out.get_device() == workspace.get_device() == gpu and
                 workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous())
@@ -811,7 +813,7 @@ def flint_grouped_linear_bf16(x, w, group_start, out, workspace, row_index=None,
         ref, m = _LINEAR_DIMS[k, n, act, f32]
         groups = w.shape[0]
         gpu = _current_gpu()
-        good = (0 < n_x <= LINEAR_MAX_ROWS and 0 < rows <= LINEAR_MAX_ROWS and
+        good = (type(act) is int and 0 < n_x <= LINEAR_MAX_ROWS and 0 < rows <= LINEAR_MAX_ROWS and
                 0 < groups <= LINEAR_MAX_GROUPS and x.dtype is _BF16 and w.dtype is _BF16 and
                 (f32 or out.dtype is _BF16) and group_start.dtype is _I32T and
                 w.shape == (groups, m, k) and group_start.shape == (groups + 1,) and
