@@ -22,10 +22,15 @@ __device__ __forceinline__ Rows group_rows(const LinearArgs& a, int g) {
   return {lo, min(max(a.start[g + 1], lo), a.n_rows) - lo};
 }
 
-// v / (1 + exp(-v)), and v (1 + erf(v / sqrt 2)) / 2 by the complement, which keeps
-// its relative accuracy where 1 + erf cancels.
+// v / (1 + exp(-v)), for v < 0 as v e / (1 + e) with e = exp(v), which does not overflow (from
+// v = -88.8 on the first form is zero, the other down to -103, where e is); and
+// v (1 + erf(v / sqrt 2)) / 2 by the complement, which keeps its relative accuracy where 1 + erf
+// cancels.
 __device__ __forceinline__ float activate(float v, int act) {
-  if (act == ACT_SILU) return v / (1.0f + expf(-v));
+  if (act == ACT_SILU) {
+    const float e = expf(-fabsf(v));
+    return (v < 0.0f ? v * e : v) / (1.0f + e);
+  }
   if (act == ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
   return v;
 }

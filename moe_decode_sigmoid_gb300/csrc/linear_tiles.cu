@@ -370,10 +370,13 @@ struct Walk {
   }
 };
 
-// silu of an output that is rounded to bf16: exponential and quotient of the fast
-// kind, off by ~|v| + 4 units of fp32's last place (2^-17 of the value at v = -87; below
-// that the value, under 1e-36, becomes zero), against a rounding of 2^-8.
-__device__ __forceinline__ float silu_bf16(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+// silu of an output that is rounded to bf16 or a pair, as activate() takes it: exponential and
+// quotient of the fast kind, off by ~|v| + 4 units of fp32's last place (2^-17 of the value at
+// v = -87), against a rounding of 2^-9 or 2^-17.
+__device__ __forceinline__ float silu_bf16(float v) {
+  const float e = __expf(-fabsf(v));
+  return __fdividef(v < 0.0f ? v * e : v, 1.0f + e);
+}
 
 // Where a lane's row of the epilogue's four 8 x 8 blocks lies.
 template <bool SWIGLU>
