@@ -132,7 +132,8 @@ def test_workspace_is_enough(layer, n):
     for k in (n // 2, 128, 1):
         if k > 0:
             m.flint_moe_prompt_bf16(x[:k], res[:k], *args, again[:k], ws)
-    m.flint_moe_prompt_bf16(x, res, *args, again, ws)
+    again = res.clone()
+    m.flint_moe_prompt_bf16(x, again, *args, again, ws)   # in place
     assert m.flint_prompt_get_device_status(ws) == m.FLINT_OK
     assert (memory[size:] == 0x5A).all()
     assert torch.equal(out, again)
