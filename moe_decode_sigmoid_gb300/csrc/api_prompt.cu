@@ -23,9 +23,9 @@ static_assert(FLINT_ACT_NONE == ACT_NONE && FLINT_ACT_SILU == ACT_SILU && FLINT_
               "the public activations are the kernels'");
 
 // Up to so many tokens the layer is flint_moe_decode_bf16, in a workspace of its own behind
-// the head.  Measured with the weights in HBM, decode against products by expert, us: 1
-// token 17 / 32, 16 90 / 104, 64 198 / 214, 96 224 / 236, 128 250 / 257, 192 279 / 262; with
-// skewed routing 64 152 / 162, 96 185 / 189, 128 202 / 198, 192 248 / 212.
+// the head.  Measured with the weights in HBM, decode against products by expert, us: 16
+// tokens 95 / 107, 64 202 / 210, 96 228 / 237, 128 257 / 257, 192 281 / 257, 256 337 / 262; with
+// skewed routing 64 152 / 159, 96 188 / 191, 128 200 / 189, 192 250 / 206.
 constexpr int DECODE_TOKENS = 128;
 static_assert(DECODE_TOKENS <= MAX_B, "a batch of the decode call");
 constexpr size_t DECODE_WS = align256(lin::WS_HEAD);

@@ -13,12 +13,15 @@
 // Groups: a CTA for every row and 16 weight rows, which works if the row is the first of a
 // group, for all of the group's.
 //
-// Bound: launch and first-load latency at a few MB of weights, and their bytes: one row of
-// 2048 -> 5120 (21 MB) takes 5.9 us from HBM and 4.5 from L2, 16 rows of 4096 -> 2048 9.0
-// and 5.4.  Tried: an L2 prefetch of the weights while the kernel before ends (8.1 us from
-// HBM), more rows here (33: 14 us; the tiled kernel 9).  Grouped, 2048 -> SwiGLU 512: 1 row
-// 3.7 us (tiled 12.7), 6 rows 9.0 (13.7), 12 rows 15.8 (15.6), and 16 rows of 4096 -> 4096
-// 116 (92).
+// Bound: launch and first-load latency at a few MB of weights, and their bytes, of which
+// less is in flight than there could be: one row of 2048 -> 5120 (21 MB) takes 5.8 us from HBM
+// and 4.5 from L2, 16 rows of 4096 -> 2048 8.8 and 5.4.  The loads of DEEP steps stand before
+// their products, but the compiler gives the kernels 44 to 74 registers, where DEEP steps of
+// weights alone take 64, and so moves some loads to their products; rows of x come with the
+// products; and 320 equal CTAs lie on 152 SMs.  Tried: an L2 prefetch of the weights while the
+// kernel before ends (8.1 us from HBM), more rows here (33: 14 us; the tiled kernel 9).
+// Grouped, 2048 -> SwiGLU 512: 1 row 7 us (from L2 3.6; tiled 12.7), 6 rows 8-9 (13.7), 12 rows
+// 15.8 (15.6), and 16 rows of 4096 -> 4096 116 (92).
 #include "linear.cuh"
 
 namespace flint {
@@ -26,7 +29,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int DEEP = 8;   // steps of weights in flight a warp
+constexpr int DEEP = 8;   // steps whose weights are loaded before the first one's products
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p, bool there) {
   uint4 v = make_uint4(0, 0, 0, 0);
@@ -149,7 +152,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
 
 template <int NB, bool GROUPED>
 cudaError_t launch_as(const LinearArgs& a, cudaStream_t stream) {
-  // Sixteen warps where eight do not have all the weights in flight at once.
+  // Sixteen warps where eight would take more than one turn of DEEP steps.
   return a.n_in > 32 * 8 * DEEP ? launch<NB, 16, GROUPED>(a, stream) : launch<NB, 8, GROUPED>(a, stream);
 }
 

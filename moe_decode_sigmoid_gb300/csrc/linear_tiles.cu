@@ -17,6 +17,9 @@
 //   warps 4-11  epilogue: bias, activation and residual on fragments of 16 outputs x
 //               8 rows, transposed to rows through shared memory 8 x 8 at a time
 // TMEM holds two accumulators: a tile's epilogue runs beside the next one's products.
+// The layer's products: gate/up leaves h as pairs of bf16 (PAIR_OUT), down takes them, hi and
+// lo on the same weights of a stage, and leaves f16 with a scale for every 32 outputs, which a
+// warp of the epilogue has (PAIR_IN).
 //
 // Groups: the tiles' costs (their rows, and COST_TILE for what a tile costs besides) are
 // laid end to end and cut into equal shares, a tile belonging to the share where it
@@ -24,10 +27,13 @@
 // over a cluster of CTAs (SPLIT), whose sums are joined in their order.
 //
 // Bound: the tensor pipe for many rows of few matrices (8192 x 2048 -> SwiGLU 4096: 142 us,
-// 1.94 PFLOP/s, in short runs; 162 at the power limit), HBM for groups (4200 rows, 512 ->
-// 2048, 256 groups 90 us, 6.2 TB/s; 49152 rows, 2048 -> SwiGLU 512 217 us, 5.3 TB/s: a tile
-// of 256 weight rows takes 9.7 us and 11 ns a row, 15.2 tiles a pair), latencies for few
-// tiles (33 x 4096 -> 2048 9.0 us).
+// 1.94 PFLOP/s, in short runs; 163 at the power limit; 8192 x 2048 -> 4096 74 us, with SiLU 76,
+// with GELU, whose erfc the epilogue takes longer for than the products, 115), HBM for groups
+// (4200 rows, 512 -> 2048, 256 groups 90 us, 6.2 TB/s; 49152 rows, 2048 -> SwiGLU 512 214-222 us,
+// 5.3 TB/s: a tile of 256 weight rows takes 9.7 us and 11 ns a row, 15.2 tiles a pair), latencies
+// for few tiles (33 x 4096 -> 2048 9.0 us; 128 x 2048 -> 5120 12.6).  The down product of pairs
+// (57344 rows, 512 -> 1024) takes 111 us: 553 MB at 5.0 TB/s beside a tensor pipe 51 % busy,
+// 13.2 K cycles a tile of 192 rows, of which its products are 6.7.
 // Tried, and not faster: L2 prefetches of the next tile's weights (285 -> 436 us for the
 // gathered gate/up: 78 MB ahead of use, L2 lost its x), the next rows' accumulators loaded
 // ahead in the epilogue, a last share weighed by where its weights come from; tiles of groups

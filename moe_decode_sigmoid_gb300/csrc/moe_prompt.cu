@@ -5,7 +5,7 @@
 //
 // Bound: the selection by latencies and the ranking's issue (8192 tokens 10.6 us: 4.7 of
 // ranking, 3.5 of counts and places, two launches; 17 tokens 3.3 us), the combine by HBM (8191
-// tokens 48.9 us, 6.2 TB/s).
+// tokens 48 us, 6.3 TB/s; half the columns of 8192 tokens' scaled f16 25 us, 6.1).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
